@@ -33,10 +33,14 @@ __all__ = [
     "pack_layer_weights_fp8", "moe_selftest_bounded_wait", "MOE_ROUTER_WEIGHT_F32",
     "MOE_ROUTER_WEIGHT_SPLIT", "moe_router_weight_split_bytes", "moe_split_router_weight",
     "split_router_weight",
+    "MOE_WEIGHTS_PACKED_INT4_G32", "MOE_WEIGHTS_PACKED_INT4_G128", "moe_packed_int4_bytes",
+    "moe_pack_weights_int4", "pack_int4", "moe_grouped_swiglu_fp8_rows", "moe_linear_int4",
+    "moe_add_rmsnorm",
 ]
 
 MOE_F32, MOE_BF16 = 0, 1
 MOE_WEIGHTS_NATURAL, MOE_WEIGHTS_PACKED, MOE_WEIGHTS_PACKED_FP8 = 0, 1, 2
+MOE_WEIGHTS_PACKED_INT4_G32, MOE_WEIGHTS_PACKED_INT4_G128 = 3, 4
 MOE_PACK_GATE_UP, MOE_PACK_PLAIN = 0, 1
 MOE_ROUTER_WEIGHT_F32, MOE_ROUTER_WEIGHT_SPLIT = 0, 1
 MOE_STAGE_COUNT = 5
@@ -97,6 +101,11 @@ _SIGS = {
     "moe_packed_fp8_bytes": ([_I64, _I64, _I64], _I64),
     "moe_selftest_bounded_wait": ([_P, _P], _I32),
     "moe_pack_weights_fp8": ([_I32, _I64, _I64, _I64, _P, _P, _P, _P], _I32),
+    "moe_packed_int4_bytes": ([_I64, _I64, _I64, _I32], _I64),
+    "moe_pack_weights_int4": ([_I32, _I64, _I64, _I64, _I32, _P, _P, _P, _P], _I32),
+    "moe_grouped_swiglu_fp8_rows": ([_CFG, _I64] + [_P] * 14 + [_SZ, _P], _I32),
+    "moe_linear_int4": ([_I64, _I32, _I32, _I32] + [_P] * 6, _I32),
+    "moe_add_rmsnorm": ([_I32, _I64, _I32, _P, _P, _P, _F] + [_P] * 5, _I32),
     "moe_router_noalloc": ([_CFG, _I64, _P, _P, _P, _P, _P, _P], _I32),
     "moe_router_weight_split_bytes": ([_CFG], _SZ),
     "moe_split_router_weight": ([_CFG, _P, _P, _P], _I32),
@@ -390,3 +399,54 @@ def pack_layer_weights(weights: dict, stream=None) -> dict:
         moe_pack_weights(kind, w3.shape[0], w3.shape[1], w3.shape[2], w3, dst, stream)
         out[key] = dst if w.dim() == 3 else dst.squeeze(0)
     return out
+
+
+def moe_packed_int4_bytes(groups, rows, cols, group_size) -> int:
+    return int(lib.moe_packed_int4_bytes(groups, rows, cols, group_size))
+
+
+def moe_pack_weights_int4(kind, groups, rows, cols, group_size, codes, scales, dst, stream=None):
+    _check(lib.moe_pack_weights_int4(kind, groups, rows, cols, group_size, _ptr(codes),
+                                     _ptr(scales), _ptr(dst), _stream(stream)),
+           "moe_pack_weights_int4")
+
+
+def pack_int4(kind, codes, scales, stream=None):
+    """One 4-bit bank packed into a new uint8 buffer: codes [G, rows, cols / 2]
+    uint8 (two a byte, the even column low) and scales [G, rows, cols /
+    group_size] bf16, kind as in moe_pack_weights (a one-time load step)."""
+    import torch
+    G, R, C = codes.shape[0], codes.shape[1], 2 * codes.shape[2]
+    group = C // scales.shape[2]
+    dst = torch.empty(max(moe_packed_int4_bytes(G, R, C, group), 0), dtype=torch.uint8,
+                      device=codes.device)
+    moe_pack_weights_int4(kind, G, R, C, group, codes.contiguous(), scales.contiguous(), dst,
+                          stream)
+    return dst
+
+
+def moe_grouped_swiglu_fp8_rows(cfg, T, x_e, x_e_scale, offsets, perm, topk_w, W_gate_up, W_down,
+                                x_shared, x_shared_scale, Ws_gate_up, Ws_down, Y, Y_shared,
+                                workspace, ws_bytes, stream=None):
+    """moe_grouped_swiglu on E4M3 rows with one fp32 scale per 128 columns (a
+    4-bit weight layout)."""
+    _check(lib.moe_grouped_swiglu_fp8_rows(
+        ctypes.byref(cfg), T, _ptr(x_e), _ptr(x_e_scale), _ptr(offsets), _ptr(perm), _ptr(topk_w),
+        _ptr(W_gate_up), _ptr(W_down), _ptr(x_shared), _ptr(x_shared_scale), _ptr(Ws_gate_up),
+        _ptr(Ws_down), _ptr(Y), _ptr(Y_shared), _ptr(workspace), ws_bytes, _stream(stream)),
+           "moe_grouped_swiglu_fp8_rows")
+
+
+def moe_linear_int4(T, in_features, out_features, group_size, x, x_scale, W, add, y, stream=None):
+    """y = x W^T (+ add) with a packed 4-bit W; x bf16, or E4M3 with x_scale."""
+    _check(lib.moe_linear_int4(T, in_features, out_features, group_size, _ptr(x), _ptr(x_scale),
+                               _ptr(W), _ptr(add), _ptr(y), _stream(stream)), "moe_linear_int4")
+
+
+def moe_add_rmsnorm(dtype, T, d, x, residual, weight, eps, h, y, y_fp8=None, y_scale=None,
+                    stream=None):
+    """h = x + residual, y = weight * h / rms(h), in `dtype` and / or in E4M3
+    with a scale per 128 columns."""
+    _check(lib.moe_add_rmsnorm(dtype, T, d, _ptr(x), _ptr(residual), _ptr(weight), float(eps),
+                               _ptr(h), _ptr(y), _ptr(y_fp8), _ptr(y_scale), _stream(stream)),
+           "moe_add_rmsnorm")

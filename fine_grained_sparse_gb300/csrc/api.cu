@@ -175,6 +175,11 @@ int32_t check_router_cfg(const moe_config* c, int64_t T) {
   return MOE_OK;
 }
 
+// Columns of one scale of a 4-bit layout; 0 for the other layouts.
+int int4_group(int layout) {
+  return layout == MOE_WEIGHTS_PACKED_INT4_G32 ? 32 : layout == MOE_WEIGHTS_PACKED_INT4_G128 ? 128 : 0;
+}
+
 int32_t check_layer_cfg(const moe_config* c, int64_t T) {
   int32_t st = check_router_cfg(c, T);
   if (st != MOE_OK) return st;
@@ -183,7 +188,7 @@ int32_t check_layer_cfg(const moe_config* c, int64_t T) {
   if (c->E_shared > 0 && c->d_ff_shared < 1) return fail(MOE_ERR_INVALID_ARG, "d_ff_shared < 1");
   if (c->d_latent < 0) return fail(MOE_ERR_INVALID_ARG, "d_latent < 0");
   if (c->weight_layout != MOE_WEIGHTS_NATURAL && c->weight_layout != MOE_WEIGHTS_PACKED &&
-      c->weight_layout != MOE_WEIGHTS_PACKED_FP8)
+      c->weight_layout != MOE_WEIGHTS_PACKED_FP8 && !int4_group(c->weight_layout))
     return fail(MOE_ERR_INVALID_ARG, "weight_layout");
   if (c->weight_layout != MOE_WEIGHTS_NATURAL && c->dtype != MOE_BF16)
     return fail(MOE_ERR_UNSUPPORTED_SHAPE, "packed weights need bf16 activations");
@@ -191,6 +196,10 @@ int32_t check_layer_cfg(const moe_config* c, int64_t T) {
       (c->d_model % 128 || c->d_ff % 128 || (c->E_shared > 0 && c->d_ff_shared % 128) ||
        c->d_latent % 128))
     return fail(MOE_ERR_UNSUPPORTED_SHAPE, "FP8 weights: d_model, d_ff, d_ff_shared, d_latent % 128");
+  if (int4_group(c->weight_layout) &&
+      (c->d_model % 128 || c->d_ff % 128 || (c->E_shared > 0 && c->d_ff_shared % 128) ||
+       c->d_latent % 128))
+    return fail(MOE_ERR_UNSUPPORTED_SHAPE, "4-bit weights: d_model, d_ff, d_ff_shared, d_latent % 128");
   if (c->dtype == MOE_BF16) {
     if (c->d_model % 128) return fail(MOE_ERR_UNSUPPORTED_SHAPE, "bf16 path: d_model % 128 != 0");
     if (c->d_ff % 64) return fail(MOE_ERR_UNSUPPORTED_SHAPE, "bf16 path: d_ff % 64 != 0");
@@ -391,6 +400,10 @@ struct ExpertIO {
   // each token row once and write its K copies
   const int32_t* topk_idx = nullptr;
   const int32_t* inv = nullptr;
+  // 4-bit layouts: x_e and x_shared are E4M3 codes with these scales (both
+  // or neither; x_shared_scale only with x_shared)
+  const float* x_scale = nullptr;         // [T, d_e / 128]
+  const float* x_shared_scale = nullptr;  // [T, d / 128]
 };
 
 // The shared experts' gate/up pass as a GEMM segment: every token of x
@@ -418,12 +431,96 @@ int32_t shared_gate_up_segment(GemmSegment& s, const moe_config* c, int64_t T, c
   return MOE_OK;
 }
 
+// The expert passes with 4-bit weights: each pass one launch over the routed
+// and the shared experts, rows read where they lie (no gathered copy: a row
+// is a few KB next to the megabytes of weights it meets).  H and H_shared are
+// plain rows in slot order.
+int32_t run_experts_int4(const moe_config* c, int64_t T, const ExpertIO& io, void* ws,
+                         cudaEvent_t ev_up, cudaEvent_t ev_down, cudaStream_t st,
+                         bool weights_in_Y) {
+  const Layout L = layout(c, T);
+  const int F = c->d_ff, Fs = c->d_ff_shared, de = d_expert(c), d = c->d_model;
+  const int S = io.x_shared ? c->E_shared : 0;
+  __nv_bfloat16* H = at<__nv_bfloat16>(ws, L.H);
+  __nv_bfloat16* Hs = at<__nv_bfloat16>(ws, L.Hs);
+  Int4Params p;
+  p.group = int4_group(c->weight_layout);
+  p.nseg = S ? 2 : 1;
+  p.swiglu = 1;
+  Int4Segment& r = p.seg[0];
+  r.W = static_cast<const uint8_t*>(io.W_gate_up);
+  r.groups = c->E_routed;
+  r.blocks = 2 * F / 16;
+  r.chunks = de / 128;
+  r.offsets = io.offsets;
+  r.x = io.x_e;
+  r.x_scale = io.x_scale;
+  r.x_ld = de;
+  r.perm = io.perm;
+  r.perm_div = c->K;
+  r.out = H;
+  r.out_ld = F;
+  if (S) {
+    Int4Segment& s = p.seg[1];
+    s.W = static_cast<const uint8_t*>(io.Ws_gate_up);
+    s.groups = S;
+    s.blocks = 2 * Fs / 16;
+    s.chunks = d / 128;
+    s.rows = T;
+    s.x = io.x_shared;
+    s.x_scale = io.x_shared_scale;
+    s.x_ld = d;
+    s.out = Hs;
+    s.out_ld = Fs;
+    s.out_group_rows = T;
+  }
+  if (ev_up) MOE_CUDA(cudaEventRecord(ev_up, st));
+  MOE_CUDA(launch_gemv_int4(p, num_sms(), st));
+  if (ev_down) MOE_CUDA(cudaEventRecord(ev_down, st));
+
+  Int4Params q;
+  q.group = p.group;
+  q.nseg = p.nseg;
+  Int4Segment& r2 = q.seg[0];
+  r2.W = static_cast<const uint8_t*>(io.W_down);
+  r2.groups = c->E_routed;
+  r2.blocks = de / 16;
+  r2.chunks = F / 128;
+  r2.offsets = io.offsets;
+  r2.x = H;
+  r2.x_ld = F;
+  r2.out = static_cast<__nv_bfloat16*>(io.Y);
+  r2.out_ld = de;
+  if (weights_in_Y && io.topk_w) {
+    r2.row_w = io.topk_w;
+    r2.row_perm = io.perm;
+  }
+  if (S) {
+    Int4Segment& s2 = q.seg[1];
+    s2.W = static_cast<const uint8_t*>(io.Ws_down);
+    s2.groups = S;
+    s2.blocks = d / 16;
+    s2.chunks = Fs / 128;
+    s2.rows = T;
+    s2.x = Hs;
+    s2.x_ld = Fs;
+    s2.x_group_rows = T;
+    s2.out = static_cast<__nv_bfloat16*>(io.Y_shared);
+    s2.out_ld = d;
+    s2.out_group_rows = T;
+  }
+  MOE_CUDA(launch_gemv_int4(q, num_sms(), st));
+  return MOE_OK;
+}
+
 // weights_in_Y: scale the routed rows of Y by their routing weights (the
 // moe_grouped_swiglu contract); the layer forward leaves Y unscaled and
 // weights the rows in its combine instead, which keeps the scale out of the
 // GEMM epilogues.
 int32_t run_experts(const moe_config* c, int64_t T, const ExpertIO& io, void* ws,
                     cudaEvent_t ev_up, cudaEvent_t ev_down, cudaStream_t st, bool weights_in_Y) {
+  if (int4_group(c->weight_layout))
+    return run_experts_int4(c, T, io, ws, ev_up, ev_down, st, weights_in_Y);
   const Layout L = layout(c, T);
   const int E = c->E_routed, K = c->K, F = c->d_ff, de = d_expert(c);
   const int S = io.x_shared ? c->E_shared : 0;
@@ -587,7 +684,7 @@ int32_t run_experts(const moe_config* c, int64_t T, const ExpertIO& io, void* ws
 }
 
 // The K3 latent projections are bf16 whatever the expert banks are: packed
-// when the banks are packed (bf16 or FP8), natural otherwise.
+// when the banks are packed (bf16, FP8 or 4-bit), natural otherwise.
 int latent_layout(const moe_config* c) {
   return c->weight_layout == MOE_WEIGHTS_NATURAL ? MOE_WEIGHTS_NATURAL : MOE_WEIGHTS_PACKED;
 }
@@ -955,27 +1052,63 @@ int32_t moe_permute(const moe_config* cfg, int64_t T, const int32_t* topk_idx, i
   return MOE_OK;
 }
 
-int32_t moe_grouped_swiglu(const moe_config* cfg, int64_t T, const void* x_e,
-                           const int32_t* offsets, const int32_t* perm, const float* topk_w,
-                           const void* W_gate_up, const void* W_down, const void* x_shared,
-                           const void* Ws_gate_up, const void* Ws_down, void* Y, void* Y_shared,
-                           void* workspace, size_t ws_bytes, void* stream) {
+namespace {
+
+// moe_grouped_swiglu and moe_grouped_swiglu_fp8_rows (fp8_rows: x_e and
+// x_shared are E4M3 codes with the given scales).
+int32_t grouped_swiglu(const moe_config* cfg, int64_t T, const void* x_e, const float* x_scale,
+                       const int32_t* offsets, const int32_t* perm, const float* topk_w,
+                       const void* W_gate_up, const void* W_down, const void* x_shared,
+                       const float* x_shared_scale, const void* Ws_gate_up, const void* Ws_down,
+                       void* Y, void* Y_shared, void* workspace, size_t ws_bytes, void* stream,
+                       bool fp8_rows) {
   int32_t st = check_layer_cfg(cfg, T);
   if (st != MOE_OK) return st;
+  if (fp8_rows && !int4_group(cfg->weight_layout))
+    return fail(MOE_ERR_UNSUPPORTED_SHAPE, "E4M3 rows need a 4-bit weight layout");
   if (!x_e || !offsets || !perm || !W_gate_up || !W_down || !Y)
     return fail(MOE_ERR_INVALID_ARG, "null pointer");
   const bool shared = x_shared != nullptr && cfg->E_shared > 0;
   if (shared && (!Ws_gate_up || !Ws_down || !Y_shared))
     return fail(MOE_ERR_INVALID_ARG, "shared expert pointers missing");
+  if (fp8_rows && (!x_scale || (shared && !x_shared_scale)))
+    return fail(MOE_ERR_INVALID_ARG, "scales of the E4M3 rows missing");
   const void* ptrs[] = {x_e, offsets, perm, topk_w, W_gate_up, W_down, x_shared, Ws_gate_up,
-                        Ws_down, Y, Y_shared, workspace};
+                        Ws_down, Y, Y_shared, workspace, x_scale, x_shared_scale};
   for (const void* q : ptrs)
     if (q && !aligned16(q)) return fail(MOE_ERR_ALIGNMENT, "pointer not 16-byte aligned");
   if (!workspace || ws_bytes < layout(cfg, T).total) return fail(MOE_ERR_WORKSPACE, "workspace too small");
   ExpertIO io = {x_e, offsets, perm, topk_w, W_gate_up, W_down, shared ? x_shared : nullptr,
                  Ws_gate_up, Ws_down, Y, Y_shared};
+  io.x_scale = x_scale;
+  io.x_shared_scale = x_shared_scale;
   return run_experts(cfg, T, io, workspace, nullptr, nullptr, static_cast<cudaStream_t>(stream),
                      true);
+}
+
+}  // namespace
+
+int32_t moe_grouped_swiglu(const moe_config* cfg, int64_t T, const void* x_e,
+                           const int32_t* offsets, const int32_t* perm, const float* topk_w,
+                           const void* W_gate_up, const void* W_down, const void* x_shared,
+                           const void* Ws_gate_up, const void* Ws_down, void* Y, void* Y_shared,
+                           void* workspace, size_t ws_bytes, void* stream) {
+  return grouped_swiglu(cfg, T, x_e, nullptr, offsets, perm, topk_w, W_gate_up, W_down, x_shared,
+                        nullptr, Ws_gate_up, Ws_down, Y, Y_shared, workspace, ws_bytes, stream,
+                        false);
+}
+
+int32_t moe_grouped_swiglu_fp8_rows(const moe_config* cfg, int64_t T, const void* x_e,
+                                    const float* x_e_scale, const int32_t* offsets,
+                                    const int32_t* perm, const float* topk_w,
+                                    const void* W_gate_up, const void* W_down,
+                                    const void* x_shared, const float* x_shared_scale,
+                                    const void* Ws_gate_up, const void* Ws_down, void* Y,
+                                    void* Y_shared, void* workspace, size_t ws_bytes,
+                                    void* stream) {
+  return grouped_swiglu(cfg, T, x_e, x_e_scale, offsets, perm, topk_w, W_gate_up, W_down, x_shared,
+                        x_shared_scale, Ws_gate_up, Ws_down, Y, Y_shared, workspace, ws_bytes,
+                        stream, true);
 }
 
 int32_t moe_combine(const moe_config* cfg, int64_t T, const void* Y, const int32_t* inv,
@@ -1029,6 +1162,98 @@ int32_t moe_pack_weights_fp8(int32_t kind, int64_t groups, int64_t rows, int64_t
   if (a < b + nb && b < a + na) return fail(MOE_ERR_INVALID_ARG, "codes and dst overlap");
   MOE_CUDA(launch_pack_weights_fp8(kind, groups, rows, cols, codes, scales, dst,
                                    static_cast<cudaStream_t>(stream)));
+  return MOE_OK;
+}
+
+int64_t moe_packed_int4_bytes(int64_t groups, int64_t rows, int64_t cols, int32_t group_size) {
+  if (groups < 1 || rows < 16 || cols < 128 || rows % 16 || cols % 128 ||
+      (group_size != 32 && group_size != 128))
+    return -1;
+  return packed_int4_bytes(groups, rows, cols, group_size);
+}
+
+int32_t moe_pack_weights_int4(int32_t kind, int64_t groups, int64_t rows, int64_t cols,
+                              int32_t group_size, const void* codes, const void* scales, void* dst,
+                              void* stream) {
+  if (kind != MOE_PACK_GATE_UP && kind != MOE_PACK_PLAIN) return fail(MOE_ERR_INVALID_ARG, "kind");
+  if (groups < 1 || rows < 16 || cols < 128) return fail(MOE_ERR_INVALID_ARG, "sizes");
+  if (rows % 16 || cols % 128) return fail(MOE_ERR_UNSUPPORTED_SHAPE, "rows % 16 or cols % 128");
+  if (group_size != 32 && group_size != 128)
+    return fail(MOE_ERR_UNSUPPORTED_SHAPE, "group_size not 32 or 128");
+  if (!codes || !scales || !dst) return fail(MOE_ERR_INVALID_ARG, "null pointer");
+  if (!aligned16(codes) || !aligned16(dst) || reinterpret_cast<uintptr_t>(scales) % 2)
+    return fail(MOE_ERR_ALIGNMENT, "codes or dst not 16-byte aligned, or scales not 2-byte aligned");
+  const char* b = static_cast<const char*>(dst);
+  const size_t nb = static_cast<size_t>(packed_int4_bytes(groups, rows, cols, group_size));
+  const char* a = static_cast<const char*>(codes);
+  const size_t na = static_cast<size_t>(groups * rows * cols) / 2;
+  if (a < b + nb && b < a + na) return fail(MOE_ERR_INVALID_ARG, "codes and dst overlap");
+  const char* s = static_cast<const char*>(scales);
+  const size_t ns = static_cast<size_t>(groups * rows * (cols / group_size)) * 2;
+  if (s < b + nb && b < s + ns) return fail(MOE_ERR_INVALID_ARG, "scales and dst overlap");
+  MOE_CUDA(launch_pack_int4(kind == MOE_PACK_GATE_UP, groups, rows, cols, group_size, codes, scales,
+                            dst, static_cast<cudaStream_t>(stream)));
+  return MOE_OK;
+}
+
+int32_t moe_linear_int4(int64_t T, int32_t in_features, int32_t out_features, int32_t group_size,
+                        const void* x, const float* x_scale, const void* W, const void* add,
+                        void* y, void* stream) {
+  if (T < 1 || T > (1ll << 30)) return fail(MOE_ERR_INVALID_ARG, "T out of range");
+  if (in_features < 128 || in_features % 128 || out_features < 16 || out_features % 16)
+    return fail(MOE_ERR_UNSUPPORTED_SHAPE, "in_features % 128 or out_features % 16");
+  if (group_size != 32 && group_size != 128)
+    return fail(MOE_ERR_UNSUPPORTED_SHAPE, "group_size not 32 or 128");
+  if (!x || !W || !y) return fail(MOE_ERR_INVALID_ARG, "null pointer");
+  if (!aligned16(x) || !aligned16(x_scale) || !aligned16(W) || !aligned16(add) || !aligned16(y))
+    return fail(MOE_ERR_ALIGNMENT, "pointer not 16-byte aligned");
+  Int4Params p;
+  p.group = group_size;
+  p.nseg = 1;
+  Int4Segment& s = p.seg[0];
+  s.W = static_cast<const uint8_t*>(W);
+  s.groups = 1;
+  s.blocks = out_features / 16;
+  s.chunks = in_features / 128;
+  s.rows = T;
+  s.x = x;
+  s.x_scale = x_scale;
+  s.x_ld = in_features;
+  s.out = static_cast<__nv_bfloat16*>(y);
+  s.out_ld = out_features;
+  s.add = static_cast<const __nv_bfloat16*>(add);
+  MOE_CUDA(launch_gemv_int4(p, num_sms(), static_cast<cudaStream_t>(stream)));
+  return MOE_OK;
+}
+
+int32_t moe_add_rmsnorm(int32_t dtype, int64_t T, int32_t d, const void* x, const void* residual,
+                        const void* weight, float eps, void* h, void* y, void* y_fp8,
+                        float* y_scale, void* stream) {
+  if (dtype != MOE_F32 && dtype != MOE_BF16) return fail(MOE_ERR_INVALID_ARG, "dtype");
+  if (T < 1 || T > (1ll << 30)) return fail(MOE_ERR_INVALID_ARG, "T out of range");
+  if (d < 1) return fail(MOE_ERR_INVALID_ARG, "d < 1");
+  if (!(eps >= 0.0f) || !std::isfinite(eps))
+    return fail(MOE_ERR_INVALID_ARG, "eps not in [0, inf)");
+  if (!x || !weight) return fail(MOE_ERR_INVALID_ARG, "null pointer");
+  if (!y && !y_fp8) return fail(MOE_ERR_INVALID_ARG, "no output: y and y_fp8 are null");
+  if (!y_fp8 != !y_scale) return fail(MOE_ERR_INVALID_ARG, "y_fp8 and y_scale go together");
+  if (y_fp8 && d % 128) return fail(MOE_ERR_UNSUPPORTED_SHAPE, "8-bit output: d % 128 != 0");
+  const void* ptrs[] = {x, residual, weight, h, y, y_fp8, y_scale};
+  for (const void* q : ptrs)
+    if (!aligned16(q)) return fail(MOE_ERR_ALIGNMENT, "pointer not 16-byte aligned");
+  NormArgs n;
+  n.bf16 = dtype == MOE_BF16;
+  n.T = T;
+  n.d = d;
+  n.a = x;
+  n.r = residual;
+  n.w = weight;
+  n.eps = eps;
+  n.h = h;
+  n.y = y;
+  n.y8 = static_cast<uint8_t*>(y_fp8);
+  n.ys = y_scale;
+  MOE_CUDA(launch_add_rmsnorm(n, static_cast<cudaStream_t>(stream)));
   return MOE_OK;
 }
 

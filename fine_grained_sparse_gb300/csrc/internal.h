@@ -278,4 +278,55 @@ struct SimtGemm {
 constexpr int kSimtTile = 16;
 cudaError_t launch_simt_gemm(const SimtGemm& g, int64_t tiles_bound, cudaStream_t stream);
 
+// ------------------------------------------------ residual sum and RMS norm
+struct NormArgs {
+  bool bf16 = true;         // type of a, r, w, h and y: bf16 or fp32
+  int64_t T = 0;
+  int d = 0;
+  const void* a = nullptr;  // [T, d]
+  const void* r = nullptr;  // [T, d] or null
+  const void* w = nullptr;  // [d]
+  float eps = 0.0f;
+  void* h = nullptr;        // [T, d] or null
+  void* y = nullptr;        // [T, d] or null
+  uint8_t* y8 = nullptr;    // [T, d] E4M3 codes, or null
+  float* ys = nullptr;      // [T, d / 128] scales (with y8)
+};
+cudaError_t launch_add_rmsnorm(const NormArgs& n, cudaStream_t stream);
+
+// --------------------------------------------------- products with 4-bit weights
+// A segment: `groups` packed banks of `blocks` 16-row blocks x `chunks`
+// 128-column chunks, each multiplied with its own rows of x.
+struct Int4Segment {
+  const uint8_t* W = nullptr;
+  int groups = 0;
+  int blocks = 0;
+  int chunks = 0;
+  const int32_t* offsets = nullptr;  // rows of group g: [offsets[g], offsets[g + 1]); or null:
+  int64_t rows = 0;                  // every group has `rows` rows
+  const void* x = nullptr;           // bf16, or E4M3 codes when x_scale is set
+  const float* x_scale = nullptr;    // [x rows, chunks]
+  int64_t x_ld = 0;
+  int64_t x_group_rows = 0;          // implicit rows: x row of group g, row t is g * this + t
+  const int32_t* perm = nullptr;     // explicit rows: x row of row r is perm[r] / perm_div
+  int perm_div = 1;
+  __nv_bfloat16* out = nullptr;      // row r (explicit) or g * out_group_rows + t (implicit)
+  int64_t out_ld = 0;
+  int64_t out_group_rows = 0;
+  const float* row_w = nullptr;      // row r scaled by row_w[row_perm[r]], or null
+  const int32_t* row_perm = nullptr;
+  const __nv_bfloat16* add = nullptr;  // added to the output (its row stride), or null
+};
+struct Int4Params {
+  Int4Segment seg[2];
+  int nseg = 0;
+  int swiglu = 0;  // gate/up pass (packed as MOE_PACK_GATE_UP) or plain store
+  int group = 32;  // columns of one scale, 32 or 128
+};
+cudaError_t launch_gemv_int4(const Int4Params& p, int num_sms, cudaStream_t stream);
+int64_t packed_int4_bytes(int64_t groups, int64_t rows, int64_t cols, int group);
+cudaError_t launch_pack_int4(int gate_up, int64_t groups, int64_t rows, int64_t cols, int group,
+                             const void* codes, const void* scales, void* dst,
+                             cudaStream_t stream);
+
 }  // namespace fgs

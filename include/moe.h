@@ -109,11 +109,22 @@ typedef enum moe_router_weight_form {
  *     scales.  The encoding, the block shape and the scale's type are not on
  *     the page; E4M3, 128 x 128 and an fp32 multiplier are this library's
  *     reading.)  Activations, H and the accumulation stay as in the bf16
- *     form; each weight enters the tensor cores as bf16(code value x scale). */
+ *     form; each weight enters the tensor cores as bf16(code value x scale).
+ *   MOE_WEIGHTS_PACKED_INT4_G32, MOE_WEIGHTS_PACKED_INT4_G128: the routed and
+ *     shared experts' W_gate_up and W_down are 4-bit codes with one bf16
+ *     scale per 32 (128) columns of a row, packed by moe_pack_weights_int4;
+ *     the latent projections stay bf16, packed by moe_pack_weights.  A decode
+ *     form: its passes are bound by reading the weights up to about 16 rows
+ *     an expert, and for larger batches the bf16 or FP8 form is faster.
+ *     Needs bf16 activations and d_model, d_ff, d_ff_shared, d_latent
+ *     multiples of 128.  The weights enter the tensor cores exactly (code - 8
+ *     as bf16 or f16) and the scales are applied in fp32. */
 typedef enum moe_weight_layout {
   MOE_WEIGHTS_NATURAL = 0,
   MOE_WEIGHTS_PACKED = 1,
-  MOE_WEIGHTS_PACKED_FP8 = 2
+  MOE_WEIGHTS_PACKED_FP8 = 2,
+  MOE_WEIGHTS_PACKED_INT4_G32 = 3,
+  MOE_WEIGHTS_PACKED_INT4_G128 = 4
 } moe_weight_layout;
 
 /* Kinds of packed matrices. */
@@ -168,6 +179,37 @@ int64_t moe_packed_fp8_bytes(int64_t groups, int64_t rows, int64_t cols);
  * MOE_ERR_INVALID_ARG / UNSUPPORTED_SHAPE / ALIGNMENT before any launch. */
 int32_t moe_pack_weights_fp8(int32_t kind, int64_t groups, int64_t rows, int64_t cols,
                              const void* codes, const float* scales, void* dst, void* stream);
+
+/* Bytes of a bank packed by moe_pack_weights_int4: groups * (rows / 16) *
+ * (cols / 128) records of 1024 + 16 * (128 / group_size) * 2 bytes; -1 for
+ * sizes moe_pack_weights_int4 rejects. */
+int64_t moe_packed_int4_bytes(int64_t groups, int64_t rows, int64_t cols, int32_t group_size);
+
+/*
+ * Rearrange a 4-bit weight bank and its group scales into the order the
+ * products read them (a one-time load step, like moe_pack_weights).
+ *   codes  [groups, rows, cols / 2] uint8, device: two codes a byte, the even
+ *          column in the low half
+ *   scales [groups, rows, cols / group_size] bf16, device: weight (g, r, c) =
+ *          (code(g, r, c) - 8) * scales[g][r][c / group_size]
+ *   dst    device buffer of moe_packed_int4_bytes(groups, rows, cols,
+ *          group_size) bytes, overlapping neither
+ * group_size 32 or 128; rows % 16 == 0 and cols % 128 == 0 (MOE_PACK_GATE_UP:
+ * rows = 2 F, the gate rows then the up rows).  codes and dst 16-byte
+ * aligned, scales 2-byte aligned.
+ * Packed order: per group, per 16-row block, per 128 columns one record.  A
+ * record's rows r = 0..15 are rows 16 b + r of the bank's group, or for
+ * MOE_PACK_GATE_UP the gate rows 8 b + r (r < 8) and the up rows F + 8 b +
+ * r - 8.  Its first 1024 bytes are 32-bit words: word i (0..7) of lane l
+ * (0..31) is at byte 512 (i / 4) + 16 l + 4 (i mod 4), and its nibbles j and
+ * j + 4 (j = 0..3, from the low end) are the codes of row l / 4 + 8 (j mod 2)
+ * at columns 32 (i / 2) + 8 (l mod 4) + 4 (i mod 2) + 2 (j / 2) and the next
+ * one.  Then, for g = 0..7, the bf16 scales of row g and of row g + 8 for the
+ * record's 128 / group_size groups.  Asynchronous on `stream`;
+ * MOE_ERR_INVALID_ARG / UNSUPPORTED_SHAPE / ALIGNMENT before any launch. */
+int32_t moe_pack_weights_int4(int32_t kind, int64_t groups, int64_t rows, int64_t cols,
+                              int32_t group_size, const void* codes, const void* scales, void* dst,
+                              void* stream);
 
 /*
  * Self-test of the library's failure detection, with no counterpart on the
@@ -338,6 +380,25 @@ int32_t moe_grouped_swiglu(const moe_config* cfg, int64_t T, const void* x_e,
                            void* workspace, size_t ws_bytes, void* stream);
 
 /*
+ * moe_grouped_swiglu on rows in 8 bits, as moe_add_rmsnorm writes them: x_e
+ * [T, d_e] and x_shared [T, d_model] (or NULL) are E4M3 codes with one fp32
+ * scale per 128 columns of a row, x_e_scale [T, d_e / 128] and
+ * x_shared_scale [T, d_model / 128] (NULL with x_shared); value (t, c) =
+ * code value * scale[t][c / 128].  In the K2 form x_e and x_shared are the
+ * same rows.  The codes enter the tensor cores exactly and the scales are
+ * applied in fp32.  cfg->weight_layout must be a 4-bit one
+ * (MOE_ERR_UNSUPPORTED_SHAPE otherwise); the other arguments and the outputs
+ * are those of moe_grouped_swiglu. */
+int32_t moe_grouped_swiglu_fp8_rows(const moe_config* cfg, int64_t T, const void* x_e,
+                                    const float* x_e_scale, const int32_t* offsets,
+                                    const int32_t* perm, const float* topk_w,
+                                    const void* W_gate_up, const void* W_down,
+                                    const void* x_shared, const float* x_shared_scale,
+                                    const void* Ws_gate_up, const void* Ws_down, void* Y,
+                                    void* Y_shared, void* workspace, size_t ws_bytes,
+                                    void* stream);
+
+/*
  * Weighted combine ("Kimi K2 MoE", section 3: shared_expert(x) + routed;
  * the routed part is the gate-weighted sum of the selected experts):
  *   y[t] = sum_{k=0..K-1} w[t, k] Y[inv[t*K + k]] + sum_s Y_shared[s, t]
@@ -364,6 +425,39 @@ int32_t moe_combine(const moe_config* cfg, int64_t T, const void* Y, const int32
 int32_t moe_linear(int64_t T, int32_t in_features, int32_t out_features, const void* x,
                    const void* W, const void* add, void* y, void* workspace, size_t ws_bytes,
                    void* stream);
+
+/*
+ * Linear map with 4-bit weights, y = x W^T (+ add), for few rows: a decode
+ * step's dense projections (the K3 latent maps in 4 bits among them).
+ *   x [T, in] bf16 with x_scale NULL, or E4M3 codes with x_scale
+ *   [T, in / 128] fp32 (value (t, c) = code value * x_scale[t][c / 128]),
+ *   W packed by moe_pack_weights_int4(MOE_PACK_PLAIN, 1, out, in,
+ *   group_size), add [T, out] bf16 or NULL, y [T, out] bf16 (y may be add).
+ * in a multiple of 128, out of 16; group_size 32 or 128.  Sums in fp32, one
+ * rounding to bf16.  Needs no workspace. */
+int32_t moe_linear_int4(int64_t T, int32_t in_features, int32_t out_features, int32_t group_size,
+                        const void* x, const float* x_scale, const void* W, const void* add,
+                        void* y, void* stream);
+
+/*
+ * Residual sum and root-mean-square norm, the step before the layer (the
+ * router's and the experts' input is x = norm(h)):
+ *   s = x + residual (x alone when residual is NULL),
+ *   v[t, c] = weight[c] * s[t, c] / sqrt(sum_c s[t, c]^2 / d + eps)
+ * in fp32 from the inputs, with the outputs each rounded once:
+ *   h [T, d]        s, the new residual stream, or NULL
+ *   y [T, d]        v, or NULL
+ *   y_fp8 [T, d]    v in 8 bits, or NULL: per 128 columns of a row,
+ *   y_scale [T, d / 128] fp32 = max |v| / 448 and E4M3 codes of v / scale
+ *                   rounded to nearest (all 0 where the maximum is 0; a group
+ *                   with a NaN has a NaN scale and NaN codes)
+ * At least one of y and y_fp8; y_fp8 and y_scale together, with d % 128 == 0.
+ * x, residual, weight [d], h and y are `dtype` (MOE_BF16 or MOE_F32); any
+ * d >= 1 otherwise.  eps >= 0.  h and y may each be x or residual itself (not
+ * both the same buffer); no other overlap is allowed.  Needs no workspace. */
+int32_t moe_add_rmsnorm(int32_t dtype, int64_t T, int32_t d, const void* x, const void* residual,
+                        const void* weight, float eps, void* h, void* y, void* y_fp8,
+                        float* y_scale, void* stream);
 
 /*
  * The whole layer forward, one stream:
