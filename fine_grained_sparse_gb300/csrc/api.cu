@@ -200,6 +200,10 @@ int32_t check_layer_cfg(const moe_config* c, int64_t T) {
       (c->d_model % 128 || c->d_ff % 128 || (c->E_shared > 0 && c->d_ff_shared % 128) ||
        c->d_latent % 128))
     return fail(MOE_ERR_UNSUPPORTED_SHAPE, "4-bit weights: d_model, d_ff, d_ff_shared, d_latent % 128");
+  if (int4_group(c->weight_layout) &&
+      (c->d_model > kInt4MaxCols || c->d_ff > kInt4MaxCols || c->d_latent > kInt4MaxCols ||
+       (c->E_shared > 0 && c->d_ff_shared > kInt4MaxCols)))
+    return fail(MOE_ERR_UNSUPPORTED_SHAPE, "4-bit weights: a width above 32768");
   if (c->dtype == MOE_BF16) {
     if (c->d_model % 128) return fail(MOE_ERR_UNSUPPORTED_SHAPE, "bf16 path: d_model % 128 != 0");
     if (c->d_ff % 64) return fail(MOE_ERR_UNSUPPORTED_SHAPE, "bf16 path: d_ff % 64 != 0");
@@ -453,6 +457,7 @@ int32_t run_experts_int4(const moe_config* c, int64_t T, const ExpertIO& io, voi
   r.blocks = 2 * F / 16;
   r.chunks = de / 128;
   r.offsets = io.offsets;
+  r.rows = T;  // the K experts of a token are distinct
   r.x = io.x_e;
   r.x_scale = io.x_scale;
   r.x_ld = de;
@@ -487,6 +492,7 @@ int32_t run_experts_int4(const moe_config* c, int64_t T, const ExpertIO& io, voi
   r2.blocks = de / 16;
   r2.chunks = F / 128;
   r2.offsets = io.offsets;
+  r2.rows = T;
   r2.x = H;
   r2.x_ld = F;
   r2.out = static_cast<__nv_bfloat16*>(io.Y);
@@ -1202,6 +1208,7 @@ int32_t moe_linear_int4(int64_t T, int32_t in_features, int32_t out_features, in
   if (T < 1 || T > (1ll << 30)) return fail(MOE_ERR_INVALID_ARG, "T out of range");
   if (in_features < 128 || in_features % 128 || out_features < 16 || out_features % 16)
     return fail(MOE_ERR_UNSUPPORTED_SHAPE, "in_features % 128 or out_features % 16");
+  if (in_features > kInt4MaxCols) return fail(MOE_ERR_UNSUPPORTED_SHAPE, "in_features above 32768");
   if (group_size != 32 && group_size != 128)
     return fail(MOE_ERR_UNSUPPORTED_SHAPE, "group_size not 32 or 128");
   if (!x || !W || !y) return fail(MOE_ERR_INVALID_ARG, "null pointer");

@@ -295,6 +295,8 @@ struct NormArgs {
 cudaError_t launch_add_rmsnorm(const NormArgs& n, cudaStream_t stream);
 
 // --------------------------------------------------- products with 4-bit weights
+// The widest x: a row of it stays in shared memory beside the ring of weights.
+constexpr int kInt4MaxCols = 32768;
 // A segment: `groups` packed banks of `blocks` 16-row blocks x `chunks`
 // 128-column chunks, each multiplied with its own rows of x.
 struct Int4Segment {
@@ -302,8 +304,8 @@ struct Int4Segment {
   int groups = 0;
   int blocks = 0;
   int chunks = 0;
-  const int32_t* offsets = nullptr;  // rows of group g: [offsets[g], offsets[g + 1]); or null:
-  int64_t rows = 0;                  // every group has `rows` rows
+  const int32_t* offsets = nullptr;  // rows of group g: [offsets[g], offsets[g + 1]); or null
+  int64_t rows = 0;                  // rows of every group; with offsets, the most of any
   const void* x = nullptr;           // bf16, or E4M3 codes when x_scale is set
   const float* x_scale = nullptr;    // [x rows, chunks]
   int64_t x_ld = 0;

@@ -117,7 +117,7 @@ typedef enum moe_router_weight_form {
  *     form: its passes are bound by reading the weights up to about 16 rows
  *     an expert, and for larger batches the bf16 or FP8 form is faster.
  *     Needs bf16 activations and d_model, d_ff, d_ff_shared, d_latent
- *     multiples of 128.  The weights enter the tensor cores exactly (code - 8
+ *     multiples of 128 and at most 32768.  The weights enter the tensor cores exactly (code - 8
  *     as bf16 or f16) and the scales are applied in fp32. */
 typedef enum moe_weight_layout {
   MOE_WEIGHTS_NATURAL = 0,
@@ -433,7 +433,7 @@ int32_t moe_linear(int64_t T, int32_t in_features, int32_t out_features, const v
  *   [T, in / 128] fp32 (value (t, c) = code value * x_scale[t][c / 128]),
  *   W packed by moe_pack_weights_int4(MOE_PACK_PLAIN, 1, out, in,
  *   group_size), add [T, out] bf16 or NULL, y [T, out] bf16 (y may be add).
- * in a multiple of 128, out of 16; group_size 32 or 128.  Sums in fp32, one
+ * in a multiple of 128, at most 32768, out one of 16; group_size 32 or 128.  Sums in fp32, one
  * rounding to bf16.  Needs no workspace. */
 int32_t moe_linear_int4(int64_t T, int32_t in_features, int32_t out_features, int32_t group_size,
                         const void* x, const float* x_scale, const void* W, const void* add,

@@ -73,6 +73,7 @@ def test_packed_bytes(kind, G, R, C, group):
     (7, 384, 1040, False), (8, 2048, 160, True), (9, 128, 2448, False), (13, 3584, 64, True),
     (16, 1152, 96, False), (17, 640, 2432, True), (31, 7168, 32, False), (33, 512, 5008, True),
     (65, 1920, 112, False), (130, 256, 80, True), (3, 18432, 16, False), (40, 12288, 48, False),
+    (2, 32768, 16, False),
 ])
 def test_linear(T, I, O, add, rows8, group):
     need_gpu()

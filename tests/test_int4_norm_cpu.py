@@ -49,6 +49,7 @@ def test_pack_refusals(fgs, args, status):
     ({"d_latent": 3584 - 64}, 2),
     ({"d_latent": 3584}, 0),
     ({"dtype": 0}, 2),
+    ({"d_model": 32896}, 2),
     ({"weight_layout": 5}, 1),
 ])
 @pytest.mark.parametrize("layout", [3, 4])
@@ -63,6 +64,7 @@ def test_validate_config(fgs, layout, kw, status):
     ((0, 256, 64, 32, P[0], None, P[1], None, P[2]), 1),       # T
     ((1, 200, 64, 32, P[0], None, P[1], None, P[2]), 2),
     ((1, 256, 72, 32, P[0], None, P[1], None, P[2]), 2),
+    ((1, 32896, 64, 32, P[0], None, P[1], None, P[2]), 2),     # too wide
     ((1, 256, 64, 16, P[0], None, P[1], None, P[2]), 2),
     ((1, 256, 64, 32, None, None, P[1], None, P[2]), 1),
     ((1, 256, 64, 32, P[0], None, P[1], None, None), 1),
