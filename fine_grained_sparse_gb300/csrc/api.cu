@@ -486,6 +486,7 @@ int32_t run_experts_int4(const moe_config* c, int64_t T, const ExpertIO& io, voi
   Int4Params q;
   q.group = p.group;
   q.nseg = p.nseg;
+  q.early = ev_down ? 0 : 1;  // nothing stands between the two launches
   Int4Segment& r2 = q.seg[0];
   r2.W = static_cast<const uint8_t*>(io.W_down);
   r2.groups = c->E_routed;
