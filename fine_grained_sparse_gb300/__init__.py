@@ -129,10 +129,28 @@ def _ptr(t) -> Optional[int]:
     return t.data_ptr()
 
 
+_current_stream = None  # () -> the current stream's handle, made on first use
+
+
+def _make_current_stream():
+    """The handle of torch's current stream.  A call of a few microseconds
+    notices the Stream object that the public accessor builds, so the raw
+    accessor is taken where torch has it."""
+    import torch
+    raw = getattr(torch._C, "_cuda_getCurrentRawStream", None)
+    device = getattr(torch._C, "_cuda_getDevice", None)
+    if raw is None or device is None:
+        return lambda: torch.cuda.current_stream().cuda_stream
+    torch.cuda.current_stream()  # the accessors need an initialised context
+    return lambda: raw(device())
+
+
 def _stream(stream) -> Optional[int]:
     if stream is None:
-        import torch
-        return torch.cuda.current_stream().cuda_stream
+        global _current_stream
+        if _current_stream is None:
+            _current_stream = _make_current_stream()
+        return _current_stream()
     if isinstance(stream, int):
         return stream
     return stream.cuda_stream

@@ -147,18 +147,21 @@ constexpr int kSlotBytes = 512;   // a block's sums for kTile tokens
 constexpr int kTileCost = 128;    // what beginning a tile costs, in records
 
 // Shared memory: the header (row weights of the tile, the scan's warp sums,
-// the CTA's first group, per group its cost before it [groups + 1] and its
-// first row [groups + 1]), each warp's ring of records, partial sums, the
-// scales of x and (256-byte aligned) x.
+// the CTA's first group; then, over the groups that have rows: the cost
+// before each [groups + 1] and its number [groups]; and the groups' first
+// rows [groups + 1]), each warp's ring of records, partial sums, the scales
+// of x and (256-byte aligned) x.
+constexpr int kMaxGroups = 1024 + 8;
+
 struct Header {
   float row_w[kTile];
   int64_t warp_sum[kWarps];
-  int first_group, pad;
-  int64_t prefix[1];
+  int at_first, pad;
+  int64_t before[1];
 };
 
 __host__ __device__ inline int header_bytes(int groups) {
-  return static_cast<int>(sizeof(Header) + 12 * (groups + 1) + 255) / 256 * 256;
+  return static_cast<int>(sizeof(Header) + 14 * (groups + 1) + 255) / 256 * 256;
 }
 
 // A token's x as f16, and fp32 scales of kTile tokens per 128 columns.
@@ -476,13 +479,16 @@ __global__ void __launch_bounds__(kThreads, 1) gemv_int4_kernel(const __grid_con
   Header* hd = reinterpret_cast<Header*>(smem);
   const int n0 = p.seg[0].groups, groups = n0 + (p.nseg > 1 ? p.seg[1].groups : 0);
   const int header = header_bytes(groups);
-  int32_t* first = reinterpret_cast<int32_t*>(hd->prefix + groups + 1);  // explicit rows' offsets
+  int32_t* first = reinterpret_cast<int32_t*>(hd->before + groups + 1);  // explicit rows' offsets
+  uint16_t* number = reinterpret_cast<uint16_t*>(first + groups + 1);
   const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
   if (!p.early) pdl_wait();
   pdl_release();
 
-  // costs of groups 3 tid .. 3 tid + 2 (at most 1032 groups), then their scan
-  constexpr int kPer = 3;
+  // Costs of groups 3 tid .. 3 tid + 2, then a scan of them and of the number
+  // of groups with rows (in the low 11 bits of the same word).
+  constexpr int kPer = (kMaxGroups + kThreads - 1) / kThreads, kCountBits = 11;
+  static_assert(kMaxGroups < 1 << kCountBits, "");
   int64_t cost[kPer], mine = 0;
 #pragma unroll
   for (int i = 0; i < kPer; ++i) {
@@ -490,7 +496,7 @@ __global__ void __launch_bounds__(kThreads, 1) gemv_int4_kernel(const __grid_con
     cost[i] = 0;
     if (k >= groups) continue;
     const Int4Segment& s = p.seg[si];
-    int64_t n = s.rows;
+    int n = static_cast<int>(s.rows);
     if (s.offsets) {
       const int32_t a = s.offsets[k], b = s.offsets[k + 1];
       first[k] = a;
@@ -498,7 +504,8 @@ __global__ void __launch_bounds__(kThreads, 1) gemv_int4_kernel(const __grid_con
       n = b - a;
     }
     if (n > 0)
-      cost[i] = (n + p.cap[si] - 1) / p.cap[si] * (static_cast<int64_t>(s.blocks) * s.chunks + kTileCost);
+      cost[i] = (static_cast<int64_t>(s.blocks) * s.chunks + kTileCost) *
+                    ((n + p.cap[si] - 1u) / p.cap[si]) << kCountBits | 1;
     mine += cost[i];
   }
   int64_t incl = mine;
@@ -515,30 +522,34 @@ __global__ void __launch_bounds__(kThreads, 1) gemv_int4_kernel(const __grid_con
     if (v < warp) at += w;
     total += w;
   }
-  const int64_t share = total / gridDim.x;
+  const int present = static_cast<int>(total & ((1 << kCountBits) - 1));
+  total >>= kCountBits;
+  const int64_t share = total < (1ll << 32) ? static_cast<uint32_t>(total) / gridDim.x
+                                            : total / gridDim.x;
   const int rest = static_cast<int>(total - share * gridDim.x), cta = blockIdx.x;
   const int64_t lo = share * cta + min(cta, rest), hi = lo + share + (cta < rest);
 #pragma unroll
   for (int i = 0; i < kPer; ++i) {
-    const int k = tid * kPer + i;
-    if (k >= groups) continue;
-    hd->prefix[k] = at;
-    if (at <= lo && lo < at + cost[i]) hd->first_group = k;
+    if (!cost[i]) continue;
+    const int pos = static_cast<int>(at & ((1 << kCountBits) - 1));
+    const int64_t b = at >> kCountBits;
+    hd->before[pos] = b;
+    number[pos] = static_cast<uint16_t>(tid * kPer + i);
+    if (b <= lo && lo < b + (cost[i] >> kCountBits)) hd->at_first = pos;
     at += cost[i];
-    if (k == groups - 1) hd->prefix[groups] = at;
   }
   __syncthreads();
 
   bool wait = p.early;
-  for (int k = lo < hi ? hd->first_group : groups; k < groups && hd->prefix[k] < hi; ++k) {
-    const int64_t before = hd->prefix[k];
-    if (hd->prefix[k + 1] == before) continue;
-    const int si = k >= n0;
+  for (int pos = lo < hi ? hd->at_first : present; pos < present; ++pos) {
+    const int64_t before = hd->before[pos];
+    if (before >= hi) break;
+    const int k = number[pos], si = k >= n0;
     const Int4Segment& s = p.seg[si];
     const int grp = si ? k - n0 : k;
-    const int64_t row = s.offsets ? first[k] : 0;
-    const int64_t n = s.offsets ? first[k + 1] - row : s.rows;
-    const int tiles = static_cast<int>((n + p.cap[si] - 1) / p.cap[si]);
+    const int row = s.offsets ? first[k] : 0;
+    const int n = s.offsets ? first[k + 1] - row : static_cast<int>(s.rows);
+    const int tiles = (n + p.cap[si] - 1u) / p.cap[si];
     const int64_t tile_cost = static_cast<int64_t>(s.blocks) * s.chunks + kTileCost;
     int t = tiles > 1 && lo > before ? static_cast<int>((lo - before) / tile_cost) : 0;
     for (; t < tiles; ++t) {
@@ -547,12 +558,12 @@ __global__ void __launch_bounds__(kThreads, 1) gemv_int4_kernel(const __grid_con
       const int r1 = blocks_before(hi - base, s.chunks, s.blocks);
       if (r1 == 0) break;
       if (r0 >= r1) continue;
-      const int64_t row0 = tiles > 1 ? n * t / tiles : 0;
+      const int row0 = tiles > 1 ? static_cast<int>(static_cast<int64_t>(n) * t / tiles) : 0;
       Tile T;
       T.W = s.W + (static_cast<int64_t>(grp) * s.blocks + r0) * s.chunks * record_bytes(kGroup);
       T.blocks = r1 - r0;
       T.first_block = r0;
-      T.n = static_cast<int>((tiles > 1 ? n * (t + 1) / tiles : n) - row0);
+      T.n = (tiles > 1 ? static_cast<int>(static_cast<int64_t>(n) * (t + 1) / tiles) : n) - row0;
       T.out_row = row0 + (s.offsets ? row : grp * s.out_group_rows);
       T.x_row = row0 + (s.offsets ? row : grp * s.x_group_rows);
       run_tile<kSwiglu, kX8, kGroup>(s, T, smem, header, wait);
