@@ -168,11 +168,13 @@ __host__ __device__ inline int header_bytes(int groups) {
 __host__ __device__ inline int x_row_bytes(int chunks) { return chunks * kChunk * 2; }
 __host__ __device__ inline int x_scale_bytes(int chunks) { return chunks * kTile * 4; }
 
-// The most tokens of one tile: their rows fit beside the rest.
+// Shared memory beside the tile's rows of x, and the most tokens of a tile.
+inline int fixed_smem(int groups, int chunks, int group) {
+  return header_bytes(groups) + kWarps * (kDepth * record_bytes(group) + kSlotBytes) +
+         x_scale_bytes(chunks) + 256;
+}
 inline int tile_cap(int groups, int chunks, int group) {
-  const int room = kSmem - header_bytes(groups) - kWarps * (kDepth * record_bytes(group) + kSlotBytes) -
-                   x_scale_bytes(chunks) - 256;
-  const int n = room / x_row_bytes(chunks);
+  const int n = (kSmem - fixed_smem(groups, chunks, group)) / x_row_bytes(chunks);
   return n < kTile ? n : kTile;
 }
 
@@ -347,12 +349,16 @@ __device__ __forceinline__ void load_x(const Int4Segment& s, const Tile& T, uint
   if (weigher) row_w[lane] = s.row_w[pair];
 }
 
+// What waits for the end of the kernel before this one: nothing any more,
+// the tile's x, or its weights too.
+enum { kWaitNone = 0, kWaitX = 1, kWaitWeights = 2 };
+
 // The tile's blocks x chunks records, dealt evenly to the warps as one
 // sequence; a block cut by a warp boundary is summed from its pieces, in
 // warp order, by the first warp that starts inside it.
 template <bool kSwiglu, bool kX8, int kGroup>
 __device__ __forceinline__ void run_tile(const Int4Segment& s, const Tile& T, uint8_t* smem,
-                                         int header, bool wait_for_x) {
+                                         int header, int wait) {
   constexpr int kRec = record_bytes(kGroup);
   Header* hd = reinterpret_cast<Header*>(smem);
   const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5, g = lane >> 2, c = lane & 3;
@@ -375,11 +381,12 @@ __device__ __forceinline__ void run_tile(const Int4Segment& s, const Tile& T, ui
     if (lane < (kRec - kCodeBytes) / 16) cp_async16(to + kCodeBytes, w + at + kCodeBytes);
     asm volatile("cp.async.commit_group;" ::: "memory");
   };
+  if (wait == kWaitWeights) pdl_wait();
   if (count > 0) {
 #pragma unroll
     for (int u = 0; u < kDepth - 1; ++u) fetch(ring + u * kRec, min(u * kRec, last));
   }
-  if (wait_for_x) pdl_wait();
+  if (wait == kWaitX) pdl_wait();
   load_x<kX8>(s, T, smem, xo, fo, hd->row_w);
   __syncthreads();
 
@@ -458,6 +465,7 @@ struct Int4Launch {
   int cap[2];  // tokens of a tile
   int early;   // the kernel before this one wrote nothing but x, and ran after
                // everything before it had ended
+  int smem;    // bytes of shared memory
 };
 
 // ceil(x / d) within [0, most]
@@ -482,7 +490,13 @@ __global__ void __launch_bounds__(kThreads, 1) gemv_int4_kernel(const __grid_con
   int32_t* first = reinterpret_cast<int32_t*>(hd->before + groups + 1);  // explicit rows' offsets
   uint16_t* number = reinterpret_cast<uint16_t*>(first + groups + 1);
   const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
-  if (!p.early) pdl_wait();
+  // Routing needs the kernels before this one, unless the launch says so;
+  // a launch without it plans its work while the kernel before it drains.
+  int wait = p.early ? kWaitX : kWaitWeights;
+  if (!p.early && p.seg[0].offsets) {
+    pdl_wait();
+    wait = kWaitNone;
+  }
   pdl_release();
 
   // Costs of groups 3 tid .. 3 tid + 2, then a scan of them and of the number
@@ -540,7 +554,6 @@ __global__ void __launch_bounds__(kThreads, 1) gemv_int4_kernel(const __grid_con
   }
   __syncthreads();
 
-  bool wait = p.early;
   for (int pos = lo < hi ? hd->at_first : present; pos < present; ++pos) {
     const int64_t before = hd->before[pos];
     if (before >= hi) break;
@@ -567,11 +580,11 @@ __global__ void __launch_bounds__(kThreads, 1) gemv_int4_kernel(const __grid_con
       T.out_row = row0 + (s.offsets ? row : grp * s.out_group_rows);
       T.x_row = row0 + (s.offsets ? row : grp * s.x_group_rows);
       run_tile<kSwiglu, kX8, kGroup>(s, T, smem, header, wait);
-      wait = false;
+      wait = kWaitNone;
       __syncthreads();  // shared memory is free for the next tile
     }
   }
-  if (wait) pdl_wait();  // a kernel ends after the one before it has
+  if (wait != kWaitNone) pdl_wait();  // a kernel ends after the one before it has
 }
 
 template <bool kSwiglu, bool kX8, int kGroup>
@@ -586,8 +599,8 @@ cudaError_t launch_kernel(const Int4Launch& p, int num_sms, cudaStream_t stream)
     if (err != cudaSuccess) return err;
     if (dev < 64) configured[dev] = 1;
   }
-  return launch_pdl(gemv_int4_kernel<kSwiglu, kX8, kGroup>, dim3(num_sms), dim3(kThreads), kSmem,
-                    stream, p);
+  return launch_pdl(gemv_int4_kernel<kSwiglu, kX8, kGroup>, dim3(num_sms), dim3(kThreads),
+                    p.smem, stream, p);
 }
 
 template <bool kSwiglu, bool kX8>
@@ -622,8 +635,12 @@ cudaError_t launch_gemv_int4(const Int4Params& p, int num_sms, cudaStream_t stre
   const bool x8 = p.seg[0].x_scale != nullptr;
   for (int i = 0; i < p.nseg; ++i) {
     l.seg[i] = p.seg[i];
-    l.cap[i] = tile_cap(groups, p.seg[i].chunks, p.group);
+    const Int4Segment& s = p.seg[i];
+    l.cap[i] = tile_cap(groups, s.chunks, p.group);
     if (l.cap[i] < 1) return cudaErrorInvalidValue;  // the callers' limit on the width
+    if (s.rows < l.cap[i]) l.cap[i] = static_cast<int>(s.rows);
+    const int need = fixed_smem(groups, s.chunks, p.group) + l.cap[i] * x_row_bytes(s.chunks);
+    l.smem = i && l.smem > need ? l.smem : need;
   }
   if (p.swiglu)
     return x8 ? launch_group<true, true>(l, p.group, num_sms, stream)

@@ -3,34 +3,63 @@
 //   s_i = a_i + r_i,  v_i = w_i s_i / sqrt(mean_i s_i^2 + eps)
 //   h = s, y = v, and per 128 columns  scale = max|v| / 448,
 //   code_i = e4m3(v_i / scale)
+// Bound by HBM for many rows (each input read once, each output written
+// once) and by latency for few.
 #include "common.cuh"
 #include "internal.h"
 
 namespace fgs {
 namespace {
 
-constexpr int kNormThreads = 256;
 constexpr int kRowGroup = 128;  // columns of a row with one scale
 
-template <typename T>
-__device__ __forceinline__ float to_f(T v);
-template <>
-__device__ __forceinline__ float to_f<float>(float v) {
-  return v;
+// N values of a row as fp32, 16 bytes (or one value) at a time.
+template <typename T, int N>
+struct Piece {
+  float v[N];
+};
+
+template <int N>
+__device__ __forceinline__ Piece<__nv_bfloat16, N> load(const __nv_bfloat16* p) {
+  Piece<__nv_bfloat16, N> o;
+  if constexpr (N == 1) {
+    o.v[0] = __bfloat162float(*p);
+  } else {
+    const uint4 u = *reinterpret_cast<const uint4*>(p);
+    const uint32_t w[4] = {u.x, u.y, u.z, u.w};
+#pragma unroll
+    for (int i = 0; i < 4; ++i) {
+      o.v[2 * i] = __uint_as_float(w[i] << 16);
+      o.v[2 * i + 1] = __uint_as_float(w[i] & 0xffff0000u);
+    }
+  }
+  return o;
 }
-template <>
-__device__ __forceinline__ float to_f<__nv_bfloat16>(__nv_bfloat16 v) {
-  return __bfloat162float(v);
+template <int N>
+__device__ __forceinline__ Piece<float, N> load(const float* p) {
+  Piece<float, N> o;
+  if constexpr (N == 1) {
+    o.v[0] = *p;
+  } else {
+    const float4 u = *reinterpret_cast<const float4*>(p);
+    o.v[0] = u.x, o.v[1] = u.y, o.v[2] = u.z, o.v[3] = u.w;
+  }
+  return o;
 }
-template <typename T>
-__device__ __forceinline__ T from_f(float v);
-template <>
-__device__ __forceinline__ float from_f<float>(float v) {
-  return v;
+template <int N>
+__device__ __forceinline__ void store(__nv_bfloat16* p, const float (&v)[N]) {
+  if constexpr (N == 1)
+    *p = __float2bfloat16_rn(v[0]);
+  else
+    *reinterpret_cast<uint4*>(p) = make_uint4(pack_bf16x2(v[0], v[1]), pack_bf16x2(v[2], v[3]),
+                                              pack_bf16x2(v[4], v[5]), pack_bf16x2(v[6], v[7]));
 }
-template <>
-__device__ __forceinline__ __nv_bfloat16 from_f<__nv_bfloat16>(float v) {
-  return __float2bfloat16_rn(v);
+template <int N>
+__device__ __forceinline__ void store(float* p, const float (&v)[N]) {
+  if constexpr (N == 1)
+    *p = v[0];
+  else
+    *reinterpret_cast<float4*>(p) = make_float4(v[0], v[1], v[2], v[3]);
 }
 
 // max that keeps NaN, as the definition's maximum over a group does
@@ -40,75 +69,157 @@ __device__ __forceinline__ float max_nan(float a, float b) {
   return r;
 }
 
-__device__ __forceinline__ uint8_t to_e4m3(float v) {
+// Two E4M3 codes, a's in the low byte.
+__device__ __forceinline__ uint32_t e4m3x2(float a, float b) {
   uint16_t r;
-  asm("cvt.rn.satfinite.e4m3x2.f32 %0, %1, %2;" : "=h"(r) : "f"(0.0f), "f"(v));
-  return static_cast<uint8_t>(r);
+  asm("cvt.rn.satfinite.e4m3x2.f32 %0, %1, %2;" : "=h"(r) : "f"(b), "f"(a));
+  return r;
 }
 
-// One block a row; a warp takes 128 columns at a time, so that a scale group
-// is one warp's values.
-template <typename T>
-__global__ void __launch_bounds__(kNormThreads)
-    add_rmsnorm_kernel(const T* a, const T* r, const T* w, float eps, int d, T* h, T* y,
-                       uint8_t* y8, float* ys) {
+template <int N>
+__device__ __forceinline__ void store_codes(uint8_t* p, const float (&v)[N], float f) {
+  if constexpr (N == 8)
+    *reinterpret_cast<uint2*>(p) =
+        make_uint2(e4m3x2(v[0] * f, v[1] * f) | e4m3x2(v[2] * f, v[3] * f) << 16,
+                   e4m3x2(v[4] * f, v[5] * f) | e4m3x2(v[6] * f, v[7] * f) << 16);
+  else if constexpr (N == 4)
+    *reinterpret_cast<uint32_t*>(p) =
+        e4m3x2(v[0] * f, v[1] * f) | e4m3x2(v[2] * f, v[3] * f) << 16;
+}
+
+struct NormPtrs {
+  const void* a;
+  const void* r;
+  const void* w;
+  void* h;
+  void* y;
+  uint8_t* y8;
+  float* ys;
+};
+
+// kThreads threads a row (a block holds kRows of them), N values at a time.
+// kKeep pieces of a thread's part stay in registers between the sum and the
+// outputs; a wider row (kKeep == 0) is read twice, the second time mostly
+// from L2.  Reads of an element come before the writes of it, so h and y may
+// be the inputs.
+template <typename T, int N, int kThreads, int kRows, int kKeep>
+__global__ void __launch_bounds__(kThreads* kRows)
+    add_rmsnorm_kernel(const NormPtrs p, float eps, int d, int64_t rows) {
+  constexpr int kWarps = kThreads / 32;
+  __shared__ float part[kRows][kWarps];
   pdl_wait();
-  __shared__ float part[kNormThreads / 32];
-  const int64_t row = blockIdx.x;
+  const int sub = kRows > 1 ? threadIdx.x / kThreads : 0;
+  const int tid = kRows > 1 ? threadIdx.x % kThreads : threadIdx.x;
+  const int64_t row = static_cast<int64_t>(blockIdx.x) * kRows + sub;
+  const bool live = row < rows;
   const int64_t base = row * d;
-  const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
+  const T* a = static_cast<const T*>(p.a) + base;
+  const T* r = p.r ? static_cast<const T*>(p.r) + base : nullptr;
+  const T* w = static_cast<const T*>(p.w);
+  const int pieces = live ? d / N : 0;
+
+  auto sum = [&](int i) {
+    Piece<T, N> s = load<N>(a + static_cast<int64_t>(i) * N);
+    if (r) {
+      const Piece<T, N> b = load<N>(r + static_cast<int64_t>(i) * N);
+#pragma unroll
+      for (int k = 0; k < N; ++k) s.v[k] += b.v[k];
+    }
+    return s;
+  };
+  Piece<T, N> keep[kKeep ? kKeep : 1];
   float q = 0.0f;
-  for (int c = threadIdx.x; c < d; c += kNormThreads) {
-    float s = to_f(a[base + c]);
-    if (r) s += to_f(r[base + c]);
-    q = fmaf(s, s, q);
+  if constexpr (kKeep > 0) {
+#pragma unroll
+    for (int j = 0; j < kKeep; ++j)
+      if (tid + j * kThreads < pieces) keep[j] = sum(tid + j * kThreads);
+#pragma unroll
+    for (int j = 0; j < kKeep; ++j)
+      if (tid + j * kThreads < pieces)
+#pragma unroll
+        for (int k = 0; k < N; ++k) q = fmaf(keep[j].v[k], keep[j].v[k], q);
+  } else {
+    for (int i = tid; i < pieces; i += kThreads) {
+      const Piece<T, N> s = sum(i);
+#pragma unroll
+      for (int k = 0; k < N; ++k) q = fmaf(s.v[k], s.v[k], q);
+    }
   }
+#pragma unroll
   for (int o = 16; o; o >>= 1) q += __shfl_xor_sync(0xffffffffu, q, o);
-  if (lane == 0) part[warp] = q;
-  __syncthreads();
-  q = 0.0f;
-  for (int i = 0; i < kNormThreads / 32; ++i) q += part[i];
-  const float rs = rsqrtf(q / static_cast<float>(d) + eps);
-  for (int c0 = warp * kRowGroup; c0 < d; c0 += kNormThreads / 32 * kRowGroup) {
-    float v[4], m = 0.0f;
-    for (int i = 0; i < 4; ++i) {
-      const int c = c0 + 32 * i + lane;
-      v[i] = 0.0f;
-      if (c < d) {
-        float s = to_f(a[base + c]);
-        if (r) s += to_f(r[base + c]);
-        if (h) h[base + c] = from_f<T>(s);
-        v[i] = s * rs * to_f(w[c]);
-        if (y) y[base + c] = from_f<T>(v[i]);
-      }
-      m = max_nan(m, fabsf(v[i]));
-    }
-    if (y8) {
-      for (int o = 16; o; o >>= 1) m = max_nan(m, __shfl_xor_sync(0xffffffffu, m, o));
-      const float scale = m / 448.0f;
-      if (lane == 0) ys[row * (d / kRowGroup) + c0 / kRowGroup] = scale;
-      for (int i = 0; i < 4; ++i) {
-        const int c = c0 + 32 * i + lane;
-        y8[base + c] = to_e4m3(scale == 0.0f ? 0.0f : v[i] / scale);
-      }
-    }
+  if constexpr (kWarps > 1) {
+    if ((tid & 31) == 0) part[sub][tid >> 5] = q;
+    __syncthreads();
+    q = 0.0f;
+#pragma unroll
+    for (int i = 0; i < kWarps; ++i) q += part[sub][i];
   }
+  const float rs = rsqrtf(q / static_cast<float>(d) + eps);
+
+  // a scale group is 128 / N neighbouring lanes of a warp, whose pieces all
+  // exist or none does
+  auto finish = [&](int i, const Piece<T, N>& s) {
+    const int64_t at = static_cast<int64_t>(i) * N;
+    const Piece<T, N> g = load<N>(w + at);
+    float v[N];
+#pragma unroll
+    for (int k = 0; k < N; ++k) v[k] = s.v[k] * rs * g.v[k];
+    if (p.h) store<N>(static_cast<T*>(p.h) + base + at, s.v);
+    if (p.y) store<N>(static_cast<T*>(p.y) + base + at, v);
+    if constexpr (N > 1) {
+      if (p.y8) {
+        constexpr int kLanes = kRowGroup / N;
+        float m = 0.0f;
+#pragma unroll
+        for (int k = 0; k < N; ++k) m = max_nan(m, fabsf(v[k]));
+        const uint32_t mask = kLanes == 32 ? 0xffffffffu
+                                           : ((1u << (kLanes & 31)) - 1) << (threadIdx.x & 31 & ~(kLanes - 1));
+#pragma unroll
+        for (int o = kLanes / 2; o; o >>= 1) m = max_nan(m, __shfl_xor_sync(mask, m, o));
+        // v / scale as v (448 / max): one rounding more than the quotient
+        const float f = m == 0.0f ? 0.0f : 448.0f / m;
+        store_codes<N>(p.y8 + base + at, v, f);
+        if ((tid & (kLanes - 1)) == 0) p.ys[row * (d / kRowGroup) + at / kRowGroup] = m / 448.0f;
+      }
+    }
+  };
+  if constexpr (kKeep > 0) {
+#pragma unroll
+    for (int j = 0; j < kKeep; ++j)
+      if (tid + j * kThreads < pieces) finish(tid + j * kThreads, keep[j]);
+  } else {
+    for (int i = tid; i < pieces; i += kThreads) finish(i, sum(i));
+  }
+}
+
+template <typename T, int N, int kThreads, int kRows, int kKeep>
+cudaError_t launch(const NormArgs& n, cudaStream_t stream) {
+  const NormPtrs p = {n.a, n.r, n.w, n.h, n.y, n.y8, n.ys};
+  return launch_pdl(add_rmsnorm_kernel<T, N, kThreads, kRows, kKeep>,
+                    dim3(static_cast<unsigned>((n.T + kRows - 1) / kRows)), dim3(kThreads * kRows),
+                    0, stream, p, n.eps, n.d, n.T);
+}
+
+// A row of few pieces takes one warp (eight rows a block), a wider one a
+// block of as many threads as leave each a piece or a few.
+template <typename T, int N>
+cudaError_t dispatch(const NormArgs& n, cudaStream_t stream) {
+  const int pieces = n.d / N;
+  if (pieces <= 32) return launch<T, N, 32, 8, 1>(n, stream);
+  if (pieces <= 128) return launch<T, N, 128, 1, 1>(n, stream);
+  if (pieces <= 256) return launch<T, N, 256, 1, 1>(n, stream);
+  if (pieces <= 512) return launch<T, N, 512, 1, 1>(n, stream);
+  if (pieces <= 1024) return launch<T, N, 1024, 1, 1>(n, stream);
+  if (pieces <= 2048) return launch<T, N, 512, 1, 4>(n, stream);
+  return launch<T, N, 1024, 1, 0>(n, stream);
 }
 
 }  // namespace
 
 cudaError_t launch_add_rmsnorm(const NormArgs& n, cudaStream_t stream) {
-  if (n.bf16) {
-    using B = __nv_bfloat16;
-    return launch_pdl(add_rmsnorm_kernel<B>, dim3(static_cast<unsigned>(n.T)), dim3(kNormThreads),
-                      0, stream, static_cast<const B*>(n.a), static_cast<const B*>(n.r),
-                      static_cast<const B*>(n.w), n.eps, n.d, static_cast<B*>(n.h),
-                      static_cast<B*>(n.y), n.y8, n.ys);
-  }
-  return launch_pdl(add_rmsnorm_kernel<float>, dim3(static_cast<unsigned>(n.T)),
-                    dim3(kNormThreads), 0, stream, static_cast<const float*>(n.a),
-                    static_cast<const float*>(n.r), static_cast<const float*>(n.w), n.eps, n.d,
-                    static_cast<float*>(n.h), static_cast<float*>(n.y), n.y8, n.ys);
+  if (n.bf16)
+    return n.d % 8 ? dispatch<__nv_bfloat16, 1>(n, stream) : dispatch<__nv_bfloat16, 8>(n, stream);
+  return n.d % 4 ? dispatch<float, 1>(n, stream) : dispatch<float, 4>(n, stream);
 }
 
 }  // namespace fgs
