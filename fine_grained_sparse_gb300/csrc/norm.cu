@@ -97,20 +97,23 @@ struct NormPtrs {
   float* ys;
 };
 
-// kThreads threads a row (a block holds kRows of them), N values at a time.
-// kKeep pieces of a thread's part stay in registers between the sum and the
-// outputs; a wider row (kKeep == 0) is read twice, the second time mostly
-// from L2.  Reads of an element come before the writes of it, so h and y may
-// be the inputs.
-template <typename T, int N, int kThreads, int kRows, int kKeep>
-__global__ void __launch_bounds__(kThreads* kRows)
+// A block a row, or (kWarpRow) a warp a row and kRowsPerBlock rows a block;
+// N values at a time.  kKeep pieces of a thread's part stay in registers
+// between the sum and the outputs; a wider row (kKeep == 0) is read twice, the
+// second time mostly from L2.  Reads of an element come before the writes of
+// it, so h and y may be the inputs.
+constexpr int kRowsPerBlock = 8;
+
+template <typename T, int N, bool kWarpRow, int kKeep, int kMaxThreads, int kMinBlocks>
+__global__ void __launch_bounds__(kMaxThreads, kMinBlocks)
     add_rmsnorm_kernel(const NormPtrs p, float eps, int d, int64_t rows) {
-  constexpr int kWarps = kThreads / 32;
-  __shared__ float part[kRows][kWarps];
+  __shared__ float part[32];
   pdl_wait();
-  const int sub = kRows > 1 ? threadIdx.x / kThreads : 0;
-  const int tid = kRows > 1 ? threadIdx.x % kThreads : threadIdx.x;
-  const int64_t row = static_cast<int64_t>(blockIdx.x) * kRows + sub;
+  const int threads = kWarpRow ? 32 : blockDim.x;
+  const int tid = kWarpRow ? threadIdx.x & 31 : threadIdx.x;
+  const int64_t row = kWarpRow
+                          ? static_cast<int64_t>(blockIdx.x) * kRowsPerBlock + threadIdx.x / 32
+                          : blockIdx.x;
   const bool live = row < rows;
   const int64_t base = row * d;
   const T* a = static_cast<const T*>(p.a) + base;
@@ -132,14 +135,14 @@ __global__ void __launch_bounds__(kThreads* kRows)
   if constexpr (kKeep > 0) {
 #pragma unroll
     for (int j = 0; j < kKeep; ++j)
-      if (tid + j * kThreads < pieces) keep[j] = sum(tid + j * kThreads);
+      if (tid + j * threads < pieces) keep[j] = sum(tid + j * threads);
 #pragma unroll
     for (int j = 0; j < kKeep; ++j)
-      if (tid + j * kThreads < pieces)
+      if (tid + j * threads < pieces)
 #pragma unroll
         for (int k = 0; k < N; ++k) q = fmaf(keep[j].v[k], keep[j].v[k], q);
   } else {
-    for (int i = tid; i < pieces; i += kThreads) {
+    for (int i = tid; i < pieces; i += threads) {
       const Piece<T, N> s = sum(i);
 #pragma unroll
       for (int k = 0; k < N; ++k) q = fmaf(s.v[k], s.v[k], q);
@@ -147,12 +150,12 @@ __global__ void __launch_bounds__(kThreads* kRows)
   }
 #pragma unroll
   for (int o = 16; o; o >>= 1) q += __shfl_xor_sync(0xffffffffu, q, o);
-  if constexpr (kWarps > 1) {
-    if ((tid & 31) == 0) part[sub][tid >> 5] = q;
+  if constexpr (!kWarpRow) {
+    if ((tid & 31) == 0) part[tid >> 5] = q;
     __syncthreads();
-    q = 0.0f;
+    q = (tid & 31) < threads / 32 ? part[tid & 31] : 0.0f;
 #pragma unroll
-    for (int i = 0; i < kWarps; ++i) q += part[sub][i];
+    for (int o = 16; o; o >>= 1) q += __shfl_xor_sync(0xffffffffu, q, o);
   }
   const float rs = rsqrtf(q / static_cast<float>(d) + eps);
 
@@ -176,8 +179,12 @@ __global__ void __launch_bounds__(kThreads* kRows)
                                            : ((1u << (kLanes & 31)) - 1) << (threadIdx.x & 31 & ~(kLanes - 1));
 #pragma unroll
         for (int o = kLanes / 2; o; o >>= 1) m = max_nan(m, __shfl_xor_sync(mask, m, o));
-        // v / scale as v (448 / max): one rounding more than the quotient
-        const float f = m == 0.0f ? 0.0f : 448.0f / m;
+        // v / scale as v (448 / max), one rounding more than the quotient;
+        // small groups are brought up first, so that 448 / max is finite
+        const float up = m < 1e-30f ? 0x1p60f : 1.0f;
+        const float f = m == 0.0f ? 0.0f : 448.0f / (m * up);
+#pragma unroll
+        for (int k = 0; k < N; ++k) v[k] *= up;
         store_codes<N>(p.y8 + base + at, v, f);
         if ((tid & (kLanes - 1)) == 0) p.ys[row * (d / kRowGroup) + at / kRowGroup] = m / 448.0f;
       }
@@ -186,32 +193,39 @@ __global__ void __launch_bounds__(kThreads* kRows)
   if constexpr (kKeep > 0) {
 #pragma unroll
     for (int j = 0; j < kKeep; ++j)
-      if (tid + j * kThreads < pieces) finish(tid + j * kThreads, keep[j]);
+      if (tid + j * threads < pieces) finish(tid + j * threads, keep[j]);
   } else {
-    for (int i = tid; i < pieces; i += kThreads) finish(i, sum(i));
+    for (int i = tid; i < pieces; i += threads) finish(i, sum(i));
   }
 }
 
-template <typename T, int N, int kThreads, int kRows, int kKeep>
-cudaError_t launch(const NormArgs& n, cudaStream_t stream) {
+template <typename T, int N, bool kWarpRow, int kKeep, int kMaxThreads, int kMinBlocks = 1>
+cudaError_t launch(const NormArgs& n, int threads, cudaStream_t stream) {
   const NormPtrs p = {n.a, n.r, n.w, n.h, n.y, n.y8, n.ys};
-  return launch_pdl(add_rmsnorm_kernel<T, N, kThreads, kRows, kKeep>,
-                    dim3(static_cast<unsigned>((n.T + kRows - 1) / kRows)), dim3(kThreads * kRows),
-                    0, stream, p, n.eps, n.d, n.T);
+  const int64_t blocks = kWarpRow ? (n.T + kRowsPerBlock - 1) / kRowsPerBlock : n.T;
+  return launch_pdl(add_rmsnorm_kernel<T, N, kWarpRow, kKeep, kMaxThreads, kMinBlocks>,
+                    dim3(static_cast<unsigned>(blocks)),
+                    dim3(kWarpRow ? 32 * kRowsPerBlock : threads), 0, stream, p, n.eps, n.d, n.T);
 }
 
-// A row of few pieces takes one warp (eight rows a block), a wider one a
-// block of as many threads as leave each a piece or a few.
+// Threads of a row.  Few rows are a matter of latency: a thread a piece.
+// Many are one of bandwidth: two pieces a thread, with the registers held to
+// three blocks of 512 an SM (8192 x 7168 bf16 with all outputs, 530 MB: 448
+// threads x 2 so held 90.4 us, not held 108.0; 896 x 1 91.5; 224 x 4 held to
+// 6 blocks 91.9, not held 100.6; 128 x 7 104.7; the copy rate allows 78.4).
+constexpr int kManyRows = 2 * 152;
+
 template <typename T, int N>
 cudaError_t dispatch(const NormArgs& n, cudaStream_t stream) {
   const int pieces = n.d / N;
-  if (pieces <= 32) return launch<T, N, 32, 8, 1>(n, stream);
-  if (pieces <= 128) return launch<T, N, 128, 1, 1>(n, stream);
-  if (pieces <= 256) return launch<T, N, 256, 1, 1>(n, stream);
-  if (pieces <= 512) return launch<T, N, 512, 1, 1>(n, stream);
-  if (pieces <= 1024) return launch<T, N, 1024, 1, 1>(n, stream);
-  if (pieces <= 2048) return launch<T, N, 512, 1, 4>(n, stream);
-  return launch<T, N, 1024, 1, 0>(n, stream);
+  auto round32 = [](int v) { return (v + 31) / 32 * 32; };
+  if (pieces <= 32) return launch<T, N, true, 1, 32 * kRowsPerBlock>(n, 32, stream);
+  if (pieces <= 128) return launch<T, N, false, 1, 1024>(n, round32(pieces), stream);
+  if (pieces <= 1024)
+    return n.T < kManyRows ? launch<T, N, false, 1, 1024>(n, round32(pieces), stream)
+                           : launch<T, N, false, 2, 512, 3>(n, round32((pieces + 1) / 2), stream);
+  if (pieces <= 4096) return launch<T, N, false, 4, 1024>(n, round32((pieces + 3) / 4), stream);
+  return launch<T, N, false, 0, 1024>(n, 1024, stream);
 }
 
 }  // namespace

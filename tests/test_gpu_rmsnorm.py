@@ -127,6 +127,28 @@ def test_large_values_and_magnitudes():
     _check(_run(3, 256, "f32", False, True, x=x), 256, "f32")
 
 
+def test_tiny_weights():
+    """Groups whose 448 / max overflows fp32 still get the codes of v / scale."""
+    need_gpu()
+    fgs = lib()
+    x = torch.randn((2, 256), generator=torch.Generator().manual_seed(4))
+    w = torch.full((256,), 2.0 ** -122)
+    w[128:] = 1.0
+    y = torch.empty((2, 256), device="cuda")
+    y8 = torch.empty((2, 256), dtype=torch.uint8, device="cuda")
+    ys = torch.empty((2, 2), device="cuda")
+    fgs.moe_add_rmsnorm(fgs.MOE_F32, 2, 256, x.cuda(), None, w.cuda(), EPS, None, y, y8, ys)
+    v = y.double().cpu().view(2, 2, 128)
+    s = ys.double().cpu()
+    # the scale is rounded once, where fp32 is subnormal to a multiple of 2^-149
+    assert ((s - v.abs().amax(2) / 448).abs() <= 2.0 ** -149 + s * 2 * U_F32).all()
+    q = v / s[..., None]
+    got = y8.cpu().view(torch.float8_e4m3fn).double().view(2, 2, 128)
+    # one E4M3 rounding of the quotient, and saturation at 448
+    lim = torch.maximum(q.abs() * 2.0 ** -4, torch.tensor(2.0 ** -10)) + q.abs() * 8 * U_F32
+    assert ((got - q.clamp(-448, 448)).abs() <= lim).all()
+
+
 @pytest.mark.parametrize("which", ["h=x y=r", "h=r y=x", "y=x"])
 @pytest.mark.parametrize("d", [100, 7168])
 def test_in_place(which, d):
