@@ -449,6 +449,7 @@ int32_t run_experts_int4(const moe_config* c, int64_t T, const ExpertIO& io, voi
   __nv_bfloat16* Hs = at<__nv_bfloat16>(ws, L.Hs);
   Int4Params p;
   p.group = int4_group(c->weight_layout);
+  p.status = at<int>(ws, L.status);
   p.nseg = S ? 2 : 1;
   p.swiglu = 1;
   Int4Segment& r = p.seg[0];
@@ -480,11 +481,12 @@ int32_t run_experts_int4(const moe_config* c, int64_t T, const ExpertIO& io, voi
     s.out_group_rows = T;
   }
   if (ev_up) MOE_CUDA(cudaEventRecord(ev_up, st));
-  MOE_CUDA(launch_gemv_int4(p, num_sms(), st));
+  MOE_CUDA(launch_int4(p, num_sms(), st));
   if (ev_down) MOE_CUDA(cudaEventRecord(ev_down, st));
 
   Int4Params q;
   q.group = p.group;
+  q.status = p.status;
   q.nseg = p.nseg;
   q.early = ev_down ? 0 : 1;  // nothing stands between the two launches
   Int4Segment& r2 = q.seg[0];
@@ -516,7 +518,7 @@ int32_t run_experts_int4(const moe_config* c, int64_t T, const ExpertIO& io, voi
     s2.out_ld = d;
     s2.out_group_rows = T;
   }
-  MOE_CUDA(launch_gemv_int4(q, num_sms(), st));
+  MOE_CUDA(launch_int4(q, num_sms(), st));
   return MOE_OK;
 }
 
@@ -1230,7 +1232,7 @@ int32_t moe_linear_int4(int64_t T, int32_t in_features, int32_t out_features, in
   s.out = static_cast<__nv_bfloat16*>(y);
   s.out_ld = out_features;
   s.add = static_cast<const __nv_bfloat16*>(add);
-  MOE_CUDA(launch_gemv_int4(p, num_sms(), static_cast<cudaStream_t>(stream)));
+  MOE_CUDA(launch_int4(p, num_sms(), static_cast<cudaStream_t>(stream)));
   return MOE_OK;
 }
 

@@ -6,21 +6,10 @@
 // c are 4-bit codes, s one bf16 scale per 32 or 128 columns of a row, x bf16
 // or E4M3 with one fp32 scale per 128 columns.  The gate/up pass stores
 // SiLU(z_gate) z_up, the other passes w_t z + add.
-#include <cuda_fp16.h>
-
-#include "common.cuh"
-#include "internal.h"
+#include "int4.cuh"
 
 namespace fgs {
 namespace {
-
-constexpr int kChunk = 128;       // columns of one packed record
-constexpr int kBlockRows = 16;    // rows of one packed record
-constexpr int kCodeBytes = kChunk * kBlockRows / 2;
-
-__host__ __device__ constexpr int record_bytes(int group) {
-  return kCodeBytes + kBlockRows * (kChunk / group) * 2;
-}
 
 // ------------------------------------------------------------------ packing
 // One warp a record.  Lane l = 4 g + c holds, in word i, the A fragment that
@@ -100,43 +89,6 @@ __device__ __forceinline__ void mma(float (&p)[4], const uint32_t (&a)[4], uint3
       : "r"(a[0]), "r"(a[1]), "r"(a[2]), "r"(a[3]), "r"(b0), "r"(b1));
 }
 
-// Eight E4M3 codes to four f16 pairs (exact).
-__device__ __forceinline__ uint4 e4m3x8_to_f16(uint2 v) {
-  uint4 o;
-  asm("{\n\t.reg .b16 a, b, c, d;\n\tmov.b32 {a, b}, %4;\n\tmov.b32 {c, d}, %5;\n\t"
-      "cvt.rn.f16x2.e4m3x2 %0, a;\n\tcvt.rn.f16x2.e4m3x2 %1, b;\n\t"
-      "cvt.rn.f16x2.e4m3x2 %2, c;\n\tcvt.rn.f16x2.e4m3x2 %3, d;\n\t}"
-      : "=r"(o.x), "=r"(o.y), "=r"(o.z), "=r"(o.w)
-      : "r"(v.x), "r"(v.y));
-  return o;
-}
-
-// Eight bf16 values per lane of a half warp (128 columns) to f16, scaled by
-// 2^(141 - e) where e is the biased exponent of the largest of the 128.  An
-// infinity or NaN counts as the largest finite value, and maxima below 2^-112
-// are left small.
-__device__ __forceinline__ uint4 bf16x8_to_f16(uint4 v, uint32_t& e) {
-  uint32_t w[4] = {v.x, v.y, v.z, v.w}, m = 0;
-#pragma unroll
-  for (int i = 0; i < 4; ++i) m = __vmaxu2(m, w[i] & 0x7fff7fffu);
-#pragma unroll
-  for (int o = 8; o; o >>= 1) m = __vmaxu2(m, __shfl_xor_sync(0xffffffffu, m, o));
-  m = max(m & 0xffffu, m >> 16);
-  e = min(max(m >> 7, 15u), 254u);
-  const float up = __uint_as_float((268u - e) << 23);
-#pragma unroll
-  for (int i = 0; i < 4; ++i) {
-    const float lo = __uint_as_float(w[i] << 16) * up;
-    const float hi = __uint_as_float(w[i] & 0xffff0000u) * up;
-    asm("cvt.rn.f16x2.f32 %0, %1, %2;" : "=r"(w[i]) : "f"(hi), "f"(lo));
-  }
-  return make_uint4(w[0], w[1], w[2], w[3]);
-}
-
-__device__ __forceinline__ void cp_async16(uint32_t dst, const void* src) {
-  asm volatile("cp.async.cg.shared.global [%0], [%1], 16;" ::"r"(dst), "l"(src) : "memory");
-}
-
 // ------------------------------------------------------------------- kernel
 constexpr int kWarps = 16;
 constexpr int kThreads = 32 * kWarps;
@@ -147,21 +99,17 @@ constexpr int kSlotBytes = 512;   // a block's sums for kTile tokens
 constexpr int kTileCost = 128;    // what beginning a tile costs, in records
 
 // Shared memory: the header (row weights of the tile, the scan's warp sums,
-// the CTA's first group; then, over the groups that have rows: the cost
-// before each [groups + 1] and its number [groups]; and the groups' first
-// rows [groups + 1]), each warp's ring of records, partial sums, the scales
-// of x and (256-byte aligned) x.
-constexpr int kMaxGroups = 1024 + 8;
-
+// the CTA's first group, the group lists), each warp's ring of records,
+// partial sums, the scales of x and (256-byte aligned) x.
 struct Header {
   float row_w[kTile];
   int64_t warp_sum[kWarps];
   int at_first, pad;
-  int64_t before[1];
+  int64_t lists[1];
 };
 
 __host__ __device__ inline int header_bytes(int groups) {
-  return static_cast<int>(sizeof(Header) + 14 * (groups + 1) + 255) / 256 * 256;
+  return static_cast<int>(sizeof(Header) + group_list_bytes(groups) + 255) / 256 * 256;
 }
 
 // A token's x as f16, and fp32 scales of kTile tokens per 128 columns.
@@ -349,10 +297,6 @@ __device__ __forceinline__ void load_x(const Int4Segment& s, const Tile& T, uint
   if (weigher) row_w[lane] = s.row_w[pair];
 }
 
-// What waits for the end of the kernel before this one: nothing any more,
-// the tile's x, or its weights too.
-enum { kWaitNone = 0, kWaitX = 1, kWaitWeights = 2 };
-
 // The tile's blocks x chunks records, dealt evenly to the warps as one
 // sequence; a block cut by a warp boundary is summed from its pieces, in
 // warp order, by the first warp that starts inside it.
@@ -459,15 +403,6 @@ __device__ __forceinline__ void run_tile(const Int4Segment& s, const Tile& T, ui
   }
 }
 
-struct Int4Launch {
-  Int4Segment seg[2];
-  int nseg;
-  int cap[2];  // tokens of a tile
-  int early;   // the kernel before this one wrote nothing but x, and ran after
-               // everything before it had ended
-  int smem;    // bytes of shared memory
-};
-
 // ceil(x / d) within [0, most]
 __device__ __forceinline__ int blocks_before(int64_t x, int d, int most) {
   if (x <= 0) return 0;
@@ -487,81 +422,40 @@ __global__ void __launch_bounds__(kThreads, 1) gemv_int4_kernel(const __grid_con
   Header* hd = reinterpret_cast<Header*>(smem);
   const int n0 = p.seg[0].groups, groups = n0 + (p.nseg > 1 ? p.seg[1].groups : 0);
   const int header = header_bytes(groups);
-  int32_t* first = reinterpret_cast<int32_t*>(hd->before + groups + 1);  // explicit rows' offsets
-  uint16_t* number = reinterpret_cast<uint16_t*>(first + groups + 1);
-  const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
   // Routing needs the kernels before this one, unless the launch says so;
   // a launch without it plans its work while the kernel before it drains.
-  int wait = p.early ? kWaitX : kWaitWeights;
-  if (!p.early && p.seg[0].offsets) {
-    pdl_wait();
-    wait = kWaitNone;
-  }
+  int wait = p.wait == kWaitWeights && p.seg[0].offsets ? kWaitNone : p.wait;
+  if (wait != p.wait) pdl_wait();
   pdl_release();
 
-  // Costs of groups 3 tid .. 3 tid + 2, then a scan of them and of the number
-  // of groups with rows (in the low 11 bits of the same word).
-  constexpr int kPer = (kMaxGroups + kThreads - 1) / kThreads, kCountBits = 11;
-  static_assert(kMaxGroups < 1 << kCountBits, "");
-  int64_t cost[kPer], mine = 0;
-#pragma unroll
-  for (int i = 0; i < kPer; ++i) {
-    const int k = tid * kPer + i, si = k >= n0;
-    cost[i] = 0;
-    if (k >= groups) continue;
-    const Int4Segment& s = p.seg[si];
-    int n = static_cast<int>(s.rows);
-    if (s.offsets) {
-      const int32_t a = s.offsets[k], b = s.offsets[k + 1];
-      first[k] = a;
-      if (k == n0 - 1) first[n0] = b;
-      n = b - a;
-    }
-    if (n > 0)
-      cost[i] = (static_cast<int64_t>(s.blocks) * s.chunks + kTileCost) *
-                    ((n + p.cap[si] - 1u) / p.cap[si]) << kCountBits | 1;
-    mine += cost[i];
-  }
-  int64_t incl = mine;
-  for (int o = 1; o < 32; o <<= 1) {
-    const int64_t v = __shfl_up_sync(0xffffffffu, incl, o);
-    if (lane >= o) incl += v;
-  }
-  if (lane == 31) hd->warp_sum[warp] = incl;
-  __syncthreads();
-  int64_t at = incl - mine, total = 0;
-#pragma unroll
-  for (int v = 0; v < kWarps; ++v) {
-    const int64_t w = hd->warp_sum[v];
-    if (v < warp) at += w;
-    total += w;
-  }
-  const int present = static_cast<int>(total & ((1 << kCountBits) - 1));
-  total >>= kCountBits;
-  const int64_t share = total < (1ll << 32) ? static_cast<uint32_t>(total) / gridDim.x
-                                            : total / gridDim.x;
-  const int rest = static_cast<int>(total - share * gridDim.x), cta = blockIdx.x;
-  const int64_t lo = share * cta + min(cta, rest), hi = lo + share + (cta < rest);
-#pragma unroll
-  for (int i = 0; i < kPer; ++i) {
-    if (!cost[i]) continue;
-    const int pos = static_cast<int>(at & ((1 << kCountBits) - 1));
-    const int64_t b = at >> kCountBits;
-    hd->before[pos] = b;
-    number[pos] = static_cast<uint16_t>(tid * kPer + i);
-    if (b <= lo && lo < b + (cost[i] >> kCountBits)) hd->at_first = pos;
-    at += cost[i];
-  }
-  __syncthreads();
+  const GroupLists lists = group_lists(hd->lists, groups);
+  int64_t lo = 0, hi = 0;
+  const GroupPlan plan = plan_groups<kThreads>(
+      p, lists, hd->warp_sum,
+      [&](int si, int n) -> int64_t {
+        if (n <= 0 || n > p.most) return 0;
+        return (static_cast<int64_t>(p.seg[si].blocks) * p.seg[si].chunks + kTileCost) *
+               ((n + p.cap[si] - 1u) / p.cap[si]);
+      },
+      [&](int64_t total) {
+        const int64_t share = total < (1ll << 32) ? static_cast<uint32_t>(total) / gridDim.x
+                                                  : total / gridDim.x;
+        const int rest = static_cast<int>(total - share * gridDim.x), cta = blockIdx.x;
+        lo = share * cta + min(cta, rest);
+        hi = lo + share + (cta < rest);
+      },
+      [&](int pos, int64_t before, int64_t cost) {
+        if (before <= lo && lo < before + cost) hd->at_first = pos;
+      });
 
-  for (int pos = lo < hi ? hd->at_first : present; pos < present; ++pos) {
-    const int64_t before = hd->before[pos];
+  for (int pos = lo < hi ? hd->at_first : plan.present; pos < plan.present; ++pos) {
+    const int64_t before = lists.before[pos];
     if (before >= hi) break;
-    const int k = number[pos], si = k >= n0;
+    const int k = lists.number[pos], si = k >= n0;
     const Int4Segment& s = p.seg[si];
     const int grp = si ? k - n0 : k;
-    const int row = s.offsets ? first[k] : 0;
-    const int n = s.offsets ? first[k + 1] - row : static_cast<int>(s.rows);
+    const int row = s.offsets ? lists.first[k] : 0;
+    const int n = s.offsets ? lists.first[k + 1] - row : static_cast<int>(s.rows);
     const int tiles = (n + p.cap[si] - 1u) / p.cap[si];
     const int64_t tile_cost = static_cast<int64_t>(s.blocks) * s.chunks + kTileCost;
     int t = tiles > 1 && lo > before ? static_cast<int>((lo - before) / tile_cost) : 0;
@@ -626,27 +520,26 @@ cudaError_t launch_pack_int4(int gate_up, int64_t groups, int64_t rows, int64_t 
   return cudaGetLastError();
 }
 
-cudaError_t launch_gemv_int4(const Int4Params& p, int num_sms, cudaStream_t stream) {
-  Int4Launch l;
-  l.nseg = p.nseg;
-  l.early = p.early;
+cudaError_t launch_gemv_int4(const Int4Launch& p, bool swiglu, int group, int num_sms,
+                             cudaStream_t stream) {
+  Int4Launch l = p;
   int groups = 0;
   for (int i = 0; i < p.nseg; ++i) groups += p.seg[i].groups;
-  const bool x8 = p.seg[0].x_scale != nullptr;
+  l.smem = 0;
   for (int i = 0; i < p.nseg; ++i) {
-    l.seg[i] = p.seg[i];
     const Int4Segment& s = p.seg[i];
-    l.cap[i] = tile_cap(groups, s.chunks, p.group);
+    l.cap[i] = tile_cap(groups, s.chunks, group);
     if (l.cap[i] < 1) return cudaErrorInvalidValue;  // the callers' limit on the width
     if (s.rows < l.cap[i]) l.cap[i] = static_cast<int>(s.rows);
-    const int need = fixed_smem(groups, s.chunks, p.group) + l.cap[i] * x_row_bytes(s.chunks);
-    l.smem = i && l.smem > need ? l.smem : need;
+    const int need = fixed_smem(groups, s.chunks, group) + l.cap[i] * x_row_bytes(s.chunks);
+    l.smem = l.smem > need ? l.smem : need;
   }
-  if (p.swiglu)
-    return x8 ? launch_group<true, true>(l, p.group, num_sms, stream)
-              : launch_group<true, false>(l, p.group, num_sms, stream);
-  return x8 ? launch_group<false, true>(l, p.group, num_sms, stream)
-            : launch_group<false, false>(l, p.group, num_sms, stream);
+  const bool x8 = p.seg[0].x_scale != nullptr;
+  if (swiglu)
+    return x8 ? launch_group<true, true>(l, group, num_sms, stream)
+              : launch_group<true, false>(l, group, num_sms, stream);
+  return x8 ? launch_group<false, true>(l, group, num_sms, stream)
+            : launch_group<false, false>(l, group, num_sms, stream);
 }
 
 }  // namespace fgs

@@ -324,11 +324,12 @@ struct Int4Params {
   int nseg = 0;
   int swiglu = 0;  // gate/up pass (packed as MOE_PACK_GATE_UP) or plain store
   int group = 32;  // columns of one scale, 32 or 128
-  // 1: the previous launch of the stream was launch_gemv_int4 and wrote
-  // nothing that this one reads but x
+  // 1: the previous launch of the stream was launch_int4 and wrote nothing
+  // that this one reads but x
   int early = 0;
+  int* status = nullptr;
 };
-cudaError_t launch_gemv_int4(const Int4Params& p, int num_sms, cudaStream_t stream);
+cudaError_t launch_int4(const Int4Params& p, int num_sms, cudaStream_t stream);
 int64_t packed_int4_bytes(int64_t groups, int64_t rows, int64_t cols, int group);
 cudaError_t launch_pack_int4(int gate_up, int64_t groups, int64_t rows, int64_t cols, int group,
                              const void* codes, const void* scales, void* dst,

@@ -73,7 +73,8 @@ def test_packed_bytes(kind, G, R, C, group):
     (7, 384, 1040, False), (8, 2048, 160, True), (9, 128, 2448, False), (13, 3584, 64, True),
     (16, 1152, 96, False), (17, 640, 2432, True), (31, 7168, 32, False), (33, 512, 5008, True),
     (65, 1920, 112, False), (130, 256, 80, True), (3, 18432, 16, False), (40, 12288, 48, False),
-    (2, 32768, 16, False),
+    (2, 32768, 16, False), (128, 128, 144, False), (129, 128, 4112, True), (257, 384, 272, False),
+    (300, 1152, 32, True), (18, 32768, 48, False),
 ])
 def test_linear(T, I, O, add, rows8, group):
     need_gpu()
@@ -223,6 +224,8 @@ def _random_idx(T, E, K, seed):
     (40, 512, 128, 48, 6, 1, 128, 256),   # latent form, most experts with a few rows
     (70, 256, 384, 8, 2, 1, 128, 0),      # tiles of rows that end inside an expert
     (3, 7168, 128, 6, 2, 1, 128, 0),      # the widest rows
+    (300, 384, 256, 5, 2, 2, 128, 0),     # several tiles of tokens an expert
+    (200, 256, 128, 6, 3, 1, 384, 512),   # and the latent form
 ])
 def test_experts(T, d, F, E, K, S, Fs, L, group, rows8):
     need_gpu()
@@ -234,6 +237,25 @@ def test_experts_all_tokens_on_one_expert(rows8):
     need_gpu()
     T = 45
     _case(T, 256, 128, 32, 1, 0, 0, 0, 32, np.full((T, 1), 31), rows8, 3)
+
+
+@pytest.mark.parametrize("rows8", [False, True])
+def test_experts_of_every_size(rows8):
+    """Experts with 0, 1, 2, ... rows in one call, over every kernel's range."""
+    need_gpu()
+    sizes = [0, 1, 2, 7, 8, 9, 15, 16, 17, 18, 31, 32, 33, 63, 0, 64, 65, 127, 128, 129, 200]
+    idx = np.concatenate([np.full(n, e) for e, n in enumerate(sizes)])
+    np.random.default_rng(3).shuffle(idx)
+    _case(len(idx), 256, 128, len(sizes), 1, 0, 0, 0, 32, idx[:, None], rows8, 11)
+
+
+def test_experts_named_twice_by_a_token():
+    """moe_grouped_swiglu takes any grouping: an expert may have more rows
+    than there are tokens."""
+    need_gpu()
+    for T in (6, 14, 40):
+        idx = np.stack([np.full(T, 3), np.full(T, 3), np.arange(T) % 5], axis=1)
+        _case(T, 256, 128, 8, 3, 1, 128, 0, 32, idx, False, 12)
 
 
 def test_experts_without_weights_and_with_rejected_pairs():
