@@ -16,13 +16,12 @@
 namespace fgs {
 namespace {
 
-constexpr int kProducers = 8;  // warps that make the operands, a row block each
-constexpr int kEpilogue = 8;   // warps that add up the chunks' sums
-constexpr int kMmaWarp = kProducers + kEpilogue;
-constexpr int kThreads = 32 * (kMmaWarp + 1);
-constexpr int kRows = 16 * kProducers;
+constexpr int kWorkers = 16;  // warps that make the operands and add up the chunks' sums
+constexpr int kThreads = 32 * (kWorkers + 1);  // and the one that issues the MMAs
+constexpr int kBlocks = 8;    // row blocks of a unit
+constexpr int kRows = 16 * kBlocks;
 constexpr int kTokens = 128;
-constexpr int kDepth = 4;             // records of a producer's ring
+constexpr int kDepth = 4;             // half records of a worker's ring
 constexpr int kOperand = 128 * 256;   // bytes of an operand stage: 128 x 128 f16
 constexpr int kAtom = 128 * 128;      // its half: 64 columns, 128-byte swizzled rows
 constexpr int kFactors = 4;           // chunks whose f and r are kept
@@ -40,8 +39,10 @@ struct Header {
   int64_t lists[1];
 };
 
+// Half a record (64 columns) with all of its scales.
+__host__ __device__ constexpr int half_bytes(int group) { return record_bytes(group) - kCodeBytes / 2; }
 __host__ __device__ constexpr int ring_bytes(int group) {
-  return kProducers * kDepth * record_bytes(group);
+  return kWorkers * kDepth * half_bytes(group);
 }
 
 inline int smem_bytes(int groups, int group) {
@@ -81,8 +82,8 @@ __device__ __forceinline__ Unit unit_at(const Int4Launch& p, const GroupLists& l
   const int m = local / tiles, t = local - m * tiles;
   const int row0 = static_cast<int>(static_cast<int64_t>(n) * t / tiles);
   x.n = static_cast<int>(static_cast<int64_t>(n) * (t + 1) / tiles) - row0;
-  x.first_block = m * kProducers;
-  x.blocks = min(kProducers, s.blocks - x.first_block);
+  x.first_block = m * kBlocks;
+  x.blocks = min(kBlocks, s.blocks - x.first_block);
   x.chunks = s.chunks;
   x.W = s.W + (static_cast<int64_t>(grp) * s.blocks + x.first_block) * s.chunks * rec;
   x.out_row = row0 + (s.offsets ? first : grp * s.out_group_rows);
@@ -90,79 +91,64 @@ __device__ __forceinline__ Unit unit_at(const Int4Launch& p, const GroupLists& l
   return x;
 }
 
-// Row of x of the token that lane piece q < 8 of half warp hw looks after:
-// token 16 q + hw of the unit (its last token beyond the end).
-__device__ __forceinline__ int64_t source_row(const Int4Launch& p, const Unit& x, int hw, int q) {
-  if (x.seg < 0) return 0;
-  const Int4Segment& s = p.seg[x.seg];
-  const int64_t row = x.x_row + min(16 * (q & 7) + hw, x.n - 1);
-  return s.perm ? s.perm[row] / s.perm_div : row;
-}
-
-// The record at `rec` (this lane's, g = lane / 4 and c = lane % 4) into the
-// a operand at `to` (rows row and row + 8, row = 16 w + g) and its row scales
-// r.  Lanes of odd g take the two 32-column parts of each half in the other
-// order, which puts the rows that are stored together on different banks.
+// Half h of a record, at `rec` (codes, then the scales; this lane's
+// g = lane / 4 and c = lane % 4), into the a operand's half at `to` (rows row
+// and row + 8, row = 16 w + g), and the rows' scales r.  Lanes of odd g take
+// the half's two 32-column parts in the other order, which puts the rows that
+// are stored together on different banks.
 template <int kGroup>
-__device__ __forceinline__ void make_a(const uint8_t* rec, uint8_t* to, int row, int lane,
+__device__ __forceinline__ void make_a(const uint8_t* rec, uint8_t* to, int row, int h, int lane,
                                        float& r0, float& r1) {
   const int g = lane >> 2, c = lane & 3, odd = g & 1;
-  uint32_t s0[4], s1[4];  // scales of rows g and g + 8 in the order of the parts, f16 pairs
+  const uint8_t* scales = rec + kCodeBytes / 2;
+  uint32_t s0[2], s1[2];  // scales of rows g and g + 8 in the order of the parts, f16 pairs
   if (kGroup == 128) {
-    const uint32_t sc = *reinterpret_cast<const uint32_t*>(rec + kCodeBytes + g * 4);
+    const uint32_t sc = *reinterpret_cast<const uint32_t*>(scales + g * 4);
     r0 = __uint_as_float(sc << 16);
     r1 = __uint_as_float(sc & 0xffff0000u) * 0.0625f;  // row g + 8 is in units of 1 / 16
   } else {
-    const uint4 sv = *reinterpret_cast<const uint4*>(rec + kCodeBytes + g * 16);
+    const uint4 sv = *reinterpret_cast<const uint4*>(scales + g * 16);
     const uint32_t turn = odd ? 0x1032u : 0x3210u;
-    const uint32_t w[4] = {__byte_perm(sv.x, 0, turn), __byte_perm(sv.y, 0, turn),
-                           __byte_perm(sv.z, 0, turn), __byte_perm(sv.w, 0, turn)};
 #pragma unroll
-    for (int h = 0; h < 2; ++h) {
-      const uint32_t m2 = __vmaxu2(w[2 * h] & 0x7fff7fffu, w[2 * h + 1] & 0x7fff7fffu);
+    for (int k = 0; k < 2; ++k) {
+      const uint32_t a = k ? sv.z : sv.x, b = k ? sv.w : sv.y;
+      const uint32_t m2 = __vmaxu2(a & 0x7fff7fffu, b & 0x7fff7fffu);
       const uint32_t e = min(max(max(m2 & 0xffffu, m2 >> 16) >> 7, 12u), 254u);
       // the largest scale to [2^11, 2^12); row g + 8's codes come times 16
-      const float down = __uint_as_float(((h ? 261u : 265u) - e) << 23);
-      (h ? r1 : r0) = __uint_as_float((e - 11u) << 23);
-#pragma unroll
-      for (int i = 0; i < 4; ++i) {
-        const uint32_t v = w[2 * h + (i >> 1)];
-        const float s = __uint_as_float(i & 1 ? v & 0xffff0000u : v << 16) * down;
-        asm("cvt.rn.f16x2.f32 %0, %1, %1;" : "=r"((h ? s1 : s0)[i]) : "f"(s));
-      }
+      const float down = __uint_as_float(((k ? 261u : 265u) - e) << 23);
+      (k ? r1 : r0) = __uint_as_float((e - 11u) << 23);
+      const uint32_t v = __byte_perm(h ? b : a, 0, turn);
+      const float lo = __uint_as_float(v << 16) * down, hi = __uint_as_float(v & 0xffff0000u) * down;
+      asm("cvt.rn.f16x2.f32 %0, %1, %1;" : "=r"((k ? s1 : s0)[0]) : "f"(lo));
+      asm("cvt.rn.f16x2.f32 %0, %1, %1;" : "=r"((k ? s1 : s0)[1]) : "f"(hi));
     }
   }
 #pragma unroll
-  for (int h = 0; h < 2; ++h) {  // halves of 64 columns
+  for (int i = 0; i < 2; ++i) {
+    const uint2 v = *reinterpret_cast<const uint2*>(rec + lane * 16 + ((i ^ odd) << 3));
+    uint32_t lo[4], hi[4];  // rows g and g + 8, eight columns
 #pragma unroll
-    for (int i = 0; i < 2; ++i) {
-      const uint2 v = *reinterpret_cast<const uint2*>(rec + h * 512 + lane * 16 + ((i ^ odd) << 3));
-      uint32_t lo[4], hi[4];  // rows g and g + 8, eight columns
+    for (int j = 0; j < 2; ++j) {
+      uint32_t w = j ? v.y : v.x;
 #pragma unroll
-      for (int j = 0; j < 2; ++j) {
-        uint32_t w = j ? v.y : v.x;
-#pragma unroll
-        for (int q = 0; q < 2; ++q) {
-          asm("sub.rn.f16x2 %0, %1, %2;" : "=r"(lo[2 * j + q])
-              : "r"((w & 0x000f000fu) | 0x64006400u), "r"(0x64086408u));  // 1024 + c - 1032
-          asm("sub.rn.f16x2 %0, %1, %2;" : "=r"(hi[2 * j + q])
-              : "r"((w & 0x00f000f0u) | 0x64006400u), "r"(0x64806480u));  // 1024 + 16 c - 1152
-          w >>= 8;
-        }
+      for (int q = 0; q < 2; ++q) {
+        asm("sub.rn.f16x2 %0, %1, %2;" : "=r"(lo[2 * j + q])
+            : "r"((w & 0x000f000fu) | 0x64006400u), "r"(0x64086408u));  // 1024 + c - 1032
+        asm("sub.rn.f16x2 %0, %1, %2;" : "=r"(hi[2 * j + q])
+            : "r"((w & 0x00f000f0u) | 0x64006400u), "r"(0x64806480u));  // 1024 + 16 c - 1152
+        w >>= 8;
       }
-      if (kGroup == 32) {
-#pragma unroll
-        for (int j = 0; j < 4; ++j) {
-          asm("mul.rn.f16x2 %0, %0, %1;" : "+r"(lo[j]) : "r"(s0[2 * h + i]));
-          asm("mul.rn.f16x2 %0, %0, %1;" : "+r"(hi[j]) : "r"(s1[2 * h + i]));
-        }
-      }
-      const int at = ((4 * (i ^ odd) + c) ^ g) << 4;
-      *reinterpret_cast<uint4*>(to + h * kAtom + row * 128 + at) =
-          make_uint4(lo[0], lo[1], lo[2], lo[3]);
-      *reinterpret_cast<uint4*>(to + h * kAtom + (row + 8) * 128 + at) =
-          make_uint4(hi[0], hi[1], hi[2], hi[3]);
     }
+    if (kGroup == 32) {
+#pragma unroll
+      for (int j = 0; j < 4; ++j) {
+        asm("mul.rn.f16x2 %0, %0, %1;" : "+r"(lo[j]) : "r"(s0[i]));
+        asm("mul.rn.f16x2 %0, %0, %1;" : "+r"(hi[j]) : "r"(s1[i]));
+      }
+    }
+    const int at = ((4 * (i ^ odd) + c) ^ g) << 4;
+    *reinterpret_cast<uint4*>(to + row * 128 + at) = make_uint4(lo[0], lo[1], lo[2], lo[3]);
+    *reinterpret_cast<uint4*>(to + (row + 8) * 128 + at) = make_uint4(hi[0], hi[1], hi[2], hi[3]);
   }
 }
 
@@ -171,15 +157,17 @@ __device__ __forceinline__ uint32_t idesc_f16_f32(uint32_t n) {
   return (1u << 4) | ((n >> 3) << 17) | ((128u >> 4) << 24);
 }
 
-// Roles: eight producer warps (row block w of the weights and the tokens
-// 2 w, 2 w + 1 mod 16), eight epilogue warps (two for each quarter of the
-// rows, half of the tokens each) and the warp that issues the MMAs.  Chunk i
-// of the CTA's units uses operand stage and TMEM region i mod 2 and factors
-// i mod 4; chunk i + 4's factors are written after stage i + 2 was read,
-// hence after the epilogue of chunk i.
+// Sixteen worker warps make the operands of chunk i (half of a row block of
+// the weights each, and the tokens of its two half warps) and then add up the
+// sums of chunk i - 1 (a quarter of the rows, a quarter of the tokens), while
+// the MMAs of chunk i run; one more warp issues those.  Chunk i of the CTA's
+// units uses operand stage and TMEM region i mod 2 and factors i mod 4.
+// Sixteen warps of both kinds of work, not eight of each: a scheduler has
+// four to choose from, and two could not hide the latencies (a chunk of 64
+// tokens took 3900 cycles).
 template <bool kSwiglu, bool kX8, int kGroup>
 __global__ void __launch_bounds__(kThreads, 1) gemm_int4_kernel(const __grid_constant__ Int4Launch p) {
-  constexpr int kRec = record_bytes(kGroup);
+  constexpr int kRec = record_bytes(kGroup), kHalf = half_bytes(kGroup);
   extern __shared__ __align__(16) uint8_t raw[];
   uint8_t* smem = raw + ((1024u - (smem_u32(raw) & 1023u)) & 1023u);
   uint8_t* ring_base = smem + 4 * kOperand;
@@ -193,14 +181,14 @@ __global__ void __launch_bounds__(kThreads, 1) gemm_int4_kernel(const __grid_con
     tmem_alloc(smem_u32(&hd->tmem), kTmemCols);
     tmem_relinquish();
   }
-  if (warp == kMmaWarp && lane == 0) {
+  if (warp == kWorkers && lane == 0) {
     for (int i = 0; i < 2; ++i) {
-      mbar_init(bar(hd->full[i]), kProducers);
+      mbar_init(bar(hd->full[i]), kWorkers);
       mbar_init(bar(hd->empty[i]), 1);
       mbar_init(bar(hd->tfull[i]), 1);
-      mbar_init(bar(hd->tempty[i]), kEpilogue);
+      mbar_init(bar(hd->tempty[i]), kWorkers);
     }
-    for (int i = 0; i < kFactors; ++i) mbar_init(bar(hd->factors[i]), kProducers);
+    for (int i = 0; i < kFactors; ++i) mbar_init(bar(hd->factors[i]), kWorkers);
     mbar_init(bar(hd->drain), 1);
     hd->abort = 0;
     fence_mbarrier_init();
@@ -218,7 +206,7 @@ __global__ void __launch_bounds__(kThreads, 1) gemm_int4_kernel(const __grid_con
       p, lists, hd->warp_sum,
       [&](int si, int n) -> int64_t {
         if (n <= p.most) return 0;
-        return static_cast<int64_t>((p.seg[si].blocks + kProducers - 1) / kProducers) *
+        return static_cast<int64_t>((p.seg[si].blocks + kBlocks - 1) / kBlocks) *
                ((n + kTokens - 1u) / kTokens);
       },
       [](int64_t) {},
@@ -227,129 +215,194 @@ __global__ void __launch_bounds__(kThreads, 1) gemm_int4_kernel(const __grid_con
       });
   int pos = u0 < plan.total ? hd->at_first : 0;
 
-  if (warp < kProducers) {
-    // ------------------------------------------------------------ operands
-    const int hw = 2 * warp + (lane >> 4), piece = lane & 15, g = lane >> 2;
-    const uint32_t ring = smem_u32(ring_base) + warp * kDepth * kRec;
-    // the ring runs ahead of the products, over the ends of units
-    int fu = u0, fpos = pos, fch = 0;
-    Unit fx = unit_at(p, lists, plan, fu, fpos, kRec);
-    auto fetch = [&](int slot) {
-      while (fx.seg >= 0 && fch == fx.chunks) {
-        fch = 0;
-        fu += gridDim.x;
-        fx = unit_at(p, lists, plan, fu, fpos, kRec);
-      }
-      if (fx.seg >= 0) {
-        if (warp < fx.blocks) {
-          const uint8_t* w = fx.W + (static_cast<int64_t>(warp) * fx.chunks + fch) * kRec + lane * 16;
-          const uint32_t to = ring + slot * kRec + lane * 16;
-          cp_async16(to, w);
-          cp_async16(to + 512, w + 512);
-          if (lane < (kRec - kCodeBytes) / 16) cp_async16(to + kCodeBytes, w + kCodeBytes);
+  if (warp < kWorkers) {
+    const int a_block = warp >> 1, a_half = warp & 1, g = lane >> 2;  // of the operand a
+    const int hw = 2 * warp + (lane >> 4), piece = lane & 15;         // of the operand b
+    const int quarter = warp & 3, row = 32 * quarter + lane;          // of the sums
+    constexpr int kTasks = kTokens / 32;
+    uint8_t* const ring = ring_base + warp * kDepth * kHalf;
+    bool first = true, ok = true;
+    int i = 0;
+    for (int u = u0; u < plan.total && ok; u += gridDim.x) {
+      const Unit x = unit_at(p, lists, plan, u, pos, kRec);
+      const Int4Segment& s = p.seg[x.seg];
+      // this worker's half records, and the last of them
+      const bool has_a = a_block < x.blocks;
+      const uint8_t* w = x.W + (has_a ? static_cast<int64_t>(a_block) * x.chunks * kRec : 0) +
+                         a_half * (kCodeBytes / 2) + lane * 16;
+      auto fetch = [&](int slot, int ch) {
+        if (has_a && ch < x.chunks) {
+          const uint32_t to = smem_u32(ring + slot * kHalf) + lane * 16;
+          const uint8_t* from = w + ch * kRec;
+          cp_async16(to, from);
+          if (lane < (kRec - kCodeBytes) / 16)
+            cp_async16(to + kCodeBytes / 2, from + kCodeBytes - a_half * (kCodeBytes / 2));
         }
-        ++fch;
-      }
-      asm volatile("cp.async.commit_group;" ::: "memory");
-    };
+        asm volatile("cp.async.commit_group;" ::: "memory");
+      };
 #pragma unroll
-    for (int u = 0; u < kDepth - 1; ++u) fetch(u);
-    if (p.wait == kWaitX) pdl_wait();
-
-    Unit x = unit_at(p, lists, plan, u0, pos, kRec);
-    int64_t src = source_row(p, x, hw, piece);
-    constexpr int kTasks = kTokens / 16;
-    uint4 xr[kTasks];
-    float xf[kTasks];
-    // chunk ch of unit `of`'s tokens 16 q + hw, whose rows of x are `rows`
-    auto load_b = [&](const Unit& of, int64_t rows, int ch) {
-      const Int4Segment& s = p.seg[of.seg];
+      for (int c = 0; c < kDepth - 1; ++c) fetch(c, c);
+      if (first && p.wait == kWaitX) pdl_wait();
+      first = false;
+      // rows of x of tokens 32 q + hw (beyond the end, of the last token)
+      int rows[kTasks];
+      {
+        const int64_t at = x.x_row + min(32 * (piece & 3) + hw, x.n - 1);
+        const int mine = static_cast<int>(s.perm ? s.perm[at] / s.perm_div : at);
 #pragma unroll
-      for (int q = 0; q < kTasks; ++q) {
-        if (16 * q + 2 * warp >= of.n) break;
-        const int64_t from = __shfl_sync(0xffffffffu, rows, (lane & 16) + q) * of.chunks + ch;
-        if (kX8) {
-          const uint2 v = *reinterpret_cast<const uint2*>(static_cast<const uint8_t*>(s.x) +
-                                                          from * kChunk + piece * 8);
-          xr[q].x = v.x;
-          xr[q].y = v.y;
-          xf[q] = s.x_scale[from];
-        } else {
-          xr[q] = *reinterpret_cast<const uint4*>(static_cast<const __nv_bfloat16*>(s.x) +
-                                                  from * kChunk + piece * 8);
-        }
+        for (int q = 0; q < kTasks; ++q) rows[q] = __shfl_sync(0xffffffffu, mine, (lane & 16) + q);
       }
-    };
-    if (x.seg >= 0) load_b(x, src, 0);
-    int i = 0, slot = 0;
-    bool ok = true;
-    for (int u = u0; x.seg >= 0 && ok;) {
-      u += gridDim.x;
-      const Unit nx = unit_at(p, lists, plan, u, pos, kRec);
-      const int64_t nsrc = source_row(p, nx, hw, piece);
-      for (int ch = 0; ch < x.chunks; ++ch, ++i) {
-        const int st = i & 1, fs = i & (kFactors - 1);
-        asm volatile("cp.async.wait_group %0;" ::"n"(kDepth - 2) : "memory");
-        __syncwarp();
-        fetch(slot == 0 ? kDepth - 1 : slot - 1);
-        if (!mbar_wait_bounded(bar(hd->empty[st]), (i >> 1 & 1) ^ 1, abort_flag, p.status)) {
-          ok = false;
-          break;
-        }
-        if (warp < x.blocks) {
-          float r0, r1;
-          const int row = 16 * warp + g;
-          make_a<kGroup>(ring_base + (warp * kDepth + slot) * kRec, smem + st * kOperand, row, lane,
-                         r0, r1);
-          if ((lane & 3) == 0) {
-            hd->r[fs][row] = r0;
-            hd->r[fs][row + 8] = r1;
-          }
-        }
-        if (++slot == kDepth) slot = 0;
-        uint8_t* b = smem + (2 + st) * kOperand;
+      uint4 xr[kTasks];
+      float xf[kTasks];
+      auto load_b = [&](int ch) {
 #pragma unroll
         for (int q = 0; q < kTasks; ++q) {
-          if (16 * q + 2 * warp >= x.n) break;
-          const int t = 16 * q + hw;
-          uint4 v;
-          float f;
+          if (32 * q + 2 * warp >= x.n) break;
+          const int64_t from = static_cast<int64_t>(rows[q]) * x.chunks + ch;
           if (kX8) {
-            v = e4m3x8_to_f16(make_uint2(xr[q].x, xr[q].y));
-            f = xf[q];
+            const uint2 v = *reinterpret_cast<const uint2*>(static_cast<const uint8_t*>(s.x) +
+                                                            from * kChunk + piece * 8);
+            xr[q].x = v.x;
+            xr[q].y = v.y;
+            xf[q] = s.x_scale[from];
           } else {
-            uint32_t e;
-            v = bf16x8_to_f16(xr[q], e);
-            f = __uint_as_float((e - 14u) << 23);  // 2^(e - 141)
+            xr[q] = *reinterpret_cast<const uint4*>(static_cast<const __nv_bfloat16*>(s.x) +
+                                                    from * kChunk + piece * 8);
           }
-          *reinterpret_cast<uint4*>(b + (piece >> 3) * kAtom + t * 128 +
-                                    (((piece & 7) ^ (t & 7)) << 4)) = v;
-          if (piece == 0) hd->f[fs][t] = f;
         }
-        if (ch + 1 < x.chunks)
-          load_b(x, src, ch + 1);
-        else if (nx.seg >= 0)
-          load_b(nx, nsrc, 0);
-        fence_proxy_async_smem();  // the tensor cores read the operands next
-        __syncwarp();
-        if (lane == 0) {
-          mbar_arrive(bar(hd->full[st]));
-          mbar_arrive(bar(hd->factors[fs]));
+      };
+      load_b(0);
+      const int cols = x.n > 64 ? 32 : 16, t0 = (warp >> 2) * cols;  // tokens of the sums
+      float weight = 1.0f;  // row weight of token t0 + lane
+      if (!kSwiglu && s.row_w && t0 + lane < x.n) weight = s.row_w[s.row_perm[x.out_row + t0 + lane]];
+      float acc[kTokens / 4];
+#pragma unroll
+      for (int j = 0; j < kTokens / 4; ++j) acc[j] = 0.0f;
+
+      // one step more than chunks: step ch makes chunk ch and adds chunk ch - 1
+      for (int ch = 0; ch <= x.chunks; ++ch) {
+        if (ch < x.chunks) {
+          const int st = i & 1, fs = i & (kFactors - 1), slot = ch & (kDepth - 1);
+          asm volatile("cp.async.wait_group %0;" ::"n"(kDepth - 2) : "memory");
+          __syncwarp();
+          fetch((ch + kDepth - 1) & (kDepth - 1), ch + kDepth - 1);
+          if (!mbar_wait_bounded(bar(hd->empty[st]), (i >> 1 & 1) ^ 1, abort_flag, p.status)) {
+            ok = false;
+            break;
+          }
+          if (has_a) {
+            float r0, r1;
+            const int ar = 16 * a_block + g;
+            make_a<kGroup>(ring + slot * kHalf, smem + st * kOperand + a_half * kAtom, ar, a_half,
+                           lane, r0, r1);
+            if (a_half == 0 && (lane & 3) == 0) {
+              hd->r[fs][ar] = r0;
+              hd->r[fs][ar + 8] = r1;
+            }
+          }
+          uint8_t* b = smem + (2 + st) * kOperand + (piece >> 3) * kAtom;
+#pragma unroll
+          for (int q = 0; q < kTasks; ++q) {
+            if (32 * q + 2 * warp >= x.n) break;
+            const int t = 32 * q + hw;
+            uint4 v;
+            float f;
+            if (kX8) {
+              v = e4m3x8_to_f16(make_uint2(xr[q].x, xr[q].y));
+              f = xf[q];
+            } else {
+              uint32_t e;
+              v = bf16x8_to_f16(xr[q], e);
+              f = __uint_as_float((e - 14u) << 23);  // 2^(e - 141)
+            }
+            *reinterpret_cast<uint4*>(b + t * 128 + (((piece & 7) ^ (t & 7)) << 4)) = v;
+            if (piece == 0) hd->f[fs][t] = f;
+          }
+          fence_proxy_async_smem();  // the tensor cores read the operands next
+          __syncwarp();
+          if (lane == 0) {
+            mbar_arrive(bar(hd->full[st]));
+            mbar_arrive(bar(hd->factors[fs]));
+          }
+          ++i;
+        }
+        if (ch > 0) {
+          const int c = i - (ch < x.chunks ? 2 : 1), st = c & 1, fs = c & (kFactors - 1);
+          if (!mbar_wait_bounded(bar(hd->factors[fs]), c >> 2 & 1, abort_flag, p.status) ||
+              !mbar_wait_bounded(bar(hd->tfull[st]), c >> 1 & 1, abort_flag, p.status)) {
+            ok = false;
+            break;
+          }
+          __syncwarp();
+          tc_fence_after();
+          const float r = hd->r[fs][row];
+          const float4* f = reinterpret_cast<const float4*>(hd->f[fs] + t0);
+          const uint32_t from = tmem + st * kTokens + t0 + (static_cast<uint32_t>(32 * quarter) << 16);
+#pragma unroll
+          for (int b = 0; b < 2; ++b) {
+            if (16 * b < cols) {
+              uint32_t v[16];
+              tmem_ld_x16(from + 16 * b, v);
+              tmem_ld_wait(v);
+#pragma unroll
+              for (int j = 0; j < 4; ++j) {
+                const float4 k = f[4 * b + j];
+                float* o = acc + 16 * b + 4 * j;
+                o[0] = fmaf(k.x * r, __uint_as_float(v[4 * j + 0]), o[0]);
+                o[1] = fmaf(k.y * r, __uint_as_float(v[4 * j + 1]), o[1]);
+                o[2] = fmaf(k.z * r, __uint_as_float(v[4 * j + 2]), o[2]);
+                o[3] = fmaf(k.w * r, __uint_as_float(v[4 * j + 3]), o[3]);
+              }
+            }
+          }
+          tc_fence_before();
+          __syncwarp();
+          if (lane == 0) mbar_arrive(bar(hd->tempty[st]));
+        }
+        if (ch + 1 < x.chunks) load_b(ch + 1);
+      }
+      if (!ok) break;
+
+      const bool live = row / 16 < x.blocks;
+      const int block = x.first_block + row / 16;
+      if (kSwiglu) {
+        // rows r < 8 of a block are gate rows, r + 8 the up rows of the same
+        // features: lanes 8 apart swap halves and each finishes half the tokens
+        const bool up = lane & 8;
+        __nv_bfloat16* out = s.out + (x.out_row + t0) * s.out_ld + block * 8 + (lane & 7);
+#pragma unroll
+        for (int j = 0; j < 16; ++j) {
+          // with 16 tokens, j and j + 8; with 32, j and j + 16
+          if (cols == 16 && j >= 8) break;
+          const float low = acc[j], high = cols == 16 ? acc[(j + 8) & 31] : acc[j + 16];
+          const float got = __shfl_xor_sync(0xffffffffu, up ? low : high, 8);
+          const float gate = up ? got : low, lin = up ? high : got;
+          const int t = j + (up ? cols / 2 : 0);
+          if (live && t0 + t < x.n)  // H is rounded to bf16, the type of the layer's activations
+            out[t * s.out_ld] = __float2bfloat16_rn(silu_f(gate) * lin);
+        }
+      } else {
+        const int64_t o = (x.out_row + t0) * s.out_ld + block * 16 + (lane & 15);
+#pragma unroll
+        for (int j = 0; j < 32; ++j) {
+          if (j >= cols) break;
+          float v = __shfl_sync(0xffffffffu, weight, j) * acc[j];
+          if (live && t0 + j < x.n) {
+            if (s.add) v += __bfloat162float(s.add[o + j * s.out_ld]);
+            s.out[o + j * s.out_ld] = __float2bfloat16_rn(v);
+          }
         }
       }
-      x = nx;
-      src = nsrc;
     }
     asm volatile("cp.async.wait_all;" ::: "memory");
-  } else if (warp == kMmaWarp) {
-    // ---------------------------------------------------------------- MMAs
+  } else {
     if (lane == 0) {
       int i = 0;
       bool ok = true;
       for (int u = u0; ok; u += gridDim.x) {
         const Unit x = unit_at(p, lists, plan, u, pos, kRec);
         if (x.seg < 0) break;
-        const uint32_t idesc = idesc_f16_f32((x.n + 31) / 32 * 32);
+        const uint32_t idesc = idesc_f16_f32(x.n > 64 ? 128 : 64);
         for (int ch = 0; ch < x.chunks; ++ch, ++i) {
           const int st = i & 1, ph = i >> 1 & 1;
           if (!mbar_wait_bounded(bar(hd->tempty[st]), ph ^ 1, abort_flag, p.status) ||
@@ -376,91 +429,6 @@ __global__ void __launch_bounds__(kThreads, 1) gemm_int4_kernel(const __grid_con
       mbar_wait_bounded(bar(hd->drain), 0, &own_abort, p.status);
     }
     __syncwarp();
-  } else {
-    // ------------------------------------------------------------ epilogue
-    const int quarter = warp & 3;               // the TMEM lanes this warp may read
-    const int half = (warp - kProducers) >> 2;  // its half of the tokens
-    const int row = 32 * quarter + lane;        // of the unit
-    int i = 0;
-    bool ok = true;
-    for (int u = u0; ok; u += gridDim.x) {
-      const Unit x = unit_at(p, lists, plan, u, pos, kRec);
-      if (x.seg < 0) break;
-      const Int4Segment& s = p.seg[x.seg];
-      const int cols = (x.n + 31) / 32 * 16;  // this warp's tokens: half * cols + 0 .. cols - 1
-      const int t0 = half * cols;
-      float w0 = 1.0f, w1 = 1.0f;  // row weights of tokens t0 + lane and t0 + 32 + lane
-      if (!kSwiglu && s.row_w) {
-        if (t0 + lane < x.n) w0 = s.row_w[s.row_perm[x.out_row + t0 + lane]];
-        if (t0 + 32 + lane < x.n) w1 = s.row_w[s.row_perm[x.out_row + t0 + 32 + lane]];
-      }
-      float acc[kTokens / 2];
-#pragma unroll
-      for (int j = 0; j < kTokens / 2; ++j) acc[j] = 0.0f;
-      for (int ch = 0; ch < x.chunks; ++ch, ++i) {
-        const int st = i & 1, fs = i & (kFactors - 1);
-        if (!mbar_wait_bounded(bar(hd->factors[fs]), i >> 2 & 1, abort_flag, p.status) ||
-            !mbar_wait_bounded(bar(hd->tfull[st]), i >> 1 & 1, abort_flag, p.status)) {
-          ok = false;
-          break;
-        }
-        __syncwarp();
-        tc_fence_after();
-        const float r = hd->r[fs][row];
-        const float4* f = reinterpret_cast<const float4*>(hd->f[fs] + t0);
-#pragma unroll
-        for (int b = 0; b < kTokens / 32; ++b) {
-          if (16 * b < cols) {
-            uint32_t v[16];
-            tmem_ld_x16(tmem + st * kTokens + t0 + 16 * b + (static_cast<uint32_t>(32 * quarter) << 16),
-                        v);
-            tmem_ld_wait(v);
-#pragma unroll
-            for (int j = 0; j < 4; ++j) {
-              const float4 k = f[4 * b + j];
-              float(&o)[kTokens / 2] = acc;
-              o[16 * b + 4 * j + 0] = fmaf(k.x * r, __uint_as_float(v[4 * j + 0]), o[16 * b + 4 * j + 0]);
-              o[16 * b + 4 * j + 1] = fmaf(k.y * r, __uint_as_float(v[4 * j + 1]), o[16 * b + 4 * j + 1]);
-              o[16 * b + 4 * j + 2] = fmaf(k.z * r, __uint_as_float(v[4 * j + 2]), o[16 * b + 4 * j + 2]);
-              o[16 * b + 4 * j + 3] = fmaf(k.w * r, __uint_as_float(v[4 * j + 3]), o[16 * b + 4 * j + 3]);
-            }
-          }
-        }
-        tc_fence_before();
-        __syncwarp();
-        if (lane == 0) mbar_arrive(bar(hd->tempty[st]));
-      }
-      if (!ok) break;
-      const bool live = row / 16 < x.blocks;
-      const int block = x.first_block + row / 16;
-      if (kSwiglu) {
-        // rows r < 8 of a block are gate rows, r + 8 the up rows of the same
-        // features: lanes 8 apart swap halves and each finishes half the tokens
-        const bool up = lane & 8;
-        const int64_t feature = block * 8 + (lane & 7);
-#pragma unroll
-        for (int j = 0; j < kTokens / 4; ++j) {
-          const float got = __shfl_xor_sync(0xffffffffu, up ? acc[j] : acc[j + kTokens / 4], 8);
-          const float gate = up ? got : acc[j], lin = up ? acc[j + kTokens / 4] : got;
-          const int k = up ? j + kTokens / 4 : j, t = t0 + k;
-          if (live && k < cols && t < x.n)
-            s.out[(x.out_row + t) * s.out_ld + feature] = __float2bfloat16_rn(silu_f(gate) * lin);
-        }
-      } else {
-        const int64_t o = block * 16 + (lane & 15);
-#pragma unroll
-        for (int j = 0; j < kTokens / 2; ++j) {
-          const float w = __shfl_sync(0xffffffffu, j < 32 ? w0 : w1, j & 31);
-          const int t = t0 + j;
-          if (live && j < cols && t < x.n) {
-            const int64_t at = (x.out_row + t) * s.out_ld + o;
-            float v = w * acc[j];
-            if (s.add) v += __bfloat162float(s.add[at]);
-            s.out[at] = __float2bfloat16_rn(v);
-          }
-        }
-      }
-    }
   }
   if (p.wait != kWaitWeights) pdl_wait();  // a kernel ends after the one before it has
   tc_fence_before();
