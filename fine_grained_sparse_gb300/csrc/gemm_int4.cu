@@ -439,26 +439,328 @@ __global__ void __launch_bounds__(kThreads, 1) gemm_int4_kernel(const __grid_con
   }
 }
 
-template <bool kSwiglu, bool kX8, int kGroup>
-cudaError_t launch_kernel(const Int4Launch& p, int num_sms, cudaStream_t stream) {
-  static int configured[64] = {0};
-  int dev = 0;
-  cudaError_t err = cudaGetDevice(&dev);
-  if (err != cudaSuccess) return err;
-  if (dev >= 64 || !configured[dev]) {
-    err = cudaFuncSetAttribute(gemm_int4_kernel<kSwiglu, kX8, kGroup>,
-                               cudaFuncAttributeMaxDynamicSharedMemorySize, 227 * 1024);
-    if (err != cudaSuccess) return err;
-    if (dev < 64) configured[dev] = 1;
-  }
-  return launch_pdl(gemm_int4_kernel<kSwiglu, kX8, kGroup>, dim3(num_sms), dim3(kThreads), p.smem,
-                    stream, p);
+// ------------------------------------------------------------- bf16 rows
+// With x in bf16 both operands are bf16 and nothing is left to apply to the
+// sums: b is x as it lies in memory, a weight (c - 8) s is the sum of two bf16
+// values (its rounding and the rest, at most 11 significant bits together),
+// and the MMAs of both run over all of K in one TMEM accumulator.
+constexpr int kStages = 3;                  // of 64 columns: a high, a low, b
+constexpr int kStageBytes = 3 * kAtom;
+
+struct HeaderB {
+  uint64_t full[kStages], empty[kStages], tfull[2], tempty[2], drain;
+  uint32_t tmem;
+  int abort;
+  int at_first, pad;
+  int64_t warp_sum[kThreads / 32];
+  int64_t lists[1];
+};
+
+inline int smem_bytes_b(int groups, int group) {
+  return 1024 + kStages * kStageBytes + ring_bytes(group) +
+         (static_cast<int>(sizeof(HeaderB)) + group_list_bytes(groups) + 15) / 16 * 16;
 }
 
-template <bool kSwiglu, bool kX8>
-cudaError_t launch_group(const Int4Launch& p, int group, int num_sms, cudaStream_t stream) {
-  return group == 32 ? launch_kernel<kSwiglu, kX8, 32>(p, num_sms, stream)
-                     : launch_kernel<kSwiglu, kX8, 128>(p, num_sms, stream);
+// Half h of a record (as make_a's) into the two halves of the a operand.
+template <int kGroup>
+__device__ __forceinline__ void make_a_split(const uint8_t* rec, uint8_t* hi_to, uint8_t* lo_to,
+                                             int row, int h, int lane) {
+  const int g = lane >> 2, c = lane & 3, odd = g & 1;
+  const uint8_t* scales = rec + kCodeBytes / 2;
+  uint32_t s[2][2];  // [row g, row g + 8][part in order], bf16 pairs
+  if (kGroup == 128) {
+    const uint32_t sc = *reinterpret_cast<const uint32_t*>(scales + g * 4);
+    s[0][0] = s[0][1] = __byte_perm(sc, 0, 0x1010);
+    s[1][0] = s[1][1] = __byte_perm(sc, 0, 0x3232);
+  } else {
+    const uint2 a = *reinterpret_cast<const uint2*>(scales + g * 16);
+    const uint2 b = *reinterpret_cast<const uint2*>(scales + g * 16 + 8);
+    const uint32_t v0 = h ? a.y : a.x, v1 = h ? b.y : b.x;
+    const uint32_t first = odd ? 0x3232u : 0x1010u, second = odd ? 0x1010u : 0x3232u;
+    s[0][0] = __byte_perm(v0, 0, first);
+    s[0][1] = __byte_perm(v0, 0, second);
+    s[1][0] = __byte_perm(v1, 0, first);
+    s[1][1] = __byte_perm(v1, 0, second);
+  }
+#pragma unroll
+  for (int i = 0; i < 2; ++i) {
+    const uint2 v = *reinterpret_cast<const uint2*>(rec + lane * 16 + ((i ^ odd) << 3));
+    uint32_t hi[2][4], lo[2][4];  // [row g, row g + 8], eight columns
+#pragma unroll
+    for (int j = 0; j < 2; ++j) {
+      const uint32_t w = j ? v.y : v.x;
+#pragma unroll
+      for (int k = 0; k < 4; ++k) {
+        uint32_t q = ((w >> (4 * k)) & 0x000f000fu) | 0x43004300u;  // 128 + c
+        uint32_t& o = hi[k & 1][2 * j + (k >> 1)];
+        uint32_t& r = lo[k & 1][2 * j + (k >> 1)];
+        asm("sub.rn.bf16x2 %0, %0, %1;" : "+r"(q) : "r"(0x43084308u));
+        asm("mul.rn.bf16x2 %0, %1, %2;" : "=r"(o) : "r"(q), "r"(s[k & 1][i]));
+        asm("{\n\t.reg .b32 n;\n\tneg.bf16x2 n, %1;\n\tfma.rn.bf16x2 %0, %2, %3, n;\n\t}"
+            : "=r"(r)
+            : "r"(o), "r"(q), "r"(s[k & 1][i]));
+      }
+    }
+    const int at = ((4 * (i ^ odd) + c) ^ g) << 4;
+#pragma unroll
+    for (int b = 0; b < 2; ++b) {
+      *reinterpret_cast<uint4*>(hi_to + (row + 8 * b) * 128 + at) =
+          make_uint4(hi[b][0], hi[b][1], hi[b][2], hi[b][3]);
+      *reinterpret_cast<uint4*>(lo_to + (row + 8 * b) * 128 + at) =
+          make_uint4(lo[b][0], lo[b][1], lo[b][2], lo[b][3]);
+    }
+  }
+}
+
+// Stage j of the CTA's units is 64 columns; the workers of parity j mod 2
+// (one for each row block) make it: they start the copies of b, convert a and
+// hand it over when the copies have landed.  A unit's outputs are written while the next unit's first stages run, from
+// the other half of TMEM.
+template <bool kSwiglu, int kGroup>
+__global__ void __launch_bounds__(kThreads, 1)
+    gemm_int4_bf16_kernel(const __grid_constant__ Int4Launch p) {
+  constexpr int kRec = record_bytes(kGroup), kHalf = half_bytes(kGroup);
+  extern __shared__ __align__(16) uint8_t raw[];
+  uint8_t* smem = raw + ((1024u - (smem_u32(raw) & 1023u)) & 1023u);
+  uint8_t* ring_base = smem + kStages * kStageBytes;
+  HeaderB* hd = reinterpret_cast<HeaderB*>(ring_base + ring_bytes(kGroup));
+  const int groups = p.seg[0].groups + (p.nseg > 1 ? p.seg[1].groups : 0);
+  const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+  volatile int* abort_flag = &hd->abort;
+  auto bar = [](uint64_t& b) { return smem_u32(&b); };
+
+  if (warp == 0) {
+    tmem_alloc(smem_u32(&hd->tmem), kTmemCols);
+    tmem_relinquish();
+  }
+  if (warp == kWorkers && lane == 0) {
+    for (int i = 0; i < kStages; ++i) {
+      mbar_init(bar(hd->full[i]), kWorkers / 2);
+      mbar_init(bar(hd->empty[i]), 1);
+    }
+    for (int i = 0; i < 2; ++i) {
+      mbar_init(bar(hd->tfull[i]), 1);
+      mbar_init(bar(hd->tempty[i]), kWorkers);
+    }
+    mbar_init(bar(hd->drain), 1);
+    hd->abort = 0;
+    fence_mbarrier_init();
+  }
+  tc_fence_before();
+  __syncthreads();
+  tc_fence_after();
+  const uint32_t tmem = hd->tmem;
+
+  if (p.wait == kWaitWeights) pdl_wait();
+  pdl_release();
+  const GroupLists lists = group_lists(hd->lists, groups);
+  const int u0 = blockIdx.x;
+  const GroupPlan plan = plan_groups<kThreads>(
+      p, lists, hd->warp_sum,
+      [&](int si, int n) -> int64_t {
+        if (n <= p.most) return 0;
+        return static_cast<int64_t>((p.seg[si].blocks + kBlocks - 1) / kBlocks) *
+               ((n + kTokens - 1u) / kTokens);
+      },
+      [](int64_t) {},
+      [&](int pos, int64_t before, int64_t cost) {
+        if (before <= u0 && u0 < before + cost) hd->at_first = pos;
+      });
+  int pos = u0 < plan.total ? hd->at_first : 0;
+
+  if (warp < kWorkers) {
+    const int parity = warp & 1, a_block = warp >> 1, g = lane >> 2;
+    const int piece = lane & 7, sub = 4 * a_block + (lane >> 3);  // of b: tokens 32 k + sub
+    const int quarter = warp & 3, row = 32 * quarter + lane;      // of the outputs
+    uint8_t* const ring = ring_base + warp * kDepth * kHalf;
+    constexpr int kTasks = kTokens / 32;
+
+    // the outputs of unit `of`, the seq-th of the CTA; false: gave up
+    auto finish = [&](const Unit& of, int seq) {
+      const int buf = seq & 1;
+      if (!mbar_wait_bounded(bar(hd->tfull[buf]), seq >> 1 & 1, abort_flag, p.status)) return false;
+      __syncwarp();
+      tc_fence_after();
+      const Int4Segment& s = p.seg[of.seg];
+      const int cols = of.n > 64 ? 32 : 16, t0 = (warp >> 2) * cols;
+      const bool live = row / 16 < of.blocks;
+      const int block = of.first_block + row / 16;
+      float weight = 1.0f;
+      if (!kSwiglu && s.row_w && t0 + lane < of.n)
+        weight = s.row_w[s.row_perm[of.out_row + t0 + lane]];
+#pragma unroll
+      for (int b = 0; b < 2; ++b) {
+        if (16 * b >= cols) break;
+        uint32_t v[16];
+        tmem_ld_x16(tmem + buf * kTokens + t0 + 16 * b + (static_cast<uint32_t>(32 * quarter) << 16),
+                    v);
+        tmem_ld_wait(v);
+        if (kSwiglu) {
+          // rows r < 8 of a block are gate rows, r + 8 the up rows of the
+          // same features: lanes 8 apart swap and each finishes half the tokens
+          const bool up = lane & 8;
+          const int first = t0 + 16 * b + (up ? 8 : 0);
+          __nv_bfloat16* out = s.out + (of.out_row + first) * s.out_ld + block * 8 + (lane & 7);
+#pragma unroll
+          for (int j = 0; j < 8; ++j) {
+            const float low = __uint_as_float(v[j]), high = __uint_as_float(v[j + 8]);
+            const float got = __shfl_xor_sync(0xffffffffu, up ? low : high, 8);
+            const float gate = up ? got : low, lin = up ? high : got;
+            if (live && first + j < of.n)  // H is rounded to bf16, the type of the activations
+              out[j * s.out_ld] = __float2bfloat16_rn(silu_f(gate) * lin);
+          }
+        } else {
+          const int64_t o = (of.out_row + t0 + 16 * b) * s.out_ld + block * 16 + (lane & 15);
+#pragma unroll
+          for (int j = 0; j < 16; ++j) {
+            float r = __shfl_sync(0xffffffffu, weight, 16 * b + j) * __uint_as_float(v[j]);
+            if (live && t0 + 16 * b + j < of.n) {
+              if (s.add) r += __bfloat162float(s.add[o + j * s.out_ld]);
+              s.out[o + j * s.out_ld] = __float2bfloat16_rn(r);
+            }
+          }
+        }
+      }
+      tc_fence_before();
+      __syncwarp();
+      if (lane == 0) mbar_arrive(bar(hd->tempty[buf]));
+      return true;
+    };
+
+    bool ok = true;
+    int seq = 0, slot = parity, phase = 0;
+    Unit of;  // whose outputs are to be written
+    of.seg = -1;
+    for (int u = u0; u < plan.total && ok; u += gridDim.x, ++seq) {
+      const Unit x = unit_at(p, lists, plan, u, pos, kRec);
+      const Int4Segment& s = p.seg[x.seg];
+      const bool has_a = a_block < x.blocks;
+      const uint8_t* w = x.W + (has_a ? static_cast<int64_t>(a_block) * x.chunks * kRec : 0) +
+                         parity * (kCodeBytes / 2) + lane * 16;
+      auto fetch = [&](int ch) {
+        if (has_a && ch < x.chunks) {
+          const uint32_t to = smem_u32(ring + (ch & (kDepth - 1)) * kHalf) + lane * 16;
+          const uint8_t* from = w + ch * kRec;
+          cp_async16(to, from);
+          if (lane < (kRec - kCodeBytes) / 16)
+            cp_async16(to + kCodeBytes / 2, from + kCodeBytes - parity * (kCodeBytes / 2));
+        }
+      };
+#pragma unroll
+      for (int c = 0; c < kDepth - 1; ++c) {
+        fetch(c);
+        asm volatile("cp.async.commit_group;" ::: "memory");
+      }
+      if (seq == 0 && p.wait == kWaitX) pdl_wait();
+      const uint8_t* xp[kTasks];  // this lane's piece of its tokens' rows
+      {
+        const int t = 32 * (lane >> 2 & 3) + 4 * a_block + (lane & 3);
+        const int64_t at = x.x_row + min(t, x.n - 1);
+        const int mine = static_cast<int>(s.perm ? s.perm[at] / s.perm_div : at);
+#pragma unroll
+        for (int k = 0; k < kTasks; ++k)
+          xp[k] = static_cast<const uint8_t*>(s.x) +
+                  static_cast<int64_t>(__shfl_sync(0xffffffffu, mine, 4 * k + (lane >> 3))) *
+                      x.chunks * (2 * kChunk) + parity * kChunk + piece * 16;
+      }
+      for (int ch = 0; ch < x.chunks; ++ch) {
+        asm volatile("cp.async.wait_group %0;" ::"n"(kDepth - 2) : "memory");
+        __syncwarp();
+        if (!mbar_wait_bounded(bar(hd->empty[slot]), phase ^ 1, abort_flag, p.status)) {
+          ok = false;
+          break;
+        }
+        uint8_t* st = smem + slot * kStageBytes;
+#pragma unroll
+        for (int k = 0; k < kTasks; ++k) {
+          const int t = 32 * k + sub;
+          if (t < x.n)
+            cp_async16(smem_u32(st + 2 * kAtom) + t * 128 + ((piece ^ (t & 7)) << 4),
+                       xp[k] + ch * (2 * kChunk));
+        }
+        asm volatile("cp.async.commit_group;" ::: "memory");
+        fetch(ch + kDepth - 1);
+        asm volatile("cp.async.commit_group;" ::: "memory");
+        if (has_a)
+          make_a_split<kGroup>(ring + (ch & (kDepth - 1)) * kHalf, st, st + kAtom, 16 * a_block + g,
+                               parity, lane);
+        // b has landed, and every half record but the one just asked for
+        asm volatile("cp.async.wait_group 1;" ::: "memory");
+        fence_proxy_async_smem();  // the tensor cores read the operands next
+        __syncwarp();
+        if (lane == 0) mbar_arrive(bar(hd->full[slot]));
+        if ((slot += 2) >= kStages) {
+          slot -= kStages;
+          phase ^= 1;
+        }
+        if (of.seg >= 0 && ch == min(1, x.chunks - 1)) {
+          if (!finish(of, seq - 1)) {
+            ok = false;
+            break;
+          }
+          of.seg = -1;
+        }
+      }
+      of = x;
+    }
+    asm volatile("cp.async.wait_all;" ::: "memory");
+    if (ok && of.seg >= 0) finish(of, seq - 1);
+  } else {
+    if (lane == 0) {
+      int slot = 0, phase = 0, seq = 0;
+      bool ok = true;
+      for (int u = u0; ok && u < plan.total; u += gridDim.x, ++seq) {
+        const Unit x = unit_at(p, lists, plan, u, pos, kRec);
+        const uint32_t idesc = idesc_bf16_f32(128, x.n > 64 ? 128 : 64);
+        const uint32_t d = tmem + (seq & 1) * kTokens;
+        if (!mbar_wait_bounded(bar(hd->tempty[seq & 1]), (seq >> 1 & 1) ^ 1, abort_flag, p.status))
+          break;
+        for (int j = 0; j < 2 * x.chunks; ++j) {
+          if (!mbar_wait_bounded(bar(hd->full[slot]), phase, abort_flag, p.status)) {
+            ok = false;
+            break;
+          }
+          tc_fence_after();
+          const uint32_t st = smem_u32(smem + slot * kStageBytes);
+          const uint64_t hi = smem_desc_sw128(st), lo = smem_desc_sw128(st + kAtom);
+          const uint64_t b = smem_desc_sw128(st + 2 * kAtom);
+#pragma unroll
+          for (int kk = 0; kk < 4; ++kk) {
+            tc_mma_bf16(d, hi + 2u * kk, b + 2u * kk, idesc, (j | kk) != 0);
+            tc_mma_bf16(d, lo + 2u * kk, b + 2u * kk, idesc, 1);
+          }
+          tc_commit(bar(hd->empty[slot]));
+          if (++slot == kStages) {
+            slot = 0;
+            phase ^= 1;
+          }
+        }
+        tc_commit(bar(hd->tfull[seq & 1]));
+      }
+      // nothing is in flight when the CTA gives its TMEM back
+      tc_commit(bar(hd->drain));
+      int own_abort = 0;
+      mbar_wait_bounded(bar(hd->drain), 0, &own_abort, p.status);
+    }
+    __syncwarp();
+  }
+  if (p.wait != kWaitWeights) pdl_wait();  // a kernel ends after the one before it has
+  tc_fence_before();
+  __syncthreads();
+  if (warp == 0) {
+    tc_fence_after();
+    tmem_dealloc(tmem, kTmemCols);
+  }
+}
+
+template <typename Kernel>
+cudaError_t launch_kernel(Kernel kernel, const Int4Launch& p, int num_sms, cudaStream_t stream) {
+  // every call: the attribute belongs to a device's context, and setting it
+  // costs little beside a launch of more than 16 rows
+  const cudaError_t err =
+      cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, p.smem);
+  if (err != cudaSuccess) return err;
+  return launch_pdl(kernel, dim3(num_sms), dim3(kThreads), p.smem, stream, p);
 }
 
 // Rows of a group up to which it is read by gemv_int4.cu.
@@ -471,13 +773,20 @@ cudaError_t launch_gemm_int4(const Int4Launch& p, bool swiglu, int group, int nu
   Int4Launch l = p;
   int groups = 0;
   for (int i = 0; i < p.nseg; ++i) groups += p.seg[i].groups;
-  l.smem = smem_bytes(groups, group);
-  const bool x8 = p.seg[0].x_scale != nullptr;
-  if (swiglu)
-    return x8 ? launch_group<true, true>(l, group, num_sms, stream)
-              : launch_group<true, false>(l, group, num_sms, stream);
-  return x8 ? launch_group<false, true>(l, group, num_sms, stream)
-            : launch_group<false, false>(l, group, num_sms, stream);
+  if (p.seg[0].x_scale) {
+    l.smem = smem_bytes(groups, group);
+    return launch_kernel(swiglu ? group == 32 ? gemm_int4_kernel<true, true, 32>
+                                              : gemm_int4_kernel<true, true, 128>
+                         : group == 32 ? gemm_int4_kernel<false, true, 32>
+                                       : gemm_int4_kernel<false, true, 128>,
+                         l, num_sms, stream);
+  }
+  l.smem = smem_bytes_b(groups, group);
+  return launch_kernel(swiglu ? group == 32 ? gemm_int4_bf16_kernel<true, 32>
+                                            : gemm_int4_bf16_kernel<true, 128>
+                       : group == 32 ? gemm_int4_bf16_kernel<false, 32>
+                                     : gemm_int4_bf16_kernel<false, 128>,
+                       l, num_sms, stream);
 }
 
 cudaError_t launch_int4(const Int4Params& q, int num_sms, cudaStream_t stream) {
