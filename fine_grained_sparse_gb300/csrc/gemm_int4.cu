@@ -443,16 +443,21 @@ __global__ void __launch_bounds__(kThreads, 1) gemm_int4_kernel(const __grid_con
 // With x in bf16 both operands are bf16 and nothing is left to apply to the
 // sums: b is x as it lies in memory, a weight (c - 8) s is the sum of two bf16
 // values (its rounding and the rest, at most 11 significant bits together),
-// and the MMAs of both run over all of K in one TMEM accumulator.
+// and the MMAs of both run over all of K in TMEM accumulators of their own,
+// issued by two warps: one thread takes about 100 cycles for each MMA beside
+// the workers, and eight a stage held everything up (linear 7168-18432, 64
+// tokens: 70 us).
 constexpr int kStages = 3;                  // of 64 columns: a high, a low, b
 constexpr int kStageBytes = 3 * kAtom;
+constexpr int kThreadsB = 32 * (kWorkers + 2);
+constexpr int kTmemColsB = 4 * kTokens;     // [unit parity][high, low][tokens]
 
 struct HeaderB {
   uint64_t full[kStages], empty[kStages], tfull[2], tempty[2], drain;
   uint32_t tmem;
   int abort;
   int at_first, pad;
-  int64_t warp_sum[kThreads / 32];
+  int64_t warp_sum[kThreadsB / 32];
   int64_t lists[1];
 };
 
@@ -517,7 +522,7 @@ __device__ __forceinline__ void make_a_split(const uint8_t* rec, uint8_t* hi_to,
 // hand it over when the copies have landed.  A unit's outputs are written while the next unit's first stages run, from
 // the other half of TMEM.
 template <bool kSwiglu, int kGroup>
-__global__ void __launch_bounds__(kThreads, 1)
+__global__ void __launch_bounds__(kThreadsB, 1)
     gemm_int4_bf16_kernel(const __grid_constant__ Int4Launch p) {
   constexpr int kRec = record_bytes(kGroup), kHalf = half_bytes(kGroup);
   extern __shared__ __align__(16) uint8_t raw[];
@@ -530,19 +535,19 @@ __global__ void __launch_bounds__(kThreads, 1)
   auto bar = [](uint64_t& b) { return smem_u32(&b); };
 
   if (warp == 0) {
-    tmem_alloc(smem_u32(&hd->tmem), kTmemCols);
+    tmem_alloc(smem_u32(&hd->tmem), kTmemColsB);
     tmem_relinquish();
   }
   if (warp == kWorkers && lane == 0) {
     for (int i = 0; i < kStages; ++i) {
       mbar_init(bar(hd->full[i]), kWorkers / 2);
-      mbar_init(bar(hd->empty[i]), 1);
+      mbar_init(bar(hd->empty[i]), 2);
     }
     for (int i = 0; i < 2; ++i) {
-      mbar_init(bar(hd->tfull[i]), 1);
+      mbar_init(bar(hd->tfull[i]), 2);
       mbar_init(bar(hd->tempty[i]), kWorkers);
     }
-    mbar_init(bar(hd->drain), 1);
+    mbar_init(bar(hd->drain), 2);
     hd->abort = 0;
     fence_mbarrier_init();
   }
@@ -555,7 +560,7 @@ __global__ void __launch_bounds__(kThreads, 1)
   pdl_release();
   const GroupLists lists = group_lists(hd->lists, groups);
   const int u0 = blockIdx.x;
-  const GroupPlan plan = plan_groups<kThreads>(
+  const GroupPlan plan = plan_groups<kThreadsB>(
       p, lists, hd->warp_sum,
       [&](int si, int n) -> int64_t {
         if (n <= p.most) return 0;
@@ -591,10 +596,16 @@ __global__ void __launch_bounds__(kThreads, 1)
 #pragma unroll
       for (int b = 0; b < 2; ++b) {
         if (16 * b >= cols) break;
-        uint32_t v[16];
-        tmem_ld_x16(tmem + buf * kTokens + t0 + 16 * b + (static_cast<uint32_t>(32 * quarter) << 16),
-                    v);
+        uint32_t v[16], v2[16];
+        const uint32_t from = tmem + 2 * buf * kTokens + t0 + 16 * b +
+                              (static_cast<uint32_t>(32 * quarter) << 16);
+        tmem_ld_x16(from, v);
+        tmem_ld_x16(from + kTokens, v2);
         tmem_ld_wait(v);
+        tmem_ld_wait(v2);
+#pragma unroll
+        for (int j = 0; j < 16; ++j)
+          v[j] = __float_as_uint(__uint_as_float(v[j]) + __uint_as_float(v2[j]));
         if (kSwiglu) {
           // rows r < 8 of a block are gate rows, r + 8 the up rows of the
           // same features: lanes 8 apart swap and each finishes half the tokens
@@ -707,12 +718,13 @@ __global__ void __launch_bounds__(kThreads, 1)
     if (ok && of.seg >= 0) finish(of, seq - 1);
   } else {
     if (lane == 0) {
+      const int low = warp - kWorkers;  // 1: the rests
       int slot = 0, phase = 0, seq = 0;
       bool ok = true;
       for (int u = u0; ok && u < plan.total; u += gridDim.x, ++seq) {
         const Unit x = unit_at(p, lists, plan, u, pos, kRec);
         const uint32_t idesc = idesc_bf16_f32(128, x.n > 64 ? 128 : 64);
-        const uint32_t d = tmem + (seq & 1) * kTokens;
+        const uint32_t d = tmem + (2 * (seq & 1) + low) * kTokens;
         if (!mbar_wait_bounded(bar(hd->tempty[seq & 1]), (seq >> 1 & 1) ^ 1, abort_flag, p.status))
           break;
         for (int j = 0; j < 2 * x.chunks; ++j) {
@@ -722,13 +734,10 @@ __global__ void __launch_bounds__(kThreads, 1)
           }
           tc_fence_after();
           const uint32_t st = smem_u32(smem + slot * kStageBytes);
-          const uint64_t hi = smem_desc_sw128(st), lo = smem_desc_sw128(st + kAtom);
-          const uint64_t b = smem_desc_sw128(st + 2 * kAtom);
+          const uint64_t a = smem_desc_sw128(st + low * kAtom), b = smem_desc_sw128(st + 2 * kAtom);
 #pragma unroll
-          for (int kk = 0; kk < 4; ++kk) {
-            tc_mma_bf16(d, hi + 2u * kk, b + 2u * kk, idesc, (j | kk) != 0);
-            tc_mma_bf16(d, lo + 2u * kk, b + 2u * kk, idesc, 1);
-          }
+          for (int kk = 0; kk < 4; ++kk)
+            tc_mma_bf16(d, a + 2u * kk, b + 2u * kk, idesc, (j | kk) != 0);
           tc_commit(bar(hd->empty[slot]));
           if (++slot == kStages) {
             slot = 0;
@@ -749,18 +758,19 @@ __global__ void __launch_bounds__(kThreads, 1)
   __syncthreads();
   if (warp == 0) {
     tc_fence_after();
-    tmem_dealloc(tmem, kTmemCols);
+    tmem_dealloc(tmem, kTmemColsB);
   }
 }
 
 template <typename Kernel>
-cudaError_t launch_kernel(Kernel kernel, const Int4Launch& p, int num_sms, cudaStream_t stream) {
+cudaError_t launch_kernel(Kernel kernel, const Int4Launch& p, int threads, int num_sms,
+                          cudaStream_t stream) {
   // every call: the attribute belongs to a device's context, and setting it
   // costs little beside a launch of more than 16 rows
   const cudaError_t err =
       cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, p.smem);
   if (err != cudaSuccess) return err;
-  return launch_pdl(kernel, dim3(num_sms), dim3(kThreads), p.smem, stream, p);
+  return launch_pdl(kernel, dim3(num_sms), dim3(threads), p.smem, stream, p);
 }
 
 // Rows of a group up to which it is read by gemv_int4.cu.
@@ -779,14 +789,14 @@ cudaError_t launch_gemm_int4(const Int4Launch& p, bool swiglu, int group, int nu
                                               : gemm_int4_kernel<true, true, 128>
                          : group == 32 ? gemm_int4_kernel<false, true, 32>
                                        : gemm_int4_kernel<false, true, 128>,
-                         l, num_sms, stream);
+                         l, kThreads, num_sms, stream);
   }
   l.smem = smem_bytes_b(groups, group);
   return launch_kernel(swiglu ? group == 32 ? gemm_int4_bf16_kernel<true, 32>
                                             : gemm_int4_bf16_kernel<true, 128>
                        : group == 32 ? gemm_int4_bf16_kernel<false, 32>
                                      : gemm_int4_bf16_kernel<false, 128>,
-                       l, num_sms, stream);
+                       l, kThreadsB, num_sms, stream);
 }
 
 cudaError_t launch_int4(const Int4Params& q, int num_sms, cudaStream_t stream) {
