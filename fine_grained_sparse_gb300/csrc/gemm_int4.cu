@@ -31,7 +31,7 @@ constexpr int kTmemCols = 2 * kTokens;
 struct Header {
   float f[kFactors][kTokens];
   float r[kFactors][kRows];
-  uint64_t full[2], empty[2], tfull[2], tempty[2], factors[kFactors], drain;
+  uint64_t full[2], empty[2], tfull[2], tempty[2], drain;
   uint32_t tmem;
   int abort;
   int at_first, pad;
@@ -64,6 +64,7 @@ struct Unit {
 // Unit u of the launch; pos: where in the group lists to look from (units
 // are asked for in ascending order).  Token tiles run fastest, so that the
 // CTAs that read the same weights do so at the same time.
+template <int kMostTokens>
 __device__ __forceinline__ Unit unit_at(const Int4Launch& p, const GroupLists& l, GroupPlan plan,
                                         int u, int& pos, int rec) {
   Unit x;
@@ -77,7 +78,7 @@ __device__ __forceinline__ Unit unit_at(const Int4Launch& p, const GroupLists& l
   const int grp = x.seg ? k - n0 : k;
   const int first = s.offsets ? l.first[k] : 0;
   const int n = s.offsets ? l.first[k + 1] - first : static_cast<int>(s.rows);
-  const uint32_t tiles = (n + kTokens - 1u) / kTokens;
+  const uint32_t tiles = (n + kMostTokens - 1u) / kMostTokens;
   const uint32_t local = u - static_cast<int>(l.before[pos]);
   const int m = local / tiles, t = local - m * tiles;
   const int row0 = static_cast<int>(static_cast<int64_t>(n) * t / tiles);
@@ -157,6 +158,44 @@ __device__ __forceinline__ uint32_t idesc_f16_f32(uint32_t n) {
   return (1u << 4) | ((n >> 3) << 17) | ((128u >> 4) << 24);
 }
 
+// A unit's outputs from the sums of row `row` and tokens t0 .. t0 + cols - 1
+// (cols 16 or 32); weight: the row weight of token t0 + lane.
+template <bool kSwiglu>
+__device__ __forceinline__ void write_unit(const Int4Segment& s, const Unit& x,
+                                           const float (&acc)[kTokens / 4], float weight, int t0,
+                                           int cols, int row, int lane) {
+  const bool live = row / 16 < x.blocks;
+  const int block = x.first_block + row / 16;
+  if (kSwiglu) {
+    // rows r < 8 of a block are gate rows, r + 8 the up rows of the same
+    // features: lanes 8 apart swap halves and each finishes half the tokens
+    const bool up = lane & 8;
+    __nv_bfloat16* out = s.out + (x.out_row + t0) * s.out_ld + block * 8 + (lane & 7);
+#pragma unroll
+    for (int j = 0; j < 16; ++j) {
+      // with 16 tokens, j and j + 8; with 32, j and j + 16
+      if (cols == 16 && j >= 8) break;
+      const float low = acc[j], high = cols == 16 ? acc[(j + 8) & 31] : acc[j + 16];
+      const float got = __shfl_xor_sync(0xffffffffu, up ? low : high, 8);
+      const float gate = up ? got : low, lin = up ? high : got;
+      const int t = j + (up ? cols / 2 : 0);
+      if (live && t0 + t < x.n)  // H is rounded to bf16, the type of the layer's activations
+        out[t * s.out_ld] = __float2bfloat16_rn(silu_f(gate) * lin);
+    }
+  } else {
+    const int64_t o = (x.out_row + t0) * s.out_ld + block * 16 + (lane & 15);
+#pragma unroll
+    for (int j = 0; j < 32; ++j) {
+      if (j >= cols) break;
+      float v = __shfl_sync(0xffffffffu, weight, j) * acc[j];
+      if (live && t0 + j < x.n) {
+        if (s.add) v += __bfloat162float(s.add[o + j * s.out_ld]);
+        s.out[o + j * s.out_ld] = __float2bfloat16_rn(v);
+      }
+    }
+  }
+}
+
 // Sixteen worker warps make the operands of chunk i (half of a row block of
 // the weights each, and the tokens of its two half warps) and then add up the
 // sums of chunk i - 1 (a quarter of the rows, a quarter of the tokens), while
@@ -165,8 +204,8 @@ __device__ __forceinline__ uint32_t idesc_f16_f32(uint32_t n) {
 // Sixteen warps of both kinds of work, not eight of each: a scheduler has
 // four to choose from, and two could not hide the latencies (a chunk of 64
 // tokens took 3900 cycles).
-template <bool kSwiglu, bool kX8, int kGroup>
-__global__ void __launch_bounds__(kThreads, 1) gemm_int4_kernel(const __grid_constant__ Int4Launch p) {
+template <bool kSwiglu, int kGroup>
+__global__ void __launch_bounds__(kThreads, 1) gemm_int4_fp8_kernel(const __grid_constant__ Int4Launch p) {
   constexpr int kRec = record_bytes(kGroup), kHalf = half_bytes(kGroup);
   extern __shared__ __align__(16) uint8_t raw[];
   uint8_t* smem = raw + ((1024u - (smem_u32(raw) & 1023u)) & 1023u);
@@ -188,7 +227,6 @@ __global__ void __launch_bounds__(kThreads, 1) gemm_int4_kernel(const __grid_con
       mbar_init(bar(hd->tfull[i]), 1);
       mbar_init(bar(hd->tempty[i]), kWorkers);
     }
-    for (int i = 0; i < kFactors; ++i) mbar_init(bar(hd->factors[i]), kWorkers);
     mbar_init(bar(hd->drain), 1);
     hd->abort = 0;
     fence_mbarrier_init();
@@ -224,7 +262,7 @@ __global__ void __launch_bounds__(kThreads, 1) gemm_int4_kernel(const __grid_con
     bool first = true, ok = true;
     int i = 0;
     for (int u = u0; u < plan.total && ok; u += gridDim.x) {
-      const Unit x = unit_at(p, lists, plan, u, pos, kRec);
+      const Unit x = unit_at<kTokens>(p, lists, plan, u, pos, kRec);
       const Int4Segment& s = p.seg[x.seg];
       // this worker's half records, and the last of them
       const bool has_a = a_block < x.blocks;
@@ -252,23 +290,16 @@ __global__ void __launch_bounds__(kThreads, 1) gemm_int4_kernel(const __grid_con
 #pragma unroll
         for (int q = 0; q < kTasks; ++q) rows[q] = __shfl_sync(0xffffffffu, mine, (lane & 16) + q);
       }
-      uint4 xr[kTasks];
+      uint2 xr[kTasks];
       float xf[kTasks];
       auto load_b = [&](int ch) {
 #pragma unroll
         for (int q = 0; q < kTasks; ++q) {
           if (32 * q + 2 * warp >= x.n) break;
           const int64_t from = static_cast<int64_t>(rows[q]) * x.chunks + ch;
-          if (kX8) {
-            const uint2 v = *reinterpret_cast<const uint2*>(static_cast<const uint8_t*>(s.x) +
-                                                            from * kChunk + piece * 8);
-            xr[q].x = v.x;
-            xr[q].y = v.y;
-            xf[q] = s.x_scale[from];
-          } else {
-            xr[q] = *reinterpret_cast<const uint4*>(static_cast<const __nv_bfloat16*>(s.x) +
-                                                    from * kChunk + piece * 8);
-          }
+          xr[q] = *reinterpret_cast<const uint2*>(static_cast<const uint8_t*>(s.x) + from * kChunk +
+                                                  piece * 8);
+          xf[q] = s.x_scale[from];
         }
       };
       load_b(0);
@@ -305,31 +336,21 @@ __global__ void __launch_bounds__(kThreads, 1) gemm_int4_kernel(const __grid_con
           for (int q = 0; q < kTasks; ++q) {
             if (32 * q + 2 * warp >= x.n) break;
             const int t = 32 * q + hw;
-            uint4 v;
-            float f;
-            if (kX8) {
-              v = e4m3x8_to_f16(make_uint2(xr[q].x, xr[q].y));
-              f = xf[q];
-            } else {
-              uint32_t e;
-              v = bf16x8_to_f16(xr[q], e);
-              f = __uint_as_float((e - 14u) << 23);  // 2^(e - 141)
-            }
-            *reinterpret_cast<uint4*>(b + t * 128 + (((piece & 7) ^ (t & 7)) << 4)) = v;
-            if (piece == 0) hd->f[fs][t] = f;
+            *reinterpret_cast<uint4*>(b + t * 128 + (((piece & 7) ^ (t & 7)) << 4)) =
+                e4m3x8_to_f16(xr[q]);
+            if (piece == 0) hd->f[fs][t] = xf[q];
           }
+          if (ch + 1 < x.chunks) load_b(ch + 1);
           fence_proxy_async_smem();  // the tensor cores read the operands next
           __syncwarp();
-          if (lane == 0) {
-            mbar_arrive(bar(hd->full[st]));
-            mbar_arrive(bar(hd->factors[fs]));
-          }
+          if (lane == 0) mbar_arrive(bar(hd->full[st]));
           ++i;
         }
         if (ch > 0) {
           const int c = i - (ch < x.chunks ? 2 : 1), st = c & 1, fs = c & (kFactors - 1);
-          if (!mbar_wait_bounded(bar(hd->factors[fs]), c >> 2 & 1, abort_flag, p.status) ||
-              !mbar_wait_bounded(bar(hd->tfull[st]), c >> 1 & 1, abort_flag, p.status)) {
+          // (the operands were full before; that wait is for f and r)
+          if (!mbar_wait_bounded(bar(hd->tfull[st]), c >> 1 & 1, abort_flag, p.status) ||
+              !mbar_wait_bounded(bar(hd->full[st]), c >> 1 & 1, abort_flag, p.status)) {
             ok = false;
             break;
           }
@@ -359,40 +380,10 @@ __global__ void __launch_bounds__(kThreads, 1) gemm_int4_kernel(const __grid_con
           __syncwarp();
           if (lane == 0) mbar_arrive(bar(hd->tempty[st]));
         }
-        if (ch + 1 < x.chunks) load_b(ch + 1);
       }
       if (!ok) break;
 
-      const bool live = row / 16 < x.blocks;
-      const int block = x.first_block + row / 16;
-      if (kSwiglu) {
-        // rows r < 8 of a block are gate rows, r + 8 the up rows of the same
-        // features: lanes 8 apart swap halves and each finishes half the tokens
-        const bool up = lane & 8;
-        __nv_bfloat16* out = s.out + (x.out_row + t0) * s.out_ld + block * 8 + (lane & 7);
-#pragma unroll
-        for (int j = 0; j < 16; ++j) {
-          // with 16 tokens, j and j + 8; with 32, j and j + 16
-          if (cols == 16 && j >= 8) break;
-          const float low = acc[j], high = cols == 16 ? acc[(j + 8) & 31] : acc[j + 16];
-          const float got = __shfl_xor_sync(0xffffffffu, up ? low : high, 8);
-          const float gate = up ? got : low, lin = up ? high : got;
-          const int t = j + (up ? cols / 2 : 0);
-          if (live && t0 + t < x.n)  // H is rounded to bf16, the type of the layer's activations
-            out[t * s.out_ld] = __float2bfloat16_rn(silu_f(gate) * lin);
-        }
-      } else {
-        const int64_t o = (x.out_row + t0) * s.out_ld + block * 16 + (lane & 15);
-#pragma unroll
-        for (int j = 0; j < 32; ++j) {
-          if (j >= cols) break;
-          float v = __shfl_sync(0xffffffffu, weight, j) * acc[j];
-          if (live && t0 + j < x.n) {
-            if (s.add) v += __bfloat162float(s.add[o + j * s.out_ld]);
-            s.out[o + j * s.out_ld] = __float2bfloat16_rn(v);
-          }
-        }
-      }
+      write_unit<kSwiglu>(s, x, acc, weight, t0, cols, row, lane);
     }
     asm volatile("cp.async.wait_all;" ::: "memory");
   } else {
@@ -400,7 +391,7 @@ __global__ void __launch_bounds__(kThreads, 1) gemm_int4_kernel(const __grid_con
       int i = 0;
       bool ok = true;
       for (int u = u0; ok; u += gridDim.x) {
-        const Unit x = unit_at(p, lists, plan, u, pos, kRec);
+        const Unit x = unit_at<kTokens>(p, lists, plan, u, pos, kRec);
         if (x.seg < 0) break;
         const uint32_t idesc = idesc_f16_f32(x.n > 64 ? 128 : 64);
         for (int ch = 0; ch < x.chunks; ++ch, ++i) {
@@ -447,13 +438,15 @@ __global__ void __launch_bounds__(kThreads, 1) gemm_int4_kernel(const __grid_con
 // issued by two warps: one thread takes about 100 cycles for each MMA beside
 // the workers, and eight a stage held everything up (linear 7168-18432, 64
 // tokens: 70 us).
-constexpr int kStages = 3;                  // of 64 columns: a high, a low, b
-constexpr int kStageBytes = 3 * kAtom;
+// Stages are 64 columns (a high, a low, b): four where no group has more than
+// 64 rows, so that each parity has two; three of 128 tokens.
+__host__ __device__ constexpr int stages(int tokens) { return tokens == 64 ? 4 : 3; }
+__host__ __device__ constexpr int stage_bytes(int tokens) { return 2 * kAtom + tokens * 128; }
 constexpr int kThreadsB = 32 * (kWorkers + 2);
 constexpr int kTmemColsB = 4 * kTokens;     // [unit parity][high, low][tokens]
 
 struct HeaderB {
-  uint64_t full[kStages], empty[kStages], tfull[2], tempty[2], drain;
+  uint64_t full[4], empty[4], tfull[2], tempty[2], drain;
   uint32_t tmem;
   int abort;
   int at_first, pad;
@@ -461,8 +454,8 @@ struct HeaderB {
   int64_t lists[1];
 };
 
-inline int smem_bytes_b(int groups, int group) {
-  return 1024 + kStages * kStageBytes + ring_bytes(group) +
+inline int smem_bytes_b(int tokens, int groups, int group) {
+  return 1024 + stages(tokens) * stage_bytes(tokens) + ring_bytes(group) +
          (static_cast<int>(sizeof(HeaderB)) + group_list_bytes(groups) + 15) / 16 * 16;
 }
 
@@ -521,9 +514,10 @@ __device__ __forceinline__ void make_a_split(const uint8_t* rec, uint8_t* hi_to,
 // (one for each row block) make it: they start the copies of b, convert a and
 // hand it over when the copies have landed.  A unit's outputs are written while the next unit's first stages run, from
 // the other half of TMEM.
-template <bool kSwiglu, int kGroup>
+template <bool kSwiglu, int kGroup, int kMostTokens>
 __global__ void __launch_bounds__(kThreadsB, 1)
     gemm_int4_bf16_kernel(const __grid_constant__ Int4Launch p) {
+  constexpr int kStages = stages(kMostTokens), kStageBytes = stage_bytes(kMostTokens);
   constexpr int kRec = record_bytes(kGroup), kHalf = half_bytes(kGroup);
   extern __shared__ __align__(16) uint8_t raw[];
   uint8_t* smem = raw + ((1024u - (smem_u32(raw) & 1023u)) & 1023u);
@@ -565,7 +559,7 @@ __global__ void __launch_bounds__(kThreadsB, 1)
       [&](int si, int n) -> int64_t {
         if (n <= p.most) return 0;
         return static_cast<int64_t>((p.seg[si].blocks + kBlocks - 1) / kBlocks) *
-               ((n + kTokens - 1u) / kTokens);
+               ((n + kMostTokens - 1u) / kMostTokens);
       },
       [](int64_t) {},
       [&](int pos, int64_t before, int64_t cost) {
@@ -578,7 +572,7 @@ __global__ void __launch_bounds__(kThreadsB, 1)
     const int piece = lane & 7, sub = 4 * a_block + (lane >> 3);  // of b: tokens 32 k + sub
     const int quarter = warp & 3, row = 32 * quarter + lane;      // of the outputs
     uint8_t* const ring = ring_base + warp * kDepth * kHalf;
-    constexpr int kTasks = kTokens / 32;
+    constexpr int kTasks = kMostTokens / 32;
 
     // the outputs of unit `of`, the seq-th of the CTA; false: gave up
     auto finish = [&](const Unit& of, int seq) {
@@ -594,7 +588,7 @@ __global__ void __launch_bounds__(kThreadsB, 1)
       if (!kSwiglu && s.row_w && t0 + lane < of.n)
         weight = s.row_w[s.row_perm[of.out_row + t0 + lane]];
 #pragma unroll
-      for (int b = 0; b < 2; ++b) {
+      for (int b = 0; b < kMostTokens / 64; ++b) {
         if (16 * b >= cols) break;
         uint32_t v[16], v2[16];
         const uint32_t from = tmem + 2 * buf * kTokens + t0 + 16 * b +
@@ -643,7 +637,7 @@ __global__ void __launch_bounds__(kThreadsB, 1)
     Unit of;  // whose outputs are to be written
     of.seg = -1;
     for (int u = u0; u < plan.total && ok; u += gridDim.x, ++seq) {
-      const Unit x = unit_at(p, lists, plan, u, pos, kRec);
+      const Unit x = unit_at<kMostTokens>(p, lists, plan, u, pos, kRec);
       const Int4Segment& s = p.seg[x.seg];
       const bool has_a = a_block < x.blocks;
       const uint8_t* w = x.W + (has_a ? static_cast<int64_t>(a_block) * x.chunks * kRec : 0) +
@@ -665,7 +659,7 @@ __global__ void __launch_bounds__(kThreadsB, 1)
       if (seq == 0 && p.wait == kWaitX) pdl_wait();
       const uint8_t* xp[kTasks];  // this lane's piece of its tokens' rows
       {
-        const int t = 32 * (lane >> 2 & 3) + 4 * a_block + (lane & 3);
+        const int t = 32 * (lane >> 2 & (kTasks - 1)) + 4 * a_block + (lane & 3);
         const int64_t at = x.x_row + min(t, x.n - 1);
         const int mine = static_cast<int>(s.perm ? s.perm[at] / s.perm_div : at);
 #pragma unroll
@@ -722,7 +716,7 @@ __global__ void __launch_bounds__(kThreadsB, 1)
       int slot = 0, phase = 0, seq = 0;
       bool ok = true;
       for (int u = u0; ok && u < plan.total; u += gridDim.x, ++seq) {
-        const Unit x = unit_at(p, lists, plan, u, pos, kRec);
+        const Unit x = unit_at<kMostTokens>(p, lists, plan, u, pos, kRec);
         const uint32_t idesc = idesc_bf16_f32(128, x.n > 64 ? 128 : 64);
         const uint32_t d = tmem + (2 * (seq & 1) + low) * kTokens;
         if (!mbar_wait_bounded(bar(hd->tempty[seq & 1]), (seq >> 1 & 1) ^ 1, abort_flag, p.status))
@@ -762,6 +756,307 @@ __global__ void __launch_bounds__(kThreadsB, 1)
   }
 }
 
+// ------------------------------------- E4M3 rows, scales of 128 columns
+// With one scale a chunk on either side the operands can stay bytes
+// (kind::f8f6f4): b is x as it lies in memory, and a code c as an E4M3 byte is
+// c 2^-9 (subnormals and the first normal binade are evenly spaced), so that
+// masks make a from the codes.  A constant first operand of -8 2^-9 adds what
+// makes the codes signed.  The products and their sums are those of the f16
+// form; a chunk's are added up in fp32 with both scales.
+constexpr int kStagesC = 3;
+constexpr int kStageBytesC = 2 * kAtom;  // a, b: 128 rows of 128 bytes
+
+// b and f are asked for a chunk ahead, when sums four chunks back may still be
+// read: eight chunks' factors are kept.
+constexpr int kFactorsC = 8;
+
+struct HeaderC {
+  float f[kFactorsC][kTokens];
+  float r[kFactorsC][kRows];
+  uint64_t full[kStagesC], empty[kStagesC], tfull[2], tempty[2], drain;
+  uint32_t tmem;
+  int abort;
+  int at_first, pad;
+  int64_t warp_sum[kThreads / 32];
+  int64_t lists[1];
+};
+
+inline int smem_bytes_c(int groups) {
+  return 1024 + kStagesC * kStageBytesC + kAtom + ring_bytes(128) +
+         (static_cast<int>(sizeof(HeaderC)) + group_list_bytes(groups) + 15) / 16 * 16;
+}
+
+// D[tmem] (+)= A[smem] * B[smem]^T, E4M3 inputs, fp32 accumulator, M = 128.
+__device__ __forceinline__ void tc_mma_e4m3(uint32_t d_tmem, uint64_t a_desc, uint64_t b_desc,
+                                            uint32_t idesc, uint32_t accumulate) {
+  asm volatile(
+      "{\n\t.reg .pred p;\n\t"
+      "setp.ne.b32 p, %4, 0;\n\t"
+      "tcgen05.mma.cta_group::1.kind::f8f6f4 [%0], %1, %2, %3, p;\n\t}" ::"r"(d_tmem),
+      "l"(a_desc), "l"(b_desc), "r"(idesc), "r"(accumulate)
+      : "memory");
+}
+
+template <bool kSwiglu>
+__global__ void __launch_bounds__(kThreads, 1)
+    gemm_int4_bytes_kernel(const __grid_constant__ Int4Launch p) {
+  constexpr int kRec = record_bytes(128), kHalf = half_bytes(128);
+  extern __shared__ __align__(16) uint8_t raw[];
+  uint8_t* smem = raw + ((1024u - (smem_u32(raw) & 1023u)) & 1023u);
+  uint8_t* bias = smem + kStagesC * kStageBytesC;
+  uint8_t* ring_base = bias + kAtom;
+  HeaderC* hd = reinterpret_cast<HeaderC*>(ring_base + ring_bytes(128));
+  const int groups = p.seg[0].groups + (p.nseg > 1 ? p.seg[1].groups : 0);
+  const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+  volatile int* abort_flag = &hd->abort;
+  auto bar = [](uint64_t& b) { return smem_u32(&b); };
+
+  if (warp == 0) {
+    tmem_alloc(smem_u32(&hd->tmem), kTmemCols);
+    tmem_relinquish();
+  }
+  if (warp == kWorkers && lane == 0) {
+    for (int i = 0; i < kStagesC; ++i) {
+      mbar_init(bar(hd->full[i]), kWorkers);
+      mbar_init(bar(hd->empty[i]), 1);
+    }
+    for (int i = 0; i < 2; ++i) {
+      mbar_init(bar(hd->tfull[i]), 1);
+      mbar_init(bar(hd->tempty[i]), kWorkers);
+    }
+    mbar_init(bar(hd->drain), 1);
+    hd->abort = 0;
+    fence_mbarrier_init();
+  }
+  for (int i = threadIdx.x; i < kAtom / 16; i += kThreads)
+    reinterpret_cast<uint4*>(bias)[i] = make_uint4(0x88888888u, 0x88888888u, 0x88888888u, 0x88888888u);
+  fence_proxy_async_smem();
+  tc_fence_before();
+  __syncthreads();
+  tc_fence_after();
+  const uint32_t tmem = hd->tmem;
+
+  if (p.wait == kWaitWeights) pdl_wait();
+  pdl_release();
+  const GroupLists lists = group_lists(hd->lists, groups);
+  const int u0 = blockIdx.x;
+  const GroupPlan plan = plan_groups<kThreads>(
+      p, lists, hd->warp_sum,
+      [&](int si, int n) -> int64_t {
+        if (n <= p.most) return 0;
+        return static_cast<int64_t>((p.seg[si].blocks + kBlocks - 1) / kBlocks) *
+               ((n + kTokens - 1u) / kTokens);
+      },
+      [](int64_t) {},
+      [&](int pos, int64_t before, int64_t cost) {
+        if (before <= u0 && u0 < before + cost) hd->at_first = pos;
+      });
+  int pos = u0 < plan.total ? hd->at_first : 0;
+
+  if (warp < kWorkers) {
+    const int a_block = warp >> 1, a_half = warp & 1, g = lane >> 2, c = lane & 3;
+    const int piece = lane & 7, sub = 4 * warp + (lane >> 3);  // of b: tokens 64 k + sub
+    const int quarter = warp & 3, row = 32 * quarter + lane;   // of the sums
+    uint8_t* const ring = ring_base + warp * kDepth * kHalf;
+    bool ok = true;
+    int i = 0, seq = 0;
+    int slot = 0;               // stage of chunk i
+    int bslot = 0, bphase = 0;  // that of the chunk whose b is asked for next, its round's parity
+    int aslot = 0, aphase = 0;  // and those of the chunk whose sums are added next
+    for (int u = u0; u < plan.total && ok; u += gridDim.x, ++seq) {
+      const Unit x = unit_at<kTokens>(p, lists, plan, u, pos, kRec);
+      const Int4Segment& s = p.seg[x.seg];
+      const bool has_a = a_block < x.blocks;
+      const uint8_t* w = x.W + (has_a ? static_cast<int64_t>(a_block) * x.chunks * kRec : 0) +
+                         a_half * (kCodeBytes / 2) + lane * 16;
+      auto fetch = [&](int ch) {
+        if (has_a && ch < x.chunks) {
+          const uint32_t to = smem_u32(ring + (ch & (kDepth - 1)) * kHalf) + lane * 16;
+          const uint8_t* from = w + ch * kRec;
+          cp_async16(to, from);
+          if (lane < (kRec - kCodeBytes) / 16)
+            cp_async16(to + kCodeBytes / 2, from + kCodeBytes - a_half * (kCodeBytes / 2));
+        }
+      };
+#pragma unroll
+      for (int k = 0; k < kDepth - 1; ++k) fetch(k);
+      if (seq == 0 && p.wait == kWaitX) pdl_wait();
+      int rows[2];
+      {
+        const int t = 64 * (lane >> 2 & 1) + 4 * warp + (lane & 3);
+        const int64_t at = x.x_row + min(t, x.n - 1);
+        const int mine = static_cast<int>(s.perm ? s.perm[at] / s.perm_div : at);
+#pragma unroll
+        for (int k = 0; k < 2; ++k) rows[k] = __shfl_sync(0xffffffffu, mine, 4 * k + (lane >> 3));
+      }
+      // chunk ch's b and scales of x, as soon as its stage is free
+      auto ask = [&](int ch, int chunk) {
+        if (!mbar_wait_bounded(bar(hd->empty[bslot]), bphase ^ 1, abort_flag, p.status)) return false;
+        uint8_t* b = smem + bslot * kStageBytesC + kAtom;
+#pragma unroll
+        for (int k = 0; k < 2; ++k) {
+          const int t = 64 * k + sub;
+          if (t < x.n) {
+            const int64_t from = static_cast<int64_t>(rows[k]) * x.chunks + ch;
+            cp_async16(smem_u32(b) + t * 128 + ((piece ^ (t & 7)) << 4),
+                       static_cast<const uint8_t*>(s.x) + from * kChunk + piece * 16);
+            if (piece == 0)
+              asm volatile("cp.async.ca.shared.global [%0], [%1], 4;" ::"r"(
+                               smem_u32(&hd->f[chunk & (kFactorsC - 1)][t])),
+                           "l"(s.x_scale + from)
+                           : "memory");
+          }
+        }
+        if (++bslot == kStagesC) {
+          bslot = 0;
+          bphase ^= 1;
+        }
+        return true;
+      };
+      ok = ask(0, i);
+      if (!ok) break;
+      asm volatile("cp.async.commit_group;" ::: "memory");
+      const int cols = x.n > 64 ? 32 : 16, t0 = (warp >> 2) * cols;  // tokens of the sums
+      float weight = 1.0f;  // row weight of token t0 + lane
+      if (!kSwiglu && s.row_w && t0 + lane < x.n) weight = s.row_w[s.row_perm[x.out_row + t0 + lane]];
+      float acc[kTokens / 4];
+#pragma unroll
+      for (int j = 0; j < kTokens / 4; ++j) acc[j] = 0.0f;
+
+      // one step more than chunks: step ch makes chunk ch and adds chunk ch - 1
+      for (int ch = 0; ch <= x.chunks; ++ch) {
+        if (ch < x.chunks) {
+          const int fs = i & (kFactorsC - 1);
+          // what was asked for a step ago (b of this chunk, half record
+          // ch + kDepth - 2) has landed; then ask for the next
+          if (ch + 1 < x.chunks && !ask(ch + 1, i + 1)) {
+            ok = false;
+            break;
+          }
+          fetch(ch + kDepth - 1);
+          asm volatile("cp.async.commit_group;" ::: "memory");
+          asm volatile("cp.async.wait_group 1;" ::: "memory");
+          __syncwarp();
+          if (has_a) {
+            const uint8_t* rec = ring + (ch & (kDepth - 1)) * kHalf;
+            const uint4 v = *reinterpret_cast<const uint4*>(rec + lane * 16);
+            const uint32_t words[4] = {v.x, v.y, v.z, v.w};
+            uint8_t* to = smem + slot * kStageBytesC + (16 * a_block + g) * 128 + (c & 1) * 8;
+#pragma unroll
+            for (int k = 0; k < 2; ++k) {  // parts of 32 columns
+              uint32_t lo[2], hi[2];       // rows g and g + 8
+#pragma unroll
+              for (int j = 0; j < 2; ++j) {
+                const uint32_t q = words[2 * k + j];  // columns in the order 0, 2, 1, 3
+                lo[j] = __byte_perm(q & 0x0f0f0f0fu, 0, 0x3120);
+                hi[j] = __byte_perm((q >> 4) & 0x0f0f0f0fu, 0, 0x3120);
+              }
+              const int at = ((4 * a_half + 2 * k + (c >> 1)) ^ g) << 4;
+              *reinterpret_cast<uint2*>(to + at) = make_uint2(lo[0], lo[1]);
+              *reinterpret_cast<uint2*>(to + 8 * 128 + at) = make_uint2(hi[0], hi[1]);
+            }
+            if (a_half == 0 && c == 0) {
+              const uint32_t sc = *reinterpret_cast<const uint32_t*>(rec + kCodeBytes / 2 + g * 4);
+              hd->r[fs][16 * a_block + g] = __uint_as_float(sc << 16) * 512.0f;
+              hd->r[fs][16 * a_block + g + 8] = __uint_as_float(sc & 0xffff0000u) * 512.0f;
+            }
+          }
+          fence_proxy_async_smem();  // the tensor cores read the operands next
+          __syncwarp();
+          if (lane == 0) mbar_arrive(bar(hd->full[slot]));
+          if (++slot == kStagesC) slot = 0;
+          ++i;
+        }
+        if (ch > 0) {
+          const int k = i - (ch < x.chunks ? 2 : 1), buf = k & 1, fs = k & (kFactorsC - 1);
+          // (the operands were full before; that wait is for f and r)
+          if (!mbar_wait_bounded(bar(hd->tfull[buf]), k >> 1 & 1, abort_flag, p.status) ||
+              !mbar_wait_bounded(bar(hd->full[aslot]), aphase, abort_flag, p.status)) {
+            ok = false;
+            break;
+          }
+          if (++aslot == kStagesC) {
+            aslot = 0;
+            aphase ^= 1;
+          }
+          __syncwarp();
+          tc_fence_after();
+          const float r = hd->r[fs][row];
+          const float4* f = reinterpret_cast<const float4*>(hd->f[fs] + t0);
+          const uint32_t from = tmem + buf * kTokens + t0 + (static_cast<uint32_t>(32 * quarter) << 16);
+#pragma unroll
+          for (int b = 0; b < 2; ++b) {
+            if (16 * b < cols) {
+              uint32_t v[16];
+              tmem_ld_x16(from + 16 * b, v);
+              tmem_ld_wait(v);
+#pragma unroll
+              for (int j = 0; j < 4; ++j) {
+                const float4 q = f[4 * b + j];
+                float* o = acc + 16 * b + 4 * j;
+                o[0] = fmaf(q.x * r, __uint_as_float(v[4 * j + 0]), o[0]);
+                o[1] = fmaf(q.y * r, __uint_as_float(v[4 * j + 1]), o[1]);
+                o[2] = fmaf(q.z * r, __uint_as_float(v[4 * j + 2]), o[2]);
+                o[3] = fmaf(q.w * r, __uint_as_float(v[4 * j + 3]), o[3]);
+              }
+            }
+          }
+          tc_fence_before();
+          __syncwarp();
+          if (lane == 0) mbar_arrive(bar(hd->tempty[buf]));
+        }
+      }
+      if (!ok) break;
+      write_unit<kSwiglu>(s, x, acc, weight, t0, cols, row, lane);
+    }
+    asm volatile("cp.async.wait_all;" ::: "memory");
+  } else {
+    if (lane == 0) {
+      int slot = 0, phase = 0, i = 0;
+      bool ok = true;
+      for (int u = u0; ok && u < plan.total; u += gridDim.x) {
+        const Unit x = unit_at<kTokens>(p, lists, plan, u, pos, kRec);
+        // both formats E4M3 (0): the bits are those of the f16 descriptor
+        const uint32_t idesc = idesc_f16_f32(x.n > 64 ? 128 : 64);
+        for (int ch = 0; ch < x.chunks; ++ch, ++i) {
+          if (!mbar_wait_bounded(bar(hd->tempty[i & 1]), (i >> 1 & 1) ^ 1, abort_flag, p.status) ||
+              !mbar_wait_bounded(bar(hd->full[slot]), phase, abort_flag, p.status)) {
+            ok = false;
+            break;
+          }
+          tc_fence_after();
+          const uint32_t st = smem_u32(smem + slot * kStageBytesC), d = tmem + (i & 1) * kTokens;
+          const uint64_t a = smem_desc_sw128(st), b = smem_desc_sw128(st + kAtom);
+          const uint64_t minus = smem_desc_sw128(smem_u32(bias));
+#pragma unroll
+          for (int kk = 0; kk < 4; ++kk) {
+            tc_mma_e4m3(d, minus, b + 2u * kk, idesc, kk != 0);
+            tc_mma_e4m3(d, a + 2u * kk, b + 2u * kk, idesc, 1);
+          }
+          tc_commit(bar(hd->empty[slot]));
+          tc_commit(bar(hd->tfull[i & 1]));
+          if (++slot == kStagesC) {
+            slot = 0;
+            phase ^= 1;
+          }
+        }
+      }
+      // nothing is in flight when the CTA gives its TMEM back
+      tc_commit(bar(hd->drain));
+      int own_abort = 0;
+      mbar_wait_bounded(bar(hd->drain), 0, &own_abort, p.status);
+    }
+    __syncwarp();
+  }
+  if (p.wait != kWaitWeights) pdl_wait();  // a kernel ends after the one before it has
+  tc_fence_before();
+  __syncthreads();
+  if (warp == 0) {
+    tc_fence_after();
+    tmem_dealloc(tmem, kTmemCols);
+  }
+}
+
 template <typename Kernel>
 cudaError_t launch_kernel(Kernel kernel, const Int4Launch& p, int threads, int num_sms,
                           cudaStream_t stream) {
@@ -774,7 +1069,7 @@ cudaError_t launch_kernel(Kernel kernel, const Int4Launch& p, int threads, int n
 }
 
 // Rows of a group up to which it is read by gemv_int4.cu.
-constexpr int kGemvRows = 16;
+constexpr int kGemvRows = 40;
 
 }  // namespace
 
@@ -784,18 +1079,28 @@ cudaError_t launch_gemm_int4(const Int4Launch& p, bool swiglu, int group, int nu
   int groups = 0;
   for (int i = 0; i < p.nseg; ++i) groups += p.seg[i].groups;
   if (p.seg[0].x_scale) {
+    if (group == 128) {
+      l.smem = smem_bytes_c(groups);
+      return launch_kernel(swiglu ? gemm_int4_bytes_kernel<true> : gemm_int4_bytes_kernel<false>, l,
+                           kThreads, num_sms, stream);
+    }
     l.smem = smem_bytes(groups, group);
-    return launch_kernel(swiglu ? group == 32 ? gemm_int4_kernel<true, true, 32>
-                                              : gemm_int4_kernel<true, true, 128>
-                         : group == 32 ? gemm_int4_kernel<false, true, 32>
-                                       : gemm_int4_kernel<false, true, 128>,
+    return launch_kernel(swiglu ? gemm_int4_fp8_kernel<true, 32> : gemm_int4_fp8_kernel<false, 32>,
                          l, kThreads, num_sms, stream);
   }
-  l.smem = smem_bytes_b(groups, group);
-  return launch_kernel(swiglu ? group == 32 ? gemm_int4_bf16_kernel<true, 32>
-                                            : gemm_int4_bf16_kernel<true, 128>
-                       : group == 32 ? gemm_int4_bf16_kernel<false, 32>
-                                     : gemm_int4_bf16_kernel<false, 128>,
+  bool small = true;
+  for (int i = 0; i < p.nseg; ++i) small = small && p.seg[i].rows <= 64;
+  l.smem = smem_bytes_b(small ? 64 : 128, groups, group);
+  if (small)
+    return launch_kernel(swiglu ? group == 32 ? gemm_int4_bf16_kernel<true, 32, 64>
+                                              : gemm_int4_bf16_kernel<true, 128, 64>
+                         : group == 32 ? gemm_int4_bf16_kernel<false, 32, 64>
+                                       : gemm_int4_bf16_kernel<false, 128, 64>,
+                         l, kThreadsB, num_sms, stream);
+  return launch_kernel(swiglu ? group == 32 ? gemm_int4_bf16_kernel<true, 32, 128>
+                                            : gemm_int4_bf16_kernel<true, 128, 128>
+                       : group == 32 ? gemm_int4_bf16_kernel<false, 32, 128>
+                                     : gemm_int4_bf16_kernel<false, 128, 128>,
                        l, kThreadsB, num_sms, stream);
 }
 
