@@ -107,6 +107,20 @@ __device__ __forceinline__ GroupPlan plan_groups(const Int4Launch& p, const Grou
   static_assert(kMaxGroups < 1 << kCountBits, "");
   const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
   const int n0 = p.seg[0].groups, groups = n0 + (p.nseg > 1 ? p.seg[1].groups : 0);
+  if (groups == 1 && !p.seg[0].offsets) {  // a linear map: nothing to scan
+    GroupPlan one;
+    one.total = cost(0, static_cast<int>(p.seg[0].rows));
+    one.present = one.total > 0;
+    with(one.total);
+    if (tid == 0 && one.present) {
+      l.before[0] = 0;
+      l.before[1] = one.total;
+      l.number[0] = 0;
+      place(0, static_cast<int64_t>(0), one.total);
+    }
+    __syncthreads();
+    return one;
+  }
   int64_t mine[kPer], sum = 0;
 #pragma unroll
   for (int i = 0; i < kPer; ++i) {
