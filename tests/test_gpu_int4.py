@@ -373,3 +373,28 @@ def test_host_forward_takes_the_layout():
     torch.cuda.synchronize()
     fgs.moe_layer_forward_host_release(ws)
     assert torch.equal(y.cpu(), yh)
+
+
+@pytest.mark.parametrize("rows8", [False, True])
+@pytest.mark.parametrize("T,L,S,group", [(1, 0, 1, 32), (5, 0, 2, 128), (50, 256, 2, 32),
+                                         (60, 0, 1, 128), (3, 256, 0, 32)])
+def test_decode_block(T, L, S, group, rows8):
+    """The norm, router, experts and combine of run_decode together against
+    its plain fp32 form."""
+    need_gpu()
+    lib()
+    from fine_grained_sparse_gb300.run_decode import Block, plain_block
+    shape = synth.custom(name="block", T=T, d_model=512, E_routed=16, K=4, E_shared=S, d_ff=256,
+                         d_ff_shared=128 if S else 0, d_latent=L)
+    b = Block(shape, T, group, rows8, keep=True)
+    g = torch.Generator(device="cuda").manual_seed(T)
+    attn, res = (torch.randn((T, 512), generator=g, device="cuda").bfloat16() for _ in range(2))
+    h, y = b(attn, res)
+    ph, py = plain_block(b, attn, res)
+    # h: one bf16 rounding, 2^-8.  y, as norms over all elements: independent
+    # roundings of x (bf16, or E4M3's 2^-4), the latent rows, H, Y, the routed
+    # sum and y; a unit of 2^-p is an error of at most 2^-p / sqrt(3) of an
+    # element in the mean, which SwiGLU's two factors at most double
+    assert float((h.float() - ph).norm() / ph.norm()) <= 2.0 ** -8
+    u = np.sqrt((2 * (2.0 ** -4 if rows8 else 2.0 ** -8)) ** 2 + 6 * (2.0 ** -8) ** 2) / np.sqrt(3)
+    assert float((y.float() - py).norm() / py.norm()) <= u
