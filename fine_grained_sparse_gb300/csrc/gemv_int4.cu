@@ -33,16 +33,23 @@ __global__ void pack_int4_kernel(const uint8_t* __restrict__ codes,
     return grp * rows + (r < 8 ? 0 : half) + block * 8 + (r & 7);
   };
   uint8_t* out = dst + rec * record_bytes(group);
-  for (int i = 0; i < 8; ++i) {
-    uint32_t w = 0;
-    for (int j = 0; j < 4; ++j) {
-      const int64_t row = src_row(g + 8 * (j & 1));
-      const int64_t col = chunk * kChunk + 32 * (i >> 1) + 8 * c + 4 * (i & 1) + 2 * (j >> 1);
-      const uint32_t b = codes[(row * cols + col) >> 1];
-      w |= (b & 15u) << (4 * j) | (b >> 4) << (4 * j + 16);
+  uint32_t words[8];
+#pragma unroll
+  for (int kk = 0; kk < 4; ++kk) {  // 32 columns, eight of them a lane's
+    const int64_t at = chunk * kChunk + 32 * kk + 8 * c;
+    const uint32_t v0 = *reinterpret_cast<const uint32_t*>(codes + (src_row(g) * cols + at) / 2);
+    const uint32_t v1 = *reinterpret_cast<const uint32_t*>(codes + (src_row(g + 8) * cols + at) / 2);
+#pragma unroll
+    for (int h = 0; h < 2; ++h) {
+      // four codes of a row from 16 bits to bits 0, 16, 8 and 24
+      const uint32_t a = v0 >> (16 * h), b = v1 >> (16 * h);
+      words[2 * kk + h] = (a & 0x0f0fu) | (a & 0xf0f0u) << 12 |
+                          ((b & 0x0f0fu) | (b & 0xf0f0u) << 12) << 4;
     }
-    *reinterpret_cast<uint32_t*>(out + (i >> 2) * 512 + lane * 16 + (i & 3) * 4) = w;
   }
+  *reinterpret_cast<uint4*>(out + lane * 16) = make_uint4(words[0], words[1], words[2], words[3]);
+  *reinterpret_cast<uint4*>(out + 512 + lane * 16) =
+      make_uint4(words[4], words[5], words[6], words[7]);
   // scales: per g, the groups of row g and then those of row g + 8
   const int per = kChunk / group;
   __nv_bfloat16* so = reinterpret_cast<__nv_bfloat16*>(out + kCodeBytes);
