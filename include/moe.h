@@ -113,12 +113,15 @@ typedef enum moe_router_weight_form {
  *   MOE_WEIGHTS_PACKED_INT4_G32, MOE_WEIGHTS_PACKED_INT4_G128: the routed and
  *     shared experts' W_gate_up and W_down are 4-bit codes with one bf16
  *     scale per 32 (128) columns of a row, packed by moe_pack_weights_int4;
- *     the latent projections stay bf16, packed by moe_pack_weights.  A decode
- *     form: its passes are bound by reading the weights up to about 16 rows
- *     an expert, and for larger batches the bf16 or FP8 form is faster.
+ *     the latent projections stay bf16, packed by moe_pack_weights.  Made for
+ *     decode: experts with up to 40 rows are bound by reading their weights
+ *     (once for every eight rows), larger ones run on the tensor cores, where
+ *     each unit of 128 weight rows and up to 128 tokens converts its weights
+ *     anew; for prefill the bf16 form is faster.
  *     Needs bf16 activations and d_model, d_ff, d_ff_shared, d_latent
- *     multiples of 128 and at most 32768.  The weights enter the tensor cores exactly (code - 8
- *     as bf16 or f16) and the scales are applied in fp32. */
+ *     multiples of 128 and at most 32768.  The weights enter the tensor cores
+ *     exactly ((code - 8) scale as f16 or two bf16 values, or code - 8 with
+ *     the scale applied in fp32) and sums are fp32. */
 typedef enum moe_weight_layout {
   MOE_WEIGHTS_NATURAL = 0,
   MOE_WEIGHTS_PACKED = 1,
@@ -433,8 +436,9 @@ int32_t moe_linear(int64_t T, int32_t in_features, int32_t out_features, const v
  *   [T, in / 128] fp32 (value (t, c) = code value * x_scale[t][c / 128]),
  *   W packed by moe_pack_weights_int4(MOE_PACK_PLAIN, 1, out, in,
  *   group_size), add [T, out] bf16 or NULL, y [T, out] bf16 (y may be add).
- * in a multiple of 128, at most 32768, out one of 16; group_size 32 or 128.  Sums in fp32, one
- * rounding to bf16.  Needs no workspace. */
+ * in a multiple of 128, at most 32768, out one of 16; group_size 32 or 128.
+ * Sums in fp32, one rounding to bf16.  Needs no workspace; a bounded device
+ * wait that expires (T > 40) is not reported by this entry point. */
 int32_t moe_linear_int4(int64_t T, int32_t in_features, int32_t out_features, int32_t group_size,
                         const void* x, const float* x_scale, const void* W, const void* add,
                         void* y, void* stream);

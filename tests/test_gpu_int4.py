@@ -398,3 +398,57 @@ def test_decode_block(T, L, S, group, rows8):
     assert float((h.float() - ph).norm() / ph.norm()) <= 2.0 ** -8
     u = np.sqrt((2 * (2.0 ** -4 if rows8 else 2.0 ** -8)) ** 2 + 6 * (2.0 ** -8) ** 2) / np.sqrt(3)
     assert float((y.float() - py).norm() / py.norm()) <= u
+
+
+@pytest.mark.parametrize("rows8", [False, True])
+def test_calls_in_a_captured_graph(rows8):
+    """The calls enqueue nothing but kernels: they can be captured, and every
+    replay reads what its inputs hold then."""
+    need_gpu()
+    fgs = lib()
+    gen = _gen(21)
+    shape = dict(T=50, d=256, F=128, E=6, K=2)
+    T, d, F, E, K = shape.values()
+    cfg = fgs.config(d_model=d, d_ff=F, E_routed=E, K=K, weight_layout=3)
+    gu, dn = (fgs.pack_int4(kind, *[t.cuda() for t in bank(gen, E, r, c, 32)])
+              for kind, r, c in ((0, 2 * F, d), (1, d, F)))
+    W = fgs.pack_int4(1, *[t.cuda() for t in bank(gen, 1, 96, d, 32)])
+    x, xs, _ = _rows(gen, T, d, rows8)
+    ws, nws = workspace(cfg, T)
+    i32 = lambda n: torch.empty(n, dtype=torch.int32, device="cuda")  # noqa: E731
+    counts, offsets, perm, inv = i32(E), i32(E + 1), i32(T * K), i32(T * K)
+    idx = torch.as_tensor(_random_idx(T, E, K, 5), dtype=torch.int32, device="cuda")
+    Y, y = (torch.zeros(s, dtype=torch.bfloat16, device="cuda") for s in ((T * K, d), (T, 96)))
+
+    def step():
+        fgs.moe_permute(cfg, T, idx, counts, offsets, perm, inv, ws, nws)
+        if rows8:
+            fgs.moe_grouped_swiglu_fp8_rows(cfg, T, x, xs, offsets, perm, None, gu, dn, None, None,
+                                            None, None, Y, None, ws, nws)
+        else:
+            fgs.moe_grouped_swiglu(cfg, T, x, offsets, perm, None, gu, dn, None, None, None, Y,
+                                   None, ws, nws)
+        fgs.moe_linear_int4(T, d, 96, 32, x, xs, W, None, y)
+
+    step()
+    torch.cuda.synchronize()
+    first = (Y.clone(), y.clone())
+    side = torch.cuda.Stream()
+    with torch.cuda.stream(side):
+        step()
+    torch.cuda.synchronize()
+    graph = torch.cuda.CUDAGraph()
+    with torch.cuda.graph(graph):
+        step()
+    Y.zero_(), y.zero_()
+    graph.replay()
+    torch.cuda.synchronize()
+    assert torch.equal(Y, first[0]) and torch.equal(y, first[1])
+    new = torch.as_tensor(_random_idx(T, E, K, 6), dtype=torch.int32, device="cuda")
+    idx.copy_(new)
+    graph.replay()
+    torch.cuda.synchronize()
+    again = Y.clone()
+    step()
+    torch.cuda.synchronize()
+    assert torch.equal(Y, again) and not torch.equal(Y, first[0])
