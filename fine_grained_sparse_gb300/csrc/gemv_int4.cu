@@ -247,9 +247,10 @@ __device__ __forceinline__ void store_block(const Int4Segment& s, const Tile& T,
 // are exact.  Pieces of a row are moved within 128 bytes by the row's number
 // (16-byte piece q of a chunk to q ^ 4 (t & 1)), so that a fragment load of
 // eight tokens meets every bank once.
-template <bool kX8>
+// between() runs after the first loads have been asked for.
+template <bool kX8, typename Between>
 __device__ __forceinline__ void load_x(const Int4Segment& s, const Tile& T, uint8_t* smem,
-                                       uint32_t xo, uint32_t fo, float* row_w) {
+                                       uint32_t xo, uint32_t fo, float* row_w, Between between) {
   const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
   const int n = T.n, chunks = s.chunks, piece = lane & 15;
   int64_t src = 0;
@@ -281,6 +282,7 @@ __device__ __forceinline__ void load_x(const Int4Segment& s, const Tile& T, uint
                                                (from * chunks + ch) * kChunk + piece * 8);
       }
     }
+    if (base == 2 * warp) between();
 #pragma unroll
     for (int u = 0; u < kAhead; ++u) {
       const int task = base + 2 * kWarps * u + (lane >> 4);
@@ -301,6 +303,7 @@ __device__ __forceinline__ void load_x(const Int4Segment& s, const Tile& T, uint
       }
     }
   }
+  if (2 * warp >= tasks) between();
   if (weigher) row_w[lane] = s.row_w[pair];
 }
 
@@ -332,13 +335,18 @@ __device__ __forceinline__ void run_tile(const Int4Segment& s, const Tile& T, ui
     if (lane < (kRec - kCodeBytes) / 16) cp_async16(to + kCodeBytes, w + at + kCodeBytes);
     asm volatile("cp.async.commit_group;" ::: "memory");
   };
-  if (wait == kWaitWeights) pdl_wait();
-  if (count > 0) {
+  auto begin = [&]() {
+    if (count > 0) {
 #pragma unroll
-    for (int u = 0; u < kDepth - 1; ++u) fetch(ring + u * kRec, min(u * kRec, last));
-  }
-  if (wait == kWaitX) pdl_wait();
-  load_x<kX8>(s, T, smem, xo, fo, hd->row_w);
+      for (int u = 0; u < kDepth - 1; ++u) fetch(ring + u * kRec, min(u * kRec, last));
+    }
+  };
+  // the weights first if x is still to come, else the first loads of x
+  if (wait == kWaitX) begin();
+  if (wait != kWaitNone) pdl_wait();
+  load_x<kX8>(s, T, smem, xo, fo, hd->row_w, [&]() {
+    if (wait != kWaitX) begin();
+  });
   __syncthreads();
 
   int block = a < (1ll << 31) ? static_cast<int>(static_cast<uint32_t>(a) / static_cast<uint32_t>(nch))
