@@ -311,8 +311,8 @@ __device__ __forceinline__ void load_x(const Int4Segment& s, const Tile& T, uint
 // sequence; a block cut by a warp boundary is summed from its pieces, in
 // warp order, by the first warp that starts inside it.
 template <bool kSwiglu, bool kX8, int kGroup>
-__device__ __forceinline__ void run_tile(const Int4Segment& s, const Tile& T, uint8_t* smem,
-                                         int header, int wait) {
+__device__ __forceinline__ void run_tile(const Int4Segment& s, const Divisor& by_chunks,
+                                         const Tile& T, uint8_t* smem, int header, int wait) {
   constexpr int kRec = record_bytes(kGroup);
   Header* hd = reinterpret_cast<Header*>(smem);
   const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5, g = lane >> 2, c = lane & 3;
@@ -349,7 +349,7 @@ __device__ __forceinline__ void run_tile(const Int4Segment& s, const Tile& T, ui
   });
   __syncthreads();
 
-  int block = a < (1ll << 31) ? static_cast<int>(static_cast<uint32_t>(a) / static_cast<uint32_t>(nch))
+  int block = a < (1ll << 31) ? static_cast<int>(divide(static_cast<uint32_t>(a), by_chunks))
                               : static_cast<int>(a / nch);
   int ch = static_cast<int>(a - static_cast<int64_t>(block) * nch);
   const int inside = ch, begun = block;  // where in its block the warp starts
@@ -419,11 +419,11 @@ __device__ __forceinline__ void run_tile(const Int4Segment& s, const Tile& T, ui
 }
 
 // ceil(x / d) within [0, most]
-__device__ __forceinline__ int blocks_before(int64_t x, int d, int most) {
+__device__ __forceinline__ int blocks_before(int64_t x, const Divisor& d, int most) {
   if (x <= 0) return 0;
-  if (x >= static_cast<int64_t>(d) * most) return most;
-  if (x < (1ll << 31)) return static_cast<int>((static_cast<uint32_t>(x) + d - 1) / d);
-  return static_cast<int>((x + d - 1) / d);
+  if (x >= static_cast<int64_t>(d.d) * most) return most;
+  if (x < (1ll << 31)) return static_cast<int>(divide(static_cast<uint32_t>(x) + d.d - 1, d));
+  return static_cast<int>((x + d.d - 1) / d.d);
 }
 
 // Blocks (of every tile of every group, in order) are dealt to the CTAs by
@@ -449,11 +449,11 @@ __global__ void __launch_bounds__(kThreads, 1) gemv_int4_kernel(const __grid_con
       p, lists, hd->warp_sum,
       [&](int si, int n) -> int64_t {
         if (n <= 0 || n > p.most) return 0;
-        return (static_cast<int64_t>(p.seg[si].blocks) * p.seg[si].chunks + kTileCost) *
-               ((n + p.cap[si] - 1u) / p.cap[si]);
+        const int64_t tile = static_cast<int64_t>(p.seg[si].blocks) * p.seg[si].chunks + kTileCost;
+        return n <= p.cap[si] ? tile : tile * ((n + p.cap[si] - 1u) / p.cap[si]);
       },
       [&](int64_t total) {
-        const int64_t share = total < (1ll << 32) ? static_cast<uint32_t>(total) / gridDim.x
+        const int64_t share = total < (1ll << 32) ? divide(static_cast<uint32_t>(total), p.ctas)
                                                   : total / gridDim.x;
         const int rest = static_cast<int>(total - share * gridDim.x), cta = blockIdx.x;
         lo = share * cta + min(cta, rest);
@@ -471,13 +471,13 @@ __global__ void __launch_bounds__(kThreads, 1) gemv_int4_kernel(const __grid_con
     const int grp = si ? k - n0 : k;
     const int row = s.offsets ? lists.first[k] : 0;
     const int n = s.offsets ? lists.first[k + 1] - row : static_cast<int>(s.rows);
-    const int tiles = (n + p.cap[si] - 1u) / p.cap[si];
+    const int tiles = n <= p.cap[si] ? 1 : (n + p.cap[si] - 1u) / p.cap[si];
     const int64_t tile_cost = static_cast<int64_t>(s.blocks) * s.chunks + kTileCost;
     int t = tiles > 1 && lo > before ? static_cast<int>((lo - before) / tile_cost) : 0;
     for (; t < tiles; ++t) {
       const int64_t base = before + t * tile_cost + kTileCost;
-      const int r0 = blocks_before(lo - base, s.chunks, s.blocks);
-      const int r1 = blocks_before(hi - base, s.chunks, s.blocks);
+      const int r0 = blocks_before(lo - base, p.chunks[si], s.blocks);
+      const int r1 = blocks_before(hi - base, p.chunks[si], s.blocks);
       if (r1 == 0) break;
       if (r0 >= r1) continue;
       const int row0 = tiles > 1 ? static_cast<int>(static_cast<int64_t>(n) * t / tiles) : 0;
@@ -488,7 +488,7 @@ __global__ void __launch_bounds__(kThreads, 1) gemv_int4_kernel(const __grid_con
       T.n = (tiles > 1 ? static_cast<int>(static_cast<int64_t>(n) * (t + 1) / tiles) : n) - row0;
       T.out_row = row0 + (s.offsets ? row : grp * s.out_group_rows);
       T.x_row = row0 + (s.offsets ? row : grp * s.x_group_rows);
-      run_tile<kSwiglu, kX8, kGroup>(s, T, smem, header, wait);
+      run_tile<kSwiglu, kX8, kGroup>(s, p.chunks[si], T, smem, header, wait);
       wait = kWaitNone;
       __syncthreads();  // shared memory is free for the next tile
     }
@@ -541,8 +541,10 @@ cudaError_t launch_gemv_int4(const Int4Launch& p, bool swiglu, int group, int nu
   int groups = 0;
   for (int i = 0; i < p.nseg; ++i) groups += p.seg[i].groups;
   l.smem = 0;
+  l.ctas = divisor(num_sms);
   for (int i = 0; i < p.nseg; ++i) {
     const Int4Segment& s = p.seg[i];
+    l.chunks[i] = divisor(s.chunks);
     l.cap[i] = tile_cap(groups, s.chunks, group);
     if (l.cap[i] < 1) return cudaErrorInvalidValue;  // the callers' limit on the width
     if (s.rows < l.cap[i]) l.cap[i] = static_cast<int>(s.rows);

@@ -52,6 +52,21 @@ __device__ __forceinline__ void cp_async16(uint32_t dst, const void* src) {
   asm volatile("cp.async.cg.shared.global [%0], [%1], 16;" ::"r"(dst), "l"(src) : "memory");
 }
 
+// Division of 32-bit numbers by one known to the host, as a product with
+// inv = ceil(2^64 / d): exact for every 32-bit x.  (A launch of a few
+// microseconds notices the divisions of its beginning.)
+struct Divisor {
+  uint32_t d;
+  uint64_t inv;
+};
+inline Divisor divisor(uint32_t d) { return {d, d > 1 ? ~0ull / d + 1 : 0}; }
+__device__ __forceinline__ uint32_t divide(uint32_t x, const Divisor& by) {
+  if (by.d == 1) return x;
+  const uint64_t high = static_cast<uint64_t>(x) * static_cast<uint32_t>(by.inv >> 32);
+  const uint64_t low = static_cast<uint64_t>(x) * static_cast<uint32_t>(by.inv);
+  return static_cast<uint32_t>((high + (low >> 32)) >> 32);
+}
+
 // What waits for the end of the kernel before this one: nothing, a tile's x,
 // or its weights (and routing) too.
 enum { kWaitNone = 0, kWaitX = 1, kWaitWeights = 2 };
@@ -62,6 +77,7 @@ struct Int4Launch {
   int most;    // gemv: groups of more rows are left to gemm; gemm: those of no more to gemv
   int wait;    // kWait...
   int cap[2];  // gemv: tokens of a tile
+  Divisor chunks[2], ctas;  // gemv: seg[i].chunks, the CTAs
   int smem;    // bytes of shared memory
   int* status; // device status word, or null
 };
