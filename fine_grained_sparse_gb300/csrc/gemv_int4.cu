@@ -366,7 +366,7 @@ __device__ __forceinline__ void run_tile(const Int4Segment& s, const Divisor& by
   const uint32_t first_slot = so + warp * kSlotBytes;  // a piece that began inside its block
   uint32_t rd = ring, wr = ring + (kDepth - 1) * kRec;
   int ahead = (kDepth - 1) * kRec;
-#pragma unroll 1
+#pragma unroll 2
   for (int i = 0; i < count; ++i) {
     asm volatile("cp.async.wait_group %0;" ::"n"(kDepth - 2) : "memory");
     __syncwarp();  // the record is there, and the one before it was read by all
