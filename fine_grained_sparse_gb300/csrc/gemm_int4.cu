@@ -158,6 +158,19 @@ __device__ __forceinline__ uint32_t idesc_f16_f32(uint32_t n) {
   return (1u << 4) | ((n >> 3) << 17) | ((128u >> 4) << 24);
 }
 
+// o[i] += (f[i] r) v[i] for four tokens, two to an instruction.
+__device__ __forceinline__ void add_scaled4(float* o, float4 f, float r, const uint32_t* v) {
+  asm("{\n\t.reg .b64 a, b, x, y, s, t, u;\n\t"
+      "mov.b64 a, {%0, %1};\n\tmov.b64 b, {%2, %3};\n\t"
+      "mov.b64 s, {%4, %5};\n\tmov.b64 t, {%6, %7};\n\tmov.b64 u, {%8, %8};\n\t"
+      "mov.b64 x, {%9, %10};\n\tmov.b64 y, {%11, %12};\n\t"
+      "mul.rn.f32x2 s, s, u;\n\tmul.rn.f32x2 t, t, u;\n\t"
+      "fma.rn.f32x2 a, s, x, a;\n\tfma.rn.f32x2 b, t, y, b;\n\t"
+      "mov.b64 {%0, %1}, a;\n\tmov.b64 {%2, %3}, b;\n\t}"
+      : "+f"(o[0]), "+f"(o[1]), "+f"(o[2]), "+f"(o[3])
+      : "f"(f.x), "f"(f.y), "f"(f.z), "f"(f.w), "f"(r), "r"(v[0]), "r"(v[1]), "r"(v[2]), "r"(v[3]));
+}
+
 // A unit's outputs from the sums of row `row` and tokens t0 .. t0 + cols - 1
 // (cols 16 or 32); weight: the row weight of token t0 + lane.
 template <bool kSwiglu>
@@ -366,14 +379,8 @@ __global__ void __launch_bounds__(kThreads, 1) gemm_int4_fp8_kernel(const __grid
               tmem_ld_x16(from + 16 * b, v);
               tmem_ld_wait(v);
 #pragma unroll
-              for (int j = 0; j < 4; ++j) {
-                const float4 k = f[4 * b + j];
-                float* o = acc + 16 * b + 4 * j;
-                o[0] = fmaf(k.x * r, __uint_as_float(v[4 * j + 0]), o[0]);
-                o[1] = fmaf(k.y * r, __uint_as_float(v[4 * j + 1]), o[1]);
-                o[2] = fmaf(k.z * r, __uint_as_float(v[4 * j + 2]), o[2]);
-                o[3] = fmaf(k.w * r, __uint_as_float(v[4 * j + 3]), o[3]);
-              }
+              for (int j = 0; j < 4; ++j)
+                add_scaled4(acc + 16 * b + 4 * j, f[4 * b + j], r, v + 4 * j);
             }
           }
           tc_fence_before();
@@ -991,14 +998,8 @@ __global__ void __launch_bounds__(kThreads, 1)
               tmem_ld_x16(from + 16 * b, v);
               tmem_ld_wait(v);
 #pragma unroll
-              for (int j = 0; j < 4; ++j) {
-                const float4 q = f[4 * b + j];
-                float* o = acc + 16 * b + 4 * j;
-                o[0] = fmaf(q.x * r, __uint_as_float(v[4 * j + 0]), o[0]);
-                o[1] = fmaf(q.y * r, __uint_as_float(v[4 * j + 1]), o[1]);
-                o[2] = fmaf(q.z * r, __uint_as_float(v[4 * j + 2]), o[2]);
-                o[3] = fmaf(q.w * r, __uint_as_float(v[4 * j + 3]), o[3]);
-              }
+              for (int j = 0; j < 4; ++j)
+                add_scaled4(acc + 16 * b + 4 * j, f[4 * b + j], r, v + 4 * j);
             }
           }
           tc_fence_before();
