@@ -1,16 +1,31 @@
 // Products of more than a few rows with 4-bit weights, on the tensor cores
 // (tcgen05): the groups that gemv_int4.cu leaves.  128 weight rows by up to
-// 128 tokens a unit,
+// 128 tokens a unit, in one of three forms:
+//
+//  bf16 rows            gemm_int4_bf16_kernel   weights as two bf16 values,
+//                       sums over all of K in TMEM
+//  E4M3 rows, groups    gemm_int4_bytes_kernel  both operands stay bytes, a
+//  of 128               chunk's sums are scaled in fp32
+//  E4M3 rows, groups    gemm_int4_fp8_kernel    both operands f16, a chunk's
+//  of 32                sums are scaled in fp32
+//
+// All products are exact.  What bounds all three is making the first operand:
+// a block of 128 x 128 weights is 16 to 18 KB of HBM, but some 4500 warp
+// instructions from codes to swizzled operand to sums (with bf16 rows, 96
+// tokens and 17 experts' groups of which 11 come here: 4520 at 2.5 a cycle and
+// SM, tensor pipe 39% active, shared-memory pipe 47%).  It is made once for
+// all of a unit's tokens, so the form pays from kGemvRows rows on.
+//
+// The f16 form is written down here, the others where they begin:
 //
 //   z[t, o] = sum over chunks of 128 columns of f[t] r[o] sum_k a[o, k] b[t, k]
 //
 // where b is the chunk of x as f16 with its factor f (as in gemv_int4.cu) and
-// a the weights as f16: for groups of 128 the codes c - 8 themselves with r
-// the scale, for groups of 32 (c - 8) s 2^-e with r = 2^e, e the exponent of
-// the largest of the row's four scales.  Both are exact: c - 8 has at most
-// three significant bits, or is the power of two -8, and s eight, which an f16
-// holds together (for scales down to 2^-28 of the largest).  A chunk's sum
-// goes from TMEM to fp32 registers, which is where f and r are applied.
+// a the weights as f16, (c - 8) s 2^-e with r = 2^e, e the exponent of the
+// largest of the row's four scales.  c - 8 has at most three significant
+// bits, or is the power of two -8, and s eight, which an f16 holds together
+// (for scales down to 2^-28 of the largest).  A chunk's sum goes from TMEM to
+// fp32 registers, which is where f and r are applied.
 #include "int4.cuh"
 
 namespace fgs {
@@ -97,32 +112,25 @@ __device__ __forceinline__ Unit unit_at(const Int4Launch& p, const GroupLists& l
 // and row + 8, row = 16 w + g), and the rows' scales r.  Lanes of odd g take
 // the half's two 32-column parts in the other order, which puts the rows that
 // are stored together on different banks.
-template <int kGroup>
 __device__ __forceinline__ void make_a(const uint8_t* rec, uint8_t* to, int row, int h, int lane,
                                        float& r0, float& r1) {
   const int g = lane >> 2, c = lane & 3, odd = g & 1;
   const uint8_t* scales = rec + kCodeBytes / 2;
   uint32_t s0[2], s1[2];  // scales of rows g and g + 8 in the order of the parts, f16 pairs
-  if (kGroup == 128) {
-    const uint32_t sc = *reinterpret_cast<const uint32_t*>(scales + g * 4);
-    r0 = __uint_as_float(sc << 16);
-    r1 = __uint_as_float(sc & 0xffff0000u) * 0.0625f;  // row g + 8 is in units of 1 / 16
-  } else {
-    const uint4 sv = *reinterpret_cast<const uint4*>(scales + g * 16);
-    const uint32_t turn = odd ? 0x1032u : 0x3210u;
+  const uint4 sv = *reinterpret_cast<const uint4*>(scales + g * 16);
+  const uint32_t turn = odd ? 0x1032u : 0x3210u;
 #pragma unroll
-    for (int k = 0; k < 2; ++k) {
-      const uint32_t a = k ? sv.z : sv.x, b = k ? sv.w : sv.y;
-      const uint32_t m2 = __vmaxu2(a & 0x7fff7fffu, b & 0x7fff7fffu);
-      const uint32_t e = min(max(max(m2 & 0xffffu, m2 >> 16) >> 7, 12u), 254u);
-      // the largest scale to [2^11, 2^12); row g + 8's codes come times 16
-      const float down = __uint_as_float(((k ? 261u : 265u) - e) << 23);
-      (k ? r1 : r0) = __uint_as_float((e - 11u) << 23);
-      const uint32_t v = __byte_perm(h ? b : a, 0, turn);
-      const float lo = __uint_as_float(v << 16) * down, hi = __uint_as_float(v & 0xffff0000u) * down;
-      asm("cvt.rn.f16x2.f32 %0, %1, %1;" : "=r"((k ? s1 : s0)[0]) : "f"(lo));
-      asm("cvt.rn.f16x2.f32 %0, %1, %1;" : "=r"((k ? s1 : s0)[1]) : "f"(hi));
-    }
+  for (int k = 0; k < 2; ++k) {
+    const uint32_t a = k ? sv.z : sv.x, b = k ? sv.w : sv.y;
+    const uint32_t m2 = __vmaxu2(a & 0x7fff7fffu, b & 0x7fff7fffu);
+    const uint32_t e = min(max(max(m2 & 0xffffu, m2 >> 16) >> 7, 12u), 254u);
+    // the largest scale to [2^11, 2^12); row g + 8's codes come times 16
+    const float down = __uint_as_float(((k ? 261u : 265u) - e) << 23);
+    (k ? r1 : r0) = __uint_as_float((e - 11u) << 23);
+    const uint32_t v = __byte_perm(h ? b : a, 0, turn);
+    const float lo = __uint_as_float(v << 16) * down, hi = __uint_as_float(v & 0xffff0000u) * down;
+    asm("cvt.rn.f16x2.f32 %0, %1, %1;" : "=r"((k ? s1 : s0)[0]) : "f"(lo));
+    asm("cvt.rn.f16x2.f32 %0, %1, %1;" : "=r"((k ? s1 : s0)[1]) : "f"(hi));
   }
 #pragma unroll
   for (int i = 0; i < 2; ++i) {
@@ -140,12 +148,10 @@ __device__ __forceinline__ void make_a(const uint8_t* rec, uint8_t* to, int row,
         w >>= 8;
       }
     }
-    if (kGroup == 32) {
 #pragma unroll
-      for (int j = 0; j < 4; ++j) {
-        asm("mul.rn.f16x2 %0, %0, %1;" : "+r"(lo[j]) : "r"(s0[i]));
-        asm("mul.rn.f16x2 %0, %0, %1;" : "+r"(hi[j]) : "r"(s1[i]));
-      }
+    for (int j = 0; j < 4; ++j) {
+      asm("mul.rn.f16x2 %0, %0, %1;" : "+r"(lo[j]) : "r"(s0[i]));
+      asm("mul.rn.f16x2 %0, %0, %1;" : "+r"(hi[j]) : "r"(s1[i]));
     }
     const int at = ((4 * (i ^ odd) + c) ^ g) << 4;
     *reinterpret_cast<uint4*>(to + row * 128 + at) = make_uint4(lo[0], lo[1], lo[2], lo[3]);
@@ -217,8 +223,9 @@ __device__ __forceinline__ void write_unit(const Int4Segment& s, const Unit& x,
 // Sixteen warps of both kinds of work, not eight of each: a scheduler has
 // four to choose from, and two could not hide the latencies (a chunk of 64
 // tokens took 3900 cycles).
-template <bool kSwiglu, int kGroup>
+template <bool kSwiglu>
 __global__ void __launch_bounds__(kThreads, 1) gemm_int4_fp8_kernel(const __grid_constant__ Int4Launch p) {
+  constexpr int kGroup = 32;
   constexpr int kRec = record_bytes(kGroup), kHalf = half_bytes(kGroup);
   extern __shared__ __align__(16) uint8_t raw[];
   uint8_t* smem = raw + ((1024u - (smem_u32(raw) & 1023u)) & 1023u);
@@ -337,7 +344,7 @@ __global__ void __launch_bounds__(kThreads, 1) gemm_int4_fp8_kernel(const __grid
           if (has_a) {
             float r0, r1;
             const int ar = 16 * a_block + g;
-            make_a<kGroup>(ring + slot * kHalf, smem + st * kOperand + a_half * kAtom, ar, a_half,
+            make_a(ring + slot * kHalf, smem + st * kOperand + a_half * kAtom, ar, a_half,
                            lane, r0, r1);
             if (a_half == 0 && (lane & 3) == 0) {
               hd->r[fs][ar] = r0;
@@ -446,7 +453,8 @@ __global__ void __launch_bounds__(kThreads, 1) gemm_int4_fp8_kernel(const __grid
 // the workers, and eight a stage held everything up (linear 7168-18432, 64
 // tokens: 70 us).
 // Stages are 64 columns (a high, a low, b): four where no group has more than
-// 64 rows, so that each parity has two; three of 128 tokens.
+// 64 rows, so that each parity has two (linear 7168-18432, 64 tokens: 53.3 us,
+// 54.4 with the three of 128 tokens); three otherwise.
 __host__ __device__ constexpr int stages(int tokens) { return tokens == 64 ? 4 : 3; }
 __host__ __device__ constexpr int stage_bytes(int tokens) { return 2 * kAtom + tokens * 128; }
 constexpr int kThreadsB = 32 * (kWorkers + 2);
@@ -519,8 +527,8 @@ __device__ __forceinline__ void make_a_split(const uint8_t* rec, uint8_t* hi_to,
 
 // Stage j of the CTA's units is 64 columns; the workers of parity j mod 2
 // (one for each row block) make it: they start the copies of b, convert a and
-// hand it over when the copies have landed.  A unit's outputs are written while the next unit's first stages run, from
-// the other half of TMEM.
+// hand it over when the copies have landed.  A unit's outputs are written
+// while the next unit's first stages run, from the other half of TMEM.
 template <bool kSwiglu, int kGroup, int kMostTokens>
 __global__ void __launch_bounds__(kThreadsB, 1)
     gemm_int4_bf16_kernel(const __grid_constant__ Int4Launch p) {
@@ -769,7 +777,8 @@ __global__ void __launch_bounds__(kThreadsB, 1)
 // c 2^-9 (subnormals and the first normal binade are evenly spaced), so that
 // masks make a from the codes.  A constant first operand of -8 2^-9 adds what
 // makes the codes signed.  The products and their sums are those of the f16
-// form; a chunk's are added up in fp32 with both scales.
+// form; a chunk's are added up in fp32 with both scales.  Experts of 512 tokens
+// (384 of them, eight with 465 rows): 2171 us a call, 2251 with the f16 form.
 constexpr int kStagesC = 3;
 constexpr int kStageBytesC = 2 * kAtom;  // a, b: 128 rows of 128 bytes
 
@@ -1062,14 +1071,17 @@ template <typename Kernel>
 cudaError_t launch_kernel(Kernel kernel, const Int4Launch& p, int threads, int num_sms,
                           cudaStream_t stream) {
   // every call: the attribute belongs to a device's context, and setting it
-  // costs little beside a launch of more than 16 rows
+  // costs little beside a launch of many rows
   const cudaError_t err =
       cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, p.smem);
   if (err != cudaSuccess) return err;
   return launch_pdl(kernel, dim3(num_sms), dim3(threads), p.smem, stream, p);
 }
 
-// Rows of a group up to which it is read by gemv_int4.cu.
+// Rows of a group up to which it is read by gemv_int4.cu: five passes of eight
+// rows, at 52 cycles a record and SM each, cost what making the operand here
+// does, about 250 (896 experts and a shared one of 24 rows: 916 us; 947 with
+// the limit at 16 rows, which sends that one here).
 constexpr int kGemvRows = 40;
 
 }  // namespace
@@ -1086,8 +1098,8 @@ cudaError_t launch_gemm_int4(const Int4Launch& p, bool swiglu, int group, int nu
                            kThreads, num_sms, stream);
     }
     l.smem = smem_bytes(groups, group);
-    return launch_kernel(swiglu ? gemm_int4_fp8_kernel<true, 32> : gemm_int4_fp8_kernel<false, 32>,
-                         l, kThreads, num_sms, stream);
+    return launch_kernel(swiglu ? gemm_int4_fp8_kernel<true> : gemm_int4_fp8_kernel<false>, l,
+                         kThreads, num_sms, stream);
   }
   bool small = true;
   for (int i = 0; i < p.nseg; ++i) small = small && p.seg[i].rows <= 64;
