@@ -632,8 +632,13 @@ __global__ void __launch_bounds__(kThreadsB, 1)
         tmem_ld_wait(v);
         tmem_ld_wait(v2);
 #pragma unroll
-        for (int j = 0; j < 16; ++j)
-          v[j] = __float_as_uint(__uint_as_float(v[j]) + __uint_as_float(v2[j]));
+        for (int j = 0; j < 16; ++j) {
+          // An infinity of x has met the weights' high parts, which are zero
+          // where the weight is and have its sign; against the rests, which
+          // may be zero or of the other sign, it says nothing.
+          const float high = __uint_as_float(v[j]), rest = __uint_as_float(v2[j]);
+          v[j] = __float_as_uint(isfinite(high) ? high + rest : high);
+        }
         if (kSwiglu) {
           // rows r < 8 of a block are gate rows, r + 8 the up rows of the
           // same features: lanes 8 apart swap and each finishes half the tokens

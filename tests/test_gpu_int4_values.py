@@ -1,0 +1,65 @@
+"""Products with 4-bit weights at values off the ordinary: infinities and NaN
+in rows, on both sides of the limit between the streamed and the tensor-core
+kernels (40 rows of a group)."""
+import numpy as np
+import pytest
+import torch
+
+from _gpu_common import lib, need_gpu
+from _int4_common import bank, dequant64
+from test_gpu_int4 import _gen, _rows
+
+pytestmark = pytest.mark.gpu
+
+# one token, the last streamed count, the first of the tensor cores, and both
+# sides of a 64- and of a 128-token unit
+TOKENS = [3, 40, 41, 64, 65, 130]
+
+
+def _linear(x, xs, q, s, group):
+    fgs = lib()
+    W = fgs.pack_int4(fgs.MOE_PACK_PLAIN, q.cuda(), s.cuda())
+    O, I = q.shape[1], 2 * q.shape[2]
+    y = torch.full((x.shape[0], O), 7.0, dtype=torch.bfloat16, device="cuda")
+    fgs.moe_linear_int4(x.shape[0], I, O, group, x, xs, W, None, y)
+    torch.cuda.synchronize()
+    return y
+
+
+@pytest.mark.parametrize("group", [32, 128])
+@pytest.mark.parametrize("T", TOKENS)
+def test_nonfinite_bf16_rows(T, group):
+    """An infinity or a NaN of x gives what the definition gives (an infinity
+    of the weight's sign, NaN at a zero weight), in its row alone."""
+    need_gpu()
+    gen = _gen(T + group)
+    q, s = bank(gen, 1, 272, 384, group)
+    x, _, x64 = _rows(gen, T, 384, False)
+    clean = _linear(x, None, q, s, group)
+    values = {0: {200: np.inf}, 1: {7: -np.inf, 130: -np.inf}, T - 1: {383: np.nan}}
+    for row, at in values.items():
+        for col, v in at.items():
+            x[row, col], x64[row, col] = v, v
+    y = _linear(x, None, q, s, group)
+    w = dequant64(q[0], s[0])
+    with np.errstate(invalid="ignore"):
+        ref = x64[sorted(values)] @ w.T
+    assert np.isinf(ref).any() and np.isnan(ref).any()
+    got = y[sorted(values)].double().cpu().numpy()
+    np.testing.assert_array_equal(got, ref)  # infinities with their signs, and NaN
+    keep = [t for t in range(T) if t not in values]
+    assert torch.equal(y[keep], clean[keep])
+
+
+@pytest.mark.parametrize("group", [32, 128])
+@pytest.mark.parametrize("T", TOKENS)
+def test_nan_codes_stay_in_their_rows(T, group):
+    need_gpu()
+    gen = _gen(T + group)
+    q, s = bank(gen, 1, 272, 384, group)
+    x, xs, _ = _rows(gen, T, 384, True)
+    clean = _linear(x, xs, q, s, group)
+    x[0, 5], x[T - 1, 383] = 0x7F, 0xFF
+    y = _linear(x, xs, q, s, group)
+    assert torch.isnan(y[[0, T - 1]]).all()
+    assert torch.equal(y[1:T - 1], clean[1:T - 1])
