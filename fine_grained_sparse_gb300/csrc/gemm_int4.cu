@@ -1,31 +1,18 @@
 // Products of more than a few rows with 4-bit weights, on the tensor cores
 // (tcgen05): the groups that gemv_int4.cu leaves.  128 weight rows by up to
-// 128 tokens a unit, in one of three forms:
+// 128 tokens a unit, in one of two forms:
 //
-//  bf16 rows            gemm_int4_bf16_kernel   weights as two bf16 values,
-//                       sums over all of K in TMEM
-//  E4M3 rows, groups    gemm_int4_bytes_kernel  both operands stay bytes, a
-//  of 128               chunk's sums are scaled in fp32
-//  E4M3 rows, groups    gemm_int4_fp8_kernel    both operands f16, a chunk's
-//  of 32                sums are scaled in fp32
+//  bf16 rows   gemm_int4_bf16_kernel   weights as two bf16 values, sums over
+//              all of K in TMEM
+//  E4M3 rows   gemm_int4_bytes_kernel  both operands stay bytes, the sums over
+//              a scale's columns are scaled in fp32
 //
-// All products are exact.  What bounds all three is making the first operand:
+// All products are exact.  What bounds both is making the first operand:
 // a block of 128 x 128 weights is 16 to 18 KB of HBM, but some 4500 warp
 // instructions from codes to swizzled operand to sums (with bf16 rows, 96
 // tokens and 17 experts' groups of which 11 come here: 4520 at 2.5 a cycle and
 // SM, tensor pipe 39% active, shared-memory pipe 47%).  It is made once for
 // all of a unit's tokens, so the form pays from kGemvRows rows on.
-//
-// The f16 form is written down here, the others where they begin:
-//
-//   z[t, o] = sum over chunks of 128 columns of f[t] r[o] sum_k a[o, k] b[t, k]
-//
-// where b is the chunk of x as f16 with its factor f (as in gemv_int4.cu) and
-// a the weights as f16, (c - 8) s 2^-e with r = 2^e, e the exponent of the
-// largest of the row's four scales.  c - 8 has at most three significant
-// bits, or is the power of two -8, and s eight, which an f16 holds together
-// (for scales down to 2^-28 of the largest).  A chunk's sum goes from TMEM to
-// fp32 registers, which is where f and r are applied.
 #include "int4.cuh"
 
 namespace fgs {
@@ -36,33 +23,13 @@ constexpr int kThreads = 32 * (kWorkers + 1);  // and the one that issues the MM
 constexpr int kBlocks = 8;    // row blocks of a unit
 constexpr int kRows = 16 * kBlocks;
 constexpr int kTokens = 128;
-constexpr int kDepth = 4;             // half records of a worker's ring
-constexpr int kOperand = 128 * 256;   // bytes of an operand stage: 128 x 128 f16
-constexpr int kAtom = 128 * 128;      // its half: 64 columns, 128-byte swizzled rows
-constexpr int kFactors = 4;           // chunks whose f and r are kept
-constexpr int kTmemCols = 2 * kTokens;
-
-// Shared memory after the operand stages (2 x a, 2 x b).
-struct Header {
-  float f[kFactors][kTokens];
-  float r[kFactors][kRows];
-  uint64_t full[2], empty[2], tfull[2], tempty[2], drain;
-  uint32_t tmem;
-  int abort;
-  int at_first, pad;
-  int64_t warp_sum[kThreads / 32];
-  int64_t lists[1];
-};
+constexpr int kDepth = 4;         // half records of a worker's ring
+constexpr int kAtom = 128 * 128;  // bytes of 128 swizzled rows of 128 bytes
 
 // Half a record (64 columns) with all of its scales.
 __host__ __device__ constexpr int half_bytes(int group) { return record_bytes(group) - kCodeBytes / 2; }
 __host__ __device__ constexpr int ring_bytes(int group) {
   return kWorkers * kDepth * half_bytes(group);
-}
-
-inline int smem_bytes(int groups, int group) {
-  return 1024 + 4 * kOperand + ring_bytes(group) +
-         (static_cast<int>(sizeof(Header)) + group_list_bytes(groups) + 15) / 16 * 16;
 }
 
 // One unit: a row tile of a group against a tile of its tokens.
@@ -120,63 +87,6 @@ __device__ __forceinline__ int next_unit(int u, int rest) {
   return u + (u < rest ? rest : static_cast<int>(gridDim.x));
 }
 
-// Half h of a record, at `rec` (codes, then the scales; this lane's
-// g = lane / 4 and c = lane % 4), into the a operand's half at `to` (rows row
-// and row + 8, row = 16 w + g), and the rows' scales r.  Lanes of odd g take
-// the half's two 32-column parts in the other order, which puts the rows that
-// are stored together on different banks.
-__device__ __forceinline__ void make_a(const uint8_t* rec, uint8_t* to, int row, int h, int lane,
-                                       float& r0, float& r1) {
-  const int g = lane >> 2, c = lane & 3, odd = g & 1;
-  const uint8_t* scales = rec + kCodeBytes / 2;
-  uint32_t s0[2], s1[2];  // scales of rows g and g + 8 in the order of the parts, f16 pairs
-  const uint4 sv = *reinterpret_cast<const uint4*>(scales + g * 16);
-  const uint32_t turn = odd ? 0x1032u : 0x3210u;
-#pragma unroll
-  for (int k = 0; k < 2; ++k) {
-    const uint32_t a = k ? sv.z : sv.x, b = k ? sv.w : sv.y;
-    const uint32_t m2 = __vmaxu2(a & 0x7fff7fffu, b & 0x7fff7fffu);
-    const uint32_t e = min(max(max(m2 & 0xffffu, m2 >> 16) >> 7, 12u), 254u);
-    // the largest scale to [2^11, 2^12); row g + 8's codes come times 16
-    const float down = __uint_as_float(((k ? 261u : 265u) - e) << 23);
-    (k ? r1 : r0) = __uint_as_float((e - 11u) << 23);
-    const uint32_t v = __byte_perm(h ? b : a, 0, turn);
-    const float lo = __uint_as_float(v << 16) * down, hi = __uint_as_float(v & 0xffff0000u) * down;
-    asm("cvt.rn.f16x2.f32 %0, %1, %1;" : "=r"((k ? s1 : s0)[0]) : "f"(lo));
-    asm("cvt.rn.f16x2.f32 %0, %1, %1;" : "=r"((k ? s1 : s0)[1]) : "f"(hi));
-  }
-#pragma unroll
-  for (int i = 0; i < 2; ++i) {
-    const uint2 v = *reinterpret_cast<const uint2*>(rec + lane * 16 + ((i ^ odd) << 3));
-    uint32_t lo[4], hi[4];  // rows g and g + 8, eight columns
-#pragma unroll
-    for (int j = 0; j < 2; ++j) {
-      uint32_t w = j ? v.y : v.x;
-#pragma unroll
-      for (int q = 0; q < 2; ++q) {
-        asm("sub.rn.f16x2 %0, %1, %2;" : "=r"(lo[2 * j + q])
-            : "r"((w & 0x000f000fu) | 0x64006400u), "r"(0x64086408u));  // 1024 + c - 1032
-        asm("sub.rn.f16x2 %0, %1, %2;" : "=r"(hi[2 * j + q])
-            : "r"((w & 0x00f000f0u) | 0x64006400u), "r"(0x64806480u));  // 1024 + 16 c - 1152
-        w >>= 8;
-      }
-    }
-#pragma unroll
-    for (int j = 0; j < 4; ++j) {
-      asm("mul.rn.f16x2 %0, %0, %1;" : "+r"(lo[j]) : "r"(s0[i]));
-      asm("mul.rn.f16x2 %0, %0, %1;" : "+r"(hi[j]) : "r"(s1[i]));
-    }
-    const int at = ((4 * (i ^ odd) + c) ^ g) << 4;
-    *reinterpret_cast<uint4*>(to + row * 128 + at) = make_uint4(lo[0], lo[1], lo[2], lo[3]);
-    *reinterpret_cast<uint4*>(to + (row + 8) * 128 + at) = make_uint4(hi[0], hi[1], hi[2], hi[3]);
-  }
-}
-
-// f16 x f16 -> fp32, both operands K-major, M = 128, N = n.
-__device__ __forceinline__ uint32_t idesc_f16_f32(uint32_t n) {
-  return (1u << 4) | ((n >> 3) << 17) | ((128u >> 4) << 24);
-}
-
 // o[i] += (f[i] r) v[i] for four tokens, two to an instruction.
 __device__ __forceinline__ void add_scaled4(float* o, float4 f, float r, const uint32_t* v) {
   asm("{\n\t.reg .b64 a, b, x, y, s, t, u;\n\t"
@@ -228,238 +138,6 @@ __device__ __forceinline__ void write_unit(const Int4Segment& s, const Unit& x,
   }
 }
 
-// Sixteen worker warps make the operands of chunk i (half of a row block of
-// the weights each, and the tokens of its two half warps) and then add up the
-// sums of chunk i - 1 (a quarter of the rows, a quarter of the tokens), while
-// the MMAs of chunk i run; one more warp issues those.  Chunk i of the CTA's
-// units uses operand stage and TMEM region i mod 2 and factors i mod 4.
-// Sixteen warps of both kinds of work, not eight of each: a scheduler has
-// four to choose from, and two could not hide the latencies (a chunk of 64
-// tokens took 3900 cycles).
-template <bool kSwiglu>
-__global__ void __launch_bounds__(kThreads, 1) gemm_int4_fp8_kernel(const __grid_constant__ Int4Launch p) {
-  constexpr int kGroup = 32;
-  constexpr int kRec = record_bytes(kGroup), kHalf = half_bytes(kGroup);
-  extern __shared__ __align__(16) uint8_t raw[];
-  uint8_t* smem = raw + ((1024u - (smem_u32(raw) & 1023u)) & 1023u);
-  uint8_t* ring_base = smem + 4 * kOperand;
-  Header* hd = reinterpret_cast<Header*>(ring_base + ring_bytes(kGroup));
-  const int groups = p.seg[0].groups + (p.nseg > 1 ? p.seg[1].groups : 0);
-  const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
-  volatile int* abort_flag = &hd->abort;
-  auto bar = [](uint64_t& b) { return smem_u32(&b); };
-
-  if (warp == 0) {
-    tmem_alloc(smem_u32(&hd->tmem), kTmemCols);
-    tmem_relinquish();
-  }
-  if (warp == kWorkers && lane == 0) {
-    for (int i = 0; i < 2; ++i) {
-      mbar_init(bar(hd->full[i]), kWorkers);
-      mbar_init(bar(hd->empty[i]), 1);
-      mbar_init(bar(hd->tfull[i]), 1);
-      mbar_init(bar(hd->tempty[i]), kWorkers);
-    }
-    mbar_init(bar(hd->drain), 1);
-    hd->abort = 0;
-    fence_mbarrier_init();
-  }
-  tc_fence_before();
-  __syncthreads();
-  tc_fence_after();
-  const uint32_t tmem = hd->tmem;
-
-  if (p.wait == kWaitWeights) pdl_wait();
-  pdl_release();
-  const GroupLists lists = group_lists(hd->lists, groups);
-  int u0 = 0, rest = 0;
-  const GroupPlan plan = plan_groups<kThreads>(
-      p, lists, hd->warp_sum,
-      [&](int si, int n) -> int64_t {
-        if (n <= p.most) return 0;
-        return static_cast<int64_t>((p.seg[si].blocks + kBlocks - 1) / kBlocks) *
-               ((n + kTokens - 1u) / kTokens);
-      },
-      [&](int64_t total) {
-        rest = static_cast<int>(total % gridDim.x);
-        u0 = first_unit(rest);
-      },
-      [&](int pos, int64_t before, int64_t cost) {
-        if (before <= u0 && u0 < before + cost) hd->at_first = pos;
-      });
-  int pos = u0 < plan.total ? hd->at_first : 0;
-
-  if (warp < kWorkers) {
-    const int a_block = warp >> 1, a_half = warp & 1, g = lane >> 2;  // of the operand a
-    const int hw = 2 * warp + (lane >> 4), piece = lane & 15;         // of the operand b
-    const int quarter = warp & 3, row = 32 * quarter + lane;          // of the sums
-    constexpr int kTasks = kTokens / 32;
-    uint8_t* const ring = ring_base + warp * kDepth * kHalf;
-    bool first = true, ok = true;
-    int i = 0;
-    for (int u = u0; u < plan.total && ok; u = next_unit(u, rest)) {
-      const Unit x = unit_at<kTokens>(p, lists, plan, u, pos, kRec);
-      const Int4Segment& s = p.seg[x.seg];
-      // this worker's half records, and the last of them
-      const bool has_a = a_block < x.blocks;
-      const uint8_t* w = x.W + (has_a ? static_cast<int64_t>(a_block) * x.chunks * kRec : 0) +
-                         a_half * (kCodeBytes / 2) + lane * 16;
-      auto fetch = [&](int slot, int ch) {
-        if (has_a && ch < x.chunks) {
-          const uint32_t to = smem_u32(ring + slot * kHalf) + lane * 16;
-          const uint8_t* from = w + ch * kRec;
-          cp_async16(to, from);
-          if (lane < (kRec - kCodeBytes) / 16)
-            cp_async16(to + kCodeBytes / 2, from + kCodeBytes - a_half * (kCodeBytes / 2));
-        }
-        asm volatile("cp.async.commit_group;" ::: "memory");
-      };
-#pragma unroll
-      for (int c = 0; c < kDepth - 1; ++c) fetch(c, c);
-      if (first && p.wait == kWaitX) pdl_wait();
-      first = false;
-      // rows of x of tokens 32 q + hw (beyond the end, of the last token)
-      int rows[kTasks];
-      {
-        const int64_t at = x.x_row + min(32 * (piece & 3) + hw, x.n - 1);
-        const int mine = static_cast<int>(s.perm ? s.perm[at] / s.perm_div : at);
-#pragma unroll
-        for (int q = 0; q < kTasks; ++q) rows[q] = __shfl_sync(0xffffffffu, mine, (lane & 16) + q);
-      }
-      uint2 xr[kTasks];
-      float xf[kTasks];
-      auto load_b = [&](int ch) {
-#pragma unroll
-        for (int q = 0; q < kTasks; ++q) {
-          if (32 * q + 2 * warp >= x.n) break;
-          const int64_t from = static_cast<int64_t>(rows[q]) * x.chunks + ch;
-          xr[q] = *reinterpret_cast<const uint2*>(static_cast<const uint8_t*>(s.x) + from * kChunk +
-                                                  piece * 8);
-          xf[q] = s.x_scale[from];
-        }
-      };
-      load_b(0);
-      const int cols = x.n > 64 ? 32 : 16, t0 = (warp >> 2) * cols;  // tokens of the sums
-      float weight = 1.0f;  // row weight of token t0 + lane
-      if (!kSwiglu && s.row_w && t0 + lane < x.n) weight = s.row_w[s.row_perm[x.out_row + t0 + lane]];
-      float acc[kTokens / 4];
-#pragma unroll
-      for (int j = 0; j < kTokens / 4; ++j) acc[j] = 0.0f;
-
-      // one step more than chunks: step ch makes chunk ch and adds chunk ch - 1
-      for (int ch = 0; ch <= x.chunks; ++ch) {
-        if (ch < x.chunks) {
-          const int st = i & 1, fs = i & (kFactors - 1), slot = ch & (kDepth - 1);
-          asm volatile("cp.async.wait_group %0;" ::"n"(kDepth - 2) : "memory");
-          __syncwarp();
-          fetch((ch + kDepth - 1) & (kDepth - 1), ch + kDepth - 1);
-          if (!mbar_wait_bounded(bar(hd->empty[st]), (i >> 1 & 1) ^ 1, abort_flag, p.status)) {
-            ok = false;
-            break;
-          }
-          if (has_a) {
-            float r0, r1;
-            const int ar = 16 * a_block + g;
-            make_a(ring + slot * kHalf, smem + st * kOperand + a_half * kAtom, ar, a_half,
-                           lane, r0, r1);
-            if (a_half == 0 && (lane & 3) == 0) {
-              hd->r[fs][ar] = r0;
-              hd->r[fs][ar + 8] = r1;
-            }
-          }
-          uint8_t* b = smem + (2 + st) * kOperand + (piece >> 3) * kAtom;
-#pragma unroll
-          for (int q = 0; q < kTasks; ++q) {
-            if (32 * q + 2 * warp >= x.n) break;
-            const int t = 32 * q + hw;
-            *reinterpret_cast<uint4*>(b + t * 128 + (((piece & 7) ^ (t & 7)) << 4)) =
-                e4m3x8_to_f16(xr[q]);
-            if (piece == 0) hd->f[fs][t] = xf[q];
-          }
-          if (ch + 1 < x.chunks) load_b(ch + 1);
-          fence_proxy_async_smem();  // the tensor cores read the operands next
-          __syncwarp();
-          if (lane == 0) mbar_arrive(bar(hd->full[st]));
-          ++i;
-        }
-        if (ch > 0) {
-          const int c = i - (ch < x.chunks ? 2 : 1), st = c & 1, fs = c & (kFactors - 1);
-          // (the operands were full before; that wait is for f and r)
-          if (!mbar_wait_bounded(bar(hd->tfull[st]), c >> 1 & 1, abort_flag, p.status) ||
-              !mbar_wait_bounded(bar(hd->full[st]), c >> 1 & 1, abort_flag, p.status)) {
-            ok = false;
-            break;
-          }
-          __syncwarp();
-          tc_fence_after();
-          const float r = hd->r[fs][row];
-          const float4* f = reinterpret_cast<const float4*>(hd->f[fs] + t0);
-          const uint32_t from = tmem + st * kTokens + t0 + (static_cast<uint32_t>(32 * quarter) << 16);
-#pragma unroll
-          for (int b = 0; b < 2; ++b) {
-            if (16 * b < cols) {
-              uint32_t v[16];
-              tmem_ld_x16(from + 16 * b, v);
-              tmem_ld_wait(v);
-#pragma unroll
-              for (int j = 0; j < 4; ++j)
-                add_scaled4(acc + 16 * b + 4 * j, f[4 * b + j], r, v + 4 * j);
-            }
-          }
-          tc_fence_before();
-          __syncwarp();
-          if (lane == 0) mbar_arrive(bar(hd->tempty[st]));
-        }
-      }
-      if (!ok) break;
-
-      write_unit<kSwiglu>(s, x, acc, weight, t0, cols, row, lane);
-    }
-    asm volatile("cp.async.wait_all;" ::: "memory");
-  } else {
-    if (lane == 0) {
-      int i = 0;
-      bool ok = true;
-      for (int u = u0; ok; u = next_unit(u, rest)) {
-        const Unit x = unit_at<kTokens>(p, lists, plan, u, pos, kRec);
-        if (x.seg < 0) break;
-        const uint32_t idesc = idesc_f16_f32(x.n > 64 ? 128 : 64);
-        for (int ch = 0; ch < x.chunks; ++ch, ++i) {
-          const int st = i & 1, ph = i >> 1 & 1;
-          if (!mbar_wait_bounded(bar(hd->tempty[st]), ph ^ 1, abort_flag, p.status) ||
-              !mbar_wait_bounded(bar(hd->full[st]), ph, abort_flag, p.status)) {
-            ok = false;
-            break;
-          }
-          tc_fence_after();
-          const uint32_t a = smem_u32(smem + st * kOperand), b = smem_u32(smem + (2 + st) * kOperand);
-#pragma unroll
-          for (int h = 0; h < 2; ++h) {
-            const uint64_t ad = smem_desc_sw128(a + h * kAtom), bd = smem_desc_sw128(b + h * kAtom);
-#pragma unroll
-            for (int kk = 0; kk < 4; ++kk)
-              tc_mma_bf16(tmem + st * kTokens, ad + 2u * kk, bd + 2u * kk, idesc, (h | kk) != 0);
-          }
-          tc_commit(bar(hd->empty[st]));
-          tc_commit(bar(hd->tfull[st]));
-        }
-      }
-      // nothing is in flight when the CTA gives its TMEM back
-      tc_commit(bar(hd->drain));
-      int own_abort = 0;
-      mbar_wait_bounded(bar(hd->drain), 0, &own_abort, p.status);
-    }
-    __syncwarp();
-  }
-  if (p.wait != kWaitWeights) pdl_wait();  // a kernel ends after the one before it has
-  tc_fence_before();
-  __syncthreads();
-  if (warp == 0) {
-    tc_fence_after();
-    tmem_dealloc(tmem, kTmemCols);
-  }
-}
-
 // ------------------------------------------------------------- bf16 rows
 // With x in bf16 both operands are bf16 and nothing is left to apply to the
 // sums: b is x as it lies in memory, a weight (c - 8) s is the sum of two bf16
@@ -490,7 +168,11 @@ inline int smem_bytes_b(int tokens, int groups, int group) {
          (static_cast<int>(sizeof(HeaderB)) + group_list_bytes(groups) + 15) / 16 * 16;
 }
 
-// Half h of a record (as make_a's) into the two halves of the a operand.
+// Half h of a record, at `rec` (codes, then the scales; this lane's
+// g = lane / 4 and c = lane % 4), into the two halves of the a operand at
+// hi_to and lo_to (rows row and row + 8, row = 16 w + g).  Lanes of odd g take
+// the half's two 32-column parts in the other order, which puts the rows that
+// are stored together on different banks.
 template <int kGroup>
 __device__ __forceinline__ void make_a_split(const uint8_t* rec, uint8_t* hi_to, uint8_t* lo_to,
                                              int row, int h, int lane) {
@@ -795,24 +477,38 @@ __global__ void __launch_bounds__(kThreadsB, 1)
   }
 }
 
-// ------------------------------------- E4M3 rows, scales of 128 columns
-// With one scale a chunk on either side the operands can stay bytes
-// (kind::f8f6f4): b is x as it lies in memory, and a code c as an E4M3 byte is
-// c 2^-9 (subnormals and the first normal binade are evenly spaced), so that
-// masks make a from the codes.  A constant first operand of -8 2^-9 adds what
-// makes the codes signed.  The products and their sums are those of the f16
-// form; a chunk's are added up in fp32 with both scales.  Experts of 512 tokens
-// (384 of them, eight with 465 rows): 2171 us a call, 2251 with the f16 form.
+// ------------------------------------------------------------- E4M3 rows
+// The operands can stay bytes (kind::f8f6f4): b is x as it lies in memory, and
+// a code c as an E4M3 byte is c 2^-9 (subnormals and the first normal binade
+// are evenly spaced), so that masks make a from the codes.  A constant first
+// operand of -8 2^-9 adds what makes the codes signed.  The sums over the
+// columns of one scale come to registers, where both scales are applied and
+// the chunks are added up in fp32.  With scales of 32 columns, one step of
+// the MMA's K, a chunk has four accumulators.  7168 to 18432 columns: 64
+// tokens 63 us with scales of 128 columns, 73 with 32; 2048 tokens 1110 and
+// 1354.  (As f16, (c - 8) s needs one accumulator a chunk in either case, but
+// holds a row's four scales together only while they are within 2^24 of one
+// another; it took 82 and 1377 us.)
 constexpr int kStagesC = 3;
 constexpr int kStageBytesC = 2 * kAtom;  // a, b: 128 rows of 128 bytes
+
+// A chunk's accumulators, one for each scale, and the chunks whose sums TMEM
+// holds: two, or one with four accumulators, whose MMAs have the time in which
+// the workers make the next chunk.
+__host__ __device__ constexpr int scales(int group) { return kChunk / group; }
+__host__ __device__ constexpr int buffers(int group) { return group == 32 ? 1 : 2; }
+__host__ __device__ constexpr int tmem_cols_c(int group) {
+  return buffers(group) * scales(group) * kTokens;
+}
 
 // b and f are asked for a chunk ahead, when sums four chunks back may still be
 // read: eight chunks' factors are kept.
 constexpr int kFactorsC = 8;
 
+template <int kGroup>
 struct HeaderC {
   float f[kFactorsC][kTokens];
-  float r[kFactorsC][kRows];
+  float r[kFactorsC][scales(kGroup)][kRows];
   uint64_t full[kStagesC], empty[kStagesC], tfull[2], tempty[2], drain;
   uint32_t tmem;
   int abort;
@@ -821,9 +517,15 @@ struct HeaderC {
   int64_t lists[1];
 };
 
-inline int smem_bytes_c(int groups) {
-  return 1024 + kStagesC * kStageBytesC + kAtom + ring_bytes(128) +
-         (static_cast<int>(sizeof(HeaderC)) + group_list_bytes(groups) + 15) / 16 * 16;
+template <int kGroup>
+int smem_bytes_c(int groups) {
+  return 1024 + kStagesC * kStageBytesC + kAtom + ring_bytes(kGroup) +
+         (static_cast<int>(sizeof(HeaderC<kGroup>)) + group_list_bytes(groups) + 15) / 16 * 16;
+}
+
+// Both operands E4M3 (format 0), K-major, fp32 sums, M = 128, N = n.
+__device__ __forceinline__ uint32_t idesc_e4m3_f32(uint32_t n) {
+  return (1u << 4) | ((n >> 3) << 17) | ((128u >> 4) << 24);
 }
 
 // D[tmem] (+)= A[smem] * B[smem]^T, E4M3 inputs, fp32 accumulator, M = 128.
@@ -837,15 +539,72 @@ __device__ __forceinline__ void tc_mma_e4m3(uint32_t d_tmem, uint64_t a_desc, ui
       : "memory");
 }
 
-template <bool kSwiglu>
+// v0[i] = r0 v0[i] + r1 v1[i] for four tokens, two to an instruction.
+__device__ __forceinline__ void join4(uint32_t* v0, float r0, const uint32_t* v1, float r1) {
+  asm("{\n\t.reg .b64 x, y, s, t, u, w;\n\t"
+      "mov.b64 u, {%4, %4};\n\tmov.b64 w, {%5, %5};\n\t"
+      "mov.b64 x, {%0, %1};\n\tmov.b64 y, {%2, %3};\n\t"
+      "mul.rn.f32x2 x, x, u;\n\tmul.rn.f32x2 y, y, u;\n\t"
+      "mov.b64 s, {%6, %7};\n\tmov.b64 t, {%8, %9};\n\t"
+      "fma.rn.f32x2 x, s, w, x;\n\tfma.rn.f32x2 y, t, w, y;\n\t"
+      "mov.b64 {%0, %1}, x;\n\tmov.b64 {%2, %3}, y;\n\t}"
+      : "+r"(v0[0]), "+r"(v0[1]), "+r"(v0[2]), "+r"(v0[3])
+      : "f"(r0), "f"(r1), "r"(v1[0]), "r"(v1[1]), "r"(v1[2]), "r"(v1[3]));
+}
+
+// o[i] += f[i] (x[i] + r0 v0[i] + r1 v1[i]) for four tokens.
+__device__ __forceinline__ void add_joined4(float* o, float4 f, const uint32_t* x0, float r0,
+                                            const uint32_t* v0, float r1, const uint32_t* v1) {
+  asm("{\n\t.reg .b64 a, b, x, y, s, t, u, w;\n\t"
+      "mov.b64 u, {%8, %8};\n\tmov.b64 w, {%9, %9};\n\t"
+      "mov.b64 x, {%10, %11};\n\tmov.b64 y, {%12, %13};\n\t"
+      "mov.b64 s, {%14, %15};\n\tmov.b64 t, {%16, %17};\n\t"
+      "fma.rn.f32x2 x, s, u, x;\n\tfma.rn.f32x2 y, t, u, y;\n\t"
+      "mov.b64 s, {%18, %19};\n\tmov.b64 t, {%20, %21};\n\t"
+      "fma.rn.f32x2 x, s, w, x;\n\tfma.rn.f32x2 y, t, w, y;\n\t"
+      "mov.b64 a, {%0, %1};\n\tmov.b64 b, {%2, %3};\n\t"
+      "mov.b64 s, {%4, %5};\n\tmov.b64 t, {%6, %7};\n\t"
+      "fma.rn.f32x2 a, s, x, a;\n\tfma.rn.f32x2 b, t, y, b;\n\t"
+      "mov.b64 {%0, %1}, a;\n\tmov.b64 {%2, %3}, b;\n\t}"
+      : "+f"(o[0]), "+f"(o[1]), "+f"(o[2]), "+f"(o[3])
+      : "f"(f.x), "f"(f.y), "f"(f.z), "f"(f.w), "f"(r0), "f"(r1), "r"(x0[0]), "r"(x0[1]),
+        "r"(x0[2]), "r"(x0[3]), "r"(v0[0]), "r"(v0[1]), "r"(v0[2]), "r"(v0[3]), "r"(v1[0]),
+        "r"(v1[1]), "r"(v1[2]), "r"(v1[3]));
+}
+
+// 32 lanes x 8 consecutive 32-bit columns of two accumulators of TMEM into
+// registers, and the wait for them.
+__device__ __forceinline__ void tmem_ld_two_x8(uint32_t from0, uint32_t from1, uint32_t (&v0)[8],
+                                               uint32_t (&v1)[8]) {
+  asm volatile(
+      "tcgen05.ld.sync.aligned.32x32b.x8.b32 {%0, %1, %2, %3, %4, %5, %6, %7}, [%16];\n\t"
+      "tcgen05.ld.sync.aligned.32x32b.x8.b32 {%8, %9, %10, %11, %12, %13, %14, %15}, [%17];\n\t"
+      "tcgen05.wait::ld.sync.aligned;"
+      : "=&r"(v0[0]), "=&r"(v0[1]), "=&r"(v0[2]), "=&r"(v0[3]), "=&r"(v0[4]), "=&r"(v0[5]),
+        "=&r"(v0[6]), "=&r"(v0[7]), "=&r"(v1[0]), "=&r"(v1[1]), "=&r"(v1[2]), "=&r"(v1[3]),
+        "=&r"(v1[4]), "=&r"(v1[5]), "=&r"(v1[6]), "=&r"(v1[7])
+      : "r"(from0), "r"(from1)
+      : "memory");
+}
+
+// Sixteen worker warps make the operands of chunk i (half of a row block of
+// the weights each, and four tokens' rows of each 64) and then add up the sums
+// of chunk i - 1 (a quarter of the rows, a quarter of the tokens), while the
+// MMAs of chunk i run; one more warp issues those.  Sixteen warps of both
+// kinds of work, not eight of each: a scheduler has four to choose from, and
+// two could not hide the latencies (a chunk of 64 tokens took 3900 cycles).
+template <bool kSwiglu, int kGroup>
 __global__ void __launch_bounds__(kThreads, 1)
     gemm_int4_bytes_kernel(const __grid_constant__ Int4Launch p) {
-  constexpr int kRec = record_bytes(128), kHalf = half_bytes(128);
+  constexpr int kRec = record_bytes(kGroup), kHalf = half_bytes(kGroup);
+  constexpr int kScales = scales(kGroup), kBuffers = buffers(kGroup);
+  constexpr int kTmemCols = tmem_cols_c(kGroup);
   extern __shared__ __align__(16) uint8_t raw[];
   uint8_t* smem = raw + ((1024u - (smem_u32(raw) & 1023u)) & 1023u);
   uint8_t* bias = smem + kStagesC * kStageBytesC;
   uint8_t* ring_base = bias + kAtom;
-  HeaderC* hd = reinterpret_cast<HeaderC*>(ring_base + ring_bytes(128));
+  using Header = HeaderC<kGroup>;
+  Header* hd = reinterpret_cast<Header*>(ring_base + ring_bytes(kGroup));
   const int groups = p.seg[0].groups + (p.nseg > 1 ? p.seg[1].groups : 0);
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
   volatile int* abort_flag = &hd->abort;
@@ -998,10 +757,18 @@ __global__ void __launch_bounds__(kThreads, 1)
               *reinterpret_cast<uint2*>(to + at) = make_uint2(lo[0], lo[1]);
               *reinterpret_cast<uint2*>(to + 8 * 128 + at) = make_uint2(hi[0], hi[1]);
             }
-            if (a_half == 0 && c == 0) {
-              const uint32_t sc = *reinterpret_cast<const uint32_t*>(rec + kCodeBytes / 2 + g * 4);
-              hd->r[fs][16 * a_block + g] = __uint_as_float(sc << 16) * 512.0f;
-              hd->r[fs][16 * a_block + g + 8] = __uint_as_float(sc & 0xffff0000u) * 512.0f;
+            const uint8_t* sc = rec + kCodeBytes / 2;
+            const int ar = 16 * a_block + g;
+            if (kScales == 1 && a_half == 0 && c == 0) {  // rows g and g + 8
+              const uint32_t v2 = *reinterpret_cast<const uint32_t*>(sc + g * 4);
+              hd->r[fs][0][ar] = __uint_as_float(v2 << 16) * 512.0f;
+              hd->r[fs][0][ar + 8] = __uint_as_float(v2 & 0xffff0000u) * 512.0f;
+            }
+            if (kScales == 4 && c < 2) {  // row g + 8 c, this half's two groups
+              const uint32_t v2 = *reinterpret_cast<const uint32_t*>(sc + g * 16 + c * 8 + a_half * 4);
+              hd->r[fs][(2 * a_half) % kScales][ar + 8 * c] = __uint_as_float(v2 << 16) * 512.0f;
+              hd->r[fs][(2 * a_half + 1) % kScales][ar + 8 * c] =
+                  __uint_as_float(v2 & 0xffff0000u) * 512.0f;
             }
           }
           fence_proxy_async_smem();  // the tensor cores read the operands next
@@ -1011,9 +778,10 @@ __global__ void __launch_bounds__(kThreads, 1)
           ++i;
         }
         if (ch > 0) {
-          const int k = i - (ch < x.chunks ? 2 : 1), buf = k & 1, fs = k & (kFactorsC - 1);
+          const int k = i - (ch < x.chunks ? 2 : 1), fs = k & (kFactorsC - 1);
+          const int buf = k & (kBuffers - 1);
           // (the operands were full before; that wait is for f and r)
-          if (!mbar_wait_bounded(bar(hd->tfull[buf]), k >> 1 & 1, abort_flag, p.status) ||
+          if (!mbar_wait_bounded(bar(hd->tfull[buf]), k >> (kBuffers - 1) & 1, abort_flag, p.status) ||
               !mbar_wait_bounded(bar(hd->full[aslot]), aphase, abort_flag, p.status)) {
             ok = false;
             break;
@@ -1024,18 +792,39 @@ __global__ void __launch_bounds__(kThreads, 1)
           }
           __syncwarp();
           tc_fence_after();
-          const float r = hd->r[fs][row];
           const float4* f = reinterpret_cast<const float4*>(hd->f[fs] + t0);
-          const uint32_t from = tmem + buf * kTokens + t0 + (static_cast<uint32_t>(32 * quarter) << 16);
+          const uint32_t from =
+              tmem + buf * kScales * kTokens + t0 + (static_cast<uint32_t>(32 * quarter) << 16);
+          if constexpr (kScales == 1) {
+            const float r = hd->r[fs][0][row];
 #pragma unroll
-          for (int b = 0; b < 2; ++b) {
-            if (16 * b < cols) {
-              uint32_t v[16];
-              tmem_ld_x16(from + 16 * b, v);
-              tmem_ld_wait(v);
+            for (int b = 0; b < 2; ++b) {
+              if (16 * b < cols) {
+                uint32_t v[16];
+                tmem_ld_x16(from + 16 * b, v);
+                tmem_ld_wait(v);
 #pragma unroll
-              for (int j = 0; j < 4; ++j)
-                add_scaled4(acc + 16 * b + 4 * j, f[4 * b + j], r, v + 4 * j);
+                for (int j = 0; j < 4; ++j)
+                  add_scaled4(acc + 16 * b + 4 * j, f[4 * b + j], r, v + 4 * j);
+              }
+            }
+          } else {
+            float r[4];
+#pragma unroll
+            for (int j = 0; j < 4; ++j) r[j] = hd->r[fs][j % kScales][row];
+#pragma unroll
+            for (int b = 0; b < 4; ++b) {
+              if (8 * b < cols) {
+                uint32_t x0[8], v0[8], v1[8];
+                tmem_ld_two_x8(from + 8 * b, from + kTokens + 8 * b, x0, v1);
+                join4(x0, r[0], v1, r[1]);
+                join4(x0 + 4, r[0], v1 + 4, r[1]);
+                tmem_ld_two_x8(from + 2 * kTokens + 8 * b, from + 3 * kTokens + 8 * b, v0, v1);
+#pragma unroll
+                for (int j = 0; j < 2; ++j)
+                  add_joined4(acc + 8 * b + 4 * j, f[2 * b + j], x0 + 4 * j, r[2], v0 + 4 * j, r[3],
+                              v1 + 4 * j);
+              }
             }
           }
           tc_fence_before();
@@ -1053,25 +842,27 @@ __global__ void __launch_bounds__(kThreads, 1)
       bool ok = true;
       for (int u = u0; ok && u < plan.total; u = next_unit(u, rest)) {
         const Unit x = unit_at<kTokens>(p, lists, plan, u, pos, kRec);
-        // both formats E4M3 (0): the bits are those of the f16 descriptor
-        const uint32_t idesc = idesc_f16_f32(x.n > 64 ? 128 : 64);
+        const uint32_t idesc = idesc_e4m3_f32(x.n > 64 ? 128 : 64);
         for (int ch = 0; ch < x.chunks; ++ch, ++i) {
-          if (!mbar_wait_bounded(bar(hd->tempty[i & 1]), (i >> 1 & 1) ^ 1, abort_flag, p.status) ||
+          const int buf = i & (kBuffers - 1);
+          if (!mbar_wait_bounded(bar(hd->tempty[buf]), (i >> (kBuffers - 1) & 1) ^ 1, abort_flag,
+                                 p.status) ||
               !mbar_wait_bounded(bar(hd->full[slot]), phase, abort_flag, p.status)) {
             ok = false;
             break;
           }
           tc_fence_after();
-          const uint32_t st = smem_u32(smem + slot * kStageBytesC), d = tmem + (i & 1) * kTokens;
+          const uint32_t st = smem_u32(smem + slot * kStageBytesC);
           const uint64_t a = smem_desc_sw128(st), b = smem_desc_sw128(st + kAtom);
           const uint64_t minus = smem_desc_sw128(smem_u32(bias));
 #pragma unroll
-          for (int kk = 0; kk < 4; ++kk) {
-            tc_mma_e4m3(d, minus, b + 2u * kk, idesc, kk != 0);
+          for (int kk = 0; kk < 4; ++kk) {  // 32 columns
+            const uint32_t d = tmem + (buf * kScales + kk % kScales) * kTokens;
+            tc_mma_e4m3(d, minus, b + 2u * kk, idesc, kk >= kScales);
             tc_mma_e4m3(d, a + 2u * kk, b + 2u * kk, idesc, 1);
           }
           tc_commit(bar(hd->empty[slot]));
-          tc_commit(bar(hd->tfull[i & 1]));
+          tc_commit(bar(hd->tfull[buf]));
           if (++slot == kStagesC) {
             slot = 0;
             phase ^= 1;
@@ -1119,14 +910,12 @@ cudaError_t launch_gemm_int4(const Int4Launch& p, bool swiglu, int group, int nu
   int groups = 0;
   for (int i = 0; i < p.nseg; ++i) groups += p.seg[i].groups;
   if (p.seg[0].x_scale) {
-    if (group == 128) {
-      l.smem = smem_bytes_c(groups);
-      return launch_kernel(swiglu ? gemm_int4_bytes_kernel<true> : gemm_int4_bytes_kernel<false>, l,
-                           kThreads, num_sms, stream);
-    }
-    l.smem = smem_bytes(groups, group);
-    return launch_kernel(swiglu ? gemm_int4_fp8_kernel<true> : gemm_int4_fp8_kernel<false>, l,
-                         kThreads, num_sms, stream);
+    l.smem = group == 32 ? smem_bytes_c<32>(groups) : smem_bytes_c<128>(groups);
+    return launch_kernel(swiglu ? group == 32 ? gemm_int4_bytes_kernel<true, 32>
+                                              : gemm_int4_bytes_kernel<true, 128>
+                         : group == 32 ? gemm_int4_bytes_kernel<false, 32>
+                                       : gemm_int4_bytes_kernel<false, 128>,
+                         l, kThreads, num_sms, stream);
   }
   bool small = true;
   for (int i = 0; i < p.nseg; ++i) small = small && p.seg[i].rows <= 64;

@@ -120,8 +120,9 @@ typedef enum moe_router_weight_form {
  *     anew; for prefill the bf16 form is faster.
  *     Needs bf16 activations and d_model, d_ff, d_ff_shared, d_latent
  *     multiples of 128 and at most 32768.  The weights enter the tensor cores
- *     exactly ((code - 8) scale as f16 or two bf16 values, or code - 8 with
- *     the scale applied in fp32) and sums are fp32. */
+ *     exactly: as code - 8, with the scale applied to the sum over its columns
+ *     in fp32, or (bf16 rows of an expert with more than 40) as two bf16
+ *     values whose sum is (code - 8) scale.  Sums are fp32. */
 typedef enum moe_weight_layout {
   MOE_WEIGHTS_NATURAL = 0,
   MOE_WEIGHTS_PACKED = 1,

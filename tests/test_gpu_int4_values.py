@@ -1,12 +1,12 @@
 """Products with 4-bit weights at values off the ordinary: infinities and NaN
-in rows, on both sides of the limit between the streamed and the tensor-core
-kernels (40 rows of a group)."""
+in rows, and scales far apart within a row, on both sides of the limit between
+the streamed and the tensor-core kernels (40 rows of a group)."""
 import numpy as np
 import pytest
 import torch
 
 from _gpu_common import lib, need_gpu
-from _int4_common import bank, dequant64
+from _int4_common import bank, close, dequant64, dot_bound
 from test_gpu_int4 import _gen, _rows
 
 pytestmark = pytest.mark.gpu
@@ -63,3 +63,26 @@ def test_nan_codes_stay_in_their_rows(T, group):
     y = _linear(x, xs, q, s, group)
     assert torch.isnan(y[[0, T - 1]]).all()
     assert torch.equal(y[1:T - 1], clean[1:T - 1])
+
+
+@pytest.mark.parametrize("rows8", [False, True])
+@pytest.mark.parametrize("group", [32, 128])
+@pytest.mark.parametrize("apart", [20, 27, 60])
+@pytest.mark.parametrize("T", [5, 48, 100])
+def test_scales_far_apart(T, apart, group, rows8):
+    """A row's scales 2^apart from one group of columns to the next, with rows
+    of x that are zero where the scales are large: what is left has to be right
+    by itself."""
+    need_gpu()
+    gen = _gen(T * 100 + apart + group)
+    q, s = bank(gen, 1, 144, 512, group)
+    # every fourth group of a row large, from another one on in every row
+    large = (torch.arange(512 // group) + torch.arange(144)[:, None]) % 4 == 0
+    s[0] = torch.where(large, s[0].float(), s[0].float() * 2.0 ** -apart).bfloat16()
+    x, xs, x64 = _rows(gen, T, 512, rows8)
+    zero = torch.arange(512) // group % 4  # row t of x is zero in groups t mod 4
+    mask = zero == torch.arange(T)[:, None] % 4
+    x[mask.cuda()] = 0
+    x64[mask.numpy()] = 0
+    w = dequant64(q[0], s[0])
+    close(_linear(x, xs, q, s, group), x64 @ w.T, dot_bound(w, x64))
