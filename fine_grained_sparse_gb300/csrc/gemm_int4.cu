@@ -87,13 +87,13 @@ __device__ __forceinline__ int next_unit(int u, int rest) {
   return u + (u < rest ? rest : static_cast<int>(gridDim.x));
 }
 
-// o[i] += (f[i] r) v[i] for four tokens, two to an instruction.
+// o[i] += f[i] (r v[i]) for four tokens, two to an instruction.
 __device__ __forceinline__ void add_scaled4(float* o, float4 f, float r, const uint32_t* v) {
   asm("{\n\t.reg .b64 a, b, x, y, s, t, u;\n\t"
       "mov.b64 a, {%0, %1};\n\tmov.b64 b, {%2, %3};\n\t"
       "mov.b64 s, {%4, %5};\n\tmov.b64 t, {%6, %7};\n\tmov.b64 u, {%8, %8};\n\t"
       "mov.b64 x, {%9, %10};\n\tmov.b64 y, {%11, %12};\n\t"
-      "mul.rn.f32x2 s, s, u;\n\tmul.rn.f32x2 t, t, u;\n\t"
+      "mul.rn.f32x2 x, x, u;\n\tmul.rn.f32x2 y, y, u;\n\t"
       "fma.rn.f32x2 a, s, x, a;\n\tfma.rn.f32x2 b, t, y, b;\n\t"
       "mov.b64 {%0, %1}, a;\n\tmov.b64 {%2, %3}, b;\n\t}"
       : "+f"(o[0]), "+f"(o[1]), "+f"(o[2]), "+f"(o[3])
@@ -523,6 +523,11 @@ int smem_bytes_c(int groups) {
          (static_cast<int>(sizeof(HeaderC<kGroup>)) + group_list_bytes(groups) + 15) / 16 * 16;
 }
 
+// The sums of one scale's columns are below 2^10 in units of the codes' 2^-9;
+// the scales enter times 2^-10, so that no product with a sum leaves fp32's
+// range where the weights are inside it, and a unit's outputs are brought back.
+constexpr float kSmall = 0x1p-10f, kBack = 0x1p19f;
+
 // Both operands E4M3 (format 0), K-major, fp32 sums, M = 128, N = n.
 __device__ __forceinline__ uint32_t idesc_e4m3_f32(uint32_t n) {
   return (1u << 4) | ((n >> 3) << 17) | ((128u >> 4) << 24);
@@ -761,14 +766,14 @@ __global__ void __launch_bounds__(kThreads, 1)
             const int ar = 16 * a_block + g;
             if (kScales == 1 && a_half == 0 && c == 0) {  // rows g and g + 8
               const uint32_t v2 = *reinterpret_cast<const uint32_t*>(sc + g * 4);
-              hd->r[fs][0][ar] = __uint_as_float(v2 << 16) * 512.0f;
-              hd->r[fs][0][ar + 8] = __uint_as_float(v2 & 0xffff0000u) * 512.0f;
+              hd->r[fs][0][ar] = __uint_as_float(v2 << 16) * kSmall;
+              hd->r[fs][0][ar + 8] = __uint_as_float(v2 & 0xffff0000u) * kSmall;
             }
             if (kScales == 4 && c < 2) {  // row g + 8 c, this half's two groups
               const uint32_t v2 = *reinterpret_cast<const uint32_t*>(sc + g * 16 + c * 8 + a_half * 4);
-              hd->r[fs][(2 * a_half) % kScales][ar + 8 * c] = __uint_as_float(v2 << 16) * 512.0f;
+              hd->r[fs][(2 * a_half) % kScales][ar + 8 * c] = __uint_as_float(v2 << 16) * kSmall;
               hd->r[fs][(2 * a_half + 1) % kScales][ar + 8 * c] =
-                  __uint_as_float(v2 & 0xffff0000u) * 512.0f;
+                  __uint_as_float(v2 & 0xffff0000u) * kSmall;
             }
           }
           fence_proxy_async_smem();  // the tensor cores read the operands next
@@ -833,6 +838,8 @@ __global__ void __launch_bounds__(kThreads, 1)
         }
       }
       if (!ok) break;
+#pragma unroll
+      for (int j = 0; j < kTokens / 4; ++j) acc[j] *= kBack;
       write_unit<kSwiglu>(s, x, acc, weight, t0, cols, row, lane);
     }
     asm volatile("cp.async.wait_all;" ::: "memory");

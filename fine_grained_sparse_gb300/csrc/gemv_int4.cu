@@ -199,10 +199,16 @@ __device__ __forceinline__ void multiply_record(float (&acc)[4], const uint8_t* 
 }
 
 // What brings the sums of rows g and g + 8 back to units of 1: the codes are
-// in units of 2^-24 and 2^-20, the scales of x 2^12 too large (half of the
-// factor there and half here, so that neither small nor large values leave
-// fp32's range).
-constexpr float kUnitX = 4096.0f, kUnitLow = 4096.0f, kUnitHigh = 256.0f;
+// in units of 2^-24 and 2^-20, and part of that is in the factors of x, so
+// that neither small nor large values leave fp32's range.  The factors of bf16
+// rows are 2^12 too large, the scales of E4M3 rows 2^6 (a group of finite rows
+// has a scale below 2^120).
+template <bool kX8>
+__device__ constexpr float unit_x() { return kX8 ? 0x1p6f : 0x1p12f; }
+template <bool kX8>
+__device__ constexpr float unit_low() { return 0x1p24f / unit_x<kX8>(); }
+template <bool kX8>
+__device__ constexpr float unit_high() { return 0x1p20f / unit_x<kX8>(); }
 
 // One tile of tokens of one group against the CTA's blocks of that group.
 struct Tile {
@@ -214,7 +220,7 @@ struct Tile {
   int64_t x_row;     // row of x (or of perm) of token 0
 };
 
-template <bool kSwiglu>
+template <bool kSwiglu, bool kX8>
 __device__ __forceinline__ void store_block(const Int4Segment& s, const Tile& T, const float* row_w,
                                             const float (&acc)[4], int block, int g, int c) {
 #pragma unroll
@@ -222,7 +228,7 @@ __device__ __forceinline__ void store_block(const Int4Segment& s, const Tile& T,
     const int t = 2 * c + h;
     if (t >= T.n) continue;
     const int64_t r = (T.out_row + t) * s.out_ld;
-    const float z[2] = {acc[h] * kUnitLow, acc[2 + h] * kUnitHigh};
+    const float z[2] = {acc[h] * unit_low<kX8>(), acc[2 + h] * unit_high<kX8>()};
     if (kSwiglu) {
       // H is rounded to bf16, the type of the layer's activations
       s.out[r + block * 8 + g] = __float2bfloat16_rn(silu_f(z[0]) * z[1]);
@@ -290,7 +296,7 @@ __device__ __forceinline__ void load_x(const Int4Segment& s, const Tile& T, uint
       const int row = task / chunks, ch = task - row * chunks;
       if (kX8) {
         v[u] = e4m3x8_to_f16(make_uint2(v[u].x, v[u].y));
-        f[u] *= kUnitX;
+        f[u] *= unit_x<true>();
       } else {
         uint32_t e;
         v[u] = bf16x8_to_f16(v[u], e);
@@ -383,7 +389,7 @@ __device__ __forceinline__ void run_tile(const Int4Segment& s, const Divisor& by
       if (mid)
         put(first_slot);
       else
-        store_block<kSwiglu>(s, T, hd->row_w, acc, T.first_block + block, g, c);
+        store_block<kSwiglu, kX8>(s, T, hd->row_w, acc, T.first_block + block, g, c);
       mid = false;
       ch = 0;
       ++block;
@@ -414,7 +420,7 @@ __device__ __forceinline__ void run_tile(const Int4Segment& s, const Divisor& by
       if (lo >= (begun + 1ll) * nch) break;
       if (lo < total * (v + 1) / kWarps) add(so + v * kSlotBytes);
     }
-    store_block<kSwiglu>(s, T, hd->row_w, acc, T.first_block + begun, g, c);
+    store_block<kSwiglu, kX8>(s, T, hd->row_w, acc, T.first_block + begun, g, c);
   }
 }
 

@@ -1,6 +1,7 @@
 """Products with 4-bit weights at values off the ordinary: infinities and NaN
-in rows, and scales far apart within a row, on both sides of the limit between
-the streamed and the tensor-core kernels (40 rows of a group)."""
+in rows, scales far apart within a row, and scales near the ends of fp32's
+range, on both sides of the limit between the streamed and the tensor-core
+kernels (40 rows of a group)."""
 import numpy as np
 import pytest
 import torch
@@ -84,5 +85,22 @@ def test_scales_far_apart(T, apart, group, rows8):
     mask = zero == torch.arange(T)[:, None] % 4
     x[mask.cuda()] = 0
     x64[mask.numpy()] = 0
+    w = dequant64(q[0], s[0])
+    close(_linear(x, xs, q, s, group), x64 @ w.T, dot_bound(w, x64))
+
+
+@pytest.mark.parametrize("group", [32, 128])
+@pytest.mark.parametrize("x_exp,s_exp", [(121, -100), (-110, 127), (-100, -18), (100, -110)])
+@pytest.mark.parametrize("T", [5, 48, 100])
+def test_scales_near_the_ends_of_the_range(T, x_exp, s_exp, group):
+    """Scales whose products with the outputs' other factors leave fp32's range
+    although the outputs are far inside it."""
+    need_gpu()
+    gen = _gen(T + x_exp + s_exp + 300)
+    q, s = bank(gen, 1, 144, 512, group)
+    s = (s.double() * 2.0 ** s_exp).bfloat16()
+    x, xs, x64 = _rows(gen, T, 512, True)
+    xs, x64 = xs * 2.0 ** x_exp, x64 * 2.0 ** x_exp
+    assert torch.isfinite(xs).all() and torch.isfinite(s).all()
     w = dequant64(q[0], s[0])
     close(_linear(x, xs, q, s, group), x64 @ w.T, dot_bound(w, x64))
