@@ -2,7 +2,7 @@
 // (moe_add_rmsnorm).  Per row of d columns:
 //   s_i = a_i + r_i,  v_i = w_i s_i / sqrt(mean_i s_i^2 + eps)
 //   h = s, y = v, and per 128 columns  scale = max|v| / 448,
-//   code_i = e4m3(v_i / scale)
+//   code_i = e4m3(v_i / scale), the quotient rounded to fp32 first
 // Bound by HBM for many rows (each input read once, each output written
 // once) and by latency for few.
 #include "common.cuh"
@@ -76,15 +76,34 @@ __device__ __forceinline__ uint32_t e4m3x2(float a, float b) {
   return r;
 }
 
+// v[i] / s correctly rounded, for s and the largest |v[i]| well inside fp32's
+// range, by Markstein's theorem (IBM J. Res. Dev. 34, 1990): from y, 1 / s
+// correctly rounded, and q within an ulp of v / s, q + y (v - q s) is v / s
+// correctly rounded.  v y may be off by 1.5 ulp, so it takes two such steps.
+// Two values to an instruction: 8192 rows of 7168 bf16 with all outputs and a
+// flushed L2 in 96.5 us, with a division for each value 102.4.
 template <int N>
-__device__ __forceinline__ void store_codes(uint8_t* p, const float (&v)[N], float f) {
+__device__ __forceinline__ void divide(float (&v)[N], float s) {
+  const float y = 1.0f / s;
+#pragma unroll
+  for (int k = 0; k + 1 < N; k += 2)
+    asm("{\n\t.reg .b64 v, q, r, y, s;\n\t"
+        "mov.b64 v, {%0, %1};\n\tmov.b64 y, {%2, %2};\n\tmov.b64 s, {%3, %3};\n\t"
+        "mul.rn.f32x2 q, v, y;\n\t"
+        "fma.rn.f32x2 r, q, s, v;\n\tfma.rn.f32x2 q, r, y, q;\n\t"
+        "fma.rn.f32x2 r, q, s, v;\n\tfma.rn.f32x2 q, r, y, q;\n\t"
+        "mov.b64 {%0, %1}, q;\n\t}"
+        : "+f"(v[k]), "+f"(v[k + 1])
+        : "f"(y), "f"(-s));
+}
+
+template <int N>
+__device__ __forceinline__ void store_codes(uint8_t* p, const float (&q)[N]) {
   if constexpr (N == 8)
-    *reinterpret_cast<uint2*>(p) =
-        make_uint2(e4m3x2(v[0] * f, v[1] * f) | e4m3x2(v[2] * f, v[3] * f) << 16,
-                   e4m3x2(v[4] * f, v[5] * f) | e4m3x2(v[6] * f, v[7] * f) << 16);
+    *reinterpret_cast<uint2*>(p) = make_uint2(e4m3x2(q[0], q[1]) | e4m3x2(q[2], q[3]) << 16,
+                                              e4m3x2(q[4], q[5]) | e4m3x2(q[6], q[7]) << 16);
   else if constexpr (N == 4)
-    *reinterpret_cast<uint32_t*>(p) =
-        e4m3x2(v[0] * f, v[1] * f) | e4m3x2(v[2] * f, v[3] * f) << 16;
+    *reinterpret_cast<uint32_t*>(p) = e4m3x2(q[0], q[1]) | e4m3x2(q[2], q[3]) << 16;
 }
 
 struct NormPtrs {
@@ -179,14 +198,15 @@ __global__ void __launch_bounds__(kMaxThreads, kMinBlocks)
                                            : ((1u << (kLanes & 31)) - 1) << (threadIdx.x & 31 & ~(kLanes - 1));
 #pragma unroll
         for (int o = kLanes / 2; o; o >>= 1) m = max_nan(m, __shfl_xor_sync(mask, m, o));
-        // v / scale as v (448 / max), one rounding more than the quotient;
-        // small groups are brought up first, so that 448 / max is finite
-        const float up = m < 1e-30f ? 0x1p60f : 1.0f;
-        const float f = m == 0.0f ? 0.0f : 448.0f / (m * up);
+        const float scale = m / 448.0f;
+        if (m > 0x1p-60f && m < 0x1p126f) {
+          divide<N>(v, scale);
+        } else {  // zero, tiny and non-finite groups
 #pragma unroll
-        for (int k = 0; k < N; ++k) v[k] *= up;
-        store_codes<N>(p.y8 + base + at, v, f);
-        if ((tid & (kLanes - 1)) == 0) p.ys[row * (d / kRowGroup) + at / kRowGroup] = m / 448.0f;
+          for (int k = 0; k < N; ++k) v[k] = scale == 0.0f ? 0.0f : v[k] / scale;
+        }
+        store_codes<N>(p.y8 + base + at, v);
+        if ((tid & (kLanes - 1)) == 0) p.ys[row * (d / kRowGroup) + at / kRowGroup] = scale;
       }
     }
   };

@@ -453,9 +453,10 @@ int32_t moe_linear_int4(int64_t T, int32_t in_features, int32_t out_features, in
  *   h [T, d]        s, the new residual stream, or NULL
  *   y [T, d]        v, or NULL
  *   y_fp8 [T, d]    v in 8 bits, or NULL: per 128 columns of a row,
- *   y_scale [T, d / 128] fp32 = max |v| / 448 and E4M3 codes of v / scale
- *                   rounded to nearest (all 0 where the maximum is 0; a group
- *                   with a NaN has a NaN scale and NaN codes)
+ *   y_scale [T, d / 128] fp32 = max |v| / 448 and E4M3 codes of the fp32
+ *                   quotient v / scale rounded to nearest, at most 448 (all 0
+ *                   where the scale is 0; a group with a NaN has a NaN scale
+ *                   and NaN codes)
  * At least one of y and y_fp8; y_fp8 and y_scale together, with d % 128 == 0.
  * x, residual, weight [d], h and y are `dtype` (MOE_BF16 or MOE_F32); any
  * d >= 1 otherwise.  eps >= 0.  h and y may each be x or residual itself (not
