@@ -35,7 +35,7 @@ __all__ = [
     "split_router_weight",
     "MOE_WEIGHTS_PACKED_INT4_G32", "MOE_WEIGHTS_PACKED_INT4_G128", "moe_packed_int4_bytes",
     "moe_pack_weights_int4", "pack_int4", "moe_grouped_swiglu_fp8_rows", "moe_linear_int4",
-    "moe_add_rmsnorm",
+    "moe_add_rmsnorm", "moe_status_word",
 ]
 
 MOE_F32, MOE_BF16 = 0, 1
@@ -88,6 +88,7 @@ _SIGS = {
     "moe_validate_config": ([_CFG, _I64], _I32),
     "moe_workspace_size": ([_CFG, _I64], _SZ),
     "moe_get_device_status": ([_P, _P], _I32),
+    "moe_status_word": ([ctypes.POINTER(_P)], _I32),
     "moe_router": ([_CFG, _I64, _P, _P, _P, _P, _P, _P, _SZ, _P], _I32),
     "moe_router_from_logits": ([_CFG, _I64, _P, _P, _P, _P, _P], _I32),
     "moe_dense_gates": ([_CFG, _I64, _P, _P, _P, _P], _I32),
@@ -209,6 +210,14 @@ def moe_workspace_size(cfg: MoeConfig, T: int) -> int:
 
 def moe_get_device_status(workspace, stream=None) -> int:
     return lib.moe_get_device_status(_ptr(workspace), _stream(stream))
+
+
+def moe_status_word() -> int:
+    """The address, on the current device, of the status word of calls without
+    a workspace (moe_linear_int4), for moe_get_device_status."""
+    word = _P()
+    _check(lib.moe_status_word(ctypes.byref(word)), "moe_status_word")
+    return word.value
 
 
 def moe_router(cfg, T, x, W_r, bias, topk_idx, topk_w, workspace=None, ws_bytes=0, stream=None):

@@ -927,6 +927,14 @@ int32_t moe_get_device_status(void* workspace, void* stream) {
   return v;
 }
 
+int32_t moe_status_word(void** word) {
+  if (!word) return fail(MOE_ERR_INVALID_ARG, "word is null");
+  int* w = nullptr;
+  MOE_CUDA(library_status_word(&w));
+  *word = w;
+  return MOE_OK;
+}
+
 int32_t moe_router(const moe_config* cfg, int64_t T, const void* x, const float* W_r,
                    const float* bias, int32_t* topk_idx, float* topk_w, void* workspace,
                    size_t ws_bytes, void* stream) {

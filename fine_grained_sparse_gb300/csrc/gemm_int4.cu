@@ -18,6 +18,11 @@
 namespace fgs {
 namespace {
 
+// Where a launch that brings no status word (a linear map has no workspace)
+// records that a wait expired, at its end: one word of the library's on each
+// device.
+__device__ int library_status;
+
 constexpr int kWorkers = 16;  // warps that make the operands and add up the chunks' sums
 constexpr int kThreads = 32 * (kWorkers + 1);  // and the one that issues the MMAs
 constexpr int kBlocks = 8;    // row blocks of a unit
@@ -464,14 +469,16 @@ __global__ void __launch_bounds__(kThreadsB, 1)
       // nothing is in flight when the CTA gives its TMEM back
       tc_commit(bar(hd->drain));
       int own_abort = 0;
-      mbar_wait_bounded(bar(hd->drain), 0, &own_abort, p.status);
+      if (!mbar_wait_bounded(bar(hd->drain), 0, &own_abort, p.status)) hd->abort = 1;
     }
     __syncwarp();
   }
   if (p.wait != kWaitWeights) pdl_wait();  // a kernel ends after the one before it has
   tc_fence_before();
   __syncthreads();
+  if (threadIdx.x == 0 && hd->abort && !p.status) record_status(&library_status, MOE_ERR_TIMEOUT);
   if (warp == 0) {
+    __syncwarp();
     tc_fence_after();
     tmem_dealloc(tmem, kTmemColsB);
   }
@@ -879,14 +886,16 @@ __global__ void __launch_bounds__(kThreads, 1)
       // nothing is in flight when the CTA gives its TMEM back
       tc_commit(bar(hd->drain));
       int own_abort = 0;
-      mbar_wait_bounded(bar(hd->drain), 0, &own_abort, p.status);
+      if (!mbar_wait_bounded(bar(hd->drain), 0, &own_abort, p.status)) hd->abort = 1;
     }
     __syncwarp();
   }
   if (p.wait != kWaitWeights) pdl_wait();  // a kernel ends after the one before it has
   tc_fence_before();
   __syncthreads();
+  if (threadIdx.x == 0 && hd->abort && !p.status) record_status(&library_status, MOE_ERR_TIMEOUT);
   if (warp == 0) {
+    __syncwarp();
     tc_fence_after();
     tmem_dealloc(tmem, kTmemCols);
   }
@@ -938,6 +947,10 @@ cudaError_t launch_gemm_int4(const Int4Launch& p, bool swiglu, int group, int nu
                        : group == 32 ? gemm_int4_bf16_kernel<false, 32, 128>
                                      : gemm_int4_bf16_kernel<false, 128, 128>,
                        l, kThreadsB, num_sms, stream);
+}
+
+cudaError_t library_status_word(int** word) {
+  return cudaGetSymbolAddress(reinterpret_cast<void**>(word), library_status);
 }
 
 cudaError_t launch_int4(const Int4Params& q, int num_sms, cudaStream_t stream) {

@@ -79,7 +79,7 @@ struct Int4Launch {
   int cap[2];  // gemv: tokens of a tile
   Divisor chunks[2], ctas;  // gemv: seg[i].chunks, the CTAs
   int smem;    // bytes of shared memory
-  int* status; // device status word, or null
+  int* status; // device status word; null: the library's
 };
 cudaError_t launch_gemv_int4(const Int4Launch& p, bool swiglu, int group, int num_sms,
                              cudaStream_t stream);

@@ -327,9 +327,11 @@ struct Int4Params {
   // 1: the previous launch of the stream was launch_int4 and wrote nothing
   // that this one reads but x
   int early = 0;
-  int* status = nullptr;
+  int* status = nullptr;  // device status word; null: the library's
 };
 cudaError_t launch_int4(const Int4Params& p, int num_sms, cudaStream_t stream);
+// The library's status word on the current device (zero-initialised).
+cudaError_t library_status_word(int** word);
 int64_t packed_int4_bytes(int64_t groups, int64_t rows, int64_t cols, int group);
 cudaError_t launch_pack_int4(int gate_up, int64_t groups, int64_t rows, int64_t cols, int group,
                              const void* codes, const void* scales, void* dst,

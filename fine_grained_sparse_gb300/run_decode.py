@@ -165,7 +165,7 @@ def main(argv=None):
         b(attn, res)
     stop.record()
     torch.cuda.synchronize()
-    status = fgs.moe_get_device_status(b.ws)
+    status = fgs.moe_get_device_status(b.ws) or fgs.moe_get_device_status(fgs.moe_status_word())
     if status:
         raise SystemExit("device status: " + fgs.moe_status_string(status))
     print(f"block of {a.T} tokens: {start.elapsed_time(stop) / a.iters * 1e3:.1f} us")

@@ -258,6 +258,13 @@ size_t moe_workspace_size(const moe_config* cfg, int64_t T);
  * since the last read. */
 int32_t moe_get_device_status(void* workspace, void* stream);
 
+/* The status word, on the current device, of the calls that take no
+ * workspace but wait on the device (moe_linear_int4): *word is passed to
+ * moe_get_device_status like a workspace.  One word a device for the whole
+ * process, MOE_OK at the start.  Returns MOE_ERR_INVALID_ARG for a null
+ * argument, MOE_ERR_CUDA without a device. */
+int32_t moe_status_word(void** word);
+
 /* Bytes of the split router weight: 6 * E_routed * d_model; 0 for a NULL
  * cfg or sizes moe_split_router_weight rejects. */
 size_t moe_router_weight_split_bytes(const moe_config* cfg);
@@ -439,7 +446,7 @@ int32_t moe_linear(int64_t T, int32_t in_features, int32_t out_features, const v
  *   group_size), add [T, out] bf16 or NULL, y [T, out] bf16 (y may be add).
  * in a multiple of 128, at most 32768, out one of 16; group_size 32 or 128.
  * Sums in fp32, one rounding to bf16.  Needs no workspace; a bounded device
- * wait that expires (T > 40) is not reported by this entry point. */
+ * wait that expires (T > 40) is recorded in the word of moe_status_word. */
 int32_t moe_linear_int4(int64_t T, int32_t in_features, int32_t out_features, int32_t group_size,
                         const void* x, const float* x_scale, const void* W, const void* add,
                         void* y, void* stream);
