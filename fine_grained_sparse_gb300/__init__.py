@@ -441,14 +441,34 @@ def moe_pack_weights_int4(kind, groups, rows, cols, group_size, codes, scales, d
 def pack_int4(kind, codes, scales, stream=None):
     """One 4-bit bank packed into a new uint8 buffer: codes [G, rows, cols / 2]
     uint8 (two a byte, the even column low) and scales [G, rows, cols /
-    group_size] bf16, kind as in moe_pack_weights (a one-time load step)."""
+    group_size] bf16, on one GPU, kind as in moe_pack_weights (a one-time load
+    step).  Raises ValueError for tensors of other types or shapes, MoeError
+    for sizes that moe_pack_weights_int4 rejects.  A given stream waits for the
+    current one, whose memory the result is."""
     import torch
+    if codes.dtype != torch.uint8 or scales.dtype != torch.bfloat16:
+        raise ValueError(f"pack_int4: uint8 codes and bfloat16 scales, not {codes.dtype} and "
+                         f"{scales.dtype}")
+    if (codes.dim() != 3 or scales.dim() != 3 or codes.shape[:2] != scales.shape[:2]
+            or scales.shape[2] < 1 or 2 * codes.shape[2] % scales.shape[2]):
+        raise ValueError(f"pack_int4: codes [G, rows, cols / 2] and scales [G, rows, cols / "
+                         f"group_size], not {list(codes.shape)} and {list(scales.shape)}")
+    if not codes.is_cuda or codes.device != scales.device:
+        raise ValueError(f"pack_int4: codes and scales on one GPU, not {codes.device} and "
+                         f"{scales.device}")
     G, R, C = codes.shape[0], codes.shape[1], 2 * codes.shape[2]
     group = C // scales.shape[2]
     dst = torch.empty(max(moe_packed_int4_bytes(G, R, C, group), 0), dtype=torch.uint8,
                       device=codes.device)
-    moe_pack_weights_int4(kind, G, R, C, group, codes.contiguous(), scales.contiguous(), dst,
-                          stream)
+    codes, scales = codes.contiguous(), scales.contiguous()
+    if stream is not None:
+        if isinstance(stream, int):
+            stream = (torch.cuda.ExternalStream(stream) if stream
+                      else torch.cuda.default_stream(codes.device))
+        stream.wait_stream(torch.cuda.current_stream())
+        for t in (codes, scales, dst):  # not handed out again while the packing runs there
+            t.record_stream(stream)
+    moe_pack_weights_int4(kind, G, R, C, group, codes, scales, dst, stream)
     return dst
 
 
