@@ -139,6 +139,7 @@ __global__ void __launch_bounds__(kMaxThreads, kMinBlocks)
   const T* r = p.r ? static_cast<const T*>(p.r) + base : nullptr;
   const T* w = static_cast<const T*>(p.w);
   const int pieces = live ? d / N : 0;
+  const uint32_t wide = pieces;  // unsigned: a step beyond the last piece may pass 2^31
 
   auto sum = [&](int i) {
     Piece<T, N> s = load<N>(a + static_cast<int64_t>(i) * N);
@@ -161,7 +162,7 @@ __global__ void __launch_bounds__(kMaxThreads, kMinBlocks)
 #pragma unroll
         for (int k = 0; k < N; ++k) q = fmaf(keep[j].v[k], keep[j].v[k], q);
   } else {
-    for (int i = tid; i < pieces; i += threads) {
+    for (uint32_t i = tid; i < wide; i += threads) {
       const Piece<T, N> s = sum(i);
 #pragma unroll
       for (int k = 0; k < N; ++k) q = fmaf(s.v[k], s.v[k], q);
@@ -215,7 +216,7 @@ __global__ void __launch_bounds__(kMaxThreads, kMinBlocks)
     for (int j = 0; j < kKeep; ++j)
       if (tid + j * threads < pieces) finish(tid + j * threads, keep[j]);
   } else {
-    for (int i = tid; i < pieces; i += threads) finish(i, sum(i));
+    for (uint32_t i = tid; i < wide; i += threads) finish(i, sum(i));
   }
 }
 
