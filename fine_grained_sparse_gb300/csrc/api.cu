@@ -1271,7 +1271,7 @@ int32_t moe_add_rmsnorm(int32_t dtype, int64_t T, int32_t d, const void* x, cons
   n.y = y;
   n.y8 = static_cast<uint8_t*>(y_fp8);
   n.ys = y_scale;
-  MOE_CUDA(launch_add_rmsnorm(n, static_cast<cudaStream_t>(stream)));
+  MOE_CUDA(launch_add_rmsnorm(n, num_sms(), static_cast<cudaStream_t>(stream)));
   return MOE_OK;
 }
 

@@ -292,7 +292,7 @@ struct NormArgs {
   uint8_t* y8 = nullptr;    // [T, d] E4M3 codes, or null
   float* ys = nullptr;      // [T, d / 128] scales (with y8)
 };
-cudaError_t launch_add_rmsnorm(const NormArgs& n, cudaStream_t stream);
+cudaError_t launch_add_rmsnorm(const NormArgs& n, int num_sms, cudaStream_t stream);
 
 // --------------------------------------------------- products with 4-bit weights
 // The widest x: a row of it stays in shared memory beside the ring of weights.
