@@ -461,7 +461,6 @@ int32_t run_experts_int4(const moe_config* c, int64_t T, const ExpertIO& io, voi
   r.rows = T;  // the K experts of a token are distinct
   r.x = io.x_e;
   r.x_scale = io.x_scale;
-  r.x_ld = de;
   r.perm = io.perm;
   r.perm_div = c->K;
   r.out = H;
@@ -475,7 +474,6 @@ int32_t run_experts_int4(const moe_config* c, int64_t T, const ExpertIO& io, voi
     s.rows = T;
     s.x = io.x_shared;
     s.x_scale = io.x_shared_scale;
-    s.x_ld = d;
     s.out = Hs;
     s.out_ld = Fs;
     s.out_group_rows = T;
@@ -497,7 +495,6 @@ int32_t run_experts_int4(const moe_config* c, int64_t T, const ExpertIO& io, voi
   r2.offsets = io.offsets;
   r2.rows = T;
   r2.x = H;
-  r2.x_ld = F;
   r2.out = static_cast<__nv_bfloat16*>(io.Y);
   r2.out_ld = de;
   if (weights_in_Y && io.topk_w) {
@@ -512,7 +509,6 @@ int32_t run_experts_int4(const moe_config* c, int64_t T, const ExpertIO& io, voi
     s2.chunks = Fs / 128;
     s2.rows = T;
     s2.x = Hs;
-    s2.x_ld = Fs;
     s2.x_group_rows = T;
     s2.out = static_cast<__nv_bfloat16*>(io.Y_shared);
     s2.out_ld = d;
@@ -1236,7 +1232,6 @@ int32_t moe_linear_int4(int64_t T, int32_t in_features, int32_t out_features, in
   s.rows = T;
   s.x = x;
   s.x_scale = x_scale;
-  s.x_ld = in_features;
   s.out = static_cast<__nv_bfloat16*>(y);
   s.out_ld = out_features;
   s.add = static_cast<const __nv_bfloat16*>(add);

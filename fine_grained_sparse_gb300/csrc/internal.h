@@ -306,9 +306,8 @@ struct Int4Segment {
   int chunks = 0;
   const int32_t* offsets = nullptr;  // rows of group g: [offsets[g], offsets[g + 1]); or null
   int64_t rows = 0;                  // rows of every group; with offsets, the most of any
-  const void* x = nullptr;           // bf16, or E4M3 codes when x_scale is set
+  const void* x = nullptr;           // bf16, or E4M3 codes when x_scale is set; rows of chunks x 128
   const float* x_scale = nullptr;    // [x rows, chunks]
-  int64_t x_ld = 0;
   int64_t x_group_rows = 0;          // implicit rows: x row of group g, row t is g * this + t
   const int32_t* perm = nullptr;     // explicit rows: x row of row r is perm[r] / perm_div
   int perm_div = 1;
