@@ -160,13 +160,24 @@ __device__ __forceinline__ void bulk_load(uint32_t dst, const void* src, uint32_
 
 // Programmatic dependent launch.  pdl_release lets the next kernel of the
 // stream (launched with programmatic stream serialization) start launching
-// once every CTA of this grid has released or exited; the persistent GEMM
-// releases when its work is done, before its teardown (released at the
-// start, waiting CTAs of the next kernel sat beside the running ones and
-// cost time), the other kernels release by exiting.  pdl_wait blocks until
+// once every CTA of this grid has released or exited.  pdl_wait blocks until
 // the previous kernel of the stream has completed and its writes are
-// visible; every kernel calls it before its first global memory access.
-// Both are no-ops for a kernel launched without the attribute.
+// visible.  Both are no-ops for a kernel launched without the attribute.
+//  - The kernels for 4-bit weights release at their start, so that the next
+//    launch plans its work while this one drains.  The persistent GEMM
+//    releases when its work is done, before its teardown (released at the
+//    start, waiting CTAs of the next kernel sat beside the running ones and
+//    cost time); the other kernels release by exiting.
+//  - A kernel may start while the one before it runs, and while that one waits
+//    for the one before it.  So every kernel launched with the attribute waits
+//    in every thread, at the latest before it ends: whoever has waited knows
+//    that all earlier kernels of the stream have ended, not only the last.
+//  - They wait before their first global memory access, but for the
+//    second launch of a pass with 4-bit weights and the down pass after its
+//    gate/up pass.  Those read weights and routing first (Int4Launch::wait):
+//    the pass's first launch with routing waits before it releases, so what was
+//    there before the pass is there, and what the pass itself wrote is read
+//    only after the wait.
 __device__ __forceinline__ void pdl_release() {
   asm volatile("griddepcontrol.launch_dependents;" ::: "memory");
 }

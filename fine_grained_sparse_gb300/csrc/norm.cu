@@ -230,10 +230,11 @@ cudaError_t launch(const NormArgs& n, int threads, cudaStream_t stream) {
 }
 
 // Threads of a row.  Few rows are a matter of latency: a thread a piece.
-// Many (two an SM) are one of bandwidth: two pieces a thread, with the registers held to
-// three blocks of 512 an SM (8192 x 7168 bf16 with all outputs, 530 MB: 448
-// threads x 2 so held 90.4 us, not held 108.0; 896 x 1 91.5; 224 x 4 held to
-// 6 blocks 91.9, not held 100.6; 128 x 7 104.7; the copy rate allows 78.4).
+// Many (two an SM) are one of bandwidth: two pieces a thread, with the
+// registers held to three blocks of 512 an SM (8192 x 7168 bf16 with all
+// outputs, 530 MB: 448 threads x 2 so held 90.4 us, not held 108.0; 896 x 1
+// 91.5; 224 x 4 held to 6 blocks 91.9, not held 100.6; 128 x 7 104.7; the copy
+// rate allows 78.4).
 template <typename T, int N>
 cudaError_t dispatch(const NormArgs& n, int num_sms, cudaStream_t stream) {
   const int pieces = n.d / N;
@@ -242,7 +243,7 @@ cudaError_t dispatch(const NormArgs& n, int num_sms, cudaStream_t stream) {
   if (pieces <= 128) return launch<T, N, false, 1, 1024>(n, round32(pieces), stream);
   if (pieces <= 1024)
     return n.T < 2 * num_sms ? launch<T, N, false, 1, 1024>(n, round32(pieces), stream)
-                           : launch<T, N, false, 2, 512, 3>(n, round32((pieces + 1) / 2), stream);
+                             : launch<T, N, false, 2, 512, 3>(n, round32((pieces + 1) / 2), stream);
   if (pieces <= 4096) return launch<T, N, false, 4, 1024>(n, round32((pieces + 3) / 4), stream);
   return launch<T, N, false, 0, 1024>(n, 1024, stream);
 }
