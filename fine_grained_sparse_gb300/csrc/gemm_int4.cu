@@ -9,10 +9,11 @@
 //
 // All products are exact.  What bounds both is making the first operand:
 // a block of 128 x 128 weights is 16 to 18 KB of HBM, but some 4500 warp
-// instructions from codes to swizzled operand to sums (with bf16 rows, 96
-// tokens and 17 experts' groups of which 11 come here: 4520 at 2.5 a cycle and
-// SM, tensor pipe 39% active, shared-memory pipe 47%).  It is made once for
-// all of a unit's tokens, so the form pays from kGemvRows rows on.
+// instructions from codes to swizzled operand to sums (96 tokens and 17
+// experts' groups of which 11 come here: 4580 with bf16 rows at 2.5 a cycle
+// and SM, tensor pipe 39% active, shared-memory pipe 48%; E4M3 rows 4460 with
+// groups of 128, 5740 with groups of 32).  It is made once for all of a unit's
+// tokens, so the form pays from kGemvRows rows on.
 #include "int4.cuh"
 
 namespace fgs {
@@ -912,10 +913,13 @@ cudaError_t launch_kernel(Kernel kernel, const Int4Launch& p, int threads, int n
   return launch_pdl(kernel, dim3(num_sms), dim3(threads), p.smem, stream, p);
 }
 
-// Rows of a group up to which it is read by gemv_int4.cu: five passes of eight
-// rows, at 52 cycles a record and SM each, cost what making the operand here
-// does, about 250 (896 experts and a shared one of 24 rows: 916 us; 947 with
-// the limit at 16 rows, which sends that one here).
+// Rows of a group up to which it is read by gemv_int4.cu.  Among many groups a
+// pass of eight rows costs 52 cycles a record and SM, HBM's rate, and making
+// the operand here about 250, whatever the rows up to 128: 896 experts of 1 or
+// 7 rows and two shared ones of 24 take 916 us, 947 with the limit at 16,
+// which sends those two here.  One group alone crosses earlier: a map from 7168
+// to 18432 columns, groups of 32, takes 59.6 us for 32 tokens and 76 to 78
+// for 33 to 40 streamed, 57.6 for 41 here (E4M3 rows 57.8, 72 to 74, 69.7).
 constexpr int kGemvRows = 40;
 
 }  // namespace

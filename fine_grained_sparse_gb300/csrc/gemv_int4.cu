@@ -249,10 +249,12 @@ __device__ __forceinline__ void store_block(const Int4Segment& s, const Tile& T,
 // with one fp32 factor per 128 columns (at fo, [chunk][kTile]), and its row
 // weights.  A half warp takes 128 columns.  bf16 values are scaled by the
 // power of two that brings the largest of them to [2^14, 2^15): exact for
-// every value above 2^-29 of it, and within 2^-40 of it below.  E4M3 values
-// are exact.  Pieces of a row are moved within 128 bytes by the row's number
-// (16-byte piece q of a chunk to q ^ 4 (t & 1)), so that a fragment load of
-// eight tokens meets every bank once.
+// every value above 2^-31 of it, and within 2^-39 of it below.  That is the
+// price of f16 fragments (bf16 ones hold every value, at 5.3 instead of 6.9
+// TB/s), and 2^-15 of what an fp32 sum loses beside the largest value.  E4M3
+// values are exact.  Pieces of a row are moved within 128 bytes by the row's
+// number (16-byte piece q of a chunk to q ^ 4 (t & 1)), so that a fragment
+// load of eight tokens meets every bank once.
 // between() runs after the first loads have been asked for.
 template <bool kX8, typename Between>
 __device__ __forceinline__ void load_x(const Int4Segment& s, const Tile& T, uint8_t* smem,

@@ -122,7 +122,10 @@ typedef enum moe_router_weight_form {
  *     multiples of 128 and at most 32768.  The weights enter the tensor cores
  *     exactly: as code - 8, with the scale applied to the sum over its columns
  *     in fp32, or (bf16 rows of an expert with more than 40) as two bf16
- *     values whose sum is (code - 8) scale.  Sums are fp32. */
+ *     values whose sum is (code - 8) scale.  E4M3 rows enter exactly, and so do
+ *     bf16 rows, except that for an expert with up to 40 of them a value below
+ *     2^-31 of the largest of its 128 columns is off by up to 2^-39 of that one.
+ *     Sums are fp32; H is rounded to bf16 as in the bf16 form. */
 typedef enum moe_weight_layout {
   MOE_WEIGHTS_NATURAL = 0,
   MOE_WEIGHTS_PACKED = 1,

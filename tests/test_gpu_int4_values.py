@@ -1,7 +1,7 @@
 """Products with 4-bit weights at values off the ordinary: infinities and NaN
-in rows, scales far apart within a row, and scales near the ends of fp32's
-range, on both sides of the limit between the streamed and the tensor-core
-kernels (40 rows of a group)."""
+in rows, scales far apart within a row, scales near the ends of fp32's range,
+and large values beside ordinary ones, on both sides of the limit between the
+streamed and the tensor-core kernels (40 rows of a group)."""
 import numpy as np
 import pytest
 import torch
@@ -104,3 +104,20 @@ def test_scales_near_the_ends_of_the_range(T, x_exp, s_exp, group):
     assert torch.isfinite(xs).all() and torch.isfinite(s).all()
     w = dequant64(q[0], s[0])
     close(_linear(x, xs, q, s, group), x64 @ w.T, dot_bound(w, x64))
+
+
+@pytest.mark.parametrize("group", [32, 128])
+@pytest.mark.parametrize("T", [5, 40, 48, 100])
+def test_large_values_beside_ordinary_ones(T, group):
+    """bf16 rows with values up to 2^30 times the smallest ones in columns whose
+    weights are zero: the others' products are right by themselves."""
+    need_gpu()
+    gen = _gen(T + group)
+    q, s = bank(gen, 1, 144, 512, group)
+    q[:, :, ::32] = 0x88  # columns 0 and 1 of every 64: code 8, weight 0
+    sign = torch.randint(0, 2, (T, 512), generator=gen) * 2 - 1
+    x = (torch.rand((T, 512), generator=gen) * 3 + 1) * sign
+    x.view(T, 8, 64)[:, :, :2] *= 2.0 ** 28
+    x = x.bfloat16()
+    w, x64 = dequant64(q[0], s[0]), x.double().numpy()
+    close(_linear(x.cuda(), None, q, s, group), x64 @ w.T, dot_bound(w, x64))
