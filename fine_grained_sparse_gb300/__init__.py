@@ -462,10 +462,11 @@ def pack_int4(kind, codes, scales, stream=None):
                       device=codes.device)
     codes, scales = codes.contiguous(), scales.contiguous()
     if stream is not None:
-        if isinstance(stream, int):
-            stream = (torch.cuda.ExternalStream(stream) if stream
+        if not isinstance(stream, torch.cuda.Stream):
+            handle = _stream(stream)
+            stream = (torch.cuda.ExternalStream(handle, device=codes.device) if handle
                       else torch.cuda.default_stream(codes.device))
-        stream.wait_stream(torch.cuda.current_stream())
+        stream.wait_stream(torch.cuda.current_stream(codes.device))
         for t in (codes, scales, dst):  # not handed out again while the packing runs there
             t.record_stream(stream)
     moe_pack_weights_int4(kind, G, R, C, group, codes, scales, dst, stream)

@@ -9,7 +9,14 @@ from test_gpu_int4 import _gen
 pytestmark = pytest.mark.gpu
 
 
-@pytest.mark.parametrize("how", ["stream", "handle", "current"])
+class _Foreign:
+    """A stream of another library: whatever has its handle as cuda_stream."""
+
+    def __init__(self, handle):
+        self.cuda_stream = handle
+
+
+@pytest.mark.parametrize("how", ["stream", "handle", "foreign", "default", "current"])
 def test_views_on_another_stream(how):
     """Copies made for the packing and the result belong to the current stream:
     work there before the call is seen, and the copies' memory is not handed out
@@ -25,7 +32,8 @@ def test_views_on_another_stream(how):
     torch.cuda.synchronize()
     torch.cuda._sleep(20_000_000)  # the current stream is behind
     late.copy_(qt)
-    stream = {"stream": side, "handle": side.cuda_stream, "current": None}[how]
+    stream = {"stream": side, "handle": side.cuda_stream, "foreign": _Foreign(side.cuda_stream),
+              "default": 0, "current": None}[how]
     got = fgs.pack_int4(fgs.MOE_PACK_GATE_UP, late, st, stream=stream)
     junk = [torch.full_like(q, 7) for _ in range(4)]  # takes freed memory of that size, if any
     torch.cuda.synchronize()
