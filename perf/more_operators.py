@@ -159,7 +159,8 @@ def _routing(g, T, K, E, bad):
     some indices outside [0, E) when ``bad`` is set."""
     popular = torch.rand((E,), generator=g, device="cuda") * math.log(10.0)
     noise = torch.rand((T, E), generator=g, device="cuda").clamp_min_(1e-9)
-    idx = (popular - torch.log(-torch.log(noise).clamp_min_(1e-9))).topk(K, dim=1).indices
+    gumbel = -torch.log((-torch.log(noise)).clamp_min_(1e-9))
+    idx = (popular + gumbel).topk(K, dim=1).indices
     if bad:
         idx[torch.rand((T, K), generator=g, device="cuda") < bad] = E
     return idx.to(torch.int32)
