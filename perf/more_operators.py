@@ -476,8 +476,8 @@ def _plain_adamw(s):
     q = torch.where(scale[:, None] > 0, r / scale[:, None], torch.zeros_like(r))
     u = _noise(s)
     # below 2^-6 the codes are 2^-9 apart, above it a mantissa's three bits
-    low = torch.floor(q * 512.0 + u.float() * 2.0 ** -16).to(torch.int32)
-    high = (q.view(torch.int32) + (u << 4) >> 20) - (120 << 3)
+    low = torch.floor(q * 512.0 + (u.float() + 0.5) * 2.0 ** -16).to(torch.int32)
+    high = (q.view(torch.int32) + (u << 4) + 8 >> 20) - (120 << 3)
     code = torch.where(q < 2.0 ** -6, low, high).clamp(0, 0x7E)
     code = torch.where((code == 0) & (r > 0), 1, code)
     s["v"].view(torch.uint8).copy_(code)
