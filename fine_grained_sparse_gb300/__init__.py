@@ -36,6 +36,9 @@ __all__ = [
     "MOE_WEIGHTS_PACKED_INT4_G32", "MOE_WEIGHTS_PACKED_INT4_G128", "moe_packed_int4_bytes",
     "moe_pack_weights_int4", "pack_int4", "moe_grouped_swiglu_fp8_rows", "moe_linear_int4",
     "moe_add_rmsnorm", "moe_status_word",
+    "moe_gather", "moe_combine_backward", "moe_router_backward", "moe_add_layernorm",
+    "MOE_NORM_RMS", "MOE_NORM_LAYER", "moe_norm_backward", "moe_norm_backward_workspace_size",
+    "AdamwTensor", "AdamwTable", "adamw_table", "moe_adamw",
 ]
 
 MOE_F32, MOE_BF16 = 0, 1
@@ -43,6 +46,7 @@ MOE_WEIGHTS_NATURAL, MOE_WEIGHTS_PACKED, MOE_WEIGHTS_PACKED_FP8 = 0, 1, 2
 MOE_WEIGHTS_PACKED_INT4_G32, MOE_WEIGHTS_PACKED_INT4_G128 = 3, 4
 MOE_PACK_GATE_UP, MOE_PACK_PLAIN = 0, 1
 MOE_ROUTER_WEIGHT_F32, MOE_ROUTER_WEIGHT_SPLIT = 0, 1
+MOE_NORM_RMS, MOE_NORM_LAYER = 0, 1
 MOE_STAGE_COUNT = 5
 STAGE_NAMES = ("router", "dispatch", "expert_gate_up", "expert_down", "combine")
 STATUS = {0: "MOE_OK", 1: "MOE_ERR_INVALID_ARG", 2: "MOE_ERR_UNSUPPORTED_SHAPE",
@@ -67,6 +71,15 @@ class MoeConfig(ctypes.Structure):
     ]
 
 
+class AdamwTensor(ctypes.Structure):
+    _fields_ = [
+        ("param", ctypes.c_void_p), ("grad", ctypes.c_void_p), ("master", ctypes.c_void_p),
+        ("exp_avg", ctypes.c_void_p), ("exp_avg_sq", ctypes.c_void_p),
+        ("exp_avg_scale", ctypes.c_void_p), ("exp_avg_sq_scale", ctypes.c_void_p),
+        ("n", ctypes.c_int64), ("weight_decay", ctypes.c_double),
+    ]
+
+
 def _load():
     path = lib_path()
     if not os.path.exists(path):
@@ -79,6 +92,7 @@ def _load():
 lib = _load()
 
 _P, _I32, _I64, _SZ, _F = ctypes.c_void_p, ctypes.c_int32, ctypes.c_int64, ctypes.c_size_t, ctypes.c_float
+_D, _U64 = ctypes.c_double, ctypes.c_uint64
 _CFG = ctypes.POINTER(MoeConfig)
 _SIGS = {
     "moe_version": ([], _I32),
@@ -107,6 +121,13 @@ _SIGS = {
     "moe_grouped_swiglu_fp8_rows": ([_CFG, _I64] + [_P] * 14 + [_SZ, _P], _I32),
     "moe_linear_int4": ([_I64, _I32, _I32, _I32] + [_P] * 6, _I32),
     "moe_add_rmsnorm": ([_I32, _I64, _I32, _P, _P, _P, _F] + [_P] * 5, _I32),
+    "moe_gather": ([_CFG, _I64] + [_P] * 6, _I32),
+    "moe_combine_backward": ([_CFG, _I64] + [_P] * 7, _I32),
+    "moe_router_backward": ([_CFG, _I64] + [_P] * 5, _I32),
+    "moe_add_layernorm": ([_I32, _I64, _I32, _P, _P, _P, _P, _F, _P, _P, _P], _I32),
+    "moe_norm_backward_workspace_size": ([_I64, _I32], _SZ),
+    "moe_norm_backward": ([_I32, _I32, _I64, _I32, _P, _P, _P, _F] + [_P] * 6 + [_SZ, _P], _I32),
+    "moe_adamw": ([_I32, _P, _I32, _I32, _I32, _D, _D, _D, _D, _I64, _P, _U64, _P], _I32),
     "moe_router_noalloc": ([_CFG, _I64, _P, _P, _P, _P, _P, _P], _I32),
     "moe_router_weight_split_bytes": ([_CFG], _SZ),
     "moe_split_router_weight": ([_CFG, _P, _P, _P], _I32),
@@ -498,3 +519,91 @@ def moe_add_rmsnorm(dtype, T, d, x, residual, weight, eps, h, y, y_fp8=None, y_s
     _check(lib.moe_add_rmsnorm(dtype, T, d, _ptr(x), _ptr(residual), _ptr(weight), float(eps),
                                _ptr(h), _ptr(y), _ptr(y_fp8), _ptr(y_scale), _stream(stream)),
            "moe_add_rmsnorm")
+
+
+def moe_gather(cfg, T, x, inv, topk_w, x_perm, w_perm=None, stream=None):
+    """x_perm[inv] = x (and w_perm[inv] = topk_w): the rows in expert order."""
+    _check(lib.moe_gather(ctypes.byref(cfg), T, _ptr(x), _ptr(inv), _ptr(topk_w), _ptr(x_perm),
+                          _ptr(w_perm), _stream(stream)), "moe_gather")
+
+
+def moe_combine_backward(cfg, T, dy, Y, inv, topk_w, dY, dtopk_w, stream=None):
+    """dY[inv] = w dy and dtopk_w = <Y[inv], dy>: the gradient of moe_combine."""
+    _check(lib.moe_combine_backward(ctypes.byref(cfg), T, _ptr(dy), _ptr(Y), _ptr(inv),
+                                    _ptr(topk_w), _ptr(dY), _ptr(dtopk_w), _stream(stream)),
+           "moe_combine_backward")
+
+
+def moe_router_backward(cfg, T, logits, topk_idx, dtopk_w, dlogits, stream=None):
+    """dlogits [T, E] of the gradient of the selected experts' weights."""
+    _check(lib.moe_router_backward(ctypes.byref(cfg), T, _ptr(logits), _ptr(topk_idx),
+                                   _ptr(dtopk_w), _ptr(dlogits), _stream(stream)),
+           "moe_router_backward")
+
+
+def moe_add_layernorm(dtype, T, d, x, residual, weight, bias, eps, h, y, stream=None):
+    """h = x + residual, y = weight * (h - mean) / sqrt(var + eps) + bias."""
+    _check(lib.moe_add_layernorm(dtype, T, d, _ptr(x), _ptr(residual), _ptr(weight), _ptr(bias),
+                                 float(eps), _ptr(h), _ptr(y), _stream(stream)),
+           "moe_add_layernorm")
+
+
+def moe_norm_backward_workspace_size(T, d) -> int:
+    return int(lib.moe_norm_backward_workspace_size(T, d))
+
+
+def moe_norm_backward(kind, dtype, T, d, x, residual, weight, eps, dy, dh, dx, dweight, dbias,
+                      workspace=None, ws_bytes=0, stream=None):
+    """The gradients of moe_add_rmsnorm (MOE_NORM_RMS) or moe_add_layernorm
+    (MOE_NORM_LAYER): dx [T, d], dweight and dbias [d] fp32, each or None."""
+    _check(lib.moe_norm_backward(kind, dtype, T, d, _ptr(x), _ptr(residual), _ptr(weight),
+                                 float(eps), _ptr(dy), _ptr(dh), _ptr(dx), _ptr(dweight),
+                                 _ptr(dbias), _ptr(workspace), ws_bytes, _stream(stream)),
+           "moe_norm_backward")
+
+
+class AdamwTable:
+    """The tensors of moe_adamw, in the C layout; keeps them alive."""
+
+    def __init__(self, entries, tensors):
+        self.entries, self.tensors = entries, tensors
+
+    def __len__(self):
+        return len(self.entries)
+
+
+def adamw_table(tensors: Sequence[dict]) -> AdamwTable:
+    """An AdamwTable of dicts with the fields of AdamwTensor: ``param``, ``grad``,
+    ``exp_avg``, ``exp_avg_sq`` and, or None, ``master``, ``exp_avg_scale``,
+    ``exp_avg_sq_scale`` (contiguous tensors on one GPU), ``n`` (param's size
+    when missing) and ``weight_decay`` (0 when missing).  Raises ValueError for
+    tensors that are not contiguous, on several devices, or smaller than n."""
+    entries = (AdamwTensor * len(tensors))()
+    device, keep = None, []
+    for e, t in zip(entries, tensors):
+        n = t.get("n")
+        e.n = n = t["param"].numel() if n is None else int(n)
+        e.weight_decay = float(t.get("weight_decay", 0.0))
+        for name in ("param", "grad", "master", "exp_avg", "exp_avg_sq", "exp_avg_scale",
+                     "exp_avg_sq_scale"):
+            x = t.get(name)
+            if x is None:
+                continue
+            if not x.is_cuda or not x.is_contiguous():
+                raise ValueError(f"adamw_table: {name} is not a contiguous tensor on a GPU")
+            device = x.device if device is None else device
+            need = -(-n // 128) if name.endswith("scale") else n
+            if x.device != device or x.numel() < need:
+                raise ValueError(f"adamw_table: {name} on {x.device} with {x.numel()} elements, "
+                                 f"not on {device} with {need}")
+            setattr(e, name, x.data_ptr())
+            keep.append(x)
+    return AdamwTable(entries, keep)
+
+
+def moe_adamw(table, param_dtype, grad_dtype, state_bits, lr, beta1, beta2, eps, step,
+              grad_scale=None, seed=0, stream=None):
+    """One AdamW step over the tensors of an AdamwTable."""
+    _check(lib.moe_adamw(len(table), ctypes.addressof(table.entries), param_dtype, grad_dtype,
+                         state_bits, lr, beta1, beta2, eps, step, _ptr(grad_scale), seed,
+                         _stream(stream)), "moe_adamw")

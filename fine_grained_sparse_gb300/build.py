@@ -21,7 +21,8 @@ BUILD = os.path.join(PKG, "_build")
 LIBDIR = os.path.join(PKG, "_lib")
 LIBNAME = "libfgsmoe.so"
 SOURCES = ["api.cu", "router.cu", "dispatch.cu", "gemm_tc.cu", "gemm_simt.cu",
-           "gemv_int4.cu", "gemm_int4.cu", "norm.cu"]
+           "gemv_int4.cu", "gemm_int4.cu", "norm.cu", "train.cu", "layernorm.cu", "norm_backward.cu",
+           "adamw.cu"]
 ARCH = ["-gencode", "arch=compute_103a,code=sm_103a"]
 
 
@@ -49,6 +50,7 @@ def _up_to_date(obj: str, src: str) -> bool:
     if not os.path.exists(obj):
         return False
     deps = [src, os.path.join(CSRC, "common.cuh"), os.path.join(CSRC, "internal.h"), os.path.join(CSRC, "int4.cuh"),
+            os.path.join(CSRC, "rows.cuh"),
             os.path.join(INCLUDE, "moe.h")]
     t = os.path.getmtime(obj)
     return all(os.path.getmtime(d) <= t for d in deps)

@@ -1239,14 +1239,24 @@ int32_t moe_linear_int4(int64_t T, int32_t in_features, int32_t out_features, in
   return MOE_OK;
 }
 
-int32_t moe_add_rmsnorm(int32_t dtype, int64_t T, int32_t d, const void* x, const void* residual,
-                        const void* weight, float eps, void* h, void* y, void* y_fp8,
-                        float* y_scale, void* stream) {
+namespace {
+
+int32_t check_norm(int32_t dtype, int64_t T, int32_t d, float eps) {
   if (dtype != MOE_F32 && dtype != MOE_BF16) return fail(MOE_ERR_INVALID_ARG, "dtype");
   if (T < 1 || T > (1ll << 30)) return fail(MOE_ERR_INVALID_ARG, "T out of range");
   if (d < 1) return fail(MOE_ERR_INVALID_ARG, "d < 1");
   if (!(eps >= 0.0f) || !std::isfinite(eps))
     return fail(MOE_ERR_INVALID_ARG, "eps not in [0, inf)");
+  return MOE_OK;
+}
+
+}  // namespace
+
+int32_t moe_add_rmsnorm(int32_t dtype, int64_t T, int32_t d, const void* x, const void* residual,
+                        const void* weight, float eps, void* h, void* y, void* y_fp8,
+                        float* y_scale, void* stream) {
+  int32_t st = check_norm(dtype, T, d, eps);
+  if (st != MOE_OK) return st;
   if (!x || !weight) return fail(MOE_ERR_INVALID_ARG, "null pointer");
   if (!y && !y_fp8) return fail(MOE_ERR_INVALID_ARG, "no output: y and y_fp8 are null");
   if (!y_fp8 != !y_scale) return fail(MOE_ERR_INVALID_ARG, "y_fp8 and y_scale go together");
@@ -1267,6 +1277,208 @@ int32_t moe_add_rmsnorm(int32_t dtype, int64_t T, int32_t d, const void* x, cons
   n.y8 = static_cast<uint8_t*>(y_fp8);
   n.ys = y_scale;
   MOE_CUDA(launch_add_rmsnorm(n, num_sms(), static_cast<cudaStream_t>(stream)));
+  return MOE_OK;
+}
+
+int32_t moe_gather(const moe_config* cfg, int64_t T, const void* x, const int32_t* inv,
+                   const float* topk_w, void* x_perm, float* w_perm, void* stream) {
+  int32_t st = check_layer_cfg(cfg, T);
+  if (st != MOE_OK) return st;
+  if (!x || !inv || !x_perm) return fail(MOE_ERR_INVALID_ARG, "null pointer");
+  if (!topk_w != !w_perm) return fail(MOE_ERR_INVALID_ARG, "topk_w and w_perm go together");
+  const void* ptrs[] = {x, inv, topk_w, x_perm, w_perm};
+  for (const void* q : ptrs)
+    if (!aligned16(q)) return fail(MOE_ERR_ALIGNMENT, "pointer not 16-byte aligned");
+  MOE_CUDA(launch_gather_rows(x, inv, topk_w, T, cfg->K, d_expert(cfg) / (16 / elem_bytes(cfg)),
+                              x_perm, w_perm, static_cast<cudaStream_t>(stream)));
+  return MOE_OK;
+}
+
+int32_t moe_combine_backward(const moe_config* cfg, int64_t T, const void* dy, const void* Y,
+                             const int32_t* inv, const float* topk_w, void* dY, float* dtopk_w,
+                             void* stream) {
+  int32_t st = check_layer_cfg(cfg, T);
+  if (st != MOE_OK) return st;
+  if (!dy || !inv) return fail(MOE_ERR_INVALID_ARG, "null pointer");
+  if (!dY && !dtopk_w) return fail(MOE_ERR_INVALID_ARG, "no output: dY and dtopk_w are null");
+  if (dtopk_w && !Y) return fail(MOE_ERR_INVALID_ARG, "dtopk_w needs Y");
+  const void* ptrs[] = {dy, Y, inv, topk_w, dY, dtopk_w};
+  for (const void* q : ptrs)
+    if (!aligned16(q)) return fail(MOE_ERR_ALIGNMENT, "pointer not 16-byte aligned");
+  MOE_CUDA(launch_combine_backward(dy, Y, inv, topk_w, T, cfg->K, d_expert(cfg),
+                                   cfg->dtype == MOE_BF16, dY, dtopk_w,
+                                   static_cast<cudaStream_t>(stream)));
+  return MOE_OK;
+}
+
+int32_t moe_router_backward(const moe_config* cfg, int64_t T, const float* logits,
+                            const int32_t* topk_idx, const float* dtopk_w, float* dlogits,
+                            void* stream) {
+  int32_t st = check_router_cfg(cfg, T);
+  if (st != MOE_OK) return st;
+  if (!logits || !topk_idx || !dtopk_w || !dlogits)
+    return fail(MOE_ERR_INVALID_ARG, "null pointer");
+  if (dlogits == logits) return fail(MOE_ERR_INVALID_ARG, "dlogits is logits");
+  const void* ptrs[] = {logits, topk_idx, dtopk_w, dlogits};
+  for (const void* q : ptrs)
+    if (!aligned16(q)) return fail(MOE_ERR_ALIGNMENT, "pointer not 16-byte aligned");
+  MOE_CUDA(launch_router_backward(logits, topk_idx, dtopk_w, T, cfg->K, cfg->E_routed,
+                                  cfg->routed_scaling_factor, cfg->K > 1 && cfg->norm_topk_prob,
+                                  dlogits, static_cast<cudaStream_t>(stream)));
+  return MOE_OK;
+}
+
+int32_t moe_add_layernorm(int32_t dtype, int64_t T, int32_t d, const void* x, const void* residual,
+                          const void* weight, const void* bias, float eps, void* h, void* y,
+                          void* stream) {
+  int32_t st = check_norm(dtype, T, d, eps);
+  if (st != MOE_OK) return st;
+  if (!x || !weight || !y) return fail(MOE_ERR_INVALID_ARG, "null pointer");
+  if (h == y) return fail(MOE_ERR_INVALID_ARG, "h and y are one buffer");
+  const void* ptrs[] = {x, residual, weight, bias, h, y};
+  for (const void* q : ptrs)
+    if (!aligned16(q)) return fail(MOE_ERR_ALIGNMENT, "pointer not 16-byte aligned");
+  LayerNormArgs n;
+  n.bf16 = dtype == MOE_BF16;
+  n.T = T;
+  n.d = d;
+  n.a = x;
+  n.r = residual;
+  n.w = weight;
+  n.b = bias;
+  n.eps = eps;
+  n.h = h;
+  n.y = y;
+  MOE_CUDA(launch_add_layernorm(n, num_sms(), static_cast<cudaStream_t>(stream)));
+  return MOE_OK;
+}
+
+size_t moe_norm_backward_workspace_size(int64_t T, int32_t d) {
+  if (T < 1 || T > (1ll << 30) || d < 1) return 0;
+  return kWsHeader + round256(8 * static_cast<size_t>(T)) +
+         round256(4 * static_cast<size_t>(norm_partial_floats(T, d)));
+}
+
+int32_t moe_norm_backward(int32_t kind, int32_t dtype, int64_t T, int32_t d, const void* x,
+                          const void* residual, const void* weight, float eps, const void* dy,
+                          const void* dh, void* dx, float* dweight, float* dbias, void* workspace,
+                          size_t ws_bytes, void* stream) {
+  if (kind != MOE_NORM_RMS && kind != MOE_NORM_LAYER) return fail(MOE_ERR_INVALID_ARG, "kind");
+  int32_t st = check_norm(dtype, T, d, eps);
+  if (st != MOE_OK) return st;
+  if (!x || !weight || !dy) return fail(MOE_ERR_INVALID_ARG, "null pointer");
+  if (!dx && !dweight && !dbias)
+    return fail(MOE_ERR_INVALID_ARG, "no output: dx, dweight and dbias are null");
+  if (dbias && kind == MOE_NORM_RMS) return fail(MOE_ERR_INVALID_ARG, "an RMS norm has no bias");
+  const void* ptrs[] = {x, residual, weight, dy, dh, dx, dweight, dbias};
+  for (const void* q : ptrs)
+    if (!aligned16(q)) return fail(MOE_ERR_ALIGNMENT, "pointer not 16-byte aligned");
+  if (dweight || dbias) {
+    if (!workspace || ws_bytes < moe_norm_backward_workspace_size(T, d))
+      return fail(MOE_ERR_WORKSPACE, "workspace too small");
+    if (!aligned16(workspace)) return fail(MOE_ERR_ALIGNMENT, "workspace not aligned");
+  }
+  NormBackwardArgs n;
+  n.layer = kind == MOE_NORM_LAYER;
+  n.bf16 = dtype == MOE_BF16;
+  n.T = T;
+  n.d = d;
+  n.a = x;
+  n.r = residual;
+  n.w = weight;
+  n.eps = eps;
+  n.dy = dy;
+  n.dh = dh;
+  n.dx = dx;
+  n.dw = dweight;
+  n.db = dbias;
+  if (dweight || dbias) {
+    n.stats = at<float2>(workspace, kWsHeader);
+    n.partials = at<float>(workspace, kWsHeader + round256(8 * static_cast<size_t>(T)));
+  }
+  MOE_CUDA(launch_norm_backward(n, static_cast<cudaStream_t>(stream)));
+  return MOE_OK;
+}
+
+namespace {
+
+// The finaliser of splitmix64.
+uint64_t mix64(uint64_t x) {
+  x += 0x9E3779B97F4A7C15ull;
+  x = (x ^ (x >> 30)) * 0xBF58476D1CE4E5B9ull;
+  x = (x ^ (x >> 27)) * 0x94D049BB133111EBull;
+  return x ^ (x >> 31);
+}
+
+int32_t check_adamw_tensor(const moe_adamw_tensor& t, int32_t param_dtype, int32_t state_bits) {
+  if (t.n < 0 || t.n > (1ll << 40)) return fail(MOE_ERR_INVALID_ARG, "n out of range");
+  if (!(t.weight_decay >= 0.0) || !std::isfinite(t.weight_decay))
+    return fail(MOE_ERR_INVALID_ARG, "weight_decay not in [0, inf)");
+  if (t.n == 0) return MOE_OK;
+  if (!t.param || !t.grad || !t.exp_avg || !t.exp_avg_sq)
+    return fail(MOE_ERR_INVALID_ARG, "null pointer");
+  if (t.master && param_dtype != MOE_BF16)
+    return fail(MOE_ERR_INVALID_ARG, "a master copy of an fp32 param");
+  const bool scales = t.exp_avg_scale && t.exp_avg_sq_scale;
+  if (state_bits == 8 && !scales) return fail(MOE_ERR_INVALID_ARG, "8-bit states need their scales");
+  if (state_bits == 32 && (t.exp_avg_scale || t.exp_avg_sq_scale))
+    return fail(MOE_ERR_INVALID_ARG, "scales of 32-bit states");
+  const void* ptrs[] = {t.param,      t.grad,          t.master,          t.exp_avg,
+                        t.exp_avg_sq, t.exp_avg_scale, t.exp_avg_sq_scale};
+  for (const void* q : ptrs)
+    if (reinterpret_cast<uintptr_t>(q) & 15u)
+      return fail(MOE_ERR_ALIGNMENT, "pointer not 16-byte aligned");
+  return MOE_OK;
+}
+
+}  // namespace
+
+int32_t moe_adamw(int32_t n_tensors, const moe_adamw_tensor* tensors_host, int32_t param_dtype,
+                  int32_t grad_dtype, int32_t state_bits, double lr, double beta1, double beta2,
+                  double eps, int64_t step, const float* grad_scale, uint64_t seed, void* stream) {
+  if (n_tensors < 0 || (n_tensors > 0 && !tensors_host))
+    return fail(MOE_ERR_INVALID_ARG, "tensors");
+  if ((param_dtype != MOE_F32 && param_dtype != MOE_BF16) ||
+      (grad_dtype != MOE_F32 && grad_dtype != MOE_BF16))
+    return fail(MOE_ERR_INVALID_ARG, "dtype");
+  if (state_bits != 8 && state_bits != 32)
+    return fail(MOE_ERR_UNSUPPORTED_SHAPE, "state_bits not 8 or 32");
+  if (!(lr >= 0.0) || !std::isfinite(lr)) return fail(MOE_ERR_INVALID_ARG, "lr not in [0, inf)");
+  if (!(beta1 >= 0.0 && beta1 < 1.0) || !(beta2 >= 0.0 && beta2 < 1.0))
+    return fail(MOE_ERR_INVALID_ARG, "beta not in [0, 1)");
+  if (!(eps >= 0.0) || !std::isfinite(eps))
+    return fail(MOE_ERR_INVALID_ARG, "eps not in [0, inf)");
+  if (step < 1) return fail(MOE_ERR_INVALID_ARG, "step < 1");
+  if (reinterpret_cast<uintptr_t>(grad_scale) & 3u)
+    return fail(MOE_ERR_ALIGNMENT, "grad_scale not 4-byte aligned");
+  for (int32_t k = 0; k < n_tensors; ++k) {
+    const int32_t st = check_adamw_tensor(tensors_host[k], param_dtype, state_bits);
+    if (st != MOE_OK) return st;
+  }
+  AdamwScalars c;
+  c.b1 = static_cast<float>(beta1);
+  c.ob1 = static_cast<float>(1.0 - beta1);
+  c.b2 = static_cast<float>(beta2);
+  c.ob2 = static_cast<float>(1.0 - beta2);
+  c.root = static_cast<float>(1.0 / std::sqrt(1.0 - std::pow(beta2, static_cast<double>(step))));
+  c.eps = static_cast<float>(eps);
+  c.size = static_cast<float>(lr / (1.0 - std::pow(beta1, static_cast<double>(step))));
+  c.grad_scale = grad_scale;
+  AdamwTensor group[kAdamwTensors];
+  for (int32_t k = 0; k < n_tensors;) {
+    int count = 0;
+    for (; count < kAdamwTensors && k + count < n_tensors; ++count) {
+      const moe_adamw_tensor& t = tensors_host[k + count];
+      group[count] = {t.param, t.grad, t.master, t.exp_avg, t.exp_avg_sq, t.exp_avg_scale,
+                      t.exp_avg_sq_scale, t.n, static_cast<float>(1.0 - lr * t.weight_decay),
+                      static_cast<uint32_t>(
+                          mix64(seed + 0x9E3779B97F4A7C15ull * static_cast<uint64_t>(k + count)) >> 32)};
+    }
+    count = adamw_group(group, count);
+    MOE_CUDA(launch_adamw(group, count, c, param_dtype == MOE_BF16, grad_dtype == MOE_BF16,
+                          state_bits == 8, static_cast<cudaStream_t>(stream)));
+    k += count;
+  }
   return MOE_OK;
 }
 

@@ -294,6 +294,85 @@ struct NormArgs {
 };
 cudaError_t launch_add_rmsnorm(const NormArgs& n, int num_sms, cudaStream_t stream);
 
+// --------------------------------------------------------------- training
+// xp[inv[t K + k]] = x[t] and, with w, wp[inv[t K + k]] = w[t K + k]; rows of
+// nvec 16-byte pieces.  K <= 32.
+cudaError_t launch_gather_rows(const void* x, const int32_t* inv, const float* w, int64_t T, int K,
+                               int nvec, void* xp, float* wp, cudaStream_t stream);
+// dY[inv[j]] = w[j] dy[j / K] (w null: 1; dY may be null or Y) and
+// dw[j] = <Y[inv[j]], dy[j / K]> (dw may be null, then Y too).  D % 8 == 0.
+cudaError_t launch_combine_backward(const void* dy, const void* Y, const int32_t* inv,
+                                    const float* w, int64_t T, int K, int D, bool bf16, void* dY,
+                                    float* dw, cudaStream_t stream);
+// dz [T, E] of the gate weights' gradient dw [T, K]; K <= 32.
+cudaError_t launch_router_backward(const float* logits, const int32_t* idx, const float* dw,
+                                   int64_t T, int K, int E, float scale, bool renorm, float* dz,
+                                   cudaStream_t stream);
+
+struct LayerNormArgs {
+  bool bf16 = true;         // type of a, r, w, b, h and y: bf16 or fp32
+  int64_t T = 0;
+  int d = 0;
+  const void* a = nullptr;  // [T, d]
+  const void* r = nullptr;  // [T, d] or null
+  const void* w = nullptr;  // [d]
+  const void* b = nullptr;  // [d] or null
+  float eps = 0.0f;
+  void* h = nullptr;        // [T, d] or null
+  void* y = nullptr;        // [T, d]
+};
+cudaError_t launch_add_layernorm(const LayerNormArgs& n, int num_sms, cudaStream_t stream);
+
+// Blocks of rows whose dweight and dbias are summed apart (two for each of a
+// GB300's 152 SMs; a fixed count, so that a workspace sized on one device fits
+// the call on another and results do not depend on the device).
+constexpr int64_t kNormParts = 304;
+struct NormBackwardArgs {
+  bool layer = false;        // layer norm, or RMS norm
+  bool bf16 = true;          // type of a, r, w, dy, dh and dx: bf16 or fp32
+  int64_t T = 0;
+  int d = 0;
+  const void* a = nullptr;   // [T, d]
+  const void* r = nullptr;   // [T, d] or null
+  const void* w = nullptr;   // [d]
+  float eps = 0.0f;
+  const void* dy = nullptr;  // [T, d]
+  const void* dh = nullptr;  // [T, d] or null
+  void* dx = nullptr;        // [T, d] or null
+  float* dw = nullptr;       // [d] or null
+  float* db = nullptr;       // [d] or null (layer norm)
+  float* partials = nullptr; // norm_partial_floats(T, d) (with dw or db)
+  float2* stats = nullptr;   // [T] (with dw or db)
+};
+int64_t norm_partial_floats(int64_t T, int64_t d);
+cudaError_t launch_norm_backward(const NormBackwardArgs& n, cudaStream_t stream);
+
+constexpr int kAdamwBlock = 128;    // elements of a state with one scale
+constexpr int kAdamwTensors = 256;  // of one launch, which takes them by value
+struct AdamwTensor {
+  void* param;
+  const void* grad;
+  float* master;  // or null
+  void* m;
+  void* v;        // 8 bits: its root
+  float* m_scale;
+  float* v_scale;
+  int64_t n;
+  float decay;    // 1 - lr weight_decay
+  uint32_t key;   // of the random bits
+};
+struct AdamwScalars {
+  float b1, ob1, b2, ob2;  // beta and 1 - beta
+  float root;              // 1 / sqrt(1 - beta2^t)
+  float eps;
+  float size;              // lr / (1 - beta1^t)
+  const float* grad_scale; // device scalar, or null
+};
+// Tensors, from the first, that one launch takes (at least one).
+int adamw_group(const AdamwTensor* t, int count);
+cudaError_t launch_adamw(const AdamwTensor* t, int count, const AdamwScalars& c, bool param_bf16,
+                         bool grad_bf16, bool bits8, cudaStream_t stream);
+
 // --------------------------------------------------- products with 4-bit weights
 // The widest x: a row of it stays in shared memory beside the ring of weights.
 constexpr int kInt4MaxCols = 32768;

@@ -1,0 +1,104 @@
+// What the norm kernels share: pieces of a row in registers, and the 8-bit
+// form of 128 values (E4M3 codes with one fp32 scale).
+#pragma once
+
+#include "common.cuh"
+
+namespace fgs {
+
+constexpr int kRowGroup = 128;  // columns of a row with one scale
+
+// N values of a row as fp32, 16 bytes (or one value) at a time.
+template <typename T, int N>
+struct Piece {
+  float v[N];
+};
+
+template <int N>
+__device__ __forceinline__ Piece<__nv_bfloat16, N> load(const __nv_bfloat16* p) {
+  Piece<__nv_bfloat16, N> o;
+  if constexpr (N == 1) {
+    o.v[0] = __bfloat162float(*p);
+  } else {
+    const uint4 u = *reinterpret_cast<const uint4*>(p);
+    const uint32_t w[4] = {u.x, u.y, u.z, u.w};
+#pragma unroll
+    for (int i = 0; i < 4; ++i) {
+      o.v[2 * i] = __uint_as_float(w[i] << 16);
+      o.v[2 * i + 1] = __uint_as_float(w[i] & 0xffff0000u);
+    }
+  }
+  return o;
+}
+template <int N>
+__device__ __forceinline__ Piece<float, N> load(const float* p) {
+  Piece<float, N> o;
+  if constexpr (N == 1) {
+    o.v[0] = *p;
+  } else {
+    const float4 u = *reinterpret_cast<const float4*>(p);
+    o.v[0] = u.x, o.v[1] = u.y, o.v[2] = u.z, o.v[3] = u.w;
+  }
+  return o;
+}
+template <int N>
+__device__ __forceinline__ void store(__nv_bfloat16* p, const float (&v)[N]) {
+  if constexpr (N == 1)
+    *p = __float2bfloat16_rn(v[0]);
+  else
+    *reinterpret_cast<uint4*>(p) = make_uint4(pack_bf16x2(v[0], v[1]), pack_bf16x2(v[2], v[3]),
+                                              pack_bf16x2(v[4], v[5]), pack_bf16x2(v[6], v[7]));
+}
+template <int N>
+__device__ __forceinline__ void store(float* p, const float (&v)[N]) {
+  if constexpr (N == 1)
+    *p = v[0];
+  else
+    *reinterpret_cast<float4*>(p) = make_float4(v[0], v[1], v[2], v[3]);
+}
+
+// max that keeps NaN, as the definition's maximum over a group does
+__device__ __forceinline__ float max_nan(float a, float b) {
+  float r;
+  asm("max.NaN.f32 %0, %1, %2;" : "=f"(r) : "f"(a), "f"(b));
+  return r;
+}
+
+// Two E4M3 codes, a's in the low byte.
+__device__ __forceinline__ uint32_t e4m3x2(float a, float b) {
+  uint16_t r;
+  asm("cvt.rn.satfinite.e4m3x2.f32 %0, %1, %2;" : "=h"(r) : "f"(b), "f"(a));
+  return r;
+}
+
+// v[i] / s correctly rounded, for s and the largest |v[i]| well inside fp32's
+// range, by Markstein's theorem (IBM J. Res. Dev. 34, 1990): from y, 1 / s
+// correctly rounded, and q within an ulp of v / s, q + y (v - q s) is v / s
+// correctly rounded.  v y may be off by 1.5 ulp, so it takes two such steps.
+// Two values to an instruction: 8192 rows of 7168 bf16 with all outputs and a
+// flushed L2 in 96.5 us, with a division for each value 102.4.
+template <int N>
+__device__ __forceinline__ void divide(float (&v)[N], float s) {
+  const float y = 1.0f / s;
+#pragma unroll
+  for (int k = 0; k + 1 < N; k += 2)
+    asm("{\n\t.reg .b64 v, q, r, y, s;\n\t"
+        "mov.b64 v, {%0, %1};\n\tmov.b64 y, {%2, %2};\n\tmov.b64 s, {%3, %3};\n\t"
+        "mul.rn.f32x2 q, v, y;\n\t"
+        "fma.rn.f32x2 r, q, s, v;\n\tfma.rn.f32x2 q, r, y, q;\n\t"
+        "fma.rn.f32x2 r, q, s, v;\n\tfma.rn.f32x2 q, r, y, q;\n\t"
+        "mov.b64 {%0, %1}, q;\n\t}"
+        : "+f"(v[k]), "+f"(v[k + 1])
+        : "f"(y), "f"(-s));
+}
+
+template <int N>
+__device__ __forceinline__ void store_codes(uint8_t* p, const float (&q)[N]) {
+  if constexpr (N == 8)
+    *reinterpret_cast<uint2*>(p) = make_uint2(e4m3x2(q[0], q[1]) | e4m3x2(q[2], q[3]) << 16,
+                                              e4m3x2(q[4], q[5]) | e4m3x2(q[6], q[7]) << 16);
+  else if constexpr (N == 4)
+    *reinterpret_cast<uint32_t*>(p) = e4m3x2(q[0], q[1]) | e4m3x2(q[2], q[3]) << 16;
+}
+
+}  // namespace fgs

@@ -59,6 +59,25 @@ typedef enum moe_status {
 
 typedef enum moe_dtype { MOE_F32 = 0, MOE_BF16 = 1 } moe_dtype;
 
+/* Norms of moe_norm_backward. */
+typedef enum moe_norm_kind { MOE_NORM_RMS = 0, MOE_NORM_LAYER = 1 } moe_norm_kind;
+
+/* One tensor of moe_adamw: n contiguous elements (0 is allowed: nothing is
+ * done) and what the step keeps for them, all on the device, each buffer
+ * 16-byte aligned. */
+typedef struct moe_adamw_tensor {
+  void* param;        /* [n] of param_dtype, updated in place                  */
+  const void* grad;   /* [n] of grad_dtype                                     */
+  float* master;      /* [n] fp32 copy of a bf16 param, or NULL: the step is
+                         taken on it and param becomes its rounded value       */
+  void* exp_avg;      /* [n] first moment: fp32, or E4M3 codes                 */
+  void* exp_avg_sq;   /* [n] second moment: fp32, or E4M3 codes of its root    */
+  float* exp_avg_scale;    /* [ceil(n / 128)] scales of the codes; NULL with   */
+  float* exp_avg_sq_scale; /* 32-bit states                                    */
+  int64_t n;          /* elements, at most 2^40                                */
+  double weight_decay;
+} moe_adamw_tensor;
+
 /* Layer configuration.  Field names follow the gate config of the
  * "Kimi K2 · Router" MoEGate listing where it has one. */
 typedef struct moe_config {
@@ -474,6 +493,137 @@ int32_t moe_linear_int4(int64_t T, int32_t in_features, int32_t out_features, in
 int32_t moe_add_rmsnorm(int32_t dtype, int64_t T, int32_t d, const void* x, const void* residual,
                         const void* weight, float eps, void* h, void* y, void* y_fp8,
                         float* y_scale, void* stream);
+
+/*
+ * Training around the experts' products.  A caller with its own expert
+ * products runs moe_router_from_logits (or moe_router), moe_permute and
+ * moe_gather, its products on the rows of each expert
+ * (x_perm[offsets[e]] .. x_perm[offsets[e + 1] - 1]), and moe_combine; and back
+ * through moe_combine_backward, its products' gradients, moe_combine again
+ * (the gradient of moe_gather) and moe_router_backward.
+ */
+
+/*
+ * The rows in expert order, and their weights:
+ *   x_perm[inv[t*K + k]] = x[t],  w_perm[inv[t*K + k]] = topk_w[t*K + k]
+ *   x [T, D] cfg->dtype, inv [T*K] from moe_permute, topk_w [T, K] fp32 or
+ *   NULL; x_perm [T*K, D] out, w_perm [T*K] fp32 out (NULL with topk_w);
+ *   D = d_e (d_latent if set, else d_model).  No buffers may overlap.
+ * An inv entry outside [0, T*K) (a pair that moe_permute rejected) is left
+ * out, so that rows from offsets[E] on stay as they were; entries inside must
+ * differ from one another.  Needs no workspace.
+ * Its gradient is moe_combine with Y = the gradient of x_perm, topk_w = NULL
+ * and y = the gradient of x; Y_shared [S, T, D] may then hold the gradients
+ * that reach x through the shared experts. */
+int32_t moe_gather(const moe_config* cfg, int64_t T, const void* x, const int32_t* inv,
+                   const float* topk_w, void* x_perm, float* w_perm, void* stream);
+
+/*
+ * Gradient of moe_combine, y[t] = sum_k w[t, k] Y[inv[t*K + k]] (+ the shared
+ * experts' outputs, whose gradient is dy itself):
+ *   dY[inv[t*K + k]] = w[t, k] dy[t]       rounded once to cfg->dtype
+ *   dtopk_w[t, k] = sum_c Y[inv[t*K + k]][c] dy[t][c]        summed in fp32
+ *   dy [T, D] and Y [T*K, D] cfg->dtype, inv as in moe_gather, topk_w [T, K]
+ *   fp32 or NULL (weight 1); dY [T*K, D] out or NULL, dtopk_w [T, K] fp32 out
+ *   or NULL (then Y is not read and may be NULL).
+ * A pair with an inv entry outside [0, T*K) has dtopk_w = 0 and no row of dY;
+ * rows of dY that belong to no pair stay as they were.  dY may be Y; no other
+ * overlap is allowed.  Needs no workspace. */
+int32_t moe_combine_backward(const moe_config* cfg, int64_t T, const void* dy, const void* Y,
+                             const int32_t* inv, const float* topk_w, void* dY, float* dtopk_w,
+                             void* stream);
+
+/*
+ * Gradient of the gate weights to the router's logits, for the selected
+ * experts of moe_router (the selection itself has none; cfg's K,
+ * norm_topk_prob and routed_scaling_factor c apply): with s = sigmoid(z),
+ * p_k = s_k / (sum_j s_j + 1e-20) over a token's selected experts,
+ *   dz_k = c p_k (dw_k - sum_j p_j dw_j) (1 - s_k), and where the weights are
+ *   not renormalised (K == 1 or norm_topk_prob == 0) dz_k = c s_k dw_k (1 - s_k)
+ *   logits z [T, E] fp32, topk_idx [T, K], dtopk_w [T, K] fp32;
+ *   dlogits [T, E] fp32 out, every entry written: 0 off the selected experts.
+ * Indices outside [0, E) are ignored, as if the token had fewer experts; an
+ * expert that a token lists more than once receives the sum of its pairs'
+ * gradients.  dlogits may not be logits.  Needs no workspace. */
+int32_t moe_router_backward(const moe_config* cfg, int64_t T, const float* logits,
+                            const int32_t* topk_idx, const float* dtopk_w, float* dlogits,
+                            void* stream);
+
+/*
+ * Residual sum and layer norm:
+ *   s = x + residual (x alone when residual is NULL), mu = mean_c s[t, c],
+ *   v[t, c] = weight[c] (s[t, c] - mu) / sqrt(mean_c (s[t, c] - mu)^2 + eps) + bias[c]
+ * in fp32 from the inputs, with the outputs each rounded once:
+ *   h [T, d]  s, the new residual stream, or NULL;  y [T, d]  v
+ * x, residual, weight [d], bias [d] (or NULL: 0), h and y are `dtype`
+ * (MOE_BF16 or MOE_F32); any d >= 1.  eps >= 0.  h and y may each be x or
+ * residual itself (not both the same buffer); no other overlap is allowed.
+ * Needs no workspace. */
+int32_t moe_add_layernorm(int32_t dtype, int64_t T, int32_t d, const void* x, const void* residual,
+                          const void* weight, const void* bias, float eps, void* h, void* y,
+                          void* stream);
+
+/* Bytes of workspace moe_norm_backward needs for T rows of d columns; 0 for
+ * sizes that it rejects. */
+size_t moe_norm_backward_workspace_size(int64_t T, int32_t d);
+
+/*
+ * Gradient of moe_add_rmsnorm's y (MOE_NORM_RMS) or moe_add_layernorm's
+ * (MOE_NORM_LAYER): with s, mu and the inverse root r as there, u = s r (RMS)
+ * or (s - mu) r (layer), g = weight * dy,
+ *   dx = r (g - u mean(g u)) + dh             RMS
+ *   dx = r (g - mean(g) - u mean(g u)) + dh   layer
+ *   dweight = sum_t dy[t] u[t],  dbias = sum_t dy[t]
+ * in fp32 from the inputs, dx rounded once.
+ *   x, residual (or NULL), weight, eps: as in the forward call, or x = its h
+ *   and residual = NULL (one tensor less to read; s is then rounded to dtype);
+ *   dy [T, d] the gradient of y; dh [T, d] the gradient that reaches s past the
+ *   norm (of the forward's h), or NULL: 0.
+ *   dx [T, d] out or NULL: the gradient of x and of residual alike; dweight,
+ *   dbias [d] fp32 out or NULL (dbias: layer norm only).
+ * At least one output.  x, residual, weight, dy, dh and dx are `dtype`.  dx may
+ * be x, residual, dy or dh; no other overlap is allowed.  The rows' sums are
+ * taken in an order that T and d alone decide.
+ *   workspace: moe_norm_backward_workspace_size(T, d) bytes, with dweight or
+ *   dbias; otherwise it may be NULL. */
+int32_t moe_norm_backward(int32_t kind, int32_t dtype, int64_t T, int32_t d, const void* x,
+                          const void* residual, const void* weight, float eps, const void* dy,
+                          const void* dh, void* dx, float* dweight, float* dbias, void* workspace,
+                          size_t ws_bytes, void* stream);
+
+/*
+ * One AdamW step over many tensors (decoupled weight decay, bias correction of
+ * step t = 1, 2, ...).  Per element, in fp32, every operation rounded by itself:
+ *   g = grad c,  m = beta1 m + (1 - beta1) g,  v = beta2 v + (1 - beta2) g g
+ *   p = p (1 - lr weight_decay)
+ *       - (m / (sqrt(v) (1 / sqrt(1 - beta2^t)) + eps)) (lr / (1 - beta1^t))
+ * with the factors in parentheses that no element enters taken in fp64 and
+ * rounded once.
+ *   tensors_host [n_tensors] (HOST memory, read during the call; the buffers
+ *   that it names are device memory, and no two of a call may overlap);
+ *   param_dtype, grad_dtype: MOE_BF16 or MOE_F32, the same for all tensors;
+ *   grad_scale: one fp32 value on the DEVICE, c above (what a clip of the
+ *   gradients' norm leaves), 4-byte aligned, or NULL: 1.
+ *   state_bits 32: exp_avg and exp_avg_sq hold m and v in fp32.
+ *   state_bits 8: exp_avg holds m and exp_avg_sq holds r = sqrt(v), as E4M3
+ *   codes with one fp32 scale per 128 elements, max|.| (1 / 448), value = code
+ *   value * scale; zeroed buffers are the state before the first step.  The
+ *   codes of m are the quotients m / scale rounded to nearest.  Those of r are
+ *   rounded up with the probability of what lies above the code below, to
+ *   the nearest 2^-16 (rounding to nearest would hold a slow v where it is),
+ *   by 16 random bits an element: of h, the MurmurHash3 finaliser of j ^ key ^ (j >> 32)
+ *   0x9E3779B9 in 32 bits, j the number of the element's pair in its tensor,
+ *   the low half for the even element, the high for the odd; key: the upper
+ *   half of the splitmix64 finaliser of seed + 0x9E3779B97F4A7C15 k, k the
+ *   number of the tensor in tensors_host.  A root above 0 never has code 0.  A
+ *   block of 128 with a value that is not finite has NaN codes or a scale
+ *   that is not finite.  Pass another seed in every step (the step's number
+ *   does).
+ * lr, step and seed are values of the call: a captured call repeats them.
+ * One launch takes up to 256 tensors.  Needs no workspace. */
+int32_t moe_adamw(int32_t n_tensors, const moe_adamw_tensor* tensors_host, int32_t param_dtype,
+                  int32_t grad_dtype, int32_t state_bits, double lr, double beta1, double beta2,
+                  double eps, int64_t step, const float* grad_scale, uint64_t seed, void* stream);
 
 /*
  * The whole layer forward, one stream:
