@@ -20,37 +20,54 @@ namespace {
 
 constexpr int kThreads = 256;
 constexpr int kStep = 8 * kThreads;  // elements of a block at a time
-constexpr int kSteps = 2;
-constexpr int64_t kChunk = static_cast<int64_t>(kStep) * kSteps;  // elements of a block
 
 struct AdamwLaunch {
   AdamwTensor t[kAdamwTensors];
   uint32_t first[kAdamwTensors + 1];  // the blocks before each tensor's
   int count;
+  int steps;  // of a block
   AdamwScalars c;
 };
 
+// Eight values of a tensor as they lie in memory, and as fp32.
+template <typename T>
+struct Raw8;
+template <>
+struct Raw8<__nv_bfloat16> {
+  uint4 u;
+  __device__ __forceinline__ void load(const __nv_bfloat16* p) {
+    u = *reinterpret_cast<const uint4*>(p);
+  }
+  __device__ __forceinline__ void unpack(float (&v)[8]) const {
+    const uint32_t w[4] = {u.x, u.y, u.z, u.w};
+#pragma unroll
+    for (int i = 0; i < 4; ++i) {
+      v[2 * i] = __uint_as_float(w[i] << 16);
+      v[2 * i + 1] = __uint_as_float(w[i] & 0xffff0000u);
+    }
+  }
+};
+template <>
+struct Raw8<float> {
+  float4 a, b;
+  __device__ __forceinline__ void load(const float* p) {
+    a = reinterpret_cast<const float4*>(p)[0];
+    b = reinterpret_cast<const float4*>(p)[1];
+  }
+  __device__ __forceinline__ void unpack(float (&v)[8]) const {
+    v[0] = a.x, v[1] = a.y, v[2] = a.z, v[3] = a.w;
+    v[4] = b.x, v[5] = b.y, v[6] = b.z, v[7] = b.w;
+  }
+};
 // Values [at, at + 8) of a tensor of n, 0 beyond its end.
 template <typename T>
-__device__ __forceinline__ void load8(const T* p, int64_t at, int64_t n, float (&v)[8]) {
-  if (at + 8 <= n) {
-    if constexpr (sizeof(T) == 2) {
-      const Piece<T, 8> x = load<8>(p + at);
+__device__ __forceinline__ void load_tail(const T* p, int64_t at, int64_t n, float (&v)[8]) {
 #pragma unroll
-      for (int k = 0; k < 8; ++k) v[k] = x.v[k];
-    } else {
-      const Piece<T, 4> x = load<4>(p + at), y = load<4>(p + at + 4);
-#pragma unroll
-      for (int k = 0; k < 4; ++k) v[k] = x.v[k], v[k + 4] = y.v[k];
-    }
-  } else {
-#pragma unroll
-    for (int k = 0; k < 8; ++k) v[k] = at + k < n ? load<1>(p + at + k).v[0] : 0.0f;
-  }
+  for (int k = 0; k < 8; ++k) v[k] = at + k < n ? load<1>(p + at + k).v[0] : 0.0f;
 }
-template <typename T>
+template <bool kFull, typename T>
 __device__ __forceinline__ void store8(T* p, int64_t at, int64_t n, const float (&v)[8]) {
-  if (at + 8 <= n) {
+  if (kFull || at + 8 <= n) {
     if constexpr (sizeof(T) == 2) {
       store<8>(p + at, v);
     } else {
@@ -68,8 +85,8 @@ __device__ __forceinline__ void store8(T* p, int64_t at, int64_t n, const float 
 }
 
 // Eight E4M3 codes, 0 beyond the end.
-__device__ __forceinline__ uint2 load_codes(const uint8_t* p, int64_t at, int64_t n) {
-  if (at + 8 <= n) return *reinterpret_cast<const uint2*>(p + at);
+__device__ __forceinline__ uint2 load_codes_tail(const void* codes, int64_t at, int64_t n) {
+  const uint8_t* p = static_cast<const uint8_t*>(codes);
   uint2 u = make_uint2(0, 0);
 #pragma unroll
   for (int k = 0; k < 8; ++k) {
@@ -78,14 +95,16 @@ __device__ __forceinline__ uint2 load_codes(const uint8_t* p, int64_t at, int64_
   }
   return u;
 }
-__device__ __forceinline__ void store_codes8(uint8_t* p, int64_t at, int64_t n, uint2 u) {
-  if (at + 8 <= n) {
+template <bool kFull>
+__device__ __forceinline__ void store_codes8(void* codes, int64_t at, int64_t n, uint2 u) {
+  uint8_t* p = static_cast<uint8_t*>(codes);
+  if (kFull || at + 8 <= n) {
     *reinterpret_cast<uint2*>(p + at) = u;
-    return;
-  }
+  } else {
 #pragma unroll
-  for (int k = 0; k < 8; ++k)
-    if (at + k < n) p[at + k] = static_cast<uint8_t>((k < 4 ? u.x : u.y) >> 8 * (k & 3));
+    for (int k = 0; k < 8; ++k)
+      if (at + k < n) p[at + k] = static_cast<uint8_t>((k < 4 ? u.x : u.y) >> 8 * (k & 3));
+  }
 }
 // Their values times a scale, each product rounded.
 __device__ __forceinline__ void decode(uint2 u, float scale, float (&v)[8]) {
@@ -102,43 +121,263 @@ __device__ __forceinline__ void decode(uint2 u, float scale, float (&v)[8]) {
   }
 }
 
-// The maximum over the 16 lanes that hold a block of 128, NaN if one is.
-__device__ __forceinline__ float block_max(const float (&v)[8]) {
-  float m = 0.0f;
-#pragma unroll
-  for (int k = 0; k < 8; ++k) m = max_nan(m, fabsf(v[k]));
+// Pairs of fp32 values, one instruction for both.
+typedef unsigned long long pair;
+__device__ __forceinline__ pair make_pair2(float a, float b) {
+  pair r;
+  asm("mov.b64 %0, {%1, %2};" : "=l"(r) : "f"(a), "f"(b));
+  return r;
+}
+__device__ __forceinline__ void split(pair v, float& a, float& b) {
+  asm("mov.b64 {%0, %1}, %2;" : "=f"(a), "=f"(b) : "l"(v));
+}
+__device__ __forceinline__ pair mul2(pair a, pair b) {
+  pair r;
+  asm("mul.rn.f32x2 %0, %1, %2;" : "=l"(r) : "l"(a), "l"(b));
+  return r;
+}
+__device__ __forceinline__ pair fma2(pair a, pair b, pair c) {
+  pair r;
+  asm("fma.rn.f32x2 %0, %1, %2, %3;" : "=l"(r) : "l"(a), "l"(b), "l"(c));
+  return r;
+}
+
+// a + b with a rounding of its own: as a 1 + b with a 1 that the compiler does
+// not know, as it makes one operation of a product and add.rn.f32x2.
+__device__ __forceinline__ pair add2(pair a, float one, pair b) {
+  return fma2(a, make_pair2(one, one), b);
+}
+
+// Square roots of values in [2^-90, 2^90], correctly rounded: from y, 1 / sqrt v
+// to 2^-22, and g = v y, a Newton step of g and the correction (v - g g) y / 2
+// (Markstein, IBM J. Res. Dev. 34, 1990); all 2^24 mantissas of both parities
+// of the exponent were compared with the exact roots.
+__device__ __forceinline__ pair sqrt2(pair v) {
+  float a, b, ya, yb;
+  split(v, a, b);
+  asm("rsqrt.approx.f32 %0, %1;" : "=f"(ya) : "f"(a));
+  asm("rsqrt.approx.f32 %0, %1;" : "=f"(yb) : "f"(b));
+  const pair y = make_pair2(ya, yb);
+  pair g = mul2(v, y);
+  const pair h = mul2(y, make_pair2(0.5f, 0.5f));
+  g = fma2(fma2(mul2(h, make_pair2(-1.0f, -1.0f)), g, make_pair2(0.5f, 0.5f)), g, g);
+  return fma2(fma2(mul2(g, make_pair2(-1.0f, -1.0f)), g, v), h, g);
+}
+
+// 1 / s within half an ulp and 2^-22 of one: the approximation and a Newton step.
+__device__ __forceinline__ float reciprocal(float s) {
+  float y;
+  asm("rcp.approx.f32 %0, %1;" : "=f"(y) : "f"(s));
+  return fmaf(fmaf(-s, y, 1.0f), y, y);
+}
+// a / d from y = reciprocal(d), nd = -d: two residual steps, as in divide().
+__device__ __forceinline__ pair quotient2(pair a, pair nd, pair y) {
+  pair q = mul2(a, y);
+  q = fma2(fma2(nd, q, a), y, q);
+  return fma2(fma2(nd, q, a), y, q);
+}
+__device__ __forceinline__ pair divide2(pair a, pair d) {
+  float x, y, rx, ry;
+  split(d, x, y);
+  asm("rcp.approx.f32 %0, %1;" : "=f"(rx) : "f"(x));
+  asm("rcp.approx.f32 %0, %1;" : "=f"(ry) : "f"(y));
+  const pair nd = mul2(d, make_pair2(-1.0f, -1.0f));
+  const pair r = make_pair2(rx, ry);
+  return quotient2(a, nd, fma2(fma2(nd, r, make_pair2(1.0f, 1.0f)), r, r));
+}
+
+// The largest of three, NaN if one is.
+__device__ __forceinline__ float max3_nan(float a, float b, float c) {
+  float r;
+  asm("max.NaN.f32 %0, %1, %2, %3;" : "=f"(r) : "f"(a), "f"(b), "f"(c));
+  return r;
+}
+__device__ __forceinline__ float max8_nan(const float (&v)[8]) {
+  return max3_nan(max3_nan(fabsf(v[0]), fabsf(v[1]), fabsf(v[2])),
+                  max3_nan(fabsf(v[3]), fabsf(v[4]), fabsf(v[5])), max_nan(fabsf(v[6]), fabsf(v[7])));
+}
+__device__ __forceinline__ float min3(float a, float b, float c) {
+  float r;
+  asm("min.f32 %0, %1, %2, %3;" : "=f"(r) : "f"(a), "f"(b), "f"(c));
+  return r;
+}
+// The maximum over the 16 lanes that hold a block of 128.
+__device__ __forceinline__ float block_max(float m) {
 #pragma unroll
   for (int o = 8; o; o >>= 1) m = max_nan(m, __shfl_xor_sync(0xffffffffu, m, o));
   return m;
 }
 
-// v / scale, correctly rounded; 0 where the scale is 0.
+// v / scale, correctly rounded; 0 where the scale is 0.  m: the largest |v|.
 __device__ __forceinline__ void quotients(float (&v)[8], float m, float scale) {
-  if (m > 0x1p-60f && m < 0x1p126f) {
-    divide<8>(v, scale);
+  if (m > 0x1p-60f && m < 0x1p100f) {
+    const float y = reciprocal(scale);
+    const pair yy = make_pair2(y, y), ns = make_pair2(-scale, -scale);
+#pragma unroll
+    for (int k = 0; k < 8; k += 2)
+      split(quotient2(make_pair2(v[k], v[k + 1]), ns, yy), v[k], v[k + 1]);
   } else {
 #pragma unroll
     for (int k = 0; k < 8; ++k) v[k] = scale == 0.0f ? 0.0f : v[k] / scale;
   }
 }
 
-// 32 random bits of pair j of elements: the finaliser of MurmurHash3.
-__device__ __forceinline__ uint32_t random_bits(uint64_t j, uint32_t key) {
-  uint32_t h = static_cast<uint32_t>(j) ^ key ^ static_cast<uint32_t>(j >> 32) * 0x9E3779B9u;
+// 32 random bits from a pair's number and the tensor's key, already mixed: the
+// finaliser of MurmurHash3.
+__device__ __forceinline__ uint32_t random_bits(uint32_t h) {
   h = (h ^ h >> 16) * 0x85EBCA6Bu;
   h = (h ^ h >> 13) * 0xC2B2AE35u;
   return h ^ h >> 16;
 }
 
-// The E4M3 code of q in [0, 448], up with the probability of what lies above
-// the code below it, to the nearest 2^-16 (a block's largest, whose quotient
-// may be an ulp from 448, keeps its code).  Below 2^-6 codes are 2^-9 apart.
-__device__ __forceinline__ uint32_t random_code(float q, uint32_t u, bool some) {
-  const int low = static_cast<int>(floorf(__fadd_rn(q * 512.0f, (__uint2float_rn(u) + 0.5f) * 0x1p-16f)));
-  const int high = (static_cast<int>(__float_as_uint(q) + (u << 4) + 8) >> 20) - (120 << 3);
-  int code = q < 0x1p-6f ? low : high;
-  code = min(max(code, some ? 1 : 0), 0x7e);
-  return static_cast<uint32_t>(code);
+// The E4M3 codes of q in [0, 448], each in the top byte: up with the
+// probability of what lies above the code below it, to the nearest 2^-16 (a
+// block's largest, whose quotient may be an ulp from 448, keeps its code).
+// Times 2^-120 the exponents of both types agree, and E4M3's subnormals are
+// fp32's: so the code is bits 20 to 26 of q 2^-120 plus the noise, 16 bits
+// below bit 20 and a half of their last.  At least code 1.
+__device__ __forceinline__ void random_codes(float a, float b, uint32_t h, uint32_t& ca,
+                                             uint32_t& cb) {
+  split(mul2(make_pair2(a, b), make_pair2(0x1p-120f, 0x1p-120f)), a, b);
+  ca = max(__float_as_uint(a) * 16u + ((h << 8 & 0xffff00u) | 0x80u), 1u << 24);
+  cb = max(__float_as_uint(b) * 16u + ((h >> 8 & 0xffff00u) | 0x80u), 1u << 24);
+}
+__device__ __forceinline__ uint32_t top_bytes(uint32_t a, uint32_t b, uint32_t c, uint32_t d) {
+  return __byte_perm(__byte_perm(a, b, 0x0073), __byte_perm(c, d, 0x0073), 0x5410);
+}
+
+// What a step reads of eight elements, as it lies in memory: loaded a step
+// ahead.  k8: codes and scales, otherwise fp32.
+template <typename P, typename G, bool k8>
+struct Inputs {
+  Raw8<G> g;
+  Raw8<P> p;
+  Raw8<float> master;
+  uint2 mc, vc;
+  float ms, vs;
+  Raw8<float> m, v;
+  __device__ __forceinline__ void load(const AdamwTensor& t, int64_t at) {
+    g.load(static_cast<const G*>(t.grad) + at);
+    if (t.master)
+      master.load(t.master + at);
+    else
+      p.load(static_cast<const P*>(t.param) + at);
+    if constexpr (k8) {
+      mc = *reinterpret_cast<const uint2*>(static_cast<const uint8_t*>(t.m) + at);
+      vc = *reinterpret_cast<const uint2*>(static_cast<const uint8_t*>(t.v) + at);
+      ms = t.m_scale[at / kAdamwBlock];
+      vs = t.v_scale[at / kAdamwBlock];
+    } else {
+      m.load(static_cast<const float*>(t.m) + at);
+      v.load(static_cast<const float*>(t.v) + at);
+    }
+  }
+};
+
+// Elements [at, at + 8) of a tensor, by a thread; with 8-bit states 16
+// neighbouring threads hold a block of 128 (whose lanes are all here).  kFull:
+// from `in`; otherwise read here, as far as the tensor goes.
+template <typename P, typename G, bool k8, bool kFull>
+__device__ __forceinline__ void step8(const AdamwTensor& t, const AdamwScalars& c, float gs,
+                                      int64_t at, const Inputs<P, G, k8>& in) {
+  const int64_t n = t.n;
+  const int64_t block = at / kAdamwBlock;
+  float p[8], g[8], m[8], v[8], r[8];
+  if constexpr (kFull) {
+    in.g.unpack(g);
+    if (t.master)
+      in.master.unpack(p);
+    else
+      in.p.unpack(p);
+    if constexpr (k8) {
+      decode(in.mc, in.ms, m);
+      decode(in.vc, in.vs, v);
+    } else {
+      in.m.unpack(m);
+      in.v.unpack(v);
+    }
+  } else {
+    load_tail(static_cast<const G*>(t.grad), at, n, g);
+    if (t.master)
+      load_tail(static_cast<const float*>(t.master), at, n, p);
+    else
+      load_tail(static_cast<const P*>(t.param), at, n, p);
+    if constexpr (k8) {
+      decode(load_codes_tail(t.m, at, n), at < n ? t.m_scale[block] : 0.0f, m);
+      decode(load_codes_tail(t.v, at, n), at < n ? t.v_scale[block] : 0.0f, v);
+    } else {
+      load_tail(static_cast<const float*>(t.m), at, n, m);
+      load_tail(static_cast<const float*>(t.v), at, n, v);
+    }
+  }
+#pragma unroll
+  for (int k = 0; k < 8; k += 2) {
+    const pair gg = mul2(make_pair2(g[k], g[k + 1]), make_pair2(gs, gs));
+    const pair mm = add2(mul2(make_pair2(m[k], m[k + 1]), make_pair2(c.b1, c.b1)), c.one,
+                         mul2(gg, make_pair2(c.ob1, c.ob1)));
+    pair vv = make_pair2(v[k], v[k + 1]);
+    if constexpr (k8) vv = mul2(vv, vv);
+    vv = add2(mul2(vv, make_pair2(c.b2, c.b2)), c.one,
+              mul2(mul2(gg, gg), make_pair2(c.ob2, c.ob2)));
+    split(mm, m[k], m[k + 1]);
+    split(vv, v[k], v[k + 1]);
+  }
+  // v in a range where no step of the fast forms underflows or overflows
+  const bool tame = min3(min3(v[0], v[1], v[2]), min3(v[3], v[4], v[5]), fminf(v[6], v[7])) >= 0x1p-90f
+                    && max8_nan(v) <= 0x1p90f;
+  uint32_t zero[2] = {0, 0};  // bytes 0xff where r is 0
+  if (tame) {
+#pragma unroll
+    for (int k = 0; k < 8; k += 2) {
+      const pair rr = sqrt2(make_pair2(v[k], v[k + 1]));
+      const pair d = add2(mul2(rr, make_pair2(c.root, c.root)), c.one, make_pair2(c.eps, c.eps));
+      const pair u = divide2(make_pair2(m[k], m[k + 1]), d);
+      const pair q = add2(mul2(make_pair2(p[k], p[k + 1]), make_pair2(t.decay, t.decay)), c.one,
+                          mul2(u, make_pair2(c.nsize, c.nsize)));
+      split(rr, r[k], r[k + 1]);
+      split(q, p[k], p[k + 1]);
+    }
+  } else {
+    // v of 0, tiny, huge or not finite
+#pragma unroll
+    for (int k = 0; k < 8; ++k) {
+      r[k] = __fsqrt_rn(v[k]);
+      const float u = __fdiv_rn(m[k], __fadd_rn(__fmul_rn(r[k], c.root), c.eps));
+      p[k] = __fsub_rn(__fmul_rn(p[k], t.decay), __fmul_rn(u, c.size));
+      if (r[k] == 0.0f) zero[k / 4] |= 0xffu << 8 * (k & 3);
+    }
+  }
+  if (t.master) store8<kFull>(t.master, at, n, p);
+  store8<kFull>(static_cast<P*>(t.param), at, n, p);
+  if constexpr (!k8) {
+    store8<kFull>(static_cast<float*>(t.m), at, n, m);
+    store8<kFull>(static_cast<float*>(t.v), at, n, v);
+  } else {
+    const float mm = block_max(max8_nan(m)), rm = block_max(max8_nan(r));
+    const float ms = __fmul_rn(mm, 1.0f / 448.0f), rs = __fmul_rn(rm, 1.0f / 448.0f);
+    quotients(m, mm, ms);
+    uint2 code = make_uint2(0x7f7f7f7fu, 0x7f7f7f7fu);  // NaN
+    if (rm < __int_as_float(0x7f800000)) {
+      quotients(r, rm, rs);
+      const uint64_t j = static_cast<uint64_t>(at) >> 1;  // a multiple of 4
+      const uint32_t mixed =
+          static_cast<uint32_t>(j) ^ t.key ^ static_cast<uint32_t>(j >> 32) * 0x9E3779B9u;
+      uint32_t b[8];
+#pragma unroll
+      for (int k = 0; k < 8; k += 2)
+        random_codes(r[k], r[k + 1], random_bits(mixed ^ k / 2), b[k], b[k + 1]);
+      code.x = top_bytes(b[0], b[1], b[2], b[3]) & ~zero[0];
+      code.y = top_bytes(b[4], b[5], b[6], b[7]) & ~zero[1];
+    }
+    const uint2 mc = make_uint2(e4m3x2(m[0], m[1]) | e4m3x2(m[2], m[3]) << 16,
+                                e4m3x2(m[4], m[5]) | e4m3x2(m[6], m[7]) << 16);
+    store_codes8<kFull>(t.m, at, n, mc);
+    store_codes8<kFull>(t.v, at, n, code);
+    if ((threadIdx.x & 15) == 0 && (kFull || at < n)) {
+      t.m_scale[block] = ms;
+      t.v_scale[block] = rs;
+    }
+  }
 }
 
 template <typename P, typename G, bool k8>
@@ -151,77 +390,22 @@ __global__ void __launch_bounds__(kThreads) adamw_kernel(const __grid_constant__
     if (a.first[mid] <= blockIdx.x) lo = mid; else hi = mid;
   }
   const AdamwTensor& t = a.t[lo];
-  const AdamwScalars& c = a.c;
   const int64_t n = t.n;
-  const int64_t begin = static_cast<int64_t>(blockIdx.x - a.first[lo]) * kChunk;
-  const float gs = c.grad_scale ? *c.grad_scale : 1.0f;
-  for (int step = 0; step < kSteps; ++step) {
-    const int64_t start = begin + static_cast<int64_t>(step) * kStep;
-    if (start >= n) break;
-    const int64_t at = start + threadIdx.x * 8;
-    const int64_t block = at / kAdamwBlock;
-    float p[8], g[8], m[8], v[8];
-    load8(static_cast<const G*>(t.grad), at, n, g);
-    if (t.master) {
-      load8(static_cast<const float*>(t.master), at, n, p);
-    } else {
-      load8(static_cast<const P*>(t.param), at, n, p);
-    }
-    if constexpr (k8) {
-      const bool some = at < n;
-      decode(load_codes(static_cast<const uint8_t*>(t.m), at, n), some ? t.m_scale[block] : 0.0f, m);
-      decode(load_codes(static_cast<const uint8_t*>(t.v), at, n), some ? t.v_scale[block] : 0.0f, v);
-#pragma unroll
-      for (int k = 0; k < 8; ++k) v[k] = __fmul_rn(v[k], v[k]);
-    } else {
-      load8(static_cast<const float*>(t.m), at, n, m);
-      load8(static_cast<const float*>(t.v), at, n, v);
-    }
-    float r[8];
-#pragma unroll
-    for (int k = 0; k < 8; ++k) {
-      g[k] = __fmul_rn(g[k], gs);
-      m[k] = __fadd_rn(__fmul_rn(m[k], c.b1), __fmul_rn(g[k], c.ob1));
-      v[k] = __fadd_rn(__fmul_rn(v[k], c.b2), __fmul_rn(__fmul_rn(g[k], g[k]), c.ob2));
-      r[k] = __fsqrt_rn(v[k]);
-      const float u = __fdiv_rn(m[k], __fadd_rn(__fmul_rn(r[k], c.root), c.eps));
-      p[k] = __fsub_rn(__fmul_rn(p[k], t.decay), __fmul_rn(u, c.size));
-    }
-    if (t.master) store8(t.master, at, n, p);
-    store8(static_cast<P*>(t.param), at, n, p);
-    if constexpr (!k8) {
-      store8(static_cast<float*>(t.m), at, n, m);
-      store8(static_cast<float*>(t.v), at, n, v);
-    } else {
-      const float mm = block_max(m), rm = block_max(r);
-      const float ms = __fmul_rn(mm, 1.0f / 448.0f), rs = __fmul_rn(rm, 1.0f / 448.0f);
-      quotients(m, mm, ms);
-      const bool fine = rm < __int_as_float(0x7f800000);
-      uint2 code = make_uint2(0x7f7f7f7fu, 0x7f7f7f7fu);  // NaN
-      bool some[8];
-#pragma unroll
-      for (int k = 0; k < 8; ++k) some[k] = r[k] > 0.0f;
-      quotients(r, rm, rs);
-      if (fine) {
-        code = make_uint2(0, 0);
-#pragma unroll
-        for (int k = 0; k < 8; k += 2) {
-          const uint32_t h = random_bits(static_cast<uint64_t>(at + k) >> 1, t.key);
-          const uint32_t two = random_code(r[k], h & 0xffff, some[k]) |
-                               random_code(r[k + 1], h >> 16, some[k + 1]) << 8;
-          if (k < 4) code.x |= two << 8 * k; else code.y |= two << 8 * (k - 4);
-        }
-      }
-      const uint2 mc = make_uint2(e4m3x2(m[0], m[1]) | e4m3x2(m[2], m[3]) << 16,
-                                  e4m3x2(m[4], m[5]) | e4m3x2(m[6], m[7]) << 16);
-      store_codes8(static_cast<uint8_t*>(t.m), at, n, mc);
-      store_codes8(static_cast<uint8_t*>(t.v), at, n, code);
-      if ((threadIdx.x & 15) == 0 && at < n) {
-        t.m_scale[block] = ms;
-        t.v_scale[block] = rs;
-      }
-    }
+  const int64_t begin = static_cast<int64_t>(blockIdx.x - a.first[lo]) * a.steps * kStep;
+  const int64_t left = n - begin;
+  // whole steps of this block, then what is left of the tensor
+  const int full = static_cast<int>(min(left / kStep, static_cast<int64_t>(a.steps)));
+  int64_t at = begin + threadIdx.x * 8;
+  const float gs = a.c.grad_scale ? *a.c.grad_scale : 1.0f;
+  Inputs<P, G, k8> in;
+  if (full > 0) in.load(t, at);
+  for (int step = 0; step < full; ++step, at += kStep) {
+    const Inputs<P, G, k8> now = in;
+    if (step + 1 < full) in.load(t, at + kStep);
+    step8<P, G, k8, true>(t, a.c, gs, at, now);
   }
+  if (full < a.steps && left > static_cast<int64_t>(full) * kStep)
+    step8<P, G, k8, false>(t, a.c, gs, at, in);
 }
 
 template <typename P, typename G, bool k8>
@@ -236,26 +420,37 @@ cudaError_t launch_bits(const AdamwLaunch& a, bool bits8, cudaStream_t stream) {
 
 }  // namespace
 
+// Blocks of a tensor for `steps` steps each.
+static int64_t blocks_of(int64_t n, int steps) {
+  const int64_t chunk = static_cast<int64_t>(kStep) * steps;
+  return (n + chunk - 1) / chunk;
+}
+
 int adamw_group(const AdamwTensor* t, int count) {
-  uint64_t blocks = 0;
+  int64_t blocks = 0;
   int k = 0;
   for (; k < count && k < kAdamwTensors; ++k) {
-    const uint64_t b = static_cast<uint64_t>((t[k].n + kChunk - 1) / kChunk);
-    if (k && blocks + b > 0x40000000u) break;
+    const int64_t b = blocks_of(t[k].n, 1);
+    if (k && blocks + b > 0x40000000) break;
     blocks += b;
   }
   return k;
 }
 
 cudaError_t launch_adamw(const AdamwTensor* t, int count, const AdamwScalars& c, bool param_bf16,
-                         bool grad_bf16, bool bits8, cudaStream_t stream) {
+                         bool grad_bf16, bool bits8, int num_sms, cudaStream_t stream) {
   AdamwLaunch a;
   a.count = count;
   a.c = c;
+  // a block a step while the GPU has room for them all, else four, each but
+  // the first read while the one before it is computed
+  int64_t blocks = 0;
+  for (int k = 0; k < count; ++k) blocks += blocks_of(t[k].n, 1);
+  a.steps = blocks <= 4 * num_sms ? 1 : 4;
   a.first[0] = 0;
   for (int k = 0; k < count; ++k) {
     a.t[k] = t[k];
-    a.first[k + 1] = a.first[k] + static_cast<uint32_t>((t[k].n + kChunk - 1) / kChunk);
+    a.first[k + 1] = a.first[k] + static_cast<uint32_t>(blocks_of(t[k].n, a.steps));
   }
   if (a.first[count] == 0) return cudaSuccess;  // every tensor is empty
   if (param_bf16)

@@ -1423,11 +1423,11 @@ int32_t check_adamw_tensor(const moe_adamw_tensor& t, int32_t param_dtype, int32
   if (state_bits == 8 && !scales) return fail(MOE_ERR_INVALID_ARG, "8-bit states need their scales");
   if (state_bits == 32 && (t.exp_avg_scale || t.exp_avg_sq_scale))
     return fail(MOE_ERR_INVALID_ARG, "scales of 32-bit states");
-  const void* ptrs[] = {t.param,      t.grad,          t.master,          t.exp_avg,
-                        t.exp_avg_sq, t.exp_avg_scale, t.exp_avg_sq_scale};
+  const void* ptrs[] = {t.param, t.grad, t.master, t.exp_avg, t.exp_avg_sq};
   for (const void* q : ptrs)
-    if (reinterpret_cast<uintptr_t>(q) & 15u)
-      return fail(MOE_ERR_ALIGNMENT, "pointer not 16-byte aligned");
+    if (!aligned16(q)) return fail(MOE_ERR_ALIGNMENT, "pointer not 16-byte aligned");
+  if ((reinterpret_cast<uintptr_t>(t.exp_avg_scale) | reinterpret_cast<uintptr_t>(t.exp_avg_sq_scale)) & 3u)
+    return fail(MOE_ERR_ALIGNMENT, "scales not 4-byte aligned");
   return MOE_OK;
 }
 
@@ -1463,6 +1463,7 @@ int32_t moe_adamw(int32_t n_tensors, const moe_adamw_tensor* tensors_host, int32
   c.root = static_cast<float>(1.0 / std::sqrt(1.0 - std::pow(beta2, static_cast<double>(step))));
   c.eps = static_cast<float>(eps);
   c.size = static_cast<float>(lr / (1.0 - std::pow(beta1, static_cast<double>(step))));
+  c.nsize = -c.size;
   c.grad_scale = grad_scale;
   AdamwTensor group[kAdamwTensors];
   for (int32_t k = 0; k < n_tensors;) {
@@ -1476,7 +1477,7 @@ int32_t moe_adamw(int32_t n_tensors, const moe_adamw_tensor* tensors_host, int32
     }
     count = adamw_group(group, count);
     MOE_CUDA(launch_adamw(group, count, c, param_dtype == MOE_BF16, grad_dtype == MOE_BF16,
-                          state_bits == 8, static_cast<cudaStream_t>(stream)));
+                          state_bits == 8, num_sms(), static_cast<cudaStream_t>(stream)));
     k += count;
   }
   return MOE_OK;

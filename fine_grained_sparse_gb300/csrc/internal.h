@@ -365,13 +365,14 @@ struct AdamwScalars {
   float b1, ob1, b2, ob2;  // beta and 1 - beta
   float root;              // 1 / sqrt(1 - beta2^t)
   float eps;
-  float size;              // lr / (1 - beta1^t)
+  float size, nsize;       // lr / (1 - beta1^t), and its negative
+  float one = 1.0f;        // a 1 that the kernel's compiler does not know
   const float* grad_scale; // device scalar, or null
 };
 // Tensors, from the first, that one launch takes (at least one).
 int adamw_group(const AdamwTensor* t, int count);
 cudaError_t launch_adamw(const AdamwTensor* t, int count, const AdamwScalars& c, bool param_bf16,
-                         bool grad_bf16, bool bits8, cudaStream_t stream);
+                         bool grad_bf16, bool bits8, int num_sms, cudaStream_t stream);
 
 // --------------------------------------------------- products with 4-bit weights
 // The widest x: a row of it stays in shared memory beside the ring of weights.

@@ -64,7 +64,7 @@ typedef enum moe_norm_kind { MOE_NORM_RMS = 0, MOE_NORM_LAYER = 1 } moe_norm_kin
 
 /* One tensor of moe_adamw: n contiguous elements (0 is allowed: nothing is
  * done) and what the step keeps for them, all on the device, each buffer
- * 16-byte aligned. */
+ * 16-byte aligned but for the scales, which may lie on any 4 bytes. */
 typedef struct moe_adamw_tensor {
   void* param;        /* [n] of param_dtype, updated in place                  */
   const void* grad;   /* [n] of grad_dtype                                     */

@@ -39,7 +39,8 @@ def _bits(n, key, first=0):
 def _values(codes, scale):
     """fp32 values of E4M3 codes (uint8) with a scale per 128."""
     v = torch.from_numpy(codes).view(torch.float8_e4m3fn).float().numpy()
-    return v * np.repeat(scale, 128)[:v.size]
+    with np.errstate(invalid="ignore"):
+        return v * np.repeat(scale, 128)[:v.size]
 
 
 def _blocks(x):
@@ -84,9 +85,8 @@ def _step32(t, c):
     rs = _blocks(r).max(1) * f32(1.0 / 448.0)
     q = _quotients(r, rs)
     w = _bits(r.size, t["key"])
-    low = np.floor(q * f32(512) + (w.astype(f32) + f32(0.5)) * f32(2.0 ** -16)).astype(np.int64)
-    high = ((q.view(np.int32).astype(np.int64) + (w << 4) + 8) >> 20) - (120 << 3)
-    code = np.clip(np.where(q < f32(2.0 ** -6), low, high), 0, 0x7e)
+    t20 = (q * f32(2.0 ** -120)).view(np.int32).astype(np.int64) + (w << 4) + 8
+    code = t20 >> 20
     t["v"] = np.where((code == 0) & (r > 0), 1, code).astype(np.uint8)
     t["vs"] = rs
 
@@ -125,9 +125,9 @@ def _device(t, param, grad):
         d["master"] = put(t["master"], torch.float32, 5)
     state = torch.uint8 if "ms" in t else torch.float32
     d["exp_avg"], d["exp_avg_sq"] = put(t["m"], state, 5), put(t["v"], state, 5)
-    if "ms" in t:
-        d["exp_avg_scale"] = put(t["ms"], torch.float32, 5)
-        d["exp_avg_sq_scale"] = put(t["vs"], torch.float32, 5)
+    if "ms" in t:  # the scales on any 4 bytes
+        for name, x in (("exp_avg_scale", t["ms"]), ("exp_avg_sq_scale", t["vs"])):
+            d[name] = torch.cat((torch.zeros(3, device="cuda"), put(x, torch.float32, 5)))[3:]
     d["n"], d["weight_decay"] = t["p"].size, t["wd"]
     return d
 

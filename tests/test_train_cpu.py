@@ -141,7 +141,7 @@ def _adamw(fgs, tensor=(), n_tensors=1, tensors=True, **over):
     ({"bits": 32}, 1),                           # scales of fp32 states
     ({"tensor": {"param": P[0] + 8}}, 3), ({"tensor": {"grad": P[1] + 2}}, 3),
     ({"tensor": {"master": P[2] + 4}}, 3), ({"tensor": {"exp_avg": P[3] + 1}}, 3),
-    ({"tensor": {"exp_avg_sq_scale": P[6] + 4}}, 3),
+    ({"tensor": {"exp_avg_scale": P[5] + 2}}, 3), ({"tensor": {"exp_avg_sq_scale": P[6] + 1}}, 3),
 ])
 def test_adamw_refusals(fgs, kw, status):
     assert _adamw(fgs, **kw) == status
