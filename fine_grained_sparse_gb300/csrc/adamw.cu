@@ -20,13 +20,16 @@ namespace {
 
 constexpr int kThreads = 256;
 constexpr int kStep = 8 * kThreads;  // elements of a block at a time
+constexpr int kSteps = 4;            // of a block in large launches
 
+// A launch's tensors, by value.  start[i] is the tensor of block i << shift.
+constexpr int kStarts = 512;
 struct AdamwLaunch {
-  AdamwTensor t[kAdamwTensors];
-  uint32_t first[kAdamwTensors + 1];  // the blocks before each tensor's
-  int count;
-  int steps;  // of a block
   AdamwScalars c;
+  int shift;
+  uint8_t start[kStarts];
+  uint32_t first[kAdamwTensors + 1];  // the blocks before each tensor's
+  AdamwTensor t[kAdamwTensors];
 };
 
 // Eight values of a tensor as they lie in memory, and as fp32.
@@ -62,8 +65,14 @@ struct Raw8<float> {
 // Values [at, at + 8) of a tensor of n, 0 beyond its end.
 template <typename T>
 __device__ __forceinline__ void load_tail(const T* p, int64_t at, int64_t n, float (&v)[8]) {
+  if (at + 8 <= n) {
+    Raw8<T> x;
+    x.load(p + at);
+    x.unpack(v);
+  } else {
 #pragma unroll
-  for (int k = 0; k < 8; ++k) v[k] = at + k < n ? load<1>(p + at + k).v[0] : 0.0f;
+    for (int k = 0; k < 8; ++k) v[k] = at + k < n ? load<1>(p + at + k).v[0] : 0.0f;
+  }
 }
 template <bool kFull, typename T>
 __device__ __forceinline__ void store8(T* p, int64_t at, int64_t n, const float (&v)[8]) {
@@ -87,6 +96,7 @@ __device__ __forceinline__ void store8(T* p, int64_t at, int64_t n, const float 
 // Eight E4M3 codes, 0 beyond the end.
 __device__ __forceinline__ uint2 load_codes_tail(const void* codes, int64_t at, int64_t n) {
   const uint8_t* p = static_cast<const uint8_t*>(codes);
+  if (at + 8 <= n) return *reinterpret_cast<const uint2*>(p + at);
   uint2 u = make_uint2(0, 0);
 #pragma unroll
   for (int k = 0; k < 8; ++k) {
@@ -119,27 +129,6 @@ __device__ __forceinline__ void decode(uint2 u, float scale, float (&v)[8]) {
     v[2 * k] = __fmul_rn(v[2 * k], scale);
     v[2 * k + 1] = __fmul_rn(v[2 * k + 1], scale);
   }
-}
-
-// Pairs of fp32 values, one instruction for both.
-typedef unsigned long long pair;
-__device__ __forceinline__ pair make_pair2(float a, float b) {
-  pair r;
-  asm("mov.b64 %0, {%1, %2};" : "=l"(r) : "f"(a), "f"(b));
-  return r;
-}
-__device__ __forceinline__ void split(pair v, float& a, float& b) {
-  asm("mov.b64 {%0, %1}, %2;" : "=f"(a), "=f"(b) : "l"(v));
-}
-__device__ __forceinline__ pair mul2(pair a, pair b) {
-  pair r;
-  asm("mul.rn.f32x2 %0, %1, %2;" : "=l"(r) : "l"(a), "l"(b));
-  return r;
-}
-__device__ __forceinline__ pair fma2(pair a, pair b, pair c) {
-  pair r;
-  asm("fma.rn.f32x2 %0, %1, %2, %3;" : "=l"(r) : "l"(a), "l"(b), "l"(c));
-  return r;
 }
 
 // a + b with a rounding of its own: as a 1 + b with a 1 that the compiler does
@@ -216,9 +205,12 @@ __device__ __forceinline__ void quotients(float (&v)[8], float m, float scale) {
 #pragma unroll
     for (int k = 0; k < 8; k += 2)
       split(quotient2(make_pair2(v[k], v[k + 1]), ns, yy), v[k], v[k + 1]);
+  } else if (scale == 0.0f) {
+#pragma unroll
+    for (int k = 0; k < 8; ++k) v[k] = 0.0f;
   } else {
 #pragma unroll
-    for (int k = 0; k < 8; ++k) v[k] = scale == 0.0f ? 0.0f : v[k] / scale;
+    for (int k = 0; k < 8; ++k) v[k] = v[k] / scale;
   }
 }
 
@@ -323,8 +315,10 @@ __device__ __forceinline__ void step8(const AdamwTensor& t, const AdamwScalars& 
     split(vv, v[k], v[k + 1]);
   }
   // v in a range where no step of the fast forms underflows or overflows
-  const bool tame = min3(min3(v[0], v[1], v[2]), min3(v[3], v[4], v[5]), fminf(v[6], v[7])) >= 0x1p-90f
-                    && max8_nan(v) <= 0x1p90f;
+  const float vmax = max8_nan(v);
+  const bool tame =
+      min3(min3(v[0], v[1], v[2]), min3(v[3], v[4], v[5]), fminf(v[6], v[7])) >= 0x1p-90f &&
+      vmax <= 0x1p90f;
   uint32_t zero[2] = {0, 0};  // bytes 0xff where r is 0
   if (tame) {
 #pragma unroll
@@ -337,6 +331,14 @@ __device__ __forceinline__ void step8(const AdamwTensor& t, const AdamwScalars& 
       split(rr, r[k], r[k + 1]);
       split(q, p[k], p[k + 1]);
     }
+  } else if (vmax == 0.0f && c.eps > 0.0f && max8_nan(m) == 0.0f) {
+    // what no gradient has reached: 0 / eps is m's 0
+#pragma unroll
+    for (int k = 0; k < 8; ++k) {
+      r[k] = 0.0f;
+      p[k] = __fadd_rn(__fmul_rn(p[k], t.decay), __fmul_rn(m[k], c.nsize));
+    }
+    zero[0] = zero[1] = 0xffffffffu;
   } else {
     // v of 0, tiny, huge or not finite
 #pragma unroll
@@ -380,42 +382,39 @@ __device__ __forceinline__ void step8(const AdamwTensor& t, const AdamwScalars& 
   }
 }
 
-template <typename P, typename G, bool k8>
-__global__ void __launch_bounds__(kThreads) adamw_kernel(const __grid_constant__ AdamwLaunch a) {
+// kMany: kSteps steps a block, each but the first read while the one before it
+// is computed; otherwise one, in fewer registers.  352M bf16 elements with a
+// master copy and 8-bit states (5.68 GB): 896 us, 6.34 TB/s, 95% of the copy
+// rate, with 72% of the issue slots taken; without the master copy 134M take
+// 338 us, 60%, bound by the instructions (about 75 an element).  With products
+// and roots one at a time instead of in pairs 938, with the library's roots and
+// quotients 1177.
+template <typename P, typename G, bool k8, bool kMany>
+__global__ void __launch_bounds__(kThreads, k8 && kMany ? 3 : 2)
+    adamw_kernel(const __grid_constant__ AdamwLaunch a) {
   pdl_wait();
   // the tensor of this block: first[lo] <= blockIdx.x < first[lo + 1]
-  int lo = 0, hi = a.count;
-  while (hi - lo > 1) {
-    const int mid = (lo + hi) >> 1;
-    if (a.first[mid] <= blockIdx.x) lo = mid; else hi = mid;
-  }
+  int lo = a.start[blockIdx.x >> a.shift];
+  while (a.first[lo + 1] <= blockIdx.x) ++lo;
   const AdamwTensor& t = a.t[lo];
   const int64_t n = t.n;
-  const int64_t begin = static_cast<int64_t>(blockIdx.x - a.first[lo]) * a.steps * kStep;
+  constexpr int kOwn = kMany ? kSteps : 1;
+  const int64_t begin = static_cast<int64_t>(blockIdx.x - a.first[lo]) * (kOwn * kStep);
   const int64_t left = n - begin;
   // whole steps of this block, then what is left of the tensor
-  const int full = static_cast<int>(min(left / kStep, static_cast<int64_t>(a.steps)));
+  const int full = static_cast<int>(min(left / kStep, static_cast<int64_t>(kOwn)));
   int64_t at = begin + threadIdx.x * 8;
   const float gs = a.c.grad_scale ? *a.c.grad_scale : 1.0f;
   Inputs<P, G, k8> in;
   if (full > 0) in.load(t, at);
   for (int step = 0; step < full; ++step, at += kStep) {
     const Inputs<P, G, k8> now = in;
-    if (step + 1 < full) in.load(t, at + kStep);
+    if (kMany && step + 1 < full) in.load(t, at + kStep);
     step8<P, G, k8, true>(t, a.c, gs, at, now);
+    if (!kMany) return;
   }
-  if (full < a.steps && left > static_cast<int64_t>(full) * kStep)
+  if (full < kOwn && at - (threadIdx.x & 31) * 8 < n)  // a warp with something left
     step8<P, G, k8, false>(t, a.c, gs, at, in);
-}
-
-template <typename P, typename G, bool k8>
-cudaError_t launch(const AdamwLaunch& a, cudaStream_t stream) {
-  return launch_pdl(adamw_kernel<P, G, k8>, dim3(a.first[a.count]), dim3(kThreads), 0, stream, a);
-}
-
-template <typename P, typename G>
-cudaError_t launch_bits(const AdamwLaunch& a, bool bits8, cudaStream_t stream) {
-  return bits8 ? launch<P, G, true>(a, stream) : launch<P, G, false>(a, stream);
 }
 
 }  // namespace
@@ -437,27 +436,53 @@ int adamw_group(const AdamwTensor* t, int count) {
   return k;
 }
 
-cudaError_t launch_adamw(const AdamwTensor* t, int count, const AdamwScalars& c, bool param_bf16,
-                         bool grad_bf16, bool bits8, int num_sms, cudaStream_t stream) {
+namespace {
+
+template <typename P, typename G, bool k8, bool kMany>
+cudaError_t launch(const AdamwTensor* t, int count, const AdamwScalars& c, cudaStream_t stream) {
   AdamwLaunch a;
-  a.count = count;
   a.c = c;
-  // a block a step while the GPU has room for them all, else four, each but
-  // the first read while the one before it is computed
-  int64_t blocks = 0;
-  for (int k = 0; k < count; ++k) blocks += blocks_of(t[k].n, 1);
-  a.steps = blocks <= 4 * num_sms ? 1 : 4;
   a.first[0] = 0;
   for (int k = 0; k < count; ++k) {
     a.t[k] = t[k];
-    a.first[k + 1] = a.first[k] + static_cast<uint32_t>(blocks_of(t[k].n, a.steps));
+    a.first[k + 1] = a.first[k] + static_cast<uint32_t>(blocks_of(t[k].n, kMany ? kSteps : 1));
   }
-  if (a.first[count] == 0) return cudaSuccess;  // every tensor is empty
+  const uint32_t blocks = a.first[count];
+  if (blocks == 0) return cudaSuccess;  // every tensor is empty
+  a.shift = 0;
+  while ((blocks - 1) >> a.shift >= kStarts) ++a.shift;
+  for (uint32_t i = 0, lo = 0; i <= (blocks - 1) >> a.shift; ++i) {
+    while (a.first[lo + 1] <= i << a.shift) ++lo;
+    a.start[i] = static_cast<uint8_t>(lo);
+  }
+  return launch_pdl(adamw_kernel<P, G, k8, kMany>, dim3(blocks), dim3(kThreads), 0, stream, a);
+}
+
+template <typename P, typename G>
+cudaError_t launch_states(const AdamwTensor* t, int count, const AdamwScalars& c, bool bits8,
+                          bool many, cudaStream_t stream) {
+  if (!bits8) return launch<P, G, false, false>(t, count, c, stream);
+  return many ? launch<P, G, true, true>(t, count, c, stream)
+              : launch<P, G, true, false>(t, count, c, stream);
+}
+
+}  // namespace
+
+cudaError_t launch_adamw(const AdamwTensor* t, int count, const AdamwScalars& c, bool param_bf16,
+                         bool grad_bf16, bool bits8, int num_sms, cudaStream_t stream) {
+  // 8-bit states: one step a block while there are few blocks, then four (3M
+  // elements of bf16 with a master copy 10.7 us with one, 11.5 with four; 16M
+  // 53.0 and 47.3; 352M 1065 and 895; eight steps 883, and 49.8 for 16M).
+  // 32-bit states need no reading ahead: 134M fp32 523 us with one step in 48
+  // registers, 533 with four in 116.
+  int64_t blocks = 0;
+  for (int k = 0; k < count; ++k) blocks += blocks_of(t[k].n, 1);
+  const bool many = blocks > 16 * num_sms;
   if (param_bf16)
-    return grad_bf16 ? launch_bits<__nv_bfloat16, __nv_bfloat16>(a, bits8, stream)
-                     : launch_bits<__nv_bfloat16, float>(a, bits8, stream);
-  return grad_bf16 ? launch_bits<float, __nv_bfloat16>(a, bits8, stream)
-                   : launch_bits<float, float>(a, bits8, stream);
+    return grad_bf16 ? launch_states<__nv_bfloat16, __nv_bfloat16>(t, count, c, bits8, many, stream)
+                     : launch_states<__nv_bfloat16, float>(t, count, c, bits8, many, stream);
+  return grad_bf16 ? launch_states<float, __nv_bfloat16>(t, count, c, bits8, many, stream)
+                   : launch_states<float, float>(t, count, c, bits8, many, stream);
 }
 
 }  // namespace fgs

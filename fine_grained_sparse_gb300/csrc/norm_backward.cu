@@ -45,167 +45,434 @@ __device__ __forceinline__ Piece<T, N> row_sum(const T* a, const T* r, int64_t a
 }
 
 // Sums of two values over a block's threads (or a warp's), the same in all of
-// them.  Callers alternate `buf`: one barrier then separates the uses.
+// them.  The halves of a warp first exchange what the other adds up, so that a
+// round of the tree serves both values.  Callers alternate between two parts:
+// one barrier then separates the uses of each.
 template <bool kWarp>
-__device__ __forceinline__ float2 block_sum(float x, float y, float2 (*part)[32], int buf) {
+__device__ __forceinline__ float2 block_sum(float x, float y, float (&part)[64]) {
+  const int lane = threadIdx.x & 31;
+  const bool low = lane < 16;
+  float v = low ? x : y;
+  v += __shfl_xor_sync(0xffffffffu, low ? y : x, 16);
 #pragma unroll
-  for (int o = 16; o; o >>= 1) {
-    x += __shfl_xor_sync(0xffffffffu, x, o);
-    y += __shfl_xor_sync(0xffffffffu, y, o);
-  }
+  for (int o = 8; o; o >>= 1) v += __shfl_xor_sync(0xffffffffu, v, o);
   if constexpr (!kWarp) {
-    const int lane = threadIdx.x & 31;
-    if (lane == 0) part[buf][threadIdx.x >> 5] = make_float2(x, y);
+    // the sums of warp i at 2 i and 2 i + 1
+    if ((lane & 15) == 0) part[threadIdx.x >> 4] = v;
     __syncthreads();
-    const float2 v = lane < blockDim.x / 32 ? part[buf][lane] : make_float2(0.f, 0.f);
-    x = v.x, y = v.y;
+    const int sums = blockDim.x / 16, i = 2 * (lane & 15) + (lane >> 4);
+    v = i < sums ? part[i] : 0.0f;
+    if (i + 32 < sums) v += part[i + 32];
 #pragma unroll
-    for (int o = 16; o; o >>= 1) {
-      x += __shfl_xor_sync(0xffffffffu, x, o);
-      y += __shfl_xor_sync(0xffffffffu, y, o);
-    }
+    for (int o = 8; o; o >>= 1) v += __shfl_xor_sync(0xffffffffu, v, o);
   }
-  return make_float2(x, y);
+  const float other = __shfl_xor_sync(0xffffffffu, v, 16);
+  return low ? make_float2(v, other) : make_float2(other, v);
 }
 
-// A block a row, or (kWarpRow) a warp a row; a thread holds the same kP pieces
-// of N columns of each of its rows.
+// N values: one, or N / 2 pairs.
+template <int N>
+struct Vec {
+  static constexpr int M = N / 2;
+  pair v[M];
+};
+template <>
+struct Vec<1> {
+  float v;
+};
+template <int N>
+__device__ __forceinline__ Vec<N> mul(const Vec<N>& a, const Vec<N>& b) {
+  Vec<N> r;
+  if constexpr (N == 1)
+    r.v = a.v * b.v;
+  else
+#pragma unroll
+    for (int i = 0; i < Vec<N>::M; ++i) r.v[i] = mul2(a.v[i], b.v[i]);
+  return r;
+}
+template <int N>
+__device__ __forceinline__ Vec<N> fma(const Vec<N>& a, const Vec<N>& b, const Vec<N>& c) {
+  Vec<N> r;
+  if constexpr (N == 1)
+    r.v = fmaf(a.v, b.v, c.v);
+  else
+#pragma unroll
+    for (int i = 0; i < Vec<N>::M; ++i) r.v[i] = fma2(a.v[i], b.v[i], c.v[i]);
+  return r;
+}
+template <int N>
+__device__ __forceinline__ Vec<N> add(const Vec<N>& a, const Vec<N>& b) {
+  Vec<N> r;
+  if constexpr (N == 1)
+    r.v = a.v + b.v;
+  else
+#pragma unroll
+    for (int i = 0; i < Vec<N>::M; ++i)
+      asm("add.rn.f32x2 %0, %1, %2;" : "=l"(r.v[i]) : "l"(a.v[i]), "l"(b.v[i]));
+  return r;
+}
+template <int N>
+__device__ __forceinline__ Vec<N> all(float a) {
+  Vec<N> r;
+  if constexpr (N == 1)
+    r.v = a;
+  else
+#pragma unroll
+    for (int i = 0; i < Vec<N>::M; ++i) r.v[i] = make_pair2(a, a);
+  return r;
+}
+template <int N>
+__device__ __forceinline__ float total(const Vec<N>& a) {
+  if constexpr (N == 1) {
+    return a.v;
+  } else {
+    float s = 0.0f;
+#pragma unroll
+    for (int i = 0; i < Vec<N>::M; ++i) {
+      float x, y;
+      split(a.v[i], x, y);
+      s += x + y;
+    }
+    return s;
+  }
+}
+
+// N values of type T in memory, of 2 to 16 bytes, and as a Vec.
+template <typename T, int N>
+struct Chunk;
+template <>
+struct Chunk<__nv_bfloat16, 8> { uint4 u; };
+template <>
+struct Chunk<__nv_bfloat16, 2> { uint32_t u; };
+template <>
+struct Chunk<__nv_bfloat16, 1> { __nv_bfloat16 u; };
+template <>
+struct Chunk<float, 4> { float4 u; };
+template <>
+struct Chunk<float, 1> { float u; };
+__device__ __forceinline__ pair bf16_pair(uint32_t w) {
+  return make_pair2(__uint_as_float(w << 16), __uint_as_float(w & 0xffff0000u));
+}
+__device__ __forceinline__ uint32_t pair_bf16(pair v) {
+  float a, b;
+  split(v, a, b);
+  return pack_bf16x2(a, b);
+}
+__device__ __forceinline__ Vec<8> unpack(const Chunk<__nv_bfloat16, 8>& c) {
+  return {{bf16_pair(c.u.x), bf16_pair(c.u.y), bf16_pair(c.u.z), bf16_pair(c.u.w)}};
+}
+__device__ __forceinline__ Vec<2> unpack(const Chunk<__nv_bfloat16, 2>& c) {
+  return {{bf16_pair(c.u)}};
+}
+__device__ __forceinline__ Vec<1> unpack(const Chunk<__nv_bfloat16, 1>& c) {
+  return {__bfloat162float(c.u)};
+}
+__device__ __forceinline__ Vec<4> unpack(const Chunk<float, 4>& c) {
+  return {{make_pair2(c.u.x, c.u.y), make_pair2(c.u.z, c.u.w)}};
+}
+__device__ __forceinline__ Vec<1> unpack(const Chunk<float, 1>& c) { return {c.u}; }
+__device__ __forceinline__ void pack(const Vec<8>& v, Chunk<__nv_bfloat16, 8>& c) {
+  c.u = make_uint4(pair_bf16(v.v[0]), pair_bf16(v.v[1]), pair_bf16(v.v[2]), pair_bf16(v.v[3]));
+}
+__device__ __forceinline__ void pack(const Vec<2>& v, Chunk<__nv_bfloat16, 2>& c) {
+  c.u = pair_bf16(v.v[0]);
+}
+__device__ __forceinline__ void pack(const Vec<1>& v, Chunk<__nv_bfloat16, 1>& c) {
+  c.u = __float2bfloat16_rn(v.v);
+}
+__device__ __forceinline__ void pack(const Vec<4>& v, Chunk<float, 4>& c) {
+  split(v.v[0], c.u.x, c.u.y);
+  split(v.v[1], c.u.z, c.u.w);
+}
+__device__ __forceinline__ void pack(const Vec<1>& v, Chunk<float, 1>& c) { c.u = v.v; }
+
+// A chunk of global memory into shared memory, past the registers and L1.
+template <int kBytes>
+__device__ __forceinline__ void copy_async(uint32_t dst, const void* src) {
+  if constexpr (kBytes == 16)
+    asm volatile("cp.async.cg.shared.global [%0], [%1], 16;" ::"r"(dst), "l"(src) : "memory");
+  else
+    asm volatile("cp.async.ca.shared.global [%0], [%1], %2;" ::"r"(dst), "l"(src), "n"(kBytes)
+                 : "memory");
+}
+__device__ __forceinline__ void commit_copies() {
+  asm volatile("cp.async.commit_group;" ::: "memory");
+}
+// Wait until at most `left` (< kMaxStages) of the thread's groups of copies are
+// under way.
+constexpr int kMaxStages = 4;
+__device__ __forceinline__ void wait_copies(int left) {
+  if (left == 0)
+    asm volatile("cp.async.wait_group 0;" ::: "memory");
+  else if (left == 1)
+    asm volatile("cp.async.wait_group 1;" ::: "memory");
+  else if (left == 2)
+    asm volatile("cp.async.wait_group 2;" ::: "memory");
+  else
+    asm volatile("cp.async.wait_group 3;" ::: "memory");
+}
+
+// A block a row, or (kWarpRow) a warp a row; a thread holds the same kP chunks
+// of N columns of each of its rows.  But for single bf16 values a thread keeps
+// the chunks of its next `stages` rows on their way into shared memory, where
+// it alone reads them: no barrier, and no register holds what is under way.
+//   dx = r g - (r r mean(g s)) r s + dh, and for the layer form
+//   dx = r g - (r r mean(g s)) r s + (dh - r mean g), s there the difference to mu
 constexpr int kRowWarps = 8;
 
-template <typename T, int N, int kP, bool kLayer, bool kWarpRow, int kMaxThreads>
-__global__ void __launch_bounds__(kMaxThreads)
-    norm_backward_kernel(const BackwardPtrs p, float eps, int d, int64_t rows) {
-  __shared__ float2 part[2][32];
+template <typename T, int N, int kP, bool kLayer, bool kWarpRow, int kMaxThreads, int kMinBlocks>
+__global__ void __launch_bounds__(kMaxThreads, kMinBlocks)
+    norm_backward_kernel(const BackwardPtrs p, float eps, int d, int64_t rows, int stages) {
+  using C = Chunk<T, N>;
+  using V = Vec<N>;
+  __shared__ float part[2][64];
+  extern __shared__ uint4 ring_bytes[];
+  C* const ring = reinterpret_cast<C*>(ring_bytes);
+  constexpr bool kRing = sizeof(C) >= 4;
   pdl_wait();
   const int threads = kWarpRow ? 32 : blockDim.x;
   const int tid = kWarpRow ? threadIdx.x & 31 : threadIdx.x;
   const int teams = kWarpRow ? kRowWarps : 1;
   const int team = kWarpRow ? threadIdx.x / 32 : 0;
-  const int pieces = d / N;
-  const T* w = static_cast<const T*>(p.w);
+  const int chunks = d / N;
+  const C* const w = static_cast<const C*>(p.w);
   const float inv_d = 1.0f / static_cast<float>(d);
-  float dw[kP][N], db[kLayer ? kP : 1][N];
+  const int64_t first = static_cast<int64_t>(blockIdx.x) * teams + team;
+  const int64_t stride = static_cast<int64_t>(gridDim.x) * teams;
+  V dw[kP], db[kLayer ? kP : 1];
 #pragma unroll
-  for (int j = 0; j < kP; ++j)
+  for (int j = 0; j < kP; ++j) {
+    dw[j] = all<N>(0.0f);
+    if constexpr (kLayer) db[j] = all<N>(0.0f);
+  }
+  // a stage: dy, x, then the residual and dh where there are any
+  const bool with_r = p.r, with_dh = p.dh && p.dx;
+  const int tensors = 2 + with_r + with_dh;
+  const int pitch = kP * blockDim.x;  // chunks of a tensor in a stage
+  const int64_t step = stride * chunks;
+  int64_t ahead = first * chunks + tid;  // of the thread's first chunk to fetch
+  int64_t left = rows - first;           // rows from there on
+  uint32_t fill = smem_u32(ring + threadIdx.x);
+  const uint32_t begin = fill, stage_bytes = tensors * pitch * sizeof(C);
+  const uint32_t end = begin + stages * stage_bytes;
+  auto fetch = [&]() {
+    if (left > 0) {
+      uint32_t to = fill;
+      auto one = [&](const void* from) {
+        const C* src = static_cast<const C*>(from) + ahead;
 #pragma unroll
-    for (int k = 0; k < N; ++k) {
-      dw[j][k] = 0.0f;
-      if constexpr (kLayer) db[j][k] = 0.0f;
+        for (int j = 0; j < kP; ++j)
+          if (tid + j * threads < chunks)
+            copy_async<sizeof(C)>(to + j * blockDim.x * static_cast<uint32_t>(sizeof(C)),
+                                  src + j * threads);
+        to += pitch * sizeof(C);
+      };
+      one(p.dy);
+      one(p.a);
+      if (with_r) one(p.r);
+      if (with_dh) one(p.dh);
     }
-  int buf = 0;
-  for (int64_t row = static_cast<int64_t>(blockIdx.x) * teams + team; row < rows;
-       row += static_cast<int64_t>(gridDim.x) * teams) {
-    const int64_t base = row * d;
-    Piece<T, N> s[kP], y[kP];
-#pragma unroll
-    for (int j = 0; j < kP; ++j) {
-      const int i = tid + j * threads;
-      if (i < pieces) {
-        s[j] = row_sum<T, N>(static_cast<const T*>(p.a),
-                             static_cast<const T*>(p.r), base + static_cast<int64_t>(i) * N);
-        y[j] = load<N>(static_cast<const T*>(p.dy) + base + static_cast<int64_t>(i) * N);
-      } else {
-#pragma unroll
-        for (int k = 0; k < N; ++k) s[j].v[k] = y[j].v[k] = 0.0f;
-      }
-    }
-    float x0 = 0.0f, x1 = 0.0f, mu = 0.0f, mg = 0.0f;
+    commit_copies();
+    ahead += step;
+    left -= stride;
+    fill += stage_bytes;
+    if (fill == end) fill = begin;
+  };
+  if constexpr (kRing)
+    for (int i = 0; i < stages; ++i) fetch();
+
+  int buf = 0, stage = 0;
+  for (int64_t row = first; row < rows; row += stride) {
+    const int64_t base = row * chunks + tid;
+    if constexpr (kRing) wait_copies(stages - 1);
+    const C* from = ring + stage * tensors * pitch + threadIdx.x;
+    // chunk j of tensor t; the last of them is dh
+    auto chunk = [&](const void* global, int t, int j) {
+      if constexpr (kRing)
+        return from[t * pitch + j * blockDim.x];
+      else
+        return static_cast<const C*>(global)[base + j * threads];
+    };
+    auto sum = [&](int j) {
+      V s = unpack(chunk(p.a, 1, j));
+      if (with_r) s = add(s, unpack(chunk(p.r, 2, j)));
+      return s;
+    };
+    float mu = 0.0f, mg = 0.0f;
     if constexpr (kLayer) {
+      V a = all<N>(0.0f), b = a;
 #pragma unroll
       for (int j = 0; j < kP; ++j) {
-        const int i = tid + j * threads;
-        if (i >= pieces) continue;
-        const Piece<T, N> g = load<N>(w + static_cast<int64_t>(i) * N);
-#pragma unroll
-        for (int k = 0; k < N; ++k) {
-          x0 += s[j].v[k];
-          x1 = fmaf(y[j].v[k], g.v[k], x1);
-        }
+        if (tid + j * threads >= chunks) continue;
+        a = add(a, sum(j));
+        b = fma(unpack(chunk(p.dy, 0, j)), unpack(w[tid + j * threads]), b);
       }
-      const float2 t = block_sum<kWarpRow>(x0, x1, part, buf);
+      const float2 t = block_sum<kWarpRow>(total(a), total(b), part[buf]);
       buf ^= 1;
       mu = t.x * inv_d;
       mg = t.y * inv_d;
-      x0 = x1 = 0.0f;
     }
+    const V vmu = all<N>(-mu);
+    V a = all<N>(0.0f), b = a;
 #pragma unroll
     for (int j = 0; j < kP; ++j) {
-      const int i = tid + j * threads;
-      if (i >= pieces) continue;
-      const Piece<T, N> g = load<N>(w + static_cast<int64_t>(i) * N);
-#pragma unroll
-      for (int k = 0; k < N; ++k) {
-        if constexpr (kLayer) s[j].v[k] -= mu;
-        x0 = fmaf(s[j].v[k], s[j].v[k], x0);
-        x1 = fmaf(y[j].v[k] * g.v[k], s[j].v[k], x1);
-      }
+      if (tid + j * threads >= chunks) continue;
+      V s = sum(j);
+      if constexpr (kLayer) s = add(s, vmu);
+      a = fma(s, s, a);
+      b = fma(mul(unpack(chunk(p.dy, 0, j)), unpack(w[tid + j * threads])), s, b);
     }
-    const float2 t = block_sum<kWarpRow>(x0, x1, part, buf);
+    const float2 t = block_sum<kWarpRow>(total(a), total(b), part[buf]);
     buf ^= 1;
     const float rs = rsqrtf(t.x * inv_d + eps);
-    const float c = rs * t.y * inv_d;  // mean(g u)
+    const float c = -rs * (rs * rs * (t.y * inv_d));
+    const V vrs = all<N>(rs), vc = all<N>(c), vg = all<N>(-rs * mg);
 #pragma unroll
     for (int j = 0; j < kP; ++j) {
-      const int i = tid + j * threads;
-      if (i >= pieces) continue;
-      const int64_t at = base + static_cast<int64_t>(i) * N;
-#pragma unroll
-      for (int k = 0; k < N; ++k) {
-        s[j].v[k] *= rs;
-        dw[j][k] = fmaf(y[j].v[k], s[j].v[k], dw[j][k]);
-        if constexpr (kLayer) db[j][k] += y[j].v[k];
-      }
+      if (tid + j * threads >= chunks) continue;
+      V s = sum(j);
+      if constexpr (kLayer) s = add(s, vmu);
+      const V y = unpack(chunk(p.dy, 0, j));
+      dw[j] = fma(mul(y, vrs), s, dw[j]);
+      if constexpr (kLayer) db[j] = add(db[j], y);
       if (p.dx) {
-        const Piece<T, N> g = load<N>(w + static_cast<int64_t>(i) * N);
-        float v[N];
-#pragma unroll
-        for (int k = 0; k < N; ++k) {
-          float f = fmaf(y[j].v[k], g.v[k], -s[j].v[k] * c);
-          if constexpr (kLayer) f -= mg;
-          v[k] = rs * f;
-        }
-        if (p.dh) {
-          const Piece<T, N> h = load<N>(static_cast<const T*>(p.dh) + at);
-#pragma unroll
-          for (int k = 0; k < N; ++k) v[k] += h.v[k];
-        }
-        store<N>(static_cast<T*>(p.dx) + at, v);
+        V v = with_dh ? unpack(chunk(p.dh, tensors - 1, j)) : all<N>(0.0f);
+        if constexpr (kLayer) v = add(v, vg);
+        v = fma(mul(y, unpack(w[tid + j * threads])), vrs, fma(s, vc, v));
+        C out;
+        pack(v, out);
+        static_cast<C*>(p.dx)[base + j * threads] = out;
       }
     }
+    if constexpr (kRing) {
+      fetch();
+      if (++stage == stages) stage = 0;
+    }
   }
+  pdl_release();  // the sum of the partial rows waits for them itself
 
   // the block's partial rows; with a warp a row, its warps' in their order
-  auto write = [&](float* to, const float (*acc)[N]) {
+  auto write = [&](float* to, const V* acc) {
     if (!to) return;
     to += static_cast<int64_t>(blockIdx.x) * d;
     if constexpr (kWarpRow) {
-      __shared__ float sum[32 * kP * N];
+      V* const sum = reinterpret_cast<V*>(ring_bytes);
       for (int turn = 0; turn < kRowWarps; ++turn) {
         __syncthreads();
         if (turn != team) continue;
 #pragma unroll
         for (int j = 0; j < kP; ++j)
-#pragma unroll
-          for (int k = 0; k < N; ++k) {
-            float& at = sum[(j * 32 + tid) * N + k];
-            at = turn ? at + acc[j][k] : acc[j][k];
-          }
+          sum[j * 32 + tid] = turn ? add(sum[j * 32 + tid], acc[j]) : acc[j];
       }
       __syncthreads();
-      for (int i = threadIdx.x; i < d; i += blockDim.x) to[i] = sum[i];
+      for (int i = threadIdx.x; i < chunks; i += blockDim.x) reinterpret_cast<V*>(to)[i] = sum[i];
       __syncthreads();
     } else {
 #pragma unroll
-      for (int j = 0; j < kP; ++j) {
-        const int i = tid + j * threads;
-        if (i >= pieces) continue;
-#pragma unroll
-        for (int k = 0; k < N; ++k) to[static_cast<int64_t>(i) * N + k] = acc[j][k];
-      }
+      for (int j = 0; j < kP; ++j)
+        if (tid + j * threads < chunks) reinterpret_cast<V*>(to)[tid + j * threads] = acc[j];
     }
   };
   write(p.pw, dw);
   if constexpr (kLayer) write(p.pb, db);
+}
+
+// dx and the rows' statistics of tensors that stay in L2, where dweight and
+// dbias are summed from a second reading (norm_backward_columns_kernel): no
+// partial rows, and every row under way at once.  A block a row, or (kWarpRow) a
+// warp a row; a thread kP chunks of it, loaded together and kept.
+template <typename T, int N, int kP, bool kLayer, bool kWarpRow, int kMaxThreads>
+__global__ void __launch_bounds__(kMaxThreads)
+    norm_backward_rows_kernel(const BackwardPtrs p, float eps, int d, int64_t rows) {
+  using C = Chunk<T, N>;
+  using V = Vec<N>;
+  __shared__ float part[64], part_mean[64];
+  pdl_wait();
+  const int threads = kWarpRow ? 32 : blockDim.x;
+  const int tid = kWarpRow ? threadIdx.x & 31 : threadIdx.x;
+  const int64_t row =
+      kWarpRow ? static_cast<int64_t>(blockIdx.x) * kRowWarps + threadIdx.x / 32 : blockIdx.x;
+  if (kWarpRow && row >= rows) return;
+  const int chunks = d / N;
+  const float inv_d = 1.0f / static_cast<float>(d);
+  const int64_t base = row * chunks;
+  C cy[kP], cs[kP], cr[kP], ch[kP], cw[kP];
+#pragma unroll
+  for (int j = 0; j < kP; ++j) {
+    const int i = tid + j * threads;
+    if (i < chunks) {
+      cy[j] = static_cast<const C*>(p.dy)[base + i];
+      cs[j] = static_cast<const C*>(p.a)[base + i];
+      cw[j] = static_cast<const C*>(p.w)[i];
+      if (p.r) cr[j] = static_cast<const C*>(p.r)[base + i];
+      if (p.dh && p.dx) ch[j] = static_cast<const C*>(p.dh)[base + i];
+    }
+  }
+  V s[kP], g[kP];
+  V a = all<N>(0.0f), b = a;
+#pragma unroll
+  for (int j = 0; j < kP; ++j) {
+    if (tid + j * threads < chunks) {
+      s[j] = unpack(cs[j]);
+      if (p.r) s[j] = add(s[j], unpack(cr[j]));
+      g[j] = mul(unpack(cy[j]), unpack(cw[j]));
+    } else {
+      s[j] = g[j] = all<N>(0.0f);
+    }
+    if constexpr (kLayer) {
+      a = add(a, s[j]);
+      b = add(b, g[j]);
+    }
+  }
+  float mu = 0.0f, mg = 0.0f;
+  if constexpr (kLayer) {
+    const float2 t = block_sum<kWarpRow>(total(a), total(b), part_mean);
+    mu = t.x * inv_d;
+    mg = t.y * inv_d;
+    a = b = all<N>(0.0f);
+  }
+#pragma unroll
+  for (int j = 0; j < kP; ++j) {
+    if constexpr (kLayer)
+      if (tid + j * threads < chunks) s[j] = add(s[j], all<N>(-mu));
+    a = fma(s[j], s[j], a);
+    b = fma(g[j], s[j], b);
+  }
+  const float2 t = block_sum<kWarpRow>(total(a), total(b), part);
+  const float rs = rsqrtf(t.x * inv_d + eps);
+  const float c = -rs * (rs * rs * (t.y * inv_d));
+  if (p.stats && tid == 0) p.stats[row] = make_float2(mu, rs);
+  if (!p.dx) return;
+#pragma unroll
+  for (int j = 0; j < kP; ++j) {
+    const int i = tid + j * threads;
+    if (i >= chunks) continue;
+    V v = p.dh ? unpack(ch[j]) : all<N>(0.0f);
+    if constexpr (kLayer) v = add(v, all<N>(-rs * mg));
+    C out;
+    pack(fma(g[j], all<N>(rs), fma(s[j], all<N>(c), v)), out);
+    static_cast<C*>(p.dx)[base + i] = out;
+  }
+}
+
+// Sums of two values over a block of 1024 threads.
+__device__ __forceinline__ float2 wide_sum(float x, float y, float2 (*part)[32], int buf) {
+#pragma unroll
+  for (int o = 16; o; o >>= 1) {
+    x += __shfl_xor_sync(0xffffffffu, x, o);
+    y += __shfl_xor_sync(0xffffffffu, y, o);
+  }
+  const int lane = threadIdx.x & 31;
+  if (lane == 0) part[buf][threadIdx.x >> 5] = make_float2(x, y);
+  __syncthreads();
+  const float2 v = lane < blockDim.x / 32 ? part[buf][lane] : make_float2(0.f, 0.f);
+  x = v.x, y = v.y;
+#pragma unroll
+  for (int o = 16; o; o >>= 1) {
+    x += __shfl_xor_sync(0xffffffffu, x, o);
+    y += __shfl_xor_sync(0xffffffffu, y, o);
+  }
+  return make_float2(x, y);
 }
 
 // Rows too wide for registers: dx and the rows' statistics, a block a row,
@@ -233,7 +500,7 @@ __global__ void __launch_bounds__(1024)
         x1 = fmaf(y.v[k], g.v[k], x1);
       }
     }
-    const float2 t = block_sum<false>(x0, x1, part, 0);
+    const float2 t = wide_sum(x0, x1, part, 0);
     mu = t.x * inv_d;
     mg = t.y * inv_d;
     x0 = x1 = 0.0f;
@@ -248,7 +515,7 @@ __global__ void __launch_bounds__(1024)
       x1 = fmaf(y.v[k] * g.v[k], u, x1);
     }
   }
-  const float2 t = block_sum<false>(x0, x1, part, 1);
+  const float2 t = wide_sum(x0, x1, part, 1);
   const float rs = rsqrtf(t.x * inv_d + eps);
   const float c = rs * t.y * inv_d;
   if (threadIdx.x == 0 && p.stats) p.stats[row] = make_float2(mu, rs);
@@ -272,122 +539,236 @@ __global__ void __launch_bounds__(1024)
   }
 }
 
-// Their dweight and dbias: a thread a column, gridDim.y parts of the rows.
-template <typename T, bool kLayer>
-__global__ void __launch_bounds__(256)
-    norm_backward_columns_kernel(const BackwardPtrs p, int d, int64_t rows) {
+// dweight and dbias from the rows and their statistics.  A cluster of eight
+// blocks sums 32 N columns: a lane a chunk, the rows dealt to the blocks' warps;
+// the warps' sums are added in each block, then the blocks' through distributed
+// shared memory, an eighth of the columns by each.
+constexpr int kColumnBlocks = 8, kColumnWarps = 8;
+
+template <typename T, int N, bool kLayer>
+__global__ void __cluster_dims__(1, kColumnBlocks, 1) __launch_bounds__(32 * kColumnWarps)
+    norm_backward_columns_kernel(const BackwardPtrs p, int d, int64_t rows, float* out_w,
+                                 float* out_b) {
+  using C = Chunk<T, N>;
+  using V = Vec<N>;
+  constexpr int kCols = 32 * N;
+  __shared__ __align__(16) float warps[kLayer ? 2 : 1][kColumnWarps][kCols];
+  __shared__ float sums[kLayer ? 2 : 1][kCols];
   pdl_wait();
-  const int64_t c = static_cast<int64_t>(blockIdx.x) * 256 + threadIdx.x;
-  if (c >= d) return;
-  const T* a = static_cast<const T*>(p.a);
-  const T* r = static_cast<const T*>(p.r);
-  float dw = 0.0f, db = 0.0f;
-  for (int64_t row = blockIdx.y; row < rows; row += gridDim.y) {
-    const float2 st = p.stats[row];
-    const float y = load<1>(static_cast<const T*>(p.dy) + row * d + c).v[0];
-    dw = fmaf(y, (row_sum<T, 1>(a, r, row * d + c).v[0] - st.x) * st.y, dw);
-    if constexpr (kLayer) db += y;
+  const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
+  const int64_t chunks = d / N, i = static_cast<int64_t>(blockIdx.x) * 32 + lane;
+  const int rank = blockIdx.y;
+  V dw = all<N>(0.0f), db = dw;
+  if (i < chunks) {
+    constexpr int kAhead = 4, kStep = kColumnBlocks * kColumnWarps;
+    for (int64_t row = rank * kColumnWarps + warp; row < rows; row += kAhead * kStep) {
+      C y[kAhead], s[kAhead], r[kAhead];
+      float2 st[kAhead];
+#pragma unroll
+      for (int a = 0; a < kAhead; ++a) {
+        const int64_t at = row + a * kStep;
+        if (at < rows) {
+          y[a] = static_cast<const C*>(p.dy)[at * chunks + i];
+          s[a] = static_cast<const C*>(p.a)[at * chunks + i];
+          if (p.r) r[a] = static_cast<const C*>(p.r)[at * chunks + i];
+          st[a] = p.stats[at];
+        }
+      }
+#pragma unroll
+      for (int a = 0; a < kAhead; ++a) {
+        if (row + a * kStep >= rows) continue;
+        V u = unpack(s[a]);
+        if (p.r) u = add(u, unpack(r[a]));
+        if constexpr (kLayer) u = add(u, all<N>(-st[a].x));
+        const V v = unpack(y[a]);
+        dw = fma(mul(v, all<N>(st[a].y)), u, dw);
+        if constexpr (kLayer) db = add(db, v);
+      }
+    }
   }
-  if (p.pw) p.pw[static_cast<int64_t>(blockIdx.y) * d + c] = dw;
-  if constexpr (kLayer)
-    if (p.pb) p.pb[static_cast<int64_t>(blockIdx.y) * d + c] = db;
+  reinterpret_cast<V*>(warps[0][warp])[lane] = dw;
+  if constexpr (kLayer) reinterpret_cast<V*>(warps[1][warp])[lane] = db;
+  __syncthreads();
+  for (int c = threadIdx.x; c < kCols; c += 32 * kColumnWarps) {
+#pragma unroll
+    for (int k = 0; k < (kLayer ? 2 : 1); ++k) {
+      float t = 0.0f;
+#pragma unroll
+      for (int w = 0; w < kColumnWarps; ++w) t += warps[k][w][c];
+      sums[k][c] = t;
+    }
+  }
+  cluster_sync_all();
+  constexpr int kMine = kCols / kColumnBlocks;
+  if (threadIdx.x < kMine * (kLayer ? 2 : 1)) {
+    const int k = threadIdx.x / kMine, c = rank * kMine + threadIdx.x % kMine;
+    const uint32_t at = smem_u32(&sums[k][c]);
+    float t = 0.0f;
+#pragma unroll
+    for (int q = 0; q < kColumnBlocks; ++q) {
+      float v;
+      asm volatile("ld.shared::cluster.f32 %0, [%1];" : "=f"(v) : "r"(cluster_map(at, q)) : "memory");
+      t += v;
+    }
+    float* out = k ? out_b : out_w;
+    const int64_t col = static_cast<int64_t>(blockIdx.x) * kCols + c;
+    if (out && col < d) out[col] = t;
+  }
+  cluster_sync_all();  // no block ends while another reads its sums
 }
 
-// out[c] = the sum of `parts` rows of partials, 32 columns a block: warp w
-// adds rows w, w + 32, ..., then the warps' sums are added in their order.
-__global__ void __launch_bounds__(1024)
+// out[c] = the sum of `parts` rows of partials: a thread adds C neighbouring
+// columns, a block's 16 warps the rows 16 apart, eight of them in flight; then
+// the warps' sums are added in their order.
+constexpr int kSumWarps = 16;
+template <int C>
+__global__ void __launch_bounds__(32 * kSumWarps)
     column_sum_kernel(const float* __restrict__ pw, const float* __restrict__ pb, int parts, int d,
                       float* __restrict__ dw, float* __restrict__ db) {
-  __shared__ float sums[32][33];
+  __shared__ float sums[kSumWarps][32 * C];
   pdl_wait();
   const float* p = blockIdx.y ? pb : pw;
   float* out = blockIdx.y ? db : dw;
   if (!out) return;
   const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
-  const int64_t c = static_cast<int64_t>(blockIdx.x) * 32 + lane;
-  float s = 0.0f;
-  if (c < d)
-    for (int i = warp; i < parts; i += 32) s += p[static_cast<int64_t>(i) * d + c];
-  sums[warp][lane] = s;
-  __syncthreads();
-  s = sums[lane][warp];  // lane: the adding warp, warp: the column
+  const int64_t c = (static_cast<int64_t>(blockIdx.x) * 32 + lane) * C;
+  float s[C];
 #pragma unroll
-  for (int o = 16; o; o >>= 1) s += __shfl_xor_sync(0xffffffffu, s, o);
-  const int64_t col = static_cast<int64_t>(blockIdx.x) * 32 + warp;
-  if (lane == 0 && col < d) out[col] = s;
+  for (int k = 0; k < C; ++k) s[k] = 0.0f;
+  if (c < d) {
+    constexpr int kAhead = 8;
+    for (int i = warp; i < parts; i += kAhead * kSumWarps) {
+      Piece<float, C> v[kAhead];
+#pragma unroll
+      for (int a = 0; a < kAhead; ++a)
+        if (i + a * kSumWarps < parts)
+          v[a] = load<C>(p + static_cast<int64_t>(i + a * kSumWarps) * d + c);
+#pragma unroll
+      for (int a = 0; a < kAhead; ++a)
+        if (i + a * kSumWarps < parts)
+#pragma unroll
+          for (int k = 0; k < C; ++k) s[k] += v[a].v[k];
+    }
+  }
+#pragma unroll
+  for (int k = 0; k < C; ++k) sums[warp][lane * C + k] = s[k];
+  __syncthreads();
+  for (int i = threadIdx.x; i < 32 * C; i += 32 * kSumWarps) {
+    float t = 0.0f;
+#pragma unroll
+    for (int a = 0; a < kSumWarps; ++a) t += sums[a][i];
+    const int64_t col = static_cast<int64_t>(blockIdx.x) * 32 * C + i;
+    if (col < d) out[col] = t;
+  }
 }
 
-constexpr int kWideParts = 32;  // parts of the rows of norm_backward_columns_kernel
+// Stages of a block's ring: as many as fit beside another block of an SM.
+constexpr int kRingBytes = 110 * 1024;
+constexpr int kMaxRing = 200 * 1024;  // one stage of the widest rows takes 128 KB
 
-template <typename T, int N, int kP, bool kLayer, bool kWarpRow, int kMaxThreads>
+template <typename T, int N, int kP, bool kLayer, bool kWarpRow, int kMaxThreads, int kMinBlocks>
 cudaError_t launch(const NormBackwardArgs& n, int threads, const BackwardPtrs& p, int parts,
                    cudaStream_t stream) {
-  return launch_pdl(norm_backward_kernel<T, N, kP, kLayer, kWarpRow, kMaxThreads>,
-                    dim3(static_cast<unsigned>(parts)),
-                    dim3(kWarpRow ? 32 * kRowWarps : threads), 0, stream, p, n.eps, n.d, n.T);
+  auto kernel = norm_backward_kernel<T, N, kP, kLayer, kWarpRow, kMaxThreads, kMinBlocks>;
+  if (kWarpRow) threads = 32 * kRowWarps;
+  int stages = 0;
+  size_t bytes = 0;
+  if (N * sizeof(T) >= 4) {
+    const int one = (2 + (p.r ? 1 : 0) + (p.dh && p.dx ? 1 : 0)) * kP * threads *
+                    static_cast<int>(N * sizeof(T));
+    stages = kRingBytes / one;
+    stages = stages < 1 ? 1 : stages > kMaxStages ? kMaxStages : stages;
+    bytes = static_cast<size_t>(stages) * one;
+  }
+  if (kWarpRow && bytes < 32 * kP * N * sizeof(float)) bytes = 32 * kP * N * sizeof(float);
+  if (bytes > 32 * 1024) {  // with the static part at most 48 KB otherwise
+    const cudaError_t err =
+        cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, kMaxRing);
+    if (err != cudaSuccess) return err;
+  }
+  return launch_pdl(kernel, dim3(static_cast<unsigned>(parts)), dim3(threads), bytes, stream, p,
+                    n.eps, n.d, n.T, stages);
 }
+
+// Statistics and dx by `rows`, and the sums over the rows, before dx is written
+// where it is an input of theirs.
+template <typename T, int N, bool kLayer, typename Rows>
+cudaError_t two_passes(const NormBackwardArgs& n, BackwardPtrs p, cudaStream_t stream, Rows rows) {
+  const bool sums = n.dw || n.db;
+  if (!sums) return rows(p);
+  const bool in_place = p.dx && (p.dx == p.dy || p.dx == p.a || p.dx == p.r);
+  p.stats = n.stats;
+  if (in_place) p.dx = nullptr;
+  cudaError_t err = rows(p);
+  if (err != cudaSuccess) return err;
+  const int64_t chunks = n.d / N;
+  err = launch_pdl(norm_backward_columns_kernel<T, N, kLayer>,
+                   dim3(static_cast<unsigned>((chunks + 31) / 32), kColumnBlocks),
+                   dim3(32 * kColumnWarps), 0, stream, p, n.d, n.T, n.dw, n.db);
+  if (err != cudaSuccess || !in_place) return err;
+  p.stats = nullptr;
+  p.dx = n.dx;
+  return rows(p);
+}
+
+// Two readings or partial rows.  A second reading of few rows that stay in L2
+// is the faster (us with it / with partial rows: layer form, bf16, 33 x 7168
+// 5.6 / 9.1, 300 x 7168 8.7 / 17.3, 1000 x 7168 19 / 28; 777 x 1000 fp32 6.8 /
+// 9.4), and so it is for rows without 16-byte pieces, which the ring of the
+// other form cannot hold (8192 x 1001 bf16 31 / 75); otherwise it loses (2000 x
+// 7168 RMS 38 / 30, 8192 x 1024 33 / 15: a warp has more than 16 rows, and the
+// tensors leave L2).
+constexpr int64_t kTwoPassRows = 1024, kTwoPassBytes = 32ll << 20;
 
 template <typename T, int N, bool kLayer>
 cudaError_t dispatch(const NormBackwardArgs& n, cudaStream_t stream) {
-  const int pieces = n.d / N;
   const bool sums = n.dw || n.db;
   BackwardPtrs p = {n.a, n.r, n.w, n.dy, n.dh, n.dx, nullptr, nullptr, nullptr};
-  auto round32 = [](int v) { return (v + 31) / 32 * 32; };
-  constexpr int kMaxP = N == 8 ? 2 : N == 4 ? 4 : 8;
-  const bool wide = pieces > 1024 * kMaxP;
-  const bool warp = pieces <= 128;
-  int parts = static_cast<int>(n.T < kNormParts ? n.T : kNormParts);
-  if (warp) {
-    const int64_t b = (n.T + kRowWarps - 1) / kRowWarps;
-    parts = static_cast<int>(b < kNormParts ? b : kNormParts);
-  }
-  if (wide) parts = n.T < kWideParts ? static_cast<int>(n.T) : kWideParts;
-  float* ws = n.partials;
+  // threads of a row with at most Q values each
+  auto threads = [&](int Q) { return (n.d + 32 * Q - 1) / (32 * Q) * 32; };
+  if (n.d > 16384)
+    return two_passes<T, N, kLayer>(n, p, stream, [&](const BackwardPtrs& q) {
+      constexpr int W = N == 2 ? 1 : N;  // a Piece is one value or 16 bytes
+      return launch_pdl(norm_backward_wide_kernel<T, W, kLayer>, dim3(static_cast<unsigned>(n.T)),
+                        dim3(1024), 0, stream, q, n.eps, n.d);
+    });
+  const bool few = n.T <= kTwoPassRows && 2 * n.T * n.d * static_cast<int64_t>(sizeof(T)) <= kTwoPassBytes;
+  const bool narrow = N * sizeof(T) < 16 && n.d > 256;
+  if ((few || narrow || !sums) && n.d <= 8192)
+    return two_passes<T, N, kLayer>(n, p, stream, [&](const BackwardPtrs& q) {
+      if (n.d <= 256)
+        return launch_pdl(norm_backward_rows_kernel<T, N, 8 / N, kLayer, true, 32 * kRowWarps>,
+                          dim3(static_cast<unsigned>((n.T + kRowWarps - 1) / kRowWarps)),
+                          dim3(32 * kRowWarps), 0, stream, q, n.eps, n.d, n.T);
+      return launch_pdl(norm_backward_rows_kernel<T, N, 8 / N, kLayer, false, 1024>,
+                        dim3(static_cast<unsigned>(n.T)), dim3(threads(8)), 0, stream, q, n.eps,
+                        n.d, n.T);
+    });
+  const bool warp = n.d <= 1024;
+  const int64_t teams = warp ? (n.T + kRowWarps - 1) / kRowWarps : n.T;
+  const int parts = static_cast<int>(teams < kNormParts ? teams : kNormParts);
   if (sums) {
-    p.pw = ws;
-    p.pb = ws + static_cast<int64_t>(parts) * n.d;
+    p.pw = n.dw ? n.partials : nullptr;
+    p.pb = n.db ? n.partials + static_cast<int64_t>(parts) * n.d : nullptr;
   }
-  if (!n.dw) p.pw = nullptr;
-  if (!n.db) p.pb = nullptr;
   cudaError_t err;
-  if (wide) {
-    // the rows' statistics, the columns' sums, then dx, which may be an input
-    const dim3 grid(static_cast<unsigned>(n.T));
-    if (sums) {
-      p.stats = n.stats;
-      p.dx = nullptr;
-      err = launch_pdl(norm_backward_wide_kernel<T, N, kLayer>, grid, dim3(1024), 0, stream, p,
-                       n.eps, n.d);
-      if (err != cudaSuccess) return err;
-      err = launch_pdl(norm_backward_columns_kernel<T, kLayer>,
-                       dim3(static_cast<unsigned>((static_cast<int64_t>(n.d) + 255) / 256), parts),
-                       dim3(256), 0, stream, p, n.d, n.T);
-      if (err != cudaSuccess) return err;
-      p.stats = nullptr;
-      p.dx = n.dx;
-    }
-    err = p.dx ? launch_pdl(norm_backward_wide_kernel<T, N, kLayer>, grid, dim3(1024), 0, stream, p,
-                            n.eps, n.d)
-               : cudaSuccess;
-  } else if (pieces <= 32) {
-    err = launch<T, N, 1, kLayer, true, 32 * kRowWarps>(n, 32, p, parts, stream);
-  } else if (warp) {
-    err = launch<T, N, 4, kLayer, true, 32 * kRowWarps>(n, 32, p, parts, stream);
-  } else if (pieces <= 512) {
-    err = launch<T, N, 1, kLayer, false, 512>(n, round32(pieces), p, parts, stream);
-  } else if (pieces <= 1024) {
-    err = launch<T, N, 2, kLayer, false, 512>(n, round32((pieces + 1) / 2), p, parts, stream);
-  } else if (N < 8 && pieces <= 2048) {
-    err = launch<T, N, 4, kLayer, false, 512>(n, round32((pieces + 3) / 4), p, parts, stream);
-  } else {
-    err = launch<T, N, kMaxP, kLayer, false, 1024>(n, round32((pieces + kMaxP - 1) / kMaxP), p,
-                                                   parts, stream);
-  }
+  if (n.d <= 256)
+    err = launch<T, N, 8 / N, kLayer, true, 32 * kRowWarps, 2>(n, 32, p, parts, stream);
+  else if (warp)
+    err = launch<T, N, 32 / N, kLayer, true, 32 * kRowWarps, 1>(n, 32, p, parts, stream);
+  else if (n.d <= 4096)
+    err = launch<T, N, 8 / N, kLayer, false, 512, 2>(n, threads(8), p, parts, stream);
+  else if (n.d <= 7168)
+    err = launch<T, N, 16 / N, kLayer, false, 448, 2>(n, threads(16), p, parts, stream);
+  else
+    err = launch<T, N, 16 / N, kLayer, false, 1024, 1>(n, threads(16), p, parts, stream);
   if (err != cudaSuccess || !sums) return err;
   const float *pw = p.pw, *pb = p.pb;
-  return launch_pdl(column_sum_kernel,
-                    dim3(static_cast<unsigned>((static_cast<int64_t>(n.d) + 31) / 32), n.db ? 2 : 1),
-                    dim3(1024), 0, stream, pw, pb, parts, n.d, n.dw, n.db);
+  constexpr int C = N >= 4 ? 4 : 1;
+  const dim3 grid(static_cast<unsigned>((static_cast<int64_t>(n.d) + 32 * C - 1) / (32 * C)),
+                  n.db ? 2 : 1);
+  return launch_pdl(column_sum_kernel<C>, grid, dim3(32 * kSumWarps), 0, stream, pw, pb, parts, n.d,
+                    n.dw, n.db);
 }
 
 template <typename T, int N>
@@ -403,9 +784,10 @@ int64_t norm_partial_floats(int64_t T, int64_t d) {
 
 cudaError_t launch_norm_backward(const NormBackwardArgs& n, cudaStream_t stream) {
   if (n.bf16)
-    return n.d % 8 ? dispatch_kind<__nv_bfloat16, 1>(n, stream)
-                   : dispatch_kind<__nv_bfloat16, 8>(n, stream);
-  return n.d % 4 ? dispatch_kind<float, 1>(n, stream) : dispatch_kind<float, 4>(n, stream);
+    return n.d % 8 == 0   ? dispatch_kind<__nv_bfloat16, 8>(n, stream)
+           : n.d % 2 == 0 ? dispatch_kind<__nv_bfloat16, 2>(n, stream)
+                          : dispatch_kind<__nv_bfloat16, 1>(n, stream);
+  return n.d % 4 == 0 ? dispatch_kind<float, 4>(n, stream) : dispatch_kind<float, 1>(n, stream);
 }
 
 }  // namespace fgs

@@ -1,5 +1,6 @@
-// What the norm kernels share: pieces of a row in registers, and the 8-bit
-// form of 128 values (E4M3 codes with one fp32 scale).
+// What the kernels over rows and tensors share: pieces of a row in registers,
+// pairs of fp32 values, and the 8-bit form of 128 values (E4M3 codes with one
+// fp32 scale).
 #pragma once
 
 #include "common.cuh"
@@ -99,6 +100,27 @@ __device__ __forceinline__ void store_codes(uint8_t* p, const float (&q)[N]) {
                                               e4m3x2(q[4], q[5]) | e4m3x2(q[6], q[7]) << 16);
   else if constexpr (N == 4)
     *reinterpret_cast<uint32_t*>(p) = e4m3x2(q[0], q[1]) | e4m3x2(q[2], q[3]) << 16;
+}
+
+// Pairs of fp32 values, one instruction for both.
+typedef unsigned long long pair;
+__device__ __forceinline__ pair make_pair2(float a, float b) {
+  pair r;
+  asm("mov.b64 %0, {%1, %2};" : "=l"(r) : "f"(a), "f"(b));
+  return r;
+}
+__device__ __forceinline__ void split(pair v, float& a, float& b) {
+  asm("mov.b64 {%0, %1}, %2;" : "=f"(a), "=f"(b) : "l"(v));
+}
+__device__ __forceinline__ pair mul2(pair a, pair b) {
+  pair r;
+  asm("mul.rn.f32x2 %0, %1, %2;" : "=l"(r) : "l"(a), "l"(b));
+  return r;
+}
+__device__ __forceinline__ pair fma2(pair a, pair b, pair c) {
+  pair r;
+  asm("fma.rn.f32x2 %0, %1, %2, %3;" : "=l"(r) : "l"(a), "l"(b), "l"(c));
+  return r;
 }
 
 }  // namespace fgs
