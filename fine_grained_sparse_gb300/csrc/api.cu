@@ -1393,6 +1393,7 @@ int32_t moe_norm_backward(int32_t kind, int32_t dtype, int64_t T, int32_t d, con
   n.dw = dweight;
   n.db = dbias;
   if (dweight || dbias) {
+    n.status = static_cast<int*>(workspace);
     n.stats = at<float2>(workspace, kWsHeader);
     n.partials = at<float>(workspace, kWsHeader + round256(8 * static_cast<size_t>(T)));
   }

@@ -343,6 +343,7 @@ struct NormBackwardArgs {
   float* db = nullptr;       // [d] or null (layer norm)
   float* partials = nullptr; // norm_partial_floats(T, d) (with dw or db)
   float2* stats = nullptr;   // [T] (with dw or db)
+  int* status = nullptr;     // device status word (with dw or db)
 };
 int64_t norm_partial_floats(int64_t T, int64_t d);
 cudaError_t launch_norm_backward(const NormBackwardArgs& n, cudaStream_t stream);

@@ -7,13 +7,24 @@
 //           dx = r (g - mean g - u mean(g u)) + dh
 //   dweight = sum over the rows of dy u,  dbias = sum over the rows of dy
 // mean(g u) is r mean(g s) (r mean(g (s - mu))), so the RMS form needs one
-// reduction over a row and the layer form two.  Bound by HBM for many rows,
-// by latency for few.
+// reduction over a row and the layer form two.
 //
-// The rows are dealt to at most kNormParts blocks; each sums its rows' dweight
-// and dbias in registers and writes one partial row of each, and a second
-// launch adds the partial rows up in a fixed order, so results do not depend
-// on timing, nor on the device.
+// Kernels
+//   norm_backward_stream_kernel   many rows of more than 1024 columns (layer form
+//       256): blocks that stay sum their rows' dweight and dbias in registers
+//       and write one partial row of each; column_sum_kernel adds those up.
+//       8192 x 7168 bf16 with dh (470 MB): RMS 80 us, 5.87 TB/s, 88% of the copy
+//       rate; layer form 106 us, 66%, bound by the issue of its instructions
+//       (the unpacking of bf16 for each of three passes over shared memory);
+//       4096 x 7168 fp32 RMS 78 us, 90%.  A row at a time from copies by every
+//       thread took 88 and 130, from registers 128 and 213.
+//   norm_backward_warps_kernel    many shorter rows, the same with a warp a row
+//   norm_backward_rows_kernel, norm_backward_columns_kernel   few rows: dx and
+//       the rows' statistics, then the sums from a second reading, which comes
+//       from L2.  777 x 1000 fp32 layer form 6.8 us: two launches.
+//   norm_backward_wide_kernel     rows of more than 16384 columns
+// Every sum is taken in an order that T and d decide, so results depend neither
+// on timing nor on the device.
 #include "common.cuh"
 #include "internal.h"
 #include "rows.cuh"
@@ -44,30 +55,35 @@ __device__ __forceinline__ Piece<T, N> row_sum(const T* a, const T* r, int64_t a
   return s;
 }
 
-// Sums of two values over a block's threads (or a warp's), the same in all of
+// Sums of two values over a warp, and over a block's threads; the same in all of
 // them.  The halves of a warp first exchange what the other adds up, so that a
-// round of the tree serves both values.  Callers alternate between two parts:
-// one barrier then separates the uses of each.
-template <bool kWarp>
-__device__ __forceinline__ float2 block_sum(float x, float y, float (&part)[64]) {
-  const int lane = threadIdx.x & 31;
-  const bool low = lane < 16;
+// round of the tree serves both values.  A `part` serves one sum at a time: with
+// a barrier between two uses of it.
+__device__ __forceinline__ float half_sums(float x, float y) {
+  const bool low = (threadIdx.x & 31) < 16;
   float v = low ? x : y;
   v += __shfl_xor_sync(0xffffffffu, low ? y : x, 16);
 #pragma unroll
   for (int o = 8; o; o >>= 1) v += __shfl_xor_sync(0xffffffffu, v, o);
-  if constexpr (!kWarp) {
-    // the sums of warp i at 2 i and 2 i + 1
-    if ((lane & 15) == 0) part[threadIdx.x >> 4] = v;
-    __syncthreads();
-    const int sums = blockDim.x / 16, i = 2 * (lane & 15) + (lane >> 4);
-    v = i < sums ? part[i] : 0.0f;
-    if (i + 32 < sums) v += part[i + 32];
-#pragma unroll
-    for (int o = 8; o; o >>= 1) v += __shfl_xor_sync(0xffffffffu, v, o);
-  }
+  return v;  // x's in the low half, y's in the high
+}
+__device__ __forceinline__ float2 both_halves(float v) {
   const float other = __shfl_xor_sync(0xffffffffu, v, 16);
-  return low ? make_float2(v, other) : make_float2(other, v);
+  return (threadIdx.x & 31) < 16 ? make_float2(v, other) : make_float2(other, v);
+}
+__device__ __forceinline__ float2 warp_sum(float x, float y) { return both_halves(half_sums(x, y)); }
+__device__ __forceinline__ float2 block_sum(float x, float y, float (&part)[64]) {
+  const int lane = threadIdx.x & 31;
+  float v = half_sums(x, y);
+  // the sums of warp i at 2 i and 2 i + 1
+  if ((lane & 15) == 0) part[threadIdx.x >> 4] = v;
+  __syncthreads();
+  const int sums = blockDim.x / 16, i = 2 * (lane & 15) + (lane >> 4);
+  v = i < sums ? part[i] : 0.0f;
+  if (i + 32 < sums) v += part[i + 32];
+#pragma unroll
+  for (int o = 8; o; o >>= 1) v += __shfl_xor_sync(0xffffffffu, v, o);
+  return both_halves(v);
 }
 
 // N values: one, or N / 2 pairs.
@@ -212,33 +228,29 @@ __device__ __forceinline__ void wait_copies(int left) {
     asm volatile("cp.async.wait_group 3;" ::: "memory");
 }
 
-// A block a row, or (kWarpRow) a warp a row; a thread holds the same kP chunks
-// of N columns of each of its rows.  But for single bf16 values a thread keeps
-// the chunks of its next `stages` rows on their way into shared memory, where
-// it alone reads them: no barrier, and no register holds what is under way.
+// Many short rows: a warp a row, a lane the same kP chunks of N columns of each
+// of its rows.  But for single bf16 values a lane keeps the chunks of its next
+// `stages` rows on their way into shared memory, where it alone reads them: no
+// barrier, and no register holds what is under way.
 //   dx = r g - (r r mean(g s)) r s + dh, and for the layer form
 //   dx = r g - (r r mean(g s)) r s + (dh - r mean g), s there the difference to mu
 constexpr int kRowWarps = 8;
 
-template <typename T, int N, int kP, bool kLayer, bool kWarpRow, int kMaxThreads, int kMinBlocks>
-__global__ void __launch_bounds__(kMaxThreads, kMinBlocks)
-    norm_backward_kernel(const BackwardPtrs p, float eps, int d, int64_t rows, int stages) {
+template <typename T, int N, int kP, bool kLayer, int kMinBlocks>
+__global__ void __launch_bounds__(32 * kRowWarps, kMinBlocks)
+    norm_backward_warps_kernel(const BackwardPtrs p, float eps, int d, int64_t rows, int stages) {
   using C = Chunk<T, N>;
   using V = Vec<N>;
-  __shared__ float part[2][64];
   extern __shared__ uint4 ring_bytes[];
   C* const ring = reinterpret_cast<C*>(ring_bytes);
   constexpr bool kRing = sizeof(C) >= 4;
   pdl_wait();
-  const int threads = kWarpRow ? 32 : blockDim.x;
-  const int tid = kWarpRow ? threadIdx.x & 31 : threadIdx.x;
-  const int teams = kWarpRow ? kRowWarps : 1;
-  const int team = kWarpRow ? threadIdx.x / 32 : 0;
+  const int lane = threadIdx.x & 31, team = threadIdx.x / 32;
   const int chunks = d / N;
   const C* const w = static_cast<const C*>(p.w);
   const float inv_d = 1.0f / static_cast<float>(d);
-  const int64_t first = static_cast<int64_t>(blockIdx.x) * teams + team;
-  const int64_t stride = static_cast<int64_t>(gridDim.x) * teams;
+  const int64_t first = static_cast<int64_t>(blockIdx.x) * kRowWarps + team;
+  const int64_t stride = static_cast<int64_t>(gridDim.x) * kRowWarps;
   V dw[kP], db[kLayer ? kP : 1];
 #pragma unroll
   for (int j = 0; j < kP; ++j) {
@@ -248,9 +260,9 @@ __global__ void __launch_bounds__(kMaxThreads, kMinBlocks)
   // a stage: dy, x, then the residual and dh where there are any
   const bool with_r = p.r, with_dh = p.dh && p.dx;
   const int tensors = 2 + with_r + with_dh;
-  const int pitch = kP * blockDim.x;  // chunks of a tensor in a stage
+  const int pitch = kP * 32 * kRowWarps;  // chunks of a tensor in a stage
   const int64_t step = stride * chunks;
-  int64_t ahead = first * chunks + tid;  // of the thread's first chunk to fetch
+  int64_t ahead = first * chunks + lane;  // of the thread's first chunk to fetch
   int64_t left = rows - first;           // rows from there on
   uint32_t fill = smem_u32(ring + threadIdx.x);
   const uint32_t begin = fill, stage_bytes = tensors * pitch * sizeof(C);
@@ -262,9 +274,9 @@ __global__ void __launch_bounds__(kMaxThreads, kMinBlocks)
         const C* src = static_cast<const C*>(from) + ahead;
 #pragma unroll
         for (int j = 0; j < kP; ++j)
-          if (tid + j * threads < chunks)
-            copy_async<sizeof(C)>(to + j * blockDim.x * static_cast<uint32_t>(sizeof(C)),
-                                  src + j * threads);
+          if (lane + 32 * j < chunks)
+            copy_async<sizeof(C)>(to + j * 32 * kRowWarps * static_cast<uint32_t>(sizeof(C)),
+                                  src + 32 * j);
         to += pitch * sizeof(C);
       };
       one(p.dy);
@@ -281,17 +293,17 @@ __global__ void __launch_bounds__(kMaxThreads, kMinBlocks)
   if constexpr (kRing)
     for (int i = 0; i < stages; ++i) fetch();
 
-  int buf = 0, stage = 0;
+  int stage = 0;
   for (int64_t row = first; row < rows; row += stride) {
-    const int64_t base = row * chunks + tid;
+    const int64_t base = row * chunks + lane;
     if constexpr (kRing) wait_copies(stages - 1);
     const C* from = ring + stage * tensors * pitch + threadIdx.x;
     // chunk j of tensor t; the last of them is dh
     auto chunk = [&](const void* global, int t, int j) {
       if constexpr (kRing)
-        return from[t * pitch + j * blockDim.x];
+        return from[t * pitch + j * 32 * kRowWarps];
       else
-        return static_cast<const C*>(global)[base + j * threads];
+        return static_cast<const C*>(global)[base + 32 * j];
     };
     auto sum = [&](int j) {
       V s = unpack(chunk(p.a, 1, j));
@@ -303,12 +315,11 @@ __global__ void __launch_bounds__(kMaxThreads, kMinBlocks)
       V a = all<N>(0.0f), b = a;
 #pragma unroll
       for (int j = 0; j < kP; ++j) {
-        if (tid + j * threads >= chunks) continue;
+        if (lane + 32 * j >= chunks) continue;
         a = add(a, sum(j));
-        b = fma(unpack(chunk(p.dy, 0, j)), unpack(w[tid + j * threads]), b);
+        b = fma(unpack(chunk(p.dy, 0, j)), unpack(w[lane + 32 * j]), b);
       }
-      const float2 t = block_sum<kWarpRow>(total(a), total(b), part[buf]);
-      buf ^= 1;
+      const float2 t = warp_sum(total(a), total(b));
       mu = t.x * inv_d;
       mg = t.y * inv_d;
     }
@@ -316,20 +327,19 @@ __global__ void __launch_bounds__(kMaxThreads, kMinBlocks)
     V a = all<N>(0.0f), b = a;
 #pragma unroll
     for (int j = 0; j < kP; ++j) {
-      if (tid + j * threads >= chunks) continue;
+      if (lane + 32 * j >= chunks) continue;
       V s = sum(j);
       if constexpr (kLayer) s = add(s, vmu);
       a = fma(s, s, a);
-      b = fma(mul(unpack(chunk(p.dy, 0, j)), unpack(w[tid + j * threads])), s, b);
+      b = fma(mul(unpack(chunk(p.dy, 0, j)), unpack(w[lane + 32 * j])), s, b);
     }
-    const float2 t = block_sum<kWarpRow>(total(a), total(b), part[buf]);
-    buf ^= 1;
+    const float2 t = warp_sum(total(a), total(b));
     const float rs = rsqrtf(t.x * inv_d + eps);
     const float c = -rs * (rs * rs * (t.y * inv_d));
     const V vrs = all<N>(rs), vc = all<N>(c), vg = all<N>(-rs * mg);
 #pragma unroll
     for (int j = 0; j < kP; ++j) {
-      if (tid + j * threads >= chunks) continue;
+      if (lane + 32 * j >= chunks) continue;
       V s = sum(j);
       if constexpr (kLayer) s = add(s, vmu);
       const V y = unpack(chunk(p.dy, 0, j));
@@ -338,10 +348,10 @@ __global__ void __launch_bounds__(kMaxThreads, kMinBlocks)
       if (p.dx) {
         V v = with_dh ? unpack(chunk(p.dh, tensors - 1, j)) : all<N>(0.0f);
         if constexpr (kLayer) v = add(v, vg);
-        v = fma(mul(y, unpack(w[tid + j * threads])), vrs, fma(s, vc, v));
+        v = fma(mul(y, unpack(w[lane + 32 * j])), vrs, fma(s, vc, v));
         C out;
         pack(v, out);
-        static_cast<C*>(p.dx)[base + j * threads] = out;
+        static_cast<C*>(p.dx)[base + 32 * j] = out;
       }
     }
     if constexpr (kRing) {
@@ -351,30 +361,225 @@ __global__ void __launch_bounds__(kMaxThreads, kMinBlocks)
   }
   pdl_release();  // the sum of the partial rows waits for them itself
 
-  // the block's partial rows; with a warp a row, its warps' in their order
+  // the block's partial rows, its warps' sums in their order
   auto write = [&](float* to, const V* acc) {
     if (!to) return;
-    to += static_cast<int64_t>(blockIdx.x) * d;
-    if constexpr (kWarpRow) {
-      V* const sum = reinterpret_cast<V*>(ring_bytes);
-      for (int turn = 0; turn < kRowWarps; ++turn) {
-        __syncthreads();
-        if (turn != team) continue;
-#pragma unroll
-        for (int j = 0; j < kP; ++j)
-          sum[j * 32 + tid] = turn ? add(sum[j * 32 + tid], acc[j]) : acc[j];
-      }
+    V* const sum = reinterpret_cast<V*>(ring_bytes);
+    for (int turn = 0; turn < kRowWarps; ++turn) {
       __syncthreads();
-      for (int i = threadIdx.x; i < chunks; i += blockDim.x) reinterpret_cast<V*>(to)[i] = sum[i];
-      __syncthreads();
-    } else {
+      if (turn != team) continue;
 #pragma unroll
       for (int j = 0; j < kP; ++j)
-        if (tid + j * threads < chunks) reinterpret_cast<V*>(to)[tid + j * threads] = acc[j];
+        sum[32 * j + lane] = turn ? add(sum[32 * j + lane], acc[j]) : acc[j];
     }
+    __syncthreads();
+    to += static_cast<int64_t>(blockIdx.x) * d;
+    for (int i = threadIdx.x; i < chunks; i += blockDim.x) reinterpret_cast<V*>(to)[i] = sum[i];
+    __syncthreads();
   };
   write(p.pw, dw);
   if constexpr (kLayer) write(p.pb, db);
+}
+
+// Sums of four values over a block of at most 16 warps, as block_sum takes two.
+__device__ __forceinline__ float4 block_sum4(float v0, float v1, float v2, float v3,
+                                             float (&part)[64]) {
+  const int lane = threadIdx.x & 31;
+  const bool high = lane & 16, odd = lane & 8;
+  float a = high ? v2 : v0, b = high ? v3 : v1;
+  a += __shfl_xor_sync(0xffffffffu, high ? v0 : v2, 16);
+  b += __shfl_xor_sync(0xffffffffu, high ? v1 : v3, 16);
+  float v = odd ? b : a;
+  v += __shfl_xor_sync(0xffffffffu, odd ? a : b, 8);
+#pragma unroll
+  for (int o = 4; o; o >>= 1) v += __shfl_xor_sync(0xffffffffu, v, o);
+  // value k of warp i at 4 i + k
+  if ((lane & 7) == 0) part[threadIdx.x >> 3] = v;
+  __syncthreads();
+  const int sums = blockDim.x / 8;
+  v = lane < sums ? part[lane] : 0.0f;
+  if (lane + 32 < sums) v += part[lane + 32];
+#pragma unroll
+  for (int o = 4; o <= 16; o <<= 1) v += __shfl_xor_sync(0xffffffffu, v, o);
+  return make_float4(__shfl_sync(0xffffffffu, v, 0), __shfl_sync(0xffffffffu, v, 1),
+                     __shfl_sync(0xffffffffu, v, 2), __shfl_sync(0xffffffffu, v, 3));
+}
+
+// Many rows of whole 16-byte chunks: a block takes kR neighbouring rows at a
+// time, a thread the same kP chunks of each.  One thread keeps bulk copies of
+// the next rows under way into a ring of shared memory; a stage is free again
+// at the first barrier of its rows' sums, as every thread then holds its chunks
+// of them.  Two rows share a barrier, the tree of their sums and the weights.
+template <typename T, int kP, int kR, bool kLayer, bool kRes, int kMaxThreads, int kMinBlocks>
+__global__ void __launch_bounds__(kMaxThreads, kMinBlocks)
+    norm_backward_stream_kernel(const BackwardPtrs p, float eps, int d, int64_t rows, int stages,
+                                int* status) {
+  constexpr int N = 16 / sizeof(T);
+  using C = Chunk<T, N>;
+  using V = Vec<N>;
+  extern __shared__ uint4 ring_bytes[];
+  __shared__ uint64_t full[kMaxStages];
+  __shared__ int aborted;
+  __shared__ float part[2][64];  // of sums in turn: a barrier then separates the uses of each
+  pdl_wait();
+  const int tid = threadIdx.x, threads = blockDim.x, chunks = d / N;
+  const C* const w = static_cast<const C*>(p.w);
+  const float inv_d = 1.0f / static_cast<float>(d);
+  const bool with_dh = p.dh && p.dx;
+  const int tensors = 2 + kRes + with_dh;
+  const int stage_chunks = tensors * kR * chunks;
+  const int64_t groups = (rows + kR - 1) / kR;
+  if (tid == 0) {
+    aborted = 0;
+    for (int i = 0; i < stages; ++i) mbar_init(smem_u32(&full[i]), 1);
+    fence_mbarrier_init();
+  }
+  __syncthreads();
+  const uint64_t policy = l2_policy_evict_first();
+  auto fetch = [&](int64_t group, int stage) {
+    const int64_t at = group * kR * chunks;
+    const uint32_t bytes = static_cast<uint32_t>(min(static_cast<int64_t>(kR), rows - group * kR)) *
+                           chunks * 16u;
+    const uint32_t bar = smem_u32(&full[stage]);
+    uint32_t to = smem_u32(ring_bytes + stage * stage_chunks);
+    mbar_arrive_expect_tx(bar, bytes * tensors);
+    auto one = [&](const void* from) {
+      bulk_load(to, static_cast<const C*>(from) + at, bytes, bar, policy);
+      to += kR * chunks * 16;
+    };
+    one(p.dy);
+    one(p.a);
+    if (kRes) one(p.r);
+    if (with_dh) one(p.dh);
+  };
+  if (tid == 0)
+    for (int i = 0; i < stages; ++i) {
+      const int64_t g = blockIdx.x + static_cast<int64_t>(i) * gridDim.x;
+      if (g < groups) fetch(g, i);
+    }
+
+  V dw[kP], db[kLayer ? kP : 1];
+#pragma unroll
+  for (int j = 0; j < kP; ++j) {
+    dw[j] = all<N>(0.0f);
+    if constexpr (kLayer) db[j] = all<N>(0.0f);
+  }
+  int stage = 0, turn = 0;
+  uint32_t parity = 0;
+  for (int64_t group = blockIdx.x; group < groups; group += gridDim.x) {
+    if (!mbar_wait_bounded(smem_u32(&full[stage]), parity, &aborted, status)) break;
+    const int live = static_cast<int>(min(static_cast<int64_t>(kR), rows - group * kR));
+    C cy[kR][kP], cs[kR][kP], cr[kRes ? kR : 1][kP], ch[kR][kP];
+    {
+      const C* from = reinterpret_cast<const C*>(ring_bytes) + stage * stage_chunks + tid;
+#pragma unroll
+      for (int r = 0; r < kR; ++r)
+#pragma unroll
+        for (int j = 0; j < kP; ++j) {
+          if (tid + j * threads >= chunks) continue;
+          const C* at = from + r * chunks + j * threads;
+          cy[r][j] = *at;
+          cs[r][j] = at[kR * chunks];
+          if constexpr (kRes) cr[r][j] = at[2 * kR * chunks];
+          if (with_dh) ch[r][j] = at[(tensors - 1) * kR * chunks];
+        }
+    }
+    auto sum = [&](int r, int j) {
+      V s = unpack(cs[r][j]);
+      if constexpr (kRes) s = add(s, unpack(cr[r][j]));
+      return s;
+    };
+    float mu[kR], mg[kR], ss[kR], gs[kR];
+    auto reduce = [&](const V (&a)[kR], const V (&b)[kR], float (&x)[kR], float (&y)[kR]) {
+      if constexpr (kR == 2) {
+        const float4 t = block_sum4(total(a[0]), total(b[0]), total(a[1]), total(b[1]), part[turn]);
+        x[0] = t.x, y[0] = t.y, x[1] = t.z, y[1] = t.w;
+      } else {
+        const float2 t = block_sum(total(a[0]), total(b[0]), part[turn]);
+        x[0] = t.x, y[0] = t.y;
+      }
+      turn ^= 1;
+    };
+    V a[kR], b[kR];
+    auto refill = [&]() {  // after the first barrier that follows the loads
+      const int64_t next = group + static_cast<int64_t>(stages) * gridDim.x;
+      if (tid == 0 && next < groups) fetch(next, stage);
+    };
+#pragma unroll
+    for (int r = 0; r < kR; ++r) a[r] = b[r] = all<N>(0.0f);
+    if constexpr (kLayer) {
+#pragma unroll
+      for (int j = 0; j < kP; ++j) {
+        if (tid + j * threads >= chunks) continue;
+        const V g = unpack(w[tid + j * threads]);
+#pragma unroll
+        for (int r = 0; r < kR; ++r) {
+          a[r] = add(a[r], sum(r, j));
+          b[r] = fma(unpack(cy[r][j]), g, b[r]);
+        }
+      }
+      reduce(a, b, mu, mg);
+      refill();
+#pragma unroll
+      for (int r = 0; r < kR; ++r) {
+        mu[r] *= -inv_d;
+        mg[r] *= inv_d;
+        a[r] = b[r] = all<N>(0.0f);
+      }
+    }
+#pragma unroll
+    for (int j = 0; j < kP; ++j) {
+      if (tid + j * threads >= chunks) continue;
+      const V g = unpack(w[tid + j * threads]);
+#pragma unroll
+      for (int r = 0; r < kR; ++r) {
+        V s = sum(r, j);
+        if constexpr (kLayer) s = add(s, all<N>(mu[r]));
+        a[r] = fma(s, s, a[r]);
+        b[r] = fma(mul(unpack(cy[r][j]), g), s, b[r]);
+      }
+    }
+    reduce(a, b, ss, gs);
+    if constexpr (!kLayer) refill();
+#pragma unroll
+    for (int r = 0; r < kR; ++r) {
+      if (r >= live) break;
+      const float rs = rsqrtf(ss[r] * inv_d + eps);
+      const float c = -rs * (rs * rs * (gs[r] * inv_d));
+      const int64_t row = group * kR + r;
+#pragma unroll
+      for (int j = 0; j < kP; ++j) {
+        if (tid + j * threads >= chunks) continue;
+        V s = sum(r, j);
+        if constexpr (kLayer) s = add(s, all<N>(mu[r]));
+        const V y = unpack(cy[r][j]);
+        dw[j] = fma(mul(y, all<N>(rs)), s, dw[j]);
+        if constexpr (kLayer) db[j] = add(db[j], y);
+        if (p.dx) {
+          V v = with_dh ? unpack(ch[r][j]) : all<N>(0.0f);
+          if constexpr (kLayer) v = add(v, all<N>(-rs * mg[r]));
+          v = fma(mul(y, unpack(w[tid + j * threads])), all<N>(rs), fma(s, all<N>(c), v));
+          C out;
+          pack(v, out);
+          static_cast<C*>(p.dx)[row * chunks + tid + j * threads] = out;
+        }
+      }
+    }
+    if (++stage == stages) {
+      stage = 0;
+      parity ^= 1;
+    }
+  }
+  pdl_release();  // the sum of the partial rows waits for them itself
+#pragma unroll
+  for (int j = 0; j < kP; ++j) {
+    const int i = tid + j * threads;
+    if (i >= chunks) continue;
+    const int64_t at = static_cast<int64_t>(blockIdx.x) * d;
+    if (p.pw) reinterpret_cast<V*>(p.pw + at)[i] = dw[j];
+    if constexpr (kLayer)
+      if (p.pb) reinterpret_cast<V*>(p.pb + at)[i] = db[j];
+  }
 }
 
 // dx and the rows' statistics of tensors that stay in L2, where dweight and
@@ -426,7 +631,7 @@ __global__ void __launch_bounds__(kMaxThreads)
   }
   float mu = 0.0f, mg = 0.0f;
   if constexpr (kLayer) {
-    const float2 t = block_sum<kWarpRow>(total(a), total(b), part_mean);
+    const float2 t = kWarpRow ? warp_sum(total(a), total(b)) : block_sum(total(a), total(b), part_mean);
     mu = t.x * inv_d;
     mg = t.y * inv_d;
     a = b = all<N>(0.0f);
@@ -438,7 +643,7 @@ __global__ void __launch_bounds__(kMaxThreads)
     a = fma(s[j], s[j], a);
     b = fma(g[j], s[j], b);
   }
-  const float2 t = block_sum<kWarpRow>(total(a), total(b), part);
+  const float2 t = kWarpRow ? warp_sum(total(a), total(b)) : block_sum(total(a), total(b), part);
   const float rs = rsqrtf(t.x * inv_d + eps);
   const float c = -rs * (rs * rs * (t.y * inv_d));
   if (p.stats && tid == 0) p.stats[row] = make_float2(mu, rs);
@@ -662,32 +867,46 @@ __global__ void __launch_bounds__(32 * kSumWarps)
   }
 }
 
-// Stages of a block's ring: as many as fit beside another block of an SM.
-constexpr int kRingBytes = 110 * 1024;
-constexpr int kMaxRing = 200 * 1024;  // one stage of the widest rows takes 128 KB
-
-template <typename T, int N, int kP, bool kLayer, bool kWarpRow, int kMaxThreads, int kMinBlocks>
-cudaError_t launch(const NormBackwardArgs& n, int threads, const BackwardPtrs& p, int parts,
-                   cudaStream_t stream) {
-  auto kernel = norm_backward_kernel<T, N, kP, kLayer, kWarpRow, kMaxThreads, kMinBlocks>;
-  if (kWarpRow) threads = 32 * kRowWarps;
+template <typename T, int N, int kP, bool kLayer, int kMinBlocks>
+cudaError_t launch_warps(const NormBackwardArgs& n, const BackwardPtrs& p, int parts,
+                         cudaStream_t stream) {
+  auto kernel = norm_backward_warps_kernel<T, N, kP, kLayer, kMinBlocks>;
+  constexpr int kThreads = 32 * kRowWarps;
   int stages = 0;
-  size_t bytes = 0;
+  size_t bytes = 32 * kP * N * sizeof(float);  // the sums at the end
   if (N * sizeof(T) >= 4) {
-    const int one = (2 + (p.r ? 1 : 0) + (p.dh && p.dx ? 1 : 0)) * kP * threads *
+    // as many as leave room for a second block on the SM
+    const int one = (2 + (p.r ? 1 : 0) + (p.dh && p.dx ? 1 : 0)) * kP * kThreads *
                     static_cast<int>(N * sizeof(T));
-    stages = kRingBytes / one;
+    stages = 110 * 1024 / one;
     stages = stages < 1 ? 1 : stages > kMaxStages ? kMaxStages : stages;
-    bytes = static_cast<size_t>(stages) * one;
+    if (bytes < static_cast<size_t>(stages) * one) bytes = static_cast<size_t>(stages) * one;
   }
-  if (kWarpRow && bytes < 32 * kP * N * sizeof(float)) bytes = 32 * kP * N * sizeof(float);
-  if (bytes > 32 * 1024) {  // with the static part at most 48 KB otherwise
-    const cudaError_t err =
-        cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, kMaxRing);
-    if (err != cudaSuccess) return err;
-  }
-  return launch_pdl(kernel, dim3(static_cast<unsigned>(parts)), dim3(threads), bytes, stream, p,
+  const cudaError_t err =
+      cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, 160 * 1024);
+  if (err != cudaSuccess) return err;
+  return launch_pdl(kernel, dim3(static_cast<unsigned>(parts)), dim3(kThreads), bytes, stream, p,
                     n.eps, n.d, n.T, stages);
+}
+
+// Blocks of an SM that share its registers and shared memory in the stream
+// kernel, for rows of d columns.
+int stream_blocks(int d) { return d > 4096 ? 1 : d > 2048 ? 2 : d > 1024 ? 4 : 8; }
+
+template <typename T, bool kLayer, bool kRes>
+cudaError_t launch_stream(const NormBackwardArgs& n, const BackwardPtrs& p, int parts,
+                          cudaStream_t stream) {
+  constexpr int N = 16 / sizeof(T), kP = 16 / N, kR = sizeof(T) == 4 || kRes ? 1 : 2;
+  auto kernel = norm_backward_stream_kernel<T, kP, kR, kLayer, kRes, 512, 1>;
+  const int chunks = n.d / N, threads = (chunks + 32 * kP - 1) / (32 * kP) * 32;
+  const int one = (2 + kRes + (p.dh && p.dx ? 1 : 0)) * kR * chunks * 16;
+  int stages = 216 * 1024 / stream_blocks(n.d) / one;
+  stages = stages < 1 ? 1 : stages > kMaxStages ? kMaxStages : stages;
+  const cudaError_t err =
+      cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, 220 * 1024);
+  if (err != cudaSuccess) return err;
+  return launch_pdl(kernel, dim3(static_cast<unsigned>(parts)), dim3(threads),
+                    static_cast<size_t>(stages) * one, stream, p, n.eps, n.d, n.T, stages, n.status);
 }
 
 // Statistics and dx by `rows`, and the sums over the rows, before dx is written
@@ -712,61 +931,63 @@ cudaError_t two_passes(const NormBackwardArgs& n, BackwardPtrs p, cudaStream_t s
 }
 
 // Two readings or partial rows.  A second reading of few rows that stay in L2
-// is the faster (us with it / with partial rows: layer form, bf16, 33 x 7168
-// 5.6 / 9.1, 300 x 7168 8.7 / 17.3, 1000 x 7168 19 / 28; 777 x 1000 fp32 6.8 /
-// 9.4), and so it is for rows without 16-byte pieces, which the ring of the
-// other form cannot hold (8192 x 1001 bf16 31 / 75); otherwise it loses (2000 x
-// 7168 RMS 38 / 30, 8192 x 1024 33 / 15: a warp has more than 16 rows, and the
-// tensors leave L2).
+// is the faster (us with it / with partial rows, bf16: layer form, 100 x 7168
+// 5.9 / 10.6, 1000 x 7168 20 / 23, 2000 x 2048 13.3 / 16.0; RMS 4.9 / 7.4, 16.2 /
+// 15.7, 12.4 / 12.0), but for short rows, a warp each (1000 x 256 6.3 / 5.4), and
+// so it is for rows without 16-byte chunks, which the bulk copies cannot take.
+// With more rows it loses (2000 x 7168 RMS 38 / 25, 8192 x 1024 33 / 15: a warp
+// of the second launch has more than 16 rows, and the tensors leave L2).
 constexpr int64_t kTwoPassRows = 1024, kTwoPassBytes = 32ll << 20;
+constexpr int kShort = 256;
 
 template <typename T, int N, bool kLayer>
 cudaError_t dispatch(const NormBackwardArgs& n, cudaStream_t stream) {
   const bool sums = n.dw || n.db;
   BackwardPtrs p = {n.a, n.r, n.w, n.dy, n.dh, n.dx, nullptr, nullptr, nullptr};
-  // threads of a row with at most Q values each
-  auto threads = [&](int Q) { return (n.d + 32 * Q - 1) / (32 * Q) * 32; };
   if (n.d > 16384)
     return two_passes<T, N, kLayer>(n, p, stream, [&](const BackwardPtrs& q) {
       constexpr int W = N == 2 ? 1 : N;  // a Piece is one value or 16 bytes
       return launch_pdl(norm_backward_wide_kernel<T, W, kLayer>, dim3(static_cast<unsigned>(n.T)),
                         dim3(1024), 0, stream, q, n.eps, n.d);
     });
-  const bool few = n.T <= kTwoPassRows && 2 * n.T * n.d * static_cast<int64_t>(sizeof(T)) <= kTwoPassBytes;
-  const bool narrow = N * sizeof(T) < 16 && n.d > 256;
-  if ((few || narrow || !sums) && n.d <= 8192)
+  const bool few = n.T <= (n.d <= kShort ? kTwoPassRows / 4 : kTwoPassRows * (1 + kLayer)) &&
+                   2 * n.T * n.d * static_cast<int64_t>(sizeof(T)) <= kTwoPassBytes;
+  const bool narrow = N * sizeof(T) < 16 && n.d > kShort;
+  if (!sums || few || narrow || n.d > 8192)
     return two_passes<T, N, kLayer>(n, p, stream, [&](const BackwardPtrs& q) {
-      if (n.d <= 256)
+      // threads of a row with at most Q values each
+      auto threads = [&](int Q) { return dim3((n.d + 32 * Q - 1) / (32 * Q) * 32); };
+      const dim3 rows(static_cast<unsigned>(n.T));
+      if (n.d <= kShort)
         return launch_pdl(norm_backward_rows_kernel<T, N, 8 / N, kLayer, true, 32 * kRowWarps>,
                           dim3(static_cast<unsigned>((n.T + kRowWarps - 1) / kRowWarps)),
                           dim3(32 * kRowWarps), 0, stream, q, n.eps, n.d, n.T);
-      return launch_pdl(norm_backward_rows_kernel<T, N, 8 / N, kLayer, false, 1024>,
-                        dim3(static_cast<unsigned>(n.T)), dim3(threads(8)), 0, stream, q, n.eps,
-                        n.d, n.T);
+      if (n.d <= 8192)
+        return launch_pdl(norm_backward_rows_kernel<T, N, 8 / N, kLayer, false, 1024>, rows,
+                          threads(8), 0, stream, q, n.eps, n.d, n.T);
+      return launch_pdl(norm_backward_rows_kernel<T, N, 16 / N, kLayer, false, 1024>, rows,
+                        threads(16), 0, stream, q, n.eps, n.d, n.T);
     });
-  const bool warp = n.d <= 1024;
-  const int64_t teams = warp ? (n.T + kRowWarps - 1) / kRowWarps : n.T;
-  const int parts = static_cast<int>(teams < kNormParts ? teams : kNormParts);
-  if (sums) {
-    p.pw = n.dw ? n.partials : nullptr;
-    p.pb = n.db ? n.partials + static_cast<int64_t>(parts) * n.d : nullptr;
+  // a block's rows from bulk copies, or a warp a row (8192 x 512 bf16: RMS 16.8
+  // and 11.2 us, layer form 20.1 and 23.0; 8192 x 1024 18.6 / 15.0, 23.6 / 28.7)
+  const bool streamed = n.d > (kLayer ? kShort : 1024);
+  const int64_t teams = streamed ? (n.T + 1) / 2 : (n.T + kRowWarps - 1) / kRowWarps;
+  const int64_t most = streamed ? 152 * stream_blocks(n.d) : kNormParts;
+  const int parts = static_cast<int>(teams < most ? teams : most);
+  p.pw = n.dw ? n.partials : nullptr;
+  p.pb = n.db ? n.partials + static_cast<int64_t>(parts) * n.d : nullptr;
+  cudaError_t err = cudaSuccess;
+  if (n.d <= kShort) {
+    err = launch_warps<T, N, 8 / N, kLayer, 2>(n, p, parts, stream);
+  } else if constexpr (N * sizeof(T) == 16) {
+    err = !streamed ? launch_warps<T, N, 32 / N, kLayer, 1>(n, p, parts, stream)
+          : n.r     ? launch_stream<T, kLayer, true>(n, p, parts, stream)
+                    : launch_stream<T, kLayer, false>(n, p, parts, stream);
   }
-  cudaError_t err;
-  if (n.d <= 256)
-    err = launch<T, N, 8 / N, kLayer, true, 32 * kRowWarps, 2>(n, 32, p, parts, stream);
-  else if (warp)
-    err = launch<T, N, 32 / N, kLayer, true, 32 * kRowWarps, 1>(n, 32, p, parts, stream);
-  else if (n.d <= 4096)
-    err = launch<T, N, 8 / N, kLayer, false, 512, 2>(n, threads(8), p, parts, stream);
-  else if (n.d <= 7168)
-    err = launch<T, N, 16 / N, kLayer, false, 448, 2>(n, threads(16), p, parts, stream);
-  else
-    err = launch<T, N, 16 / N, kLayer, false, 1024, 1>(n, threads(16), p, parts, stream);
-  if (err != cudaSuccess || !sums) return err;
+  if (err != cudaSuccess) return err;
   const float *pw = p.pw, *pb = p.pb;
   constexpr int C = N >= 4 ? 4 : 1;
-  const dim3 grid(static_cast<unsigned>((static_cast<int64_t>(n.d) + 32 * C - 1) / (32 * C)),
-                  n.db ? 2 : 1);
+  const dim3 grid(static_cast<unsigned>((n.d + 32 * C - 1) / (32 * C)), n.db ? 2 : 1);
   return launch_pdl(column_sum_kernel<C>, grid, dim3(32 * kSumWarps), 0, stream, pw, pb, parts, n.d,
                     n.dw, n.db);
 }
@@ -779,7 +1000,9 @@ cudaError_t dispatch_kind(const NormBackwardArgs& n, cudaStream_t stream) {
 }  // namespace
 
 int64_t norm_partial_floats(int64_t T, int64_t d) {
-  return 2 * d * (T < kNormParts ? T : kNormParts);
+  if (d > 8192) return 0;  // read twice
+  const int64_t most = d > 2048 ? kNormParts : 152 * 8;  // of any of the forms
+  return 2 * d * (T < most ? T : most);
 }
 
 cudaError_t launch_norm_backward(const NormBackwardArgs& n, cudaStream_t stream) {

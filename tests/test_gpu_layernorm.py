@@ -175,6 +175,28 @@ def test_backward_rows(T, d, dtype, kind):
 
 
 @pytest.mark.parametrize("kind", ["rms", "layer"])
+@pytest.mark.parametrize("residual,dh", [(False, True), (True, True), (False, False), (True, False)])
+@pytest.mark.parametrize("T,d,dtype", [(1025, 264, "bf16"), (1027, 520, "f32"), (1029, 1032, "bf16"),
+                                       (2501, 1000, "f32"), (2455, 136, "bf16"), (1433, 2048, "bf16"),
+                                       (1100, 4096, "f32"), (2467, 7168, "bf16"),
+                                       (1201, 8192, "bf16"), (1031, 7172, "f32"),
+                                       (1025, 9000, "f32"), (1300, 8200, "bf16")])
+def test_backward_many_rows(T, d, dtype, residual, dh, kind):
+    """Rows that a block takes one after the other, or two at a time with one
+    left over; all outputs, then dx in place of the gradient."""
+    need_gpu()
+    fgs = lib()
+    x, r, w, _, dy, g = _inputs(T, d, dtype)
+    r, g = r if residual else None, g if dh else None
+    got = _backward(fgs, kind, dtype, x, r, w, dy, g)
+    _check_backward(kind, dtype, x, r, w, dy, g, got)
+    t = dy.cuda()
+    again = _backward(fgs, kind, dtype, x, r, w, t, g, dx=t)
+    for name in got:
+        assert got[name] is None or torch.equal(got[name], again[name])
+
+
+@pytest.mark.parametrize("kind", ["rms", "layer"])
 @pytest.mark.parametrize("d", [96, 1000, 7168, 20000])
 @pytest.mark.parametrize("want", [("dx",), ("dw",), ("dw", "db"), ("dx", "dw"), ("db",)])
 def test_backward_some_outputs(want, d, kind):
@@ -209,11 +231,12 @@ def test_backward_repeats():
     """The same sums every time, and on a workspace of any contents."""
     need_gpu()
     fgs = lib()
-    x, r, w, _, dy, dh = _inputs(2000, 1024, "bf16")
-    a = _backward(fgs, "layer", "bf16", x, r, w, dy, dh)
-    for _ in range(5):
-        b = _backward(fgs, "layer", "bf16", x, r, w, dy, dh)
-        assert all(torch.equal(a[k], b[k]) for k in a)
+    for T, d in ((2000, 1024), (700, 1024), (3000, 200)):
+        x, r, w, _, dy, dh = _inputs(T, d, "bf16")
+        a = _backward(fgs, "layer", "bf16", x, r, w, dy, dh)
+        for _ in range(5):
+            b = _backward(fgs, "layer", "bf16", x, r, w, dy, dh)
+            assert all(torch.equal(a[k], b[k]) for k in a)
 
 
 def test_backward_values():
