@@ -146,9 +146,10 @@ for _name, (_args, _res) in _SIGS.items():
 def _ptr(t) -> Optional[int]:
     if t is None:
         return None
-    if isinstance(t, int):
+    try:
+        return t.data_ptr()
+    except AttributeError:  # a raw pointer
         return t
-    return t.data_ptr()
 
 
 _current_stream = None  # () -> the current stream's handle, made on first use

@@ -22,16 +22,6 @@ constexpr int kThreads = 256;
 constexpr int kStep = 8 * kThreads;  // elements of a block at a time
 constexpr int kSteps = 4;            // of a block in large launches
 
-// A launch's tensors, by value.  start[i] is the tensor of block i << shift.
-constexpr int kStarts = 512;
-struct AdamwLaunch {
-  AdamwScalars c;
-  int shift;
-  uint8_t start[kStarts];
-  uint32_t first[kAdamwTensors + 1];  // the blocks before each tensor's
-  AdamwTensor t[kAdamwTensors];
-};
-
 // Eight values of a tensor as they lie in memory, and as fp32.
 template <typename T>
 struct Raw8;
@@ -391,7 +381,7 @@ __device__ __forceinline__ void step8(const AdamwTensor& t, const AdamwScalars& 
 // quotients 1177.
 template <typename P, typename G, bool k8, bool kMany>
 __global__ void __launch_bounds__(kThreads, k8 && kMany ? 3 : 2)
-    adamw_kernel(const __grid_constant__ AdamwLaunch a) {
+    adamw_kernel(const __grid_constant__ AdamwGroup a) {
   pdl_wait();
   // the tensor of this block: first[lo] <= blockIdx.x < first[lo + 1]
   int lo = a.start[blockIdx.x >> a.shift];
@@ -417,72 +407,71 @@ __global__ void __launch_bounds__(kThreads, k8 && kMany ? 3 : 2)
     step8<P, G, k8, false>(t, a.c, gs, at, in);
 }
 
-}  // namespace
-
 // Blocks of a tensor for `steps` steps each.
-static int64_t blocks_of(int64_t n, int steps) {
+int64_t blocks_of(int64_t n, int steps) {
   const int64_t chunk = static_cast<int64_t>(kStep) * steps;
   return (n + chunk - 1) / chunk;
 }
 
-int adamw_group(const AdamwTensor* t, int count) {
-  int64_t blocks = 0;
-  int k = 0;
-  for (; k < count && k < kAdamwTensors; ++k) {
-    const int64_t b = blocks_of(t[k].n, 1);
-    if (k && blocks + b > 0x40000000) break;
-    blocks += b;
-  }
-  return k;
-}
-
-namespace {
-
 template <typename P, typename G, bool k8, bool kMany>
-cudaError_t launch(const AdamwTensor* t, int count, const AdamwScalars& c, cudaStream_t stream) {
-  AdamwLaunch a;
-  a.c = c;
+cudaError_t launch(AdamwGroup& a, int count, cudaStream_t stream) {
   a.first[0] = 0;
-  for (int k = 0; k < count; ++k) {
-    a.t[k] = t[k];
-    a.first[k + 1] = a.first[k] + static_cast<uint32_t>(blocks_of(t[k].n, kMany ? kSteps : 1));
-  }
+  for (int k = 0; k < count; ++k)
+    a.first[k + 1] = a.first[k] + static_cast<uint32_t>(blocks_of(a.t[k].n, kMany ? kSteps : 1));
   const uint32_t blocks = a.first[count];
   if (blocks == 0) return cudaSuccess;  // every tensor is empty
   a.shift = 0;
-  while ((blocks - 1) >> a.shift >= kStarts) ++a.shift;
+  while ((blocks - 1) >> a.shift >= kAdamwStarts) ++a.shift;
   for (uint32_t i = 0, lo = 0; i <= (blocks - 1) >> a.shift; ++i) {
     while (a.first[lo + 1] <= i << a.shift) ++lo;
     a.start[i] = static_cast<uint8_t>(lo);
   }
-  return launch_pdl(adamw_kernel<P, G, k8, kMany>, dim3(blocks), dim3(kThreads), 0, stream, a);
+  // launch_pdl, but without further copies of the 19 KB
+  cudaLaunchConfig_t cfg = {};
+  cfg.gridDim = dim3(blocks);
+  cfg.blockDim = dim3(kThreads);
+  cfg.stream = stream;
+  cudaLaunchAttribute attr[1];
+  attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
+  attr[0].val.programmaticStreamSerializationAllowed = 1;
+  cfg.attrs = attr;
+  cfg.numAttrs = pdl_enabled() ? 1 : 0;
+  void* args[] = {&a};
+  note_launch();
+  return cudaLaunchKernelExC(&cfg, reinterpret_cast<const void*>(adamw_kernel<P, G, k8, kMany>),
+                             args);
 }
 
 template <typename P, typename G>
-cudaError_t launch_states(const AdamwTensor* t, int count, const AdamwScalars& c, bool bits8,
-                          bool many, cudaStream_t stream) {
-  if (!bits8) return launch<P, G, false, false>(t, count, c, stream);
-  return many ? launch<P, G, true, true>(t, count, c, stream)
-              : launch<P, G, true, false>(t, count, c, stream);
+cudaError_t launch_states(AdamwGroup& a, int count, bool bits8, bool many, cudaStream_t stream) {
+  if (!bits8) return launch<P, G, false, false>(a, count, stream);
+  return many ? launch<P, G, true, true>(a, count, stream)
+              : launch<P, G, true, false>(a, count, stream);
 }
 
 }  // namespace
 
-cudaError_t launch_adamw(const AdamwTensor* t, int count, const AdamwScalars& c, bool param_bf16,
-                         bool grad_bf16, bool bits8, int num_sms, cudaStream_t stream) {
+cudaError_t launch_adamw(AdamwGroup& a, int count, bool param_bf16, bool grad_bf16, bool bits8,
+                         int num_sms, int* taken, cudaStream_t stream) {
+  int64_t blocks = 0;
+  int k = 0;
+  for (; k < count; ++k) {
+    const int64_t b = blocks_of(a.t[k].n, 1);
+    if (k && blocks + b > 0x40000000) break;
+    blocks += b;
+  }
+  *taken = k;
   // 8-bit states: one step a block while there are few blocks, then four (3M
   // elements of bf16 with a master copy 10.7 us with one, 11.5 with four; 16M
   // 53.0 and 47.3; 352M 1065 and 895; eight steps 883, and 49.8 for 16M).
   // 32-bit states need no reading ahead: 134M fp32 523 us with one step in 48
   // registers, 533 with four in 116.
-  int64_t blocks = 0;
-  for (int k = 0; k < count; ++k) blocks += blocks_of(t[k].n, 1);
   const bool many = blocks > 16 * num_sms;
   if (param_bf16)
-    return grad_bf16 ? launch_states<__nv_bfloat16, __nv_bfloat16>(t, count, c, bits8, many, stream)
-                     : launch_states<__nv_bfloat16, float>(t, count, c, bits8, many, stream);
-  return grad_bf16 ? launch_states<float, __nv_bfloat16>(t, count, c, bits8, many, stream)
-                   : launch_states<float, float>(t, count, c, bits8, many, stream);
+    return grad_bf16 ? launch_states<__nv_bfloat16, __nv_bfloat16>(a, k, bits8, many, stream)
+                     : launch_states<__nv_bfloat16, float>(a, k, bits8, many, stream);
+  return grad_bf16 ? launch_states<float, __nv_bfloat16>(a, k, bits8, many, stream)
+                   : launch_states<float, float>(a, k, bits8, many, stream);
 }
 
 }  // namespace fgs

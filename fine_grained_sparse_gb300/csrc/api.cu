@@ -1456,7 +1456,8 @@ int32_t moe_adamw(int32_t n_tensors, const moe_adamw_tensor* tensors_host, int32
     const int32_t st = check_adamw_tensor(tensors_host[k], param_dtype, state_bits);
     if (st != MOE_OK) return st;
   }
-  AdamwScalars c;
+  AdamwGroup a;
+  AdamwScalars& c = a.c;
   c.b1 = static_cast<float>(beta1);
   c.ob1 = static_cast<float>(1.0 - beta1);
   c.b2 = static_cast<float>(beta2);
@@ -1465,20 +1466,19 @@ int32_t moe_adamw(int32_t n_tensors, const moe_adamw_tensor* tensors_host, int32
   c.eps = static_cast<float>(eps);
   c.size = static_cast<float>(lr / (1.0 - std::pow(beta1, static_cast<double>(step))));
   c.nsize = -c.size;
+  c.one = 1.0f;
   c.grad_scale = grad_scale;
-  AdamwTensor group[kAdamwTensors];
   for (int32_t k = 0; k < n_tensors;) {
     int count = 0;
     for (; count < kAdamwTensors && k + count < n_tensors; ++count) {
       const moe_adamw_tensor& t = tensors_host[k + count];
-      group[count] = {t.param, t.grad, t.master, t.exp_avg, t.exp_avg_sq, t.exp_avg_scale,
-                      t.exp_avg_sq_scale, t.n, static_cast<float>(1.0 - lr * t.weight_decay),
-                      static_cast<uint32_t>(
-                          mix64(seed + 0x9E3779B97F4A7C15ull * static_cast<uint64_t>(k + count)) >> 32)};
+      a.t[count] = {t.param, t.grad, t.master, t.exp_avg, t.exp_avg_sq, t.exp_avg_scale,
+                    t.exp_avg_sq_scale, t.n, static_cast<float>(1.0 - lr * t.weight_decay),
+                    static_cast<uint32_t>(
+                        mix64(seed + 0x9E3779B97F4A7C15ull * static_cast<uint64_t>(k + count)) >> 32)};
     }
-    count = adamw_group(group, count);
-    MOE_CUDA(launch_adamw(group, count, c, param_dtype == MOE_BF16, grad_dtype == MOE_BF16,
-                          state_bits == 8, num_sms(), static_cast<cudaStream_t>(stream)));
+    MOE_CUDA(launch_adamw(a, count, param_dtype == MOE_BF16, grad_dtype == MOE_BF16,
+                          state_bits == 8, num_sms(), &count, static_cast<cudaStream_t>(stream)));
     k += count;
   }
   return MOE_OK;

@@ -367,13 +367,23 @@ struct AdamwScalars {
   float root;              // 1 / sqrt(1 - beta2^t)
   float eps;
   float size, nsize;       // lr / (1 - beta1^t), and its negative
-  float one = 1.0f;        // a 1 that the kernel's compiler does not know
+  float one;               // a 1 that the kernel's compiler does not know
   const float* grad_scale; // device scalar, or null
 };
-// Tensors, from the first, that one launch takes (at least one).
-int adamw_group(const AdamwTensor* t, int count);
-cudaError_t launch_adamw(const AdamwTensor* t, int count, const AdamwScalars& c, bool param_bf16,
-                         bool grad_bf16, bool bits8, int num_sms, cudaStream_t stream);
+// A launch, by value: its tensors, and what the launch itself fills in, the
+// blocks before each tensor's and the tensor of block i << shift.
+constexpr int kAdamwStarts = 512;
+struct AdamwGroup {
+  AdamwScalars c;
+  int shift;
+  uint8_t start[kAdamwStarts];
+  uint32_t first[kAdamwTensors + 1];
+  AdamwTensor t[kAdamwTensors];
+};
+// The first of up to `count` tensors of `a` (at least one), as many as a grid
+// takes; *taken receives their number.
+cudaError_t launch_adamw(AdamwGroup& a, int count, bool param_bf16, bool grad_bf16, bool bits8,
+                         int num_sms, int* taken, cudaStream_t stream);
 
 // --------------------------------------------------- products with 4-bit weights
 // The widest x: a row of it stays in shared memory beside the ring of weights.

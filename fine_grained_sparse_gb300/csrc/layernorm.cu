@@ -12,88 +12,140 @@
 namespace fgs {
 namespace {
 
-constexpr int kRowsPerBlock = 8;
+constexpr int kRowWarps = 8;
 
-// As add_rmsnorm_kernel: a block a row, or (kWarpRow) a warp a row; N values at
-// a time; kKeep pieces of a thread's part stay in registers, a wider row
-// (kKeep == 0) is read three times.  Reads of an element come before the writes
-// of it, so h and y may be the inputs.
-template <typename T, int N, bool kWarpRow, int kKeep, int kMaxThreads, int kMinBlocks>
+// A block kR neighbouring rows, or (kWarpRow) a warp; a thread the same kP
+// chunks of N columns of each, in registers.  Two rows share the barriers and
+// trees of their sums, and the weights.  Reads of an element come before the
+// writes of it, so h and y may be the inputs.
+template <typename T, int N, int kP, int kR, bool kWarpRow, int kMaxThreads, int kMinBlocks>
 __global__ void __launch_bounds__(kMaxThreads, kMinBlocks)
     add_layernorm_kernel(const LayerNormArgs p) {
-  __shared__ float part[2][32];
+  using C = Chunk<T, N>;
+  using V = Vec<N>;
+  __shared__ float part[64], part_mean[64];
   pdl_wait();
-  const int d = p.d;
   const int threads = kWarpRow ? 32 : blockDim.x;
   const int tid = kWarpRow ? threadIdx.x & 31 : threadIdx.x;
-  const int64_t row = kWarpRow
-                          ? static_cast<int64_t>(blockIdx.x) * kRowsPerBlock + threadIdx.x / 32
-                          : blockIdx.x;
-  const bool live = row < p.T;
-  const int64_t base = row * d;
+  const int64_t row0 = kR * (kWarpRow ? static_cast<int64_t>(blockIdx.x) * kRowWarps + threadIdx.x / 32
+                                      : blockIdx.x);
+  if (kWarpRow && row0 >= p.T) return;
+  const int live = static_cast<int>(min(static_cast<int64_t>(kR), p.T - row0));
+  const int chunks = p.d / N;
+  const float inv_d = 1.0f / static_cast<float>(p.d);
+  auto sums = [&](const V (&a)[kR], float (&x)[kR], float (&to)[64]) {
+    const float one = total(a[0]), two = kR > 1 ? total(a[kR - 1]) : 0.0f;
+    const float2 t = kWarpRow ? warp_sum(one, two) : block_sum(one, two, to);
+    x[0] = t.x * inv_d;
+    x[kR - 1] = kR > 1 ? t.y * inv_d : x[0];
+  };
+  V s[kR][kP], a[kR];
+  {
+    C x[kR][kP], r[kR][kP];
+#pragma unroll
+    for (int k = 0; k < kR; ++k)
+#pragma unroll
+      for (int j = 0; j < kP; ++j) {
+        const int i = tid + j * threads;
+        if (i >= chunks || k >= live) continue;
+        const int64_t at = (row0 + k) * chunks + i;
+        x[k][j] = static_cast<const C*>(p.a)[at];
+        if (p.r) r[k][j] = static_cast<const C*>(p.r)[at];
+      }
+#pragma unroll
+    for (int k = 0; k < kR; ++k) {
+      a[k] = all<N>(0.0f);
+#pragma unroll
+      for (int j = 0; j < kP; ++j) {
+        if (tid + j * threads < chunks && k < live) {
+          s[k][j] = unpack(x[k][j]);
+          if (p.r) s[k][j] = add(s[k][j], unpack(r[k][j]));
+          a[k] = add(a[k], s[k][j]);
+        } else {
+          s[k][j] = all<N>(0.0f);
+        }
+      }
+    }
+  }
+  if (p.h) {
+#pragma unroll
+    for (int k = 0; k < kR; ++k)
+#pragma unroll
+      for (int j = 0; j < kP; ++j) {
+        const int i = tid + j * threads;
+        if (i >= chunks || k >= live) continue;
+        C out;
+        pack(s[k][j], out);
+        static_cast<C*>(p.h)[(row0 + k) * chunks + i] = out;
+      }
+  }
+  float mu[kR], rs[kR];
+  sums(a, mu, part_mean);
+#pragma unroll
+  for (int k = 0; k < kR; ++k) {
+    a[k] = all<N>(0.0f);
+#pragma unroll
+    for (int j = 0; j < kP; ++j) {
+      if (tid + j * threads >= chunks) continue;
+      s[k][j] = add(s[k][j], all<N>(-mu[k]));
+      a[k] = fma(s[k][j], s[k][j], a[k]);
+    }
+  }
+  sums(a, rs, part);
+#pragma unroll
+  for (int k = 0; k < kR; ++k) rs[k] = rsqrtf(rs[k] + p.eps);
+#pragma unroll
+  for (int j = 0; j < kP; ++j) {
+    const int i = tid + j * threads;
+    if (i >= chunks) continue;
+    const V g = unpack(static_cast<const C*>(p.w)[i]);
+    const V b = p.b ? unpack(static_cast<const C*>(p.b)[i]) : all<N>(0.0f);
+#pragma unroll
+    for (int k = 0; k < kR; ++k) {
+      if (k >= live) continue;
+      C out;
+      pack(fma(mul(s[k][j], all<N>(rs[k])), g, b), out);
+      static_cast<C*>(p.y)[(row0 + k) * chunks + i] = out;
+    }
+  }
+}
+
+// Rows too wide for registers: a block a row, which it reads three times.
+template <typename T, int N>
+__global__ void __launch_bounds__(1024) add_layernorm_wide_kernel(const LayerNormArgs p) {
+  __shared__ float part[64], part_mean[64];
+  pdl_wait();
+  const int64_t base = blockIdx.x * static_cast<int64_t>(p.d);
   const T* a = static_cast<const T*>(p.a) + base;
   const T* r = p.r ? static_cast<const T*>(p.r) + base : nullptr;
-  const int pieces = live ? d / N : 0;
-  const uint32_t wide = pieces;  // unsigned: a step beyond the last piece may pass 2^31
-
-  auto sum = [&](int i) {
-    Piece<T, N> s = load<N>(a + static_cast<int64_t>(i) * N);
+  const uint32_t pieces = p.d / N;  // unsigned: a step beyond the last piece may pass 2^31
+  const float inv_d = 1.0f / static_cast<float>(p.d);
+  auto sum = [&](int64_t at) {
+    Piece<T, N> s = load<N>(a + at);
     if (r) {
-      const Piece<T, N> b = load<N>(r + static_cast<int64_t>(i) * N);
+      const Piece<T, N> b = load<N>(r + at);
 #pragma unroll
       for (int k = 0; k < N; ++k) s.v[k] += b.v[k];
     }
     return s;
   };
-  auto mean = [&](float q, int use) {
+  float q = 0.0f;
+  for (uint32_t i = threadIdx.x; i < pieces; i += 1024) {
+    const Piece<T, N> s = sum(static_cast<int64_t>(i) * N);
 #pragma unroll
-    for (int o = 16; o; o >>= 1) q += __shfl_xor_sync(0xffffffffu, q, o);
-    if constexpr (!kWarpRow) {
-      if ((tid & 31) == 0) part[use][tid >> 5] = q;
-      __syncthreads();
-      q = (tid & 31) < threads / 32 ? part[use][tid & 31] : 0.0f;
-#pragma unroll
-      for (int o = 16; o; o >>= 1) q += __shfl_xor_sync(0xffffffffu, q, o);
-    }
-    return q / static_cast<float>(d);
-  };
-  Piece<T, N> keep[kKeep ? kKeep : 1];
-  float q = 0.0f, mu, rs;
-  if constexpr (kKeep > 0) {
-#pragma unroll
-    for (int j = 0; j < kKeep; ++j)
-      if (tid + j * threads < pieces) keep[j] = sum(tid + j * threads);
-#pragma unroll
-    for (int j = 0; j < kKeep; ++j)
-      if (tid + j * threads < pieces)
-#pragma unroll
-        for (int k = 0; k < N; ++k) q += keep[j].v[k];
-    mu = mean(q, 0);
-    q = 0.0f;
-#pragma unroll
-    for (int j = 0; j < kKeep; ++j)
-      if (tid + j * threads < pieces)
-#pragma unroll
-        for (int k = 0; k < N; ++k) q = fmaf(keep[j].v[k] - mu, keep[j].v[k] - mu, q);
-  } else {
-    for (uint32_t i = tid; i < wide; i += threads) {
-      const Piece<T, N> s = sum(i);
-#pragma unroll
-      for (int k = 0; k < N; ++k) q += s.v[k];
-    }
-    mu = mean(q, 0);
-    q = 0.0f;
-    for (uint32_t i = tid; i < wide; i += threads) {
-      const Piece<T, N> s = sum(i);
-#pragma unroll
-      for (int k = 0; k < N; ++k) q = fmaf(s.v[k] - mu, s.v[k] - mu, q);
-    }
+    for (int k = 0; k < N; ++k) q += s.v[k];
   }
-  rs = rsqrtf(mean(q, 1) + p.eps);
-
-  auto finish = [&](int i, const Piece<T, N>& s) {
+  const float mu = block_sum(q, 0.0f, part_mean).x * inv_d;
+  q = 0.0f;
+  for (uint32_t i = threadIdx.x; i < pieces; i += 1024) {
+    const Piece<T, N> s = sum(static_cast<int64_t>(i) * N);
+#pragma unroll
+    for (int k = 0; k < N; ++k) q = fmaf(s.v[k] - mu, s.v[k] - mu, q);
+  }
+  const float rs = rsqrtf(block_sum(q, 0.0f, part).x * inv_d + p.eps);
+  for (uint32_t i = threadIdx.x; i < pieces; i += 1024) {
     const int64_t at = static_cast<int64_t>(i) * N;
-    const Piece<T, N> g = load<N>(static_cast<const T*>(p.w) + at);
+    const Piece<T, N> s = sum(at), g = load<N>(static_cast<const T*>(p.w) + at);
     float v[N];
 #pragma unroll
     for (int k = 0; k < N; ++k) v[k] = (s.v[k] - mu) * rs * g.v[k];
@@ -104,44 +156,57 @@ __global__ void __launch_bounds__(kMaxThreads, kMinBlocks)
     }
     if (p.h) store<N>(static_cast<T*>(p.h) + base + at, s.v);
     store<N>(static_cast<T*>(p.y) + base + at, v);
-  };
-  if constexpr (kKeep > 0) {
-#pragma unroll
-    for (int j = 0; j < kKeep; ++j)
-      if (tid + j * threads < pieces) finish(tid + j * threads, keep[j]);
-  } else {
-    for (uint32_t i = tid; i < wide; i += threads) finish(i, sum(i));
   }
 }
 
-template <typename T, int N, bool kWarpRow, int kKeep, int kMaxThreads, int kMinBlocks = 1>
+template <typename T, int N, int kP, int kR, bool kWarpRow, int kMaxThreads, int kMinBlocks = 1>
 cudaError_t launch(const LayerNormArgs& n, int threads, cudaStream_t stream) {
-  const int64_t blocks = kWarpRow ? (n.T + kRowsPerBlock - 1) / kRowsPerBlock : n.T;
-  return launch_pdl(add_layernorm_kernel<T, N, kWarpRow, kKeep, kMaxThreads, kMinBlocks>,
-                    dim3(static_cast<unsigned>(blocks)),
-                    dim3(kWarpRow ? 32 * kRowsPerBlock : threads), 0, stream, n);
+  constexpr int kRows = kR * (kWarpRow ? kRowWarps : 1);
+  return launch_pdl(add_layernorm_kernel<T, N, kP, kR, kWarpRow, kMaxThreads, kMinBlocks>,
+                    dim3(static_cast<unsigned>((n.T + kRows - 1) / kRows)), dim3(threads), 0, stream,
+                    n);
 }
 
 template <typename T, int N>
 cudaError_t dispatch(const LayerNormArgs& n, int num_sms, cudaStream_t stream) {
-  const int pieces = n.d / N;
-  auto round32 = [](int v) { return (v + 31) / 32 * 32; };
-  if (pieces <= 32) return launch<T, N, true, 1, 32 * kRowsPerBlock>(n, 32, stream);
-  if (pieces <= 128) return launch<T, N, false, 1, 1024>(n, round32(pieces), stream);
-  if (pieces <= 1024)
-    return n.T < 2 * num_sms ? launch<T, N, false, 1, 1024>(n, round32(pieces), stream)
-                             : launch<T, N, false, 2, 512, 3>(n, round32((pieces + 1) / 2), stream);
-  if (pieces <= 4096) return launch<T, N, false, 4, 1024>(n, round32((pieces + 3) / 4), stream);
-  return launch<T, N, false, 0, 1024>(n, 1024, stream);
+  // threads of a row with at most Q values each
+  auto threads = [&](int Q) { return (n.d + 32 * Q - 1) / (32 * Q) * 32; };
+  constexpr int kWarps = 32 * kRowWarps;
+  if (n.d > 16384) {
+    constexpr int W = N == 2 ? 1 : N;  // a Piece is one value or 16 bytes
+    return launch_pdl(add_layernorm_wide_kernel<T, W>, dim3(static_cast<unsigned>(n.T)), dim3(1024),
+                      0, stream, n);
+  }
+  if (n.d > 8192) return launch<T, N, 16 / N, 1, false, 1024>(n, threads(16), stream);
+  if (n.T < 2 * num_sms)
+    return n.d <= 256 ? launch<T, N, 8 / N, 1, true, kWarps>(n, kWarps, stream)
+                      : launch<T, N, 8 / N, 1, false, 1024>(n, threads(8), stream);
+  // many rows: two at a time where bf16 makes the instructions count (8192 x 7168
+  // with a residual, 470 MB: 70.1 us, the copy rate; a row a block, without pairs
+  // of values, 82.3; three such blocks an SM spill, 137), one where fp32 does not
+  // (8191 x 3584, 235 MB: 38.8 us, 90% of it; 32768 x 1000 40.6, 96%)
+  if (n.d <= 256) return launch<T, N, 8 / N, 2, true, kWarps>(n, kWarps, stream);
+  if constexpr (sizeof(T) == 4) {
+    if (n.d <= 2048) return launch<T, N, 8 / N, 1, false, 256, 8>(n, threads(8), stream);
+    if (n.d <= 4096) return launch<T, N, 16 / N, 1, false, 256, 4>(n, threads(16), stream);
+    return launch<T, N, 16 / N, 1, false, 512, 1>(n, threads(16), stream);
+  } else {
+    if (n.d <= 512) return launch<T, N, 16 / N, 2, true, kWarps>(n, kWarps, stream);
+    if (n.d <= 1024) return launch<T, N, 32 / N, 2, true, kWarps>(n, kWarps, stream);
+    if (n.d <= 7168) return launch<T, N, 16 / N, 2, false, 448, 2>(n, threads(16), stream);
+    return launch<T, N, 16 / N, 2, false, 512, 2>(n, threads(16), stream);
+  }
 }
 
 }  // namespace
 
 cudaError_t launch_add_layernorm(const LayerNormArgs& n, int num_sms, cudaStream_t stream) {
   if (n.bf16)
-    return n.d % 8 ? dispatch<__nv_bfloat16, 1>(n, num_sms, stream)
-                   : dispatch<__nv_bfloat16, 8>(n, num_sms, stream);
-  return n.d % 4 ? dispatch<float, 1>(n, num_sms, stream) : dispatch<float, 4>(n, num_sms, stream);
+    return n.d % 8 == 0   ? dispatch<__nv_bfloat16, 8>(n, num_sms, stream)
+           : n.d % 2 == 0 ? dispatch<__nv_bfloat16, 2>(n, num_sms, stream)
+                          : dispatch<__nv_bfloat16, 1>(n, num_sms, stream);
+  return n.d % 4 == 0 ? dispatch<float, 4>(n, num_sms, stream)
+                      : dispatch<float, 1>(n, num_sms, stream);
 }
 
 }  // namespace fgs

@@ -55,153 +55,6 @@ __device__ __forceinline__ Piece<T, N> row_sum(const T* a, const T* r, int64_t a
   return s;
 }
 
-// Sums of two values over a warp, and over a block's threads; the same in all of
-// them.  The halves of a warp first exchange what the other adds up, so that a
-// round of the tree serves both values.  A `part` serves one sum at a time: with
-// a barrier between two uses of it.
-__device__ __forceinline__ float half_sums(float x, float y) {
-  const bool low = (threadIdx.x & 31) < 16;
-  float v = low ? x : y;
-  v += __shfl_xor_sync(0xffffffffu, low ? y : x, 16);
-#pragma unroll
-  for (int o = 8; o; o >>= 1) v += __shfl_xor_sync(0xffffffffu, v, o);
-  return v;  // x's in the low half, y's in the high
-}
-__device__ __forceinline__ float2 both_halves(float v) {
-  const float other = __shfl_xor_sync(0xffffffffu, v, 16);
-  return (threadIdx.x & 31) < 16 ? make_float2(v, other) : make_float2(other, v);
-}
-__device__ __forceinline__ float2 warp_sum(float x, float y) { return both_halves(half_sums(x, y)); }
-__device__ __forceinline__ float2 block_sum(float x, float y, float (&part)[64]) {
-  const int lane = threadIdx.x & 31;
-  float v = half_sums(x, y);
-  // the sums of warp i at 2 i and 2 i + 1
-  if ((lane & 15) == 0) part[threadIdx.x >> 4] = v;
-  __syncthreads();
-  const int sums = blockDim.x / 16, i = 2 * (lane & 15) + (lane >> 4);
-  v = i < sums ? part[i] : 0.0f;
-  if (i + 32 < sums) v += part[i + 32];
-#pragma unroll
-  for (int o = 8; o; o >>= 1) v += __shfl_xor_sync(0xffffffffu, v, o);
-  return both_halves(v);
-}
-
-// N values: one, or N / 2 pairs.
-template <int N>
-struct Vec {
-  static constexpr int M = N / 2;
-  pair v[M];
-};
-template <>
-struct Vec<1> {
-  float v;
-};
-template <int N>
-__device__ __forceinline__ Vec<N> mul(const Vec<N>& a, const Vec<N>& b) {
-  Vec<N> r;
-  if constexpr (N == 1)
-    r.v = a.v * b.v;
-  else
-#pragma unroll
-    for (int i = 0; i < Vec<N>::M; ++i) r.v[i] = mul2(a.v[i], b.v[i]);
-  return r;
-}
-template <int N>
-__device__ __forceinline__ Vec<N> fma(const Vec<N>& a, const Vec<N>& b, const Vec<N>& c) {
-  Vec<N> r;
-  if constexpr (N == 1)
-    r.v = fmaf(a.v, b.v, c.v);
-  else
-#pragma unroll
-    for (int i = 0; i < Vec<N>::M; ++i) r.v[i] = fma2(a.v[i], b.v[i], c.v[i]);
-  return r;
-}
-template <int N>
-__device__ __forceinline__ Vec<N> add(const Vec<N>& a, const Vec<N>& b) {
-  Vec<N> r;
-  if constexpr (N == 1)
-    r.v = a.v + b.v;
-  else
-#pragma unroll
-    for (int i = 0; i < Vec<N>::M; ++i)
-      asm("add.rn.f32x2 %0, %1, %2;" : "=l"(r.v[i]) : "l"(a.v[i]), "l"(b.v[i]));
-  return r;
-}
-template <int N>
-__device__ __forceinline__ Vec<N> all(float a) {
-  Vec<N> r;
-  if constexpr (N == 1)
-    r.v = a;
-  else
-#pragma unroll
-    for (int i = 0; i < Vec<N>::M; ++i) r.v[i] = make_pair2(a, a);
-  return r;
-}
-template <int N>
-__device__ __forceinline__ float total(const Vec<N>& a) {
-  if constexpr (N == 1) {
-    return a.v;
-  } else {
-    float s = 0.0f;
-#pragma unroll
-    for (int i = 0; i < Vec<N>::M; ++i) {
-      float x, y;
-      split(a.v[i], x, y);
-      s += x + y;
-    }
-    return s;
-  }
-}
-
-// N values of type T in memory, of 2 to 16 bytes, and as a Vec.
-template <typename T, int N>
-struct Chunk;
-template <>
-struct Chunk<__nv_bfloat16, 8> { uint4 u; };
-template <>
-struct Chunk<__nv_bfloat16, 2> { uint32_t u; };
-template <>
-struct Chunk<__nv_bfloat16, 1> { __nv_bfloat16 u; };
-template <>
-struct Chunk<float, 4> { float4 u; };
-template <>
-struct Chunk<float, 1> { float u; };
-__device__ __forceinline__ pair bf16_pair(uint32_t w) {
-  return make_pair2(__uint_as_float(w << 16), __uint_as_float(w & 0xffff0000u));
-}
-__device__ __forceinline__ uint32_t pair_bf16(pair v) {
-  float a, b;
-  split(v, a, b);
-  return pack_bf16x2(a, b);
-}
-__device__ __forceinline__ Vec<8> unpack(const Chunk<__nv_bfloat16, 8>& c) {
-  return {{bf16_pair(c.u.x), bf16_pair(c.u.y), bf16_pair(c.u.z), bf16_pair(c.u.w)}};
-}
-__device__ __forceinline__ Vec<2> unpack(const Chunk<__nv_bfloat16, 2>& c) {
-  return {{bf16_pair(c.u)}};
-}
-__device__ __forceinline__ Vec<1> unpack(const Chunk<__nv_bfloat16, 1>& c) {
-  return {__bfloat162float(c.u)};
-}
-__device__ __forceinline__ Vec<4> unpack(const Chunk<float, 4>& c) {
-  return {{make_pair2(c.u.x, c.u.y), make_pair2(c.u.z, c.u.w)}};
-}
-__device__ __forceinline__ Vec<1> unpack(const Chunk<float, 1>& c) { return {c.u}; }
-__device__ __forceinline__ void pack(const Vec<8>& v, Chunk<__nv_bfloat16, 8>& c) {
-  c.u = make_uint4(pair_bf16(v.v[0]), pair_bf16(v.v[1]), pair_bf16(v.v[2]), pair_bf16(v.v[3]));
-}
-__device__ __forceinline__ void pack(const Vec<2>& v, Chunk<__nv_bfloat16, 2>& c) {
-  c.u = pair_bf16(v.v[0]);
-}
-__device__ __forceinline__ void pack(const Vec<1>& v, Chunk<__nv_bfloat16, 1>& c) {
-  c.u = __float2bfloat16_rn(v.v);
-}
-__device__ __forceinline__ void pack(const Vec<4>& v, Chunk<float, 4>& c) {
-  split(v.v[0], c.u.x, c.u.y);
-  split(v.v[1], c.u.z, c.u.w);
-}
-__device__ __forceinline__ void pack(const Vec<1>& v, Chunk<float, 1>& c) { c.u = v.v; }
-
 // A chunk of global memory into shared memory, past the registers and L1.
 template <int kBytes>
 __device__ __forceinline__ void copy_async(uint32_t dst, const void* src) {

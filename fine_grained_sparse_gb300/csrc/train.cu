@@ -155,7 +155,7 @@ __global__ void __launch_bounds__(kThreads) combine_backward_kernel(
 // A warp per token: lane k holds pair k.  The row of dz is zeroed, then the
 // pairs' entries are written over the zeros; an expert that a token lists
 // more than once receives the sum of its pairs, from the first of them.
-constexpr int kRouterWarps = 8;
+constexpr int kRouterWarps = 4;
 __global__ void __launch_bounds__(32 * kRouterWarps) router_backward_kernel(
     const float* __restrict__ z, const int32_t* __restrict__ idx, const float* __restrict__ dw,
     int64_t T, int K, int E, float scale, int renorm, float* __restrict__ dz) {
@@ -164,18 +164,19 @@ __global__ void __launch_bounds__(32 * kRouterWarps) router_backward_kernel(
   const int64_t t = static_cast<int64_t>(blockIdx.x) * kRouterWarps + (threadIdx.x >> 5);
   if (t >= T) return;
   float* row = dz + t * E;
+  const int at = lane < K ? __ldg(idx + t * K + lane) : -1;
+  const float d0 = lane < K ? __ldg(dw + t * K + lane) : 0.0f;
+  const bool in = at >= 0 && at < E;
+  const float zk = in ? __ldg(z + t * E + at) : 0.0f;
   if (E % 4 == 0) {
     for (int e = lane; e < E / 4; e += 32)
       reinterpret_cast<float4*>(row)[e] = make_float4(0.f, 0.f, 0.f, 0.f);
   } else {
     for (int e = lane; e < E; e += 32) row[e] = 0.0f;
   }
-  const int at = lane < K ? __ldg(idx + t * K + lane) : -1;
-  const bool in = at >= 0 && at < E;
   float g = 0.0f;
   {
-    const float zk = in ? __ldg(z + t * E + at) : 0.0f;
-    const float d = in ? __ldg(dw + t * K + lane) : 0.0f;
+    const float d = in ? d0 : 0.0f;
     // sigmoid(z), times 2^64 so that it holds where e^z is below fp32's range,
     // and 1 - sigmoid(z), each without cancellation
     const float h = expf(-0.5f * fabsf(zk)), e = h * h;
