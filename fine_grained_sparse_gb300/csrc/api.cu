@@ -1306,7 +1306,7 @@ int32_t moe_combine_backward(const moe_config* cfg, int64_t T, const void* dy, c
   for (const void* q : ptrs)
     if (!aligned16(q)) return fail(MOE_ERR_ALIGNMENT, "pointer not 16-byte aligned");
   MOE_CUDA(launch_combine_backward(dy, Y, inv, topk_w, T, cfg->K, d_expert(cfg),
-                                   cfg->dtype == MOE_BF16, dY, dtopk_w,
+                                   cfg->dtype == MOE_BF16, num_sms(), dY, dtopk_w,
                                    static_cast<cudaStream_t>(stream)));
   return MOE_OK;
 }

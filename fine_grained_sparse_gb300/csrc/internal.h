@@ -302,8 +302,8 @@ cudaError_t launch_gather_rows(const void* x, const int32_t* inv, const float* w
 // dY[inv[j]] = w[j] dy[j / K] (w null: 1; dY may be null or Y) and
 // dw[j] = <Y[inv[j]], dy[j / K]> (dw may be null, then Y too).  D % 8 == 0.
 cudaError_t launch_combine_backward(const void* dy, const void* Y, const int32_t* inv,
-                                    const float* w, int64_t T, int K, int D, bool bf16, void* dY,
-                                    float* dw, cudaStream_t stream);
+                                    const float* w, int64_t T, int K, int D, bool bf16, int num_sms,
+                                    void* dY, float* dw, cudaStream_t stream);
 // dz [T, E] of the gate weights' gradient dw [T, K]; K <= 32.
 cudaError_t launch_router_backward(const float* logits, const int32_t* idx, const float* dw,
                                    int64_t T, int K, int E, float scale, bool renorm, float* dz,
