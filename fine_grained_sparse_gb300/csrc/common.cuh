@@ -167,7 +167,8 @@ __device__ __forceinline__ void bulk_load(uint32_t dst, const void* src, uint32_
 //    launch plans its work while this one drains.  The persistent GEMM
 //    releases when its work is done, before its teardown (released at the
 //    start, waiting CTAs of the next kernel sat beside the running ones and
-//    cost time); the other kernels release by exiting.
+//    cost time); the norm gradients' persistent kernels release before they
+//    write their partial rows; the other kernels release by exiting.
 //  - A kernel may start while the one before it runs, and while that one waits
 //    for the one before it.  So every kernel launched with the attribute waits
 //    in every thread, at the latest before it ends: whoever has waited knows
