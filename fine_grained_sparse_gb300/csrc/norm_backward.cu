@@ -85,8 +85,10 @@ __device__ __forceinline__ void wait_copies(int left) {
 // of its rows.  But for single bf16 values a lane keeps the chunks of its next
 // `stages` rows on their way into shared memory, where it alone reads them: no
 // barrier, and no register holds what is under way.
-//   dx = r g - (r r mean(g s)) r s + dh, and for the layer form
-//   dx = r g - (r r mean(g s)) r s + (dh - r mean g), s there the difference to mu
+//   dx = r g - (r mean(g u)) u + dh, and for the layer form
+//   dx = r g - (r mean(g u)) u + (dh - r mean g)
+// with u = s r taken first: r r mean(g s) by itself overflows for rows of values
+// below 2^-64.
 constexpr int kRowWarps = 8;
 
 template <typename T, int N, int kP, bool kLayer, int kMinBlocks>
@@ -188,7 +190,7 @@ __global__ void __launch_bounds__(32 * kRowWarps, kMinBlocks)
     }
     const float2 t = warp_sum(total(a), total(b));
     const float rs = rsqrtf(t.x * inv_d + eps);
-    const float c = -rs * (rs * rs * (t.y * inv_d));
+    const float c = -rs * (rs * (t.y * inv_d));
     const V vrs = all<N>(rs), vc = all<N>(c), vg = all<N>(-rs * mg);
 #pragma unroll
     for (int j = 0; j < kP; ++j) {
@@ -196,7 +198,8 @@ __global__ void __launch_bounds__(32 * kRowWarps, kMinBlocks)
       V s = sum(j);
       if constexpr (kLayer) s = add(s, vmu);
       const V y = unpack(chunk(p.dy, 0, j));
-      dw[j] = fma(mul(y, vrs), s, dw[j]);
+      s = mul(s, vrs);
+      dw[j] = fma(y, s, dw[j]);
       if constexpr (kLayer) db[j] = add(db[j], y);
       if (p.dx) {
         V v = with_dh ? unpack(chunk(p.dh, tensors - 1, j)) : all<N>(0.0f);
@@ -319,8 +322,11 @@ __global__ void __launch_bounds__(kMaxThreads, kMinBlocks)
   }
   int stage = 0, turn = 0;
   uint32_t parity = 0;
-  for (int64_t group = blockIdx.x; group < groups; group += gridDim.x) {
-    if (!mbar_wait_bounded(smem_u32(&full[stage]), parity, &aborted, status)) break;
+  int64_t group = blockIdx.x;
+  for (; group < groups; group += gridDim.x) {
+    if (!__all_sync(0xffffffffu,
+                    mbar_wait_bounded(smem_u32(&full[stage]), parity, &aborted, status)))
+      break;
     const int live = static_cast<int>(min(static_cast<int64_t>(kR), rows - group * kR));
     C cy[kR][kP], cs[kR][kP], cr[kRes ? kR : 1][kP], ch[kR][kP];
     {
@@ -398,7 +404,7 @@ __global__ void __launch_bounds__(kMaxThreads, kMinBlocks)
     for (int r = 0; r < kR; ++r) {
       if (r >= live) break;
       const float rs = rsqrtf(ss[r] * inv_d + eps);
-      const float c = -rs * (rs * rs * (gs[r] * inv_d));
+      const float c = -rs * (rs * (gs[r] * inv_d));
       const int64_t row = group * kR + r;
 #pragma unroll
       for (int j = 0; j < kP; ++j) {
@@ -406,7 +412,8 @@ __global__ void __launch_bounds__(kMaxThreads, kMinBlocks)
         V s = sum(r, j);
         if constexpr (kLayer) s = add(s, all<N>(mu[r]));
         const V y = unpack(cy[r][j]);
-        dw[j] = fma(mul(y, all<N>(rs)), s, dw[j]);
+        s = mul(s, all<N>(rs));
+        dw[j] = fma(y, s, dw[j]);
         if constexpr (kLayer) db[j] = add(db[j], y);
         if (p.dx) {
           V v = with_dh ? unpack(ch[r][j]) : all<N>(0.0f);
@@ -423,6 +430,16 @@ __global__ void __launch_bounds__(kMaxThreads, kMinBlocks)
       parity ^= 1;
     }
   }
+  // After a wait that expired: no copy of the block's may be under way at its end.
+  if (tid == 0)
+    for (int i = 0; i < stages && group < groups; ++i, group += gridDim.x) {
+      int own = 0;
+      if (!mbar_wait_bounded(smem_u32(&full[stage]), parity, &own, status)) break;
+      if (++stage == stages) {
+        stage = 0;
+        parity ^= 1;
+      }
+    }
   pdl_release();  // the sum of the partial rows waits for them itself
 #pragma unroll
   for (int j = 0; j < kP; ++j) {
@@ -498,7 +515,7 @@ __global__ void __launch_bounds__(kMaxThreads)
   }
   const float2 t = kWarpRow ? warp_sum(total(a), total(b)) : block_sum(total(a), total(b), part);
   const float rs = rsqrtf(t.x * inv_d + eps);
-  const float c = -rs * (rs * rs * (t.y * inv_d));
+  const float c = -rs * (rs * (t.y * inv_d));
   if (p.stats && tid == 0) p.stats[row] = make_float2(mu, rs);
   if (!p.dx) return;
 #pragma unroll
@@ -508,7 +525,7 @@ __global__ void __launch_bounds__(kMaxThreads)
     V v = p.dh ? unpack(ch[j]) : all<N>(0.0f);
     if constexpr (kLayer) v = add(v, all<N>(-rs * mg));
     C out;
-    pack(fma(g[j], all<N>(rs), fma(s[j], all<N>(c), v)), out);
+    pack(fma(g[j], all<N>(rs), fma(mul(s[j], all<N>(rs)), all<N>(c), v)), out);
     static_cast<C*>(p.dx)[base + i] = out;
   }
 }
@@ -639,7 +656,7 @@ __global__ void __cluster_dims__(1, kColumnBlocks, 1) __launch_bounds__(32 * kCo
         if (p.r) u = add(u, unpack(r[a]));
         if constexpr (kLayer) u = add(u, all<N>(-st[a].x));
         const V v = unpack(y[a]);
-        dw = fma(mul(v, all<N>(st[a].y)), u, dw);
+        dw = fma(v, mul(u, all<N>(st[a].y)), dw);
         if constexpr (kLayer) db = add(db, v);
       }
     }

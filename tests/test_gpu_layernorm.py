@@ -227,6 +227,57 @@ def test_backward_in_place(d, kind):
             assert full[name] is None or torch.equal(got[name], full[name])
 
 
+@pytest.mark.parametrize("kind", ["rms", "layer"])
+@pytest.mark.parametrize("T,d,dtype", [(1030, 1032, "bf16"), (1027, 520, "f32"), (2455, 136, "bf16")])
+def test_backward_many_rows_in_place(T, d, dtype, kind):
+    """dx in place of each input, and some of the outputs alone, where a block
+    keeps copies of its next rows under way."""
+    need_gpu()
+    fgs = lib()
+    x, r, w, _, dy, dh = _inputs(T, d, dtype)
+    full = _backward(fgs, kind, dtype, x, r, w, dy, dh)
+    for at in range(4):
+        t = [v.cuda() for v in (x, r, dy, dh)]
+        got = _backward(fgs, kind, dtype, t[0], t[1], w, t[2], t[3], dx=t[at])
+        for name in full:
+            assert full[name] is None or torch.equal(got[name], full[name])
+    for want in (("dw",), ("dw", "db"), ("dx", "dw"), ("dx", "db")):
+        if kind == "rms" and "db" in want:
+            continue
+        got = _backward(fgs, kind, dtype, x, r, w, dy, dh, want=want)
+        for name in want:
+            assert torch.equal(got[name], full[name])
+
+
+@pytest.mark.parametrize("kind", ["rms", "layer"])
+@pytest.mark.parametrize("T,d,dtype", [(5, 7168, "f32"), (40, 20000, "bf16"), (1500, 200, "bf16"),
+                                       (3000, 256, "f32"), (1030, 1032, "bf16"), (1027, 4096, "f32")])
+def test_backward_small_values(T, d, dtype, kind):
+    """Rows of 2^-65 with eps 0: the inverse root's square is past fp32's range,
+    the gradient is not.
+
+    The squares, above 2^-131 in the mean, are subnormal: each of the d + 64 sums
+    is off by half of 2^-149, which is 1.4 2^-150 of the mean for d >= 200, and so
+    is the mean's own rounding, 2^-150.  Relative to the variance 2^-17.7, to its
+    root 2^-18.7; 2^-18 is allowed."""
+    need_gpu()
+    fgs = lib()
+    x, _, w, _, dy, dh = _inputs(T, d, dtype)
+    x = x * 2.0 ** -62  # exact: rows of 2^-65 to 2^-59
+    got = _backward(fgs, kind, dtype, x, None, w, dy, dh, eps=0.0)
+    X, W, DY, DH = n64(x), n64(w), n64(dy), n64(dh)
+    want, lim = norm_backward64(kind, X, None, W, 0.0, DY, DH)
+    _, v, r, _ = norm64(kind, X, None, W, None, 0.0)
+    g = DY * W
+    c = (g * v).mean(1, keepdims=True)
+    root = 2.0 ** -18
+    more = (root * (r * np.abs(want[0] / r) + 2 * r * np.abs(v * c)) * 1.01,
+            root * np.abs(DY * v).sum(0), 0.0)
+    for name, a, b, e, rounding in zip(("dx", "dw", "db"), want, lim, more, (U[dtype], u, u)):
+        if got[name] is not None:
+            close(got[name], a, b + e, rounding)
+
+
 def test_backward_repeats():
     """The same sums every time, and on a workspace of any contents."""
     need_gpu()

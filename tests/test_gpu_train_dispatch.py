@@ -327,3 +327,63 @@ def test_captured_and_on_another_stream():
         x64 = n64(x)
         close(dw, np.repeat((x64 * x64).sum(1, keepdims=True), K, 1),
               (chain(D) + 1) * u * (x64 * x64).sum(1, keepdims=True), 0.0)
+
+
+def test_offsets_past_32_bits():
+    """Rows in expert order of more than 2^32 elements: the gather and the
+    combine's gradient, checked at the first and last pairs of every expert."""
+    need_gpu()
+    fgs = lib()
+    T, K, E, D = 40000, 16, 32, 7168  # 4.59e9 elements
+    cfg = _cfg(fgs, D, K, E, "bf16")
+    gen = torch.Generator().manual_seed(3)
+    idx = routing(T, K, E, gen)
+    inv_host, kept = slots(idx, E)
+    assert kept * D > 2 ** 32
+    inv = torch.from_numpy(inv_host).cuda()
+    x = torch.randn((T, D), device="cuda", dtype=torch.bfloat16)
+    w = torch.rand((T, K), device="cuda")
+    xp = torch.empty((kept, D), dtype=torch.bfloat16, device="cuda")
+    wp = torch.empty(kept, device="cuda")
+    fgs.moe_gather(cfg, T, x, inv, w, xp, wp)
+    pairs = torch.cat([torch.arange(64), torch.arange(T * K - 64, T * K)]).cuda()
+    at = inv.long()
+    pairs = torch.cat([pairs, at.argsort()[torch.arange(0, kept, 4999, device="cuda")],
+                       at.argsort()[-64:]])
+    rows = at[pairs]
+    assert torch.equal(xp[rows], x[pairs // K])
+    assert torch.equal(wp[rows], w.reshape(-1)[pairs])
+    dy = torch.randn((T, D), device="cuda", dtype=torch.bfloat16)
+    dw = torch.empty((T, K), device="cuda")
+    Y = xp[rows].clone()
+    fgs.moe_combine_backward(cfg, T, dy, xp, inv, w, xp, dw)  # dY in place of Y
+    g = dy[pairs // K].double()
+    close(xp[rows].cpu(), n64(w.reshape(-1)[pairs, None].double() * g),
+          0.0, U["bf16"] + 2 * u)  # the product in fp32, then rounded
+    want = (Y.double() * g)
+    close(dw.reshape(-1)[pairs].cpu(), n64(want.sum(1)),
+          n64(want.abs().sum(1)) * (chain(D) + 2) * u, u)
+
+
+def test_router_backward_offsets_past_32_bits():
+    need_gpu()
+    fgs = lib()
+    T, K, E = 4_800_001, 8, 896  # 4.3e9 logits
+    z = torch.zeros((T, E), device="cuda")
+    gen = torch.Generator().manual_seed(4)
+    n = 50
+    tail = torch.randn((n, E), generator=gen)
+    idx = routing(n, K, E, gen)
+    g = torch.randn((n, K), generator=gen)
+    z[-n:] = tail.cuda()
+    all_idx = torch.zeros((T, K), dtype=torch.int32, device="cuda")
+    all_idx[-n:] = idx.cuda()
+    dw = torch.zeros((T, K), device="cuda")
+    dw[-n:] = g.cuda()
+    dz = torch.full((T, E), 9.0, device="cuda")
+    cfg = _cfg(fgs, 128, K, E, "bf16")
+    fgs.moe_router_backward(cfg, T, z, all_idx, dw, dz)
+    want, lim = router_backward64(n64(tail), idx.numpy(), n64(g), E,
+                                  cfg.routed_scaling_factor, True)
+    close(dz[-n:].cpu(), want, lim, u)
+    assert int((dz[:-n] != 0).sum()) == 0
