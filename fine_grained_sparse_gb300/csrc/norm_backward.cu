@@ -7,24 +7,23 @@
 //           dx = r (g - mean g - u mean(g u)) + dh
 //   dweight = sum over the rows of dy u,  dbias = sum over the rows of dy
 // mean(g u) is r mean(g s) (r mean(g (s - mu))), so the RMS form needs one
-// reduction over a row and the layer form two.
+// reduction over a row; the layer form two, or one about a pivot (below).
 //
 // Kernels
-//   norm_backward_stream_kernel   many rows of more than 1024 columns (layer form
+//   norm_backward_stream_kernel   many rows of more than 512 columns (layer form
 //       256): blocks that stay sum their rows' dweight and dbias in registers
 //       and write one partial row of each; column_sum_kernel adds those up.
-//       8192 x 7168 bf16 with dh (470 MB): RMS 80 us, 5.87 TB/s, 88% of the copy
-//       rate; layer form 106 us, 66%, bound by the issue of its instructions
-//       (the unpacking of bf16 for each of three passes over shared memory);
-//       4096 x 7168 fp32 RMS 78 us, 90%.  A row at a time from copies by every
-//       thread took 88 and 130, from registers 128 and 213.
+//       8192 x 7168 bf16 with dh (470 MB): RMS 73.9 us, 6.36 TB/s, 95% of the copy
+//       rate; layer form 77.1 us, 91%; 4096 x 7168 fp32 RMS 72.7 us, 97%; 57344 x
+//       1024 75.3 and 76.4.  What is lost is the launch of the sums of the partial
+//       rows and the start of the copies.
 //   norm_backward_warps_kernel    many shorter rows, the same with a warp a row
 //   norm_backward_rows_kernel, norm_backward_columns_kernel   few rows: dx and
 //       the rows' statistics, then the sums from a second reading, which comes
 //       from L2.  777 x 1000 fp32 layer form 6.8 us: two launches.
 //   norm_backward_wide_kernel     rows of more than 16384 columns
-// Every sum is taken in an order that T and d decide, so results depend neither
-// on timing nor on the device.
+// Every sum is taken in an order that the sizes, the types and the given arguments
+// decide, so results depend neither on timing nor on the device.
 #include "common.cuh"
 #include "internal.h"
 #include "rows.cuh"
@@ -69,7 +68,7 @@ __device__ __forceinline__ void commit_copies() {
 }
 // Wait until at most `left` (< kMaxStages) of the thread's groups of copies are
 // under way.
-constexpr int kMaxStages = 4;
+constexpr int kMaxStages = 4, kStreamStages = 4;
 __device__ __forceinline__ void wait_copies(int left) {
   if (left == 0)
     asm volatile("cp.async.wait_group 0;" ::: "memory");
@@ -237,9 +236,10 @@ __global__ void __launch_bounds__(32 * kRowWarps, kMinBlocks)
   if constexpr (kLayer) write(p.pb, db);
 }
 
-// Sums of four values over a block of at most 16 warps, as block_sum takes two.
+// Sums of four values over a block of at most 16 warps, as block_sum takes two;
+// `part` of 64 values.
 __device__ __forceinline__ float4 block_sum4(float v0, float v1, float v2, float v3,
-                                             float (&part)[64]) {
+                                             float* part) {
   const int lane = threadIdx.x & 31;
   const bool high = lane & 16, odd = lane & 8;
   float a = high ? v2 : v0, b = high ? v3 : v1;
@@ -261,30 +261,40 @@ __device__ __forceinline__ float4 block_sum4(float v0, float v1, float v2, float
                      __shfl_sync(0xffffffffu, v, 2), __shfl_sync(0xffffffffu, v, 3));
 }
 
-// Many rows of whole 16-byte chunks: a block takes kR neighbouring rows at a
-// time, a thread the same kP chunks of each.  One thread keeps bulk copies of
-// the next rows under way into a ring of shared memory; a stage is free again
-// at the first barrier of its rows' sums, as every thread then holds its chunks
-// of them.  Two rows share a barrier, the tree of their sums and the weights.
-template <typename T, int kP, int kR, bool kLayer, bool kRes, int kMaxThreads, int kMinBlocks>
-__global__ void __launch_bounds__(kMaxThreads, kMinBlocks)
+// Many rows of whole 16-byte chunks, a block a row at a time, a thread the same
+// kP chunks of each (kFull: all of them in the row).  One thread keeps bulk copies
+// of the next rows under way into a ring of shared memory; a stage is free again
+// at the barrier of its row's sums, as every thread then holds its chunks of it, x
+// as fp32 values.  (bf16, 8192 x 7168: unpacked for each use 79.6 us, two rows at a
+// time so that they share a barrier 77.9; layer form 102.3 and 96.1.)
+//
+// The layer form takes its sums about a pivot P, the mean of the row's first 32
+// values:
+//   mean(s - P) = m, mu = P + m, mean (s - mu)^2 = mean (s - P)^2 - m^2,
+//   sum g (s - mu) = sum g (s - P) - m sum g
+// which needs one reduction (77.1 us) and not two (83.4).  32 values are off the
+// mean by at most sqrt(d / 32) standard deviations, whatever the row, as their
+// squares cannot exceed the row's; so m^2 is at most d / 32 variances, and taking it
+// off costs no more than that many roundings, which is what a sum of d in 32 lanes
+// may cost in any case.  For rows like one another's values m is a fifth of a
+// standard deviation, and it costs nothing.
+template <typename T, int kP, bool kLayer, bool kRes, bool kFull>
+__global__ void __launch_bounds__(512, 1)
     norm_backward_stream_kernel(const BackwardPtrs p, float eps, int d, int64_t rows, int stages,
                                 int* status) {
   constexpr int N = 16 / sizeof(T);
   using C = Chunk<T, N>;
   using V = Vec<N>;
   extern __shared__ uint4 ring_bytes[];
-  __shared__ uint64_t full[kMaxStages];
+  __shared__ uint64_t full[kStreamStages];
   __shared__ int aborted;
   __shared__ float part[2][64];  // of sums in turn: a barrier then separates the uses of each
   pdl_wait();
   const int tid = threadIdx.x, threads = blockDim.x, chunks = d / N;
-  const C* const w = static_cast<const C*>(p.w);
   const float inv_d = 1.0f / static_cast<float>(d);
   const bool with_dh = p.dh && p.dx;
   const int tensors = 2 + kRes + with_dh;
-  const int stage_chunks = tensors * kR * chunks;
-  const int64_t groups = (rows + kR - 1) / kR;
+  const uint32_t bytes = chunks * 16u;
   if (tid == 0) {
     aborted = 0;
     for (int i = 0; i < stages; ++i) mbar_init(smem_u32(&full[i]), 1);
@@ -292,137 +302,122 @@ __global__ void __launch_bounds__(kMaxThreads, kMinBlocks)
   }
   __syncthreads();
   const uint64_t policy = l2_policy_evict_first();
-  auto fetch = [&](int64_t group, int stage) {
-    const int64_t at = group * kR * chunks;
-    const uint32_t bytes = static_cast<uint32_t>(min(static_cast<int64_t>(kR), rows - group * kR)) *
-                           chunks * 16u;
+  auto fetch = [&](int64_t row, int stage) {
     const uint32_t bar = smem_u32(&full[stage]);
-    uint32_t to = smem_u32(ring_bytes + stage * stage_chunks);
+    uint32_t to = smem_u32(ring_bytes + stage * tensors * chunks);
     mbar_arrive_expect_tx(bar, bytes * tensors);
     auto one = [&](const void* from) {
-      bulk_load(to, static_cast<const C*>(from) + at, bytes, bar, policy);
-      to += kR * chunks * 16;
+      bulk_load(to, static_cast<const C*>(from) + row * chunks, bytes, bar, policy);
+      to += bytes;
     };
     one(p.dy);
     one(p.a);
     if (kRes) one(p.r);
     if (with_dh) one(p.dh);
   };
+  int64_t row = blockIdx.x;
   if (tid == 0)
     for (int i = 0; i < stages; ++i) {
-      const int64_t g = blockIdx.x + static_cast<int64_t>(i) * gridDim.x;
-      if (g < groups) fetch(g, i);
+      const int64_t at = row + static_cast<int64_t>(i) * gridDim.x;
+      if (at < rows) fetch(at, i);
     }
 
+  auto has = [&](int j) { return kFull || tid + j * threads < chunks; };
+  C cw[kP];
   V dw[kP], db[kLayer ? kP : 1];
 #pragma unroll
   for (int j = 0; j < kP; ++j) {
     dw[j] = all<N>(0.0f);
     if constexpr (kLayer) db[j] = all<N>(0.0f);
+    if (has(j)) cw[j] = static_cast<const C*>(p.w)[tid + j * threads];
   }
   int stage = 0, turn = 0;
   uint32_t parity = 0;
-  int64_t group = blockIdx.x;
-  for (; group < groups; group += gridDim.x) {
+  for (; row < rows; row += gridDim.x) {
     if (!__all_sync(0xffffffffu,
                     mbar_wait_bounded(smem_u32(&full[stage]), parity, &aborted, status)))
       break;
-    const int live = static_cast<int>(min(static_cast<int64_t>(kR), rows - group * kR));
-    C cy[kR][kP], cs[kR][kP], cr[kRes ? kR : 1][kP], ch[kR][kP];
-    {
-      const C* from = reinterpret_cast<const C*>(ring_bytes) + stage * stage_chunks + tid;
-#pragma unroll
-      for (int r = 0; r < kR; ++r)
-#pragma unroll
-        for (int j = 0; j < kP; ++j) {
-          if (tid + j * threads >= chunks) continue;
-          const C* at = from + r * chunks + j * threads;
-          cy[r][j] = *at;
-          cs[r][j] = at[kR * chunks];
-          if constexpr (kRes) cr[r][j] = at[2 * kR * chunks];
-          if (with_dh) ch[r][j] = at[(tensors - 1) * kR * chunks];
-        }
-    }
-    auto sum = [&](int r, int j) {
-      V s = unpack(cs[r][j]);
-      if constexpr (kRes) s = add(s, unpack(cr[r][j]));
-      return s;
-    };
-    float mu[kR], mg[kR], ss[kR], gs[kR];
-    auto reduce = [&](const V (&a)[kR], const V (&b)[kR], float (&x)[kR], float (&y)[kR]) {
-      if constexpr (kR == 2) {
-        const float4 t = block_sum4(total(a[0]), total(b[0]), total(a[1]), total(b[1]), part[turn]);
-        x[0] = t.x, y[0] = t.y, x[1] = t.z, y[1] = t.w;
-      } else {
-        const float2 t = block_sum(total(a[0]), total(b[0]), part[turn]);
-        x[0] = t.x, y[0] = t.y;
-      }
-      turn ^= 1;
-    };
-    V a[kR], b[kR];
-    auto refill = [&]() {  // after the first barrier that follows the loads
-      const int64_t next = group + static_cast<int64_t>(stages) * gridDim.x;
-      if (tid == 0 && next < groups) fetch(next, stage);
-    };
-#pragma unroll
-    for (int r = 0; r < kR; ++r) a[r] = b[r] = all<N>(0.0f);
-    if constexpr (kLayer) {
-#pragma unroll
-      for (int j = 0; j < kP; ++j) {
-        if (tid + j * threads >= chunks) continue;
-        const V g = unpack(w[tid + j * threads]);
-#pragma unroll
-        for (int r = 0; r < kR; ++r) {
-          a[r] = add(a[r], sum(r, j));
-          b[r] = fma(unpack(cy[r][j]), g, b[r]);
-        }
-      }
-      reduce(a, b, mu, mg);
-      refill();
-#pragma unroll
-      for (int r = 0; r < kR; ++r) {
-        mu[r] *= -inv_d;
-        mg[r] *= inv_d;
-        a[r] = b[r] = all<N>(0.0f);
-      }
-    }
+    C cy[kP], ch[kP];
+    V vs[kP], vy[kLayer ? 1 : kP];
+    const C* from = reinterpret_cast<const C*>(ring_bytes) + stage * tensors * chunks + tid;
 #pragma unroll
     for (int j = 0; j < kP; ++j) {
-      if (tid + j * threads >= chunks) continue;
-      const V g = unpack(w[tid + j * threads]);
-#pragma unroll
-      for (int r = 0; r < kR; ++r) {
-        V s = sum(r, j);
-        if constexpr (kLayer) s = add(s, all<N>(mu[r]));
-        a[r] = fma(s, s, a[r]);
-        b[r] = fma(mul(unpack(cy[r][j]), g), s, b[r]);
-      }
+      if (!has(j)) continue;
+      const C* at = from + j * threads;
+      cy[j] = *at;
+      vs[j] = unpack(at[chunks]);
+      if constexpr (kRes) vs[j] = add(vs[j], unpack(at[2 * chunks]));
+      if constexpr (!kLayer) vy[j] = unpack(cy[j]);
+      if (with_dh) ch[j] = at[(tensors - 1) * chunks];
     }
-    reduce(a, b, ss, gs);
-    if constexpr (!kLayer) refill();
+    auto dy = [&](int j) {
+      if constexpr (kLayer)
+        return unpack(cy[j]);
+      else
+        return vy[j];
+    };
+    auto refill = [&]() {  // after the first barrier that follows the loads
+      const int64_t next = row + static_cast<int64_t>(stages) * gridDim.x;
+      if (tid == 0 && next < rows) fetch(next, stage);
+    };
+    float mg = 0.0f, ms, gs;
+    V a = all<N>(0.0f), b = a;
+    if constexpr (kLayer) {
+      const T* v = reinterpret_cast<const T*>(from - tid + chunks) + (tid & 31);
+      float pivot = static_cast<float>(*v);
+      if constexpr (kRes) pivot += static_cast<float>(v[d]);
 #pragma unroll
-    for (int r = 0; r < kR; ++r) {
-      if (r >= live) break;
-      const float rs = rsqrtf(ss[r] * inv_d + eps);
-      const float c = -rs * (rs * (gs[r] * inv_d));
-      const int64_t row = group * kR + r;
+      for (int o = 16; o; o >>= 1) pivot += __shfl_xor_sync(0xffffffffu, pivot, o);
+      pivot *= 1.0f / 32;
+      const V np = all<N>(-pivot);
+      V m = a, g = a;
 #pragma unroll
       for (int j = 0; j < kP; ++j) {
-        if (tid + j * threads >= chunks) continue;
-        V s = sum(r, j);
-        if constexpr (kLayer) s = add(s, all<N>(mu[r]));
-        const V y = unpack(cy[r][j]);
-        s = mul(s, all<N>(rs));
-        dw[j] = fma(y, s, dw[j]);
-        if constexpr (kLayer) db[j] = add(db[j], y);
-        if (p.dx) {
-          V v = with_dh ? unpack(ch[r][j]) : all<N>(0.0f);
-          if constexpr (kLayer) v = add(v, all<N>(-rs * mg[r]));
-          v = fma(mul(y, unpack(w[tid + j * threads])), all<N>(rs), fma(s, all<N>(c), v));
-          C out;
-          pack(v, out);
-          static_cast<C*>(p.dx)[row * chunks + tid + j * threads] = out;
-        }
+        if (!has(j)) continue;
+        const V y = mul(dy(j), unpack(cw[j]));
+        vs[j] = add(vs[j], np);
+        m = add(m, vs[j]);
+        a = fma(vs[j], vs[j], a);
+        g = add(g, y);
+        b = fma(y, vs[j], b);
+      }
+      const float4 t = block_sum4(total(a), total(b), total(m), total(g), part[turn]);
+      const float mu = t.z * inv_d;
+      mg = t.w * inv_d;
+      ms = fmaf(-mu, mu, t.x * inv_d);
+      gs = fmaf(-mu, t.w, t.y);
+      const V nm = all<N>(-mu);
+#pragma unroll
+      for (int j = 0; j < kP; ++j)
+        if (has(j)) vs[j] = add(vs[j], nm);
+    } else {
+#pragma unroll
+      for (int j = 0; j < kP; ++j) {
+        if (!has(j)) continue;
+        a = fma(vs[j], vs[j], a);
+        b = fma(mul(dy(j), unpack(cw[j])), vs[j], b);
+      }
+      const float2 t = block_sum(total(a), total(b), part[turn]);
+      ms = t.x * inv_d;
+      gs = t.y;
+    }
+    turn ^= 1;
+    refill();
+    const float rs = rsqrtf(ms + eps);
+    const V vrs = all<N>(rs), c = all<N>(-rs * (rs * (gs * inv_d))), vg = all<N>(-rs * mg);
+#pragma unroll
+    for (int j = 0; j < kP; ++j) {
+      if (!has(j)) continue;
+      const V y = dy(j), s = mul(vs[j], vrs);
+      dw[j] = fma(y, s, dw[j]);
+      if constexpr (kLayer) db[j] = add(db[j], y);
+      if (p.dx) {
+        V v = with_dh ? unpack(ch[j]) : all<N>(0.0f);
+        if constexpr (kLayer) v = add(v, vg);
+        v = fma(mul(y, unpack(cw[j])), vrs, fma(s, c, v));
+        C out;
+        pack(v, out);
+        static_cast<C*>(p.dx)[row * chunks + tid + j * threads] = out;
       }
     }
     if (++stage == stages) {
@@ -432,7 +427,7 @@ __global__ void __launch_bounds__(kMaxThreads, kMinBlocks)
   }
   // After a wait that expired: no copy of the block's may be under way at its end.
   if (tid == 0)
-    for (int i = 0; i < stages && group < groups; ++i, group += gridDim.x) {
+    for (int i = 0; i < stages && row < rows; ++i, row += gridDim.x) {
       int own = 0;
       if (!mbar_wait_bounded(smem_u32(&full[stage]), parity, &own, status)) break;
       if (++stage == stages) {
@@ -443,9 +438,9 @@ __global__ void __launch_bounds__(kMaxThreads, kMinBlocks)
   pdl_release();  // the sum of the partial rows waits for them itself
 #pragma unroll
   for (int j = 0; j < kP; ++j) {
-    const int i = tid + j * threads;
-    if (i >= chunks) continue;
+    if (!has(j)) continue;
     const int64_t at = static_cast<int64_t>(blockIdx.x) * d;
+    const int i = tid + j * threads;
     if (p.pw) reinterpret_cast<V*>(p.pw + at)[i] = dw[j];
     if constexpr (kLayer)
       if (p.pb) reinterpret_cast<V*>(p.pb + at)[i] = db[j];
@@ -760,18 +755,29 @@ cudaError_t launch_warps(const NormBackwardArgs& n, const BackwardPtrs& p, int p
 }
 
 // Blocks of an SM that share its registers and shared memory in the stream
-// kernel, for rows of d columns.
-int stream_blocks(int d) { return d > 4096 ? 1 : d > 2048 ? 2 : d > 1024 ? 4 : 8; }
+// kernel.  With rows of at most 512 columns a block is a warp: 16 of them where
+// each has at least 8 rows (57344 x 512 layer form 45.2 us, with 8 blocks 49.3; 8192
+// x 512 15.5 and 13.4).
+int stream_blocks(int64_t T, int64_t d) {
+  return d > 4096 ? 1 : d > 2048 ? 2 : d > 1024 ? 4 : d > 512 || T < 8 * 16 * 152 ? 8 : 16;
+}
 
 template <typename T, bool kLayer, bool kRes>
 cudaError_t launch_stream(const NormBackwardArgs& n, const BackwardPtrs& p, int parts,
                           cudaStream_t stream) {
-  constexpr int N = 16 / sizeof(T), kP = 16 / N, kR = sizeof(T) == 4 || kRes ? 1 : 2;
-  auto kernel = norm_backward_stream_kernel<T, kP, kR, kLayer, kRes, 512, 1>;
+  constexpr int N = 16 / sizeof(T), kP = 16 / N;
   const int chunks = n.d / N, threads = (chunks + 32 * kP - 1) / (32 * kP) * 32;
-  const int one = (2 + kRes + (p.dh && p.dx ? 1 : 0)) * kR * chunks * 16;
-  int stages = 216 * 1024 / stream_blocks(n.d) / one;
-  stages = stages < 1 ? 1 : stages > kMaxStages ? kMaxStages : stages;
+  auto kernel = threads * kP == chunks ? norm_backward_stream_kernel<T, kP, kLayer, kRes, true>
+                                       : norm_backward_stream_kernel<T, kP, kLayer, kRes, false>;
+  const int one = (2 + kRes + (p.dh && p.dx ? 1 : 0)) * chunks * 16;
+  // What is under way on an SM: 132 KB and two rows at least.  Less leaves the
+  // memory waiting, more makes reads and writes get in each other's way (8192 x 7168
+  // RMS, of 43 KB a row, two rows 75.5 us, three 73.7, four 77.6, five 80.3; 57344 x
+  // 1024, of 48 KB in eight blocks, two 75.1, three 78.8, four 84).
+  const int room = 216 * 1024 / stream_blocks(n.T, n.d) / one;
+  int stages = 132 * 1024 / stream_blocks(n.T, n.d) / one;
+  stages = stages < 2 ? 2 : stages > kStreamStages ? kStreamStages : stages;
+  if (stages > room) stages = room;
   const cudaError_t err =
       cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, 220 * 1024);
   if (err != cudaSuccess) return err;
@@ -802,12 +808,17 @@ cudaError_t two_passes(const NormBackwardArgs& n, BackwardPtrs p, cudaStream_t s
 
 // Two readings or partial rows.  A second reading of few rows that stay in L2
 // is the faster (us with it / with partial rows, bf16: layer form, 100 x 7168
-// 5.9 / 10.6, 1000 x 7168 20 / 23, 2000 x 2048 13.3 / 16.0; RMS 4.9 / 7.4, 16.2 /
-// 15.7, 12.4 / 12.0), but for short rows, a warp each (1000 x 256 6.3 / 5.4), and
-// so it is for rows without 16-byte chunks, which the bulk copies cannot take.
-// With more rows it loses (2000 x 7168 RMS 38 / 25, 8192 x 1024 33 / 15: a warp
-// of the second launch has more than 16 rows, and the tensors leave L2).
-constexpr int64_t kTwoPassRows = 1024, kTwoPassBytes = 32ll << 20;
+// 5.9 / 10.6, 1000 x 4096 12.1 / 14, 1500 x 2048 10.6 / 11.8, 1500 x 4096 16.0 / 16.0;
+// RMS 700 x 4096 8.4 / 9.6, 1000 x 2048 7.7 / 7.7), but for short rows, a warp each
+// (1000 x 256 6.3 / 5.4), and so it is for rows without 16-byte chunks, which the
+// bulk copies cannot take.  With more of them it loses (RMS 700 x 7168 12.5 / 11.0,
+// 1000 x 4096 10.7 / 9.8; layer form 2000 x 1024 10.7 / 10.0, 2000 x 4096 20.4 / 17.6,
+// fp32 1500 x 1024 9.6 / 8.0): a warp of the second launch has more rows, and the
+// tensors leave L2.
+template <typename T, bool kLayer>
+constexpr int64_t kTwoPassRows = kLayer && sizeof(T) == 2 ? 1536 : 1024;
+template <bool kLayer>
+constexpr int64_t kTwoPassBytes = (kLayer ? 24ll : 13ll) << 20;
 constexpr int kShort = 256;
 
 template <typename T, int N, bool kLayer>
@@ -820,8 +831,8 @@ cudaError_t dispatch(const NormBackwardArgs& n, cudaStream_t stream) {
       return launch_pdl(norm_backward_wide_kernel<T, W, kLayer>, dim3(static_cast<unsigned>(n.T)),
                         dim3(1024), 0, stream, q, n.eps, n.d);
     });
-  const bool few = n.T <= (n.d <= kShort ? kTwoPassRows / 4 : kTwoPassRows * (1 + kLayer)) &&
-                   2 * n.T * n.d * static_cast<int64_t>(sizeof(T)) <= kTwoPassBytes;
+  const bool few = n.T <= (n.d <= kShort ? 256 : kTwoPassRows<T, kLayer>) &&
+                   2 * n.T * n.d * static_cast<int64_t>(sizeof(T)) <= kTwoPassBytes<kLayer>;
   const bool narrow = N * sizeof(T) < 16 && n.d > kShort;
   if (!sums || few || narrow || n.d > 8192)
     return two_passes<T, N, kLayer>(n, p, stream, [&](const BackwardPtrs& q) {
@@ -838,11 +849,17 @@ cudaError_t dispatch(const NormBackwardArgs& n, cudaStream_t stream) {
       return launch_pdl(norm_backward_rows_kernel<T, N, 16 / N, kLayer, false, 1024>, rows,
                         threads(16), 0, stream, q, n.eps, n.d, n.T);
     });
-  // a block's rows from bulk copies, or a warp a row (8192 x 512 bf16: RMS 16.8
-  // and 11.2 us, layer form 20.1 and 23.0; 8192 x 1024 18.6 / 15.0, 23.6 / 28.7)
-  const bool streamed = n.d > (kLayer ? kShort : 1024);
-  const int64_t teams = streamed ? (n.T + 1) / 2 : (n.T + kRowWarps - 1) / kRowWarps;
-  const int64_t most = streamed ? 152 * stream_blocks(n.d) : kNormParts;
+  // A block's rows from bulk copies, or a warp a row (bf16 RMS, 8192 x 512 11.2 and
+  // 10.6 us, 4096 x 1024 11.1 / 10.4, 8192 x 1024 14.2 / 13.9, 16384 x 1024 21.5 / 30,
+  // 57344 x 1024 75 / 84; layer form 8192 x 512 13.4 / 23, 8192 x 1024 17 / 29).  Of
+  // short rows a block has four at least: fewer make more partial rows than pay
+  // (2500 x 512 10.3 and 9.2 us).
+  const bool streamed =
+      kLayer ? n.d > kShort
+             : n.d > 1024 ||
+                   (n.d > 512 && n.T * n.d * static_cast<int64_t>(sizeof(T)) > 16 << 20);
+  const int64_t teams = streamed ? (n.T + 3) / 4 : (n.T + kRowWarps - 1) / kRowWarps;
+  const int64_t most = streamed ? 152 * stream_blocks(n.T, n.d) : kNormParts;
   const int parts = static_cast<int>(teams < most ? teams : most);
   p.pw = n.dw ? n.partials : nullptr;
   p.pb = n.db ? n.partials + static_cast<int64_t>(parts) * n.d : nullptr;
@@ -875,7 +892,7 @@ cudaError_t dispatch_kind(const NormBackwardArgs& n, cudaStream_t stream) {
 
 int64_t norm_partial_floats(int64_t T, int64_t d) {
   if (d > 8192) return 0;  // read twice
-  const int64_t most = d > 2048 ? kNormParts : 152 * 8;  // of any of the forms
+  const int64_t blocks = 152 * stream_blocks(T, d), most = blocks < kNormParts ? kNormParts : blocks;
   return 2 * d * (T < most ? T : most);
 }
 

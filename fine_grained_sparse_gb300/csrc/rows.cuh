@@ -125,8 +125,8 @@ __device__ __forceinline__ pair fma2(pair a, pair b, pair c) {
 
 // Sums of two values over a warp, and over a block's threads; the same in all of
 // them.  The halves of a warp first exchange what the other adds up, so that a
-// round of the tree serves both values.  A `part` serves one sum at a time: with
-// a barrier between two uses of it.
+// round of the tree serves both values.  A `part`, 64 values, serves one sum at a
+// time: with a barrier between two uses of it.
 __device__ __forceinline__ float half_sums(float x, float y) {
   const bool low = (threadIdx.x & 31) < 16;
   float v = low ? x : y;
@@ -140,7 +140,7 @@ __device__ __forceinline__ float2 both_halves(float v) {
   return (threadIdx.x & 31) < 16 ? make_float2(v, other) : make_float2(other, v);
 }
 __device__ __forceinline__ float2 warp_sum(float x, float y) { return both_halves(half_sums(x, y)); }
-__device__ __forceinline__ float2 block_sum(float x, float y, float (&part)[64]) {
+__device__ __forceinline__ float2 block_sum(float x, float y, float* part) {
   const int lane = threadIdx.x & 31;
   float v = half_sums(x, y);
   // the sums of warp i at 2 i and 2 i + 1
@@ -210,14 +210,13 @@ __device__ __forceinline__ float total(const Vec<N>& a) {
   if constexpr (N == 1) {
     return a.v;
   } else {
-    float s = 0.0f;
+    pair s = a.v[0];
 #pragma unroll
-    for (int i = 0; i < Vec<N>::M; ++i) {
-      float x, y;
-      split(a.v[i], x, y);
-      s += x + y;
-    }
-    return s;
+    for (int i = 1; i < Vec<N>::M; ++i)
+      asm("add.rn.f32x2 %0, %1, %2;" : "=l"(s) : "l"(s), "l"(a.v[i]));
+    float x, y;
+    split(s, x, y);
+    return x + y;
   }
 }
 
