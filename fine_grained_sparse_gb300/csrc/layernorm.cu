@@ -2,7 +2,8 @@
 //   s_i = x_i + r_i,  mu = mean s,  v_i = w_i (s_i - mu) / sqrt(mean (s - mu)^2 + eps) + b_i
 //   h = s, y = v
 // The variance is taken from the differences to the mean, in a second pass
-// over the row's registers: sums of squares lose it where |mu| is large.
+// over the row's registers, or to a pivot near it: sums of squares lose it where
+// |mu| is large.
 // Bound by HBM for many rows (each input read once, each output written
 // once) and by latency for few.
 #include "common.cuh"
@@ -110,6 +111,126 @@ __global__ void __launch_bounds__(kMaxThreads, kMinBlocks)
   }
 }
 
+// Many rows that are not whole 16-byte chunks.  A block's rows are a multiple of N
+// apart, so that each begins at the same value of its first chunk: the block holds
+// the weights for that shift, reads the chunks that a row reaches into, the next
+// row's while it works on one, and clears what there belongs to the rows beside it.
+// The sums are taken about a pivot, the mean of the row's first 32 values (at most
+// sqrt(d / 32) standard deviations off the mean, whatever the row):
+//   mu = pivot + m, m = mean(s - pivot), variance = mean (s - pivot)^2 - m^2
+// 8192 x 7001 bf16 with a residual 105 us, 4.4 TB/s, by single values 231; 16384 x
+// 1001 32.7 and 55.7; 4096 x 7001 fp32 103 and 204.
+template <typename T, int kP, int kMaxThreads, int kMinBlocks>
+__global__ void __launch_bounds__(kMaxThreads, kMinBlocks)
+    add_layernorm_shift_kernel(const LayerNormArgs p) {
+  constexpr int N = 16 / sizeof(T);
+  using C = Chunk<T, N>;
+  using V = Vec<N>;
+  __shared__ float part[2][64];  // of sums in turn
+  pdl_wait();
+  const int tid = threadIdx.x, threads = blockDim.x, d = p.d;
+  const int shift = static_cast<int>(blockIdx.x * static_cast<int64_t>(d) % N);
+  const int chunks = (shift + d + N - 1) / N;
+  const float inv_d = 1.0f / static_cast<float>(d);
+  auto edge = [&](int j, int& lo, int& hi) {
+    const int c = tid + j * threads;
+    lo = c ? 0 : shift, hi = min(N, shift + d - c * N);
+    return hi - lo < N;
+  };
+  // the weights and two rows; a thread's chunks, which it alone reads (in
+  // registers the weights would be kept as fp32 values)
+  extern __shared__ uint4 ring[];
+  const int tensors = p.r ? 2 : 1;
+  auto slot = [&](int stage, int t, int j) {
+    return reinterpret_cast<C*>(ring) + ((2 + stage * tensors + t) * kP + j) * threads + tid;
+  };
+  auto weight = [&](int t, int j) { return reinterpret_cast<C*>(ring) + (t * kP + j) * threads + tid; };
+#pragma unroll
+  for (int j = 0; j < kP; ++j) {
+    const int at = (tid + j * threads) * N - shift;
+    *weight(0, j) = gather<T, N>(static_cast<const T*>(p.w), at, d);
+    *weight(1, j) = gather<T, N>(static_cast<const T*>(p.b), at, p.b ? d : 0);
+  }
+  float first = 0.0f;
+  auto fetch = [&](int64_t row, int stage) {
+    const int64_t at = row * d / N;
+    // the last row's last chunk may reach past the tensors' end
+    const bool cut = row == p.T - 1 && p.T * d % N;
+    auto one = [&](const void* from, int t) {
+#pragma unroll
+      for (int j = 0; j < kP; ++j) {
+        const int c = tid + j * threads;
+        if (c >= chunks) continue;
+        if (cut && c == chunks - 1) {
+          const int at = c * N - shift;
+#pragma unroll 1
+          for (int k = 0; at + k < d; ++k)
+            reinterpret_cast<T*>(slot(stage, t, j))[k] = static_cast<const T*>(from)[row * d + at + k];
+        } else
+          copy_async<16>(smem_u32(slot(stage, t, j)), static_cast<const C*>(from) + at + c);
+      }
+      first += static_cast<float>(static_cast<const T*>(from)[row * d + (tid & 31)]);
+    };
+    first = 0.0f;
+    one(p.a, 0);
+    if (p.r) one(p.r, 1);
+  };
+  int64_t row = blockIdx.x;
+  if (row < p.T) fetch(row, 0);
+  commit_copies();
+  for (int turn = 0; row < p.T; row += gridDim.x, turn ^= 1) {
+    float pivot = first;
+#pragma unroll
+    for (int o = 16; o; o >>= 1) pivot += __shfl_xor_sync(0xffffffffu, pivot, o);
+    pivot *= 1.0f / 32;
+    if (row + gridDim.x < p.T) fetch(row + gridDim.x, turn ^ 1);
+    commit_copies();
+    asm volatile("cp.async.wait_group 1;" ::: "memory");
+    V s[kP];
+#pragma unroll
+    for (int j = 0; j < kP; ++j) {
+      if (tid + j * threads >= chunks) continue;
+      s[j] = unpack(*slot(turn, 0, j));
+      if (p.r) s[j] = add(s[j], unpack(*slot(turn, 1, j)));
+    }
+    const int64_t at = row * d / N;
+    auto put = [&](void* to, int j, const V& v) {
+      C* const dst = static_cast<C*>(to) + at + tid + j * threads;
+      C out;
+      pack(v, out);
+      int lo, hi;
+      if (edge(j, lo, hi)) {
+        C* const own = slot(turn, 0, j);  // its values are in registers by now
+        *own = out;
+#pragma unroll 1
+        for (int k = lo; k < hi; ++k)
+          reinterpret_cast<T*>(dst)[k] = reinterpret_cast<const T*>(own)[k];
+      } else {
+        *dst = out;
+      }
+    };
+    V m = all<N>(0.0f), q = m;
+    const V np = all<N>(-pivot);
+#pragma unroll
+    for (int j = 0; j < kP; ++j) {
+      if (tid + j * threads >= chunks) continue;
+      if (p.h) put(p.h, j, s[j]);
+      int lo, hi;
+      if (edge(j, lo, hi)) clip(s[j], lo, hi, pivot);  // 0 to the sums
+      s[j] = add(s[j], np);
+      m = add(m, s[j]);
+      q = fma(s[j], s[j], q);
+    }
+    const float2 t = block_sum(total(m), total(q), part[turn]);
+    const float mu = t.x * inv_d;
+    const V rs = all<N>(rsqrtf(fmaf(-mu, mu, t.y * inv_d) + p.eps)), nm = all<N>(-mu);
+#pragma unroll
+    for (int j = 0; j < kP; ++j)
+      if (tid + j * threads < chunks)
+        put(p.y, j, fma(mul(add(s[j], nm), rs), unpack(*weight(0, j)), unpack(*weight(1, j))));
+  }
+}
+
 // Rows too wide for registers: a block a row, which it reads three times.
 template <typename T, int N>
 __global__ void __launch_bounds__(1024) add_layernorm_wide_kernel(const LayerNormArgs p) {
@@ -181,6 +302,23 @@ cudaError_t dispatch(const LayerNormArgs& n, int num_sms, cudaStream_t stream) {
   if (n.T < 2 * num_sms)
     return n.d <= 256 ? launch<T, N, 8 / N, 1, true, kWarps>(n, kWarps, stream)
                       : launch<T, N, 8 / N, 1, false, 1024>(n, threads(8), stream);
+  if constexpr (N == 1) {
+    // (8192 x 7002, in pairs of values, 111 us and 104 here, 16384 x 1002 30.1 and 32.6;
+    // 32768 x 501, a warp two rows, 36.8 and 52.8)
+    constexpr int kChunk = 16 / sizeof(T), kMost = sizeof(T) == 2 ? 512 : 1024;
+    const int wide = (span_chunks<kChunk>(n.d) + 63) / 64 * 32;
+    if (n.d > 512 && wide <= kMost) {
+      int64_t blocks = static_cast<int64_t>(num_sms) * (1024 / wide < 16 ? 1024 / wide : 16);
+      if (blocks > n.T) blocks = n.T;
+      auto kernel = add_layernorm_shift_kernel<T, 2, kMost, 1024 / kMost>;
+      const size_t bytes = (2 + 2 * (n.r ? 2 : 1)) * 2 * 16 * static_cast<size_t>(wide);
+      const cudaError_t err =
+          cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, 200 * 1024);
+      if (err != cudaSuccess) return err;
+      return launch_pdl(kernel, dim3(static_cast<unsigned>((blocks + 7) / 8 * 8)), dim3(wide), bytes,
+                        stream, n);
+    }
+  }
   // many rows: two at a time where bf16 makes the instructions count (8192 x 7168
   // with a residual, 470 MB: 70.1 us, the copy rate; a row a block, without pairs
   // of values, 82.3; three such blocks an SM spill, 137), one where fp32 does not

@@ -54,18 +54,6 @@ __device__ __forceinline__ Piece<T, N> row_sum(const T* a, const T* r, int64_t a
   return s;
 }
 
-// A chunk of global memory into shared memory, past the registers and L1.
-template <int kBytes>
-__device__ __forceinline__ void copy_async(uint32_t dst, const void* src) {
-  if constexpr (kBytes == 16)
-    asm volatile("cp.async.cg.shared.global [%0], [%1], 16;" ::"r"(dst), "l"(src) : "memory");
-  else
-    asm volatile("cp.async.ca.shared.global [%0], [%1], %2;" ::"r"(dst), "l"(src), "n"(kBytes)
-                 : "memory");
-}
-__device__ __forceinline__ void commit_copies() {
-  asm volatile("cp.async.commit_group;" ::: "memory");
-}
 // Wait until at most `left` (< kMaxStages) of the thread's groups of copies are
 // under way.
 constexpr int kMaxStages = 4, kStreamStages = 4;
@@ -261,8 +249,8 @@ __device__ __forceinline__ float4 block_sum4(float v0, float v1, float v2, float
                      __shfl_sync(0xffffffffu, v, 2), __shfl_sync(0xffffffffu, v, 3));
 }
 
-// Many rows of whole 16-byte chunks, a block a row at a time, a thread the same
-// kP chunks of each (kFull: all of them in the row).  One thread keeps bulk copies
+// Many rows, a block a row at a time, a thread the same kP 16-byte chunks of each
+// (kFull: all of them in the row).  One thread keeps bulk copies
 // of the next rows under way into a ring of shared memory; a stage is free again
 // at the barrier of its row's sums, as every thread then holds its chunks of it, x
 // as fp32 values.  (bf16, 8192 x 7168: unpacked for each use 79.6 us, two rows at a
@@ -278,7 +266,14 @@ __device__ __forceinline__ float4 block_sum4(float v0, float v1, float v2, float
 // off costs no more than that many roundings, which is what a sum of d in 32 lanes
 // may cost in any case.  For rows like one another's values m is a fifth of a
 // standard deviation, and it costs nothing.
-template <typename T, int kP, bool kLayer, bool kRes, bool kFull>
+//
+// kShift: rows that are not whole chunks begin inside one.  A block's rows are a
+// multiple of N apart, so that all of them begin at the same value of their first
+// chunk: the block holds the weights and sums for that shift, copies the chunks that
+// the row reaches into, and clears what there belongs to the rows beside it.
+// (8192 x 7001 bf16 RMS 77.8 us, layer form 104; from two readings of single values
+// 246 and 264.)
+template <typename T, int kP, bool kLayer, bool kRes, bool kFull, bool kShift>
 __global__ void __launch_bounds__(512, 1)
     norm_backward_stream_kernel(const BackwardPtrs p, float eps, int d, int64_t rows, int stages,
                                 int* status) {
@@ -290,11 +285,24 @@ __global__ void __launch_bounds__(512, 1)
   __shared__ int aborted;
   __shared__ float part[2][64];  // of sums in turn: a barrier then separates the uses of each
   pdl_wait();
-  const int tid = threadIdx.x, threads = blockDim.x, chunks = d / N;
+  const int tid = threadIdx.x, threads = blockDim.x;
+  // values before the row in its first chunk, the chunks it reaches into, and the
+  // most that any row does
+  const int shift = kShift ? static_cast<int>(blockIdx.x * static_cast<int64_t>(d) % N) : 0;
+  const int chunks = kShift ? (shift + d + N - 1) / N : d / N;
+  const int pitch = kShift ? span_chunks<N>(d) : chunks;
+  auto chunk_of = [&](int64_t row) { return kShift ? row * d / N : row * chunks; };
+  // the last row's last chunk may reach past the tensor's end
+  auto cut = [&](int64_t row) { return kShift && row == rows - 1 && rows * d % N; };
+  // the values of chunk j that are the row's, where they are not all
+  auto edge = [&](int j, int& lo, int& hi) {
+    const int c = tid + j * threads;
+    lo = c ? 0 : shift, hi = min(N, shift + d - c * N);
+    return kShift && hi - lo < N;
+  };
   const float inv_d = 1.0f / static_cast<float>(d);
   const bool with_dh = p.dh && p.dx;
   const int tensors = 2 + kRes + with_dh;
-  const uint32_t bytes = chunks * 16u;
   if (tid == 0) {
     aborted = 0;
     for (int i = 0; i < stages; ++i) mbar_init(smem_u32(&full[i]), 1);
@@ -304,11 +312,13 @@ __global__ void __launch_bounds__(512, 1)
   const uint64_t policy = l2_policy_evict_first();
   auto fetch = [&](int64_t row, int stage) {
     const uint32_t bar = smem_u32(&full[stage]);
-    uint32_t to = smem_u32(ring_bytes + stage * tensors * chunks);
+    uint32_t to = smem_u32(ring_bytes + stage * tensors * pitch);
+    const uint32_t bytes = (chunks - cut(row)) * 16u;
+    const int64_t at = chunk_of(row);
     mbar_arrive_expect_tx(bar, bytes * tensors);
     auto one = [&](const void* from) {
-      bulk_load(to, static_cast<const C*>(from) + row * chunks, bytes, bar, policy);
-      to += bytes;
+      bulk_load(to, static_cast<const C*>(from) + at, bytes, bar, policy);
+      to += pitch * 16u;
     };
     one(p.dy);
     one(p.a);
@@ -329,7 +339,11 @@ __global__ void __launch_bounds__(512, 1)
   for (int j = 0; j < kP; ++j) {
     dw[j] = all<N>(0.0f);
     if constexpr (kLayer) db[j] = all<N>(0.0f);
-    if (has(j)) cw[j] = static_cast<const C*>(p.w)[tid + j * threads];
+    if (!has(j)) continue;
+    if constexpr (kShift)
+      cw[j] = gather<T, N>(static_cast<const T*>(p.w), (tid + j * threads) * N - shift, d);
+    else
+      cw[j] = static_cast<const C*>(p.w)[tid + j * threads];
   }
   int stage = 0, turn = 0;
   uint32_t parity = 0;
@@ -339,16 +353,44 @@ __global__ void __launch_bounds__(512, 1)
       break;
     C cy[kP], ch[kP];
     V vs[kP], vy[kLayer ? 1 : kP];
-    const C* from = reinterpret_cast<const C*>(ring_bytes) + stage * tensors * chunks + tid;
+    C* const base = reinterpret_cast<C*>(ring_bytes) + stage * tensors * pitch;
+    if (cut(row)) {
+      const int have = (chunks - 1) * N;
+      const int64_t at = rows * d - (shift + d - have) + tid;
+      auto one = [&](const void* src, int t) {
+        if (tid < shift + d - have)
+          reinterpret_cast<T*>(base + t * pitch)[have + tid] = static_cast<const T*>(src)[at];
+      };
+      one(p.dy, 0);
+      one(p.a, 1);
+      if (kRes) one(p.r, 2);
+      if (with_dh) one(p.dh, tensors - 1);
+      __syncthreads();
+    }
+    float pivot = 0.0f;
+    if constexpr (kLayer) {
+      const T* v = reinterpret_cast<const T*>(base + pitch) + shift + (tid & 31);
+      pivot = static_cast<float>(*v);
+      if constexpr (kRes) pivot += static_cast<float>(v[pitch * N]);
+#pragma unroll
+      for (int o = 16; o; o >>= 1) pivot += __shfl_xor_sync(0xffffffffu, pivot, o);
+      pivot *= 1.0f / 32;
+    }
+    const C* from = base + tid;
 #pragma unroll
     for (int j = 0; j < kP; ++j) {
       if (!has(j)) continue;
       const C* at = from + j * threads;
       cy[j] = *at;
-      vs[j] = unpack(at[chunks]);
-      if constexpr (kRes) vs[j] = add(vs[j], unpack(at[2 * chunks]));
+      vs[j] = unpack(at[pitch]);
+      if constexpr (kRes) vs[j] = add(vs[j], unpack(at[2 * pitch]));
+      if (with_dh) ch[j] = at[(tensors - 1) * pitch];
+      int lo, hi;
+      if (edge(j, lo, hi)) {
+        clip(cy[j], lo, hi);
+        clip(vs[j], lo, hi, pivot);  // 0 to the sums
+      }
       if constexpr (!kLayer) vy[j] = unpack(cy[j]);
-      if (with_dh) ch[j] = at[(tensors - 1) * chunks];
     }
     auto dy = [&](int j) {
       if constexpr (kLayer)
@@ -363,12 +405,6 @@ __global__ void __launch_bounds__(512, 1)
     float mg = 0.0f, ms, gs;
     V a = all<N>(0.0f), b = a;
     if constexpr (kLayer) {
-      const T* v = reinterpret_cast<const T*>(from - tid + chunks) + (tid & 31);
-      float pivot = static_cast<float>(*v);
-      if constexpr (kRes) pivot += static_cast<float>(v[d]);
-#pragma unroll
-      for (int o = 16; o; o >>= 1) pivot += __shfl_xor_sync(0xffffffffu, pivot, o);
-      pivot *= 1.0f / 32;
       const V np = all<N>(-pivot);
       V m = a, g = a;
 #pragma unroll
@@ -415,9 +451,15 @@ __global__ void __launch_bounds__(512, 1)
         V v = with_dh ? unpack(ch[j]) : all<N>(0.0f);
         if constexpr (kLayer) v = add(v, vg);
         v = fma(mul(y, unpack(cw[j])), vrs, fma(s, c, v));
-        C out;
-        pack(v, out);
-        static_cast<C*>(p.dx)[row * chunks + tid + j * threads] = out;
+        C* const to = static_cast<C*>(p.dx) + chunk_of(row) + tid + j * threads;
+        int lo, hi;
+        if (edge(j, lo, hi)) {
+          store_part(reinterpret_cast<T*>(to), v, lo, hi);
+        } else {
+          C out;
+          pack(v, out);
+          *to = out;
+        }
       }
     }
     if (++stage == stages) {
@@ -441,9 +483,17 @@ __global__ void __launch_bounds__(512, 1)
     if (!has(j)) continue;
     const int64_t at = static_cast<int64_t>(blockIdx.x) * d;
     const int i = tid + j * threads;
-    if (p.pw) reinterpret_cast<V*>(p.pw + at)[i] = dw[j];
+    auto write = [&](float* to, const V& v) {
+      int lo = 0, hi = N;
+      edge(j, lo, hi);
+      if constexpr (kShift)
+        store_part(to + at + i * N - shift, v, lo, hi);
+      else
+        reinterpret_cast<V*>(to + at)[i] = v;
+    };
+    if (p.pw) write(p.pw, dw[j]);
     if constexpr (kLayer)
-      if (p.pb) reinterpret_cast<V*>(p.pb + at)[i] = db[j];
+      if (p.pb) write(p.pb, db[j]);
   }
 }
 
@@ -762,13 +812,15 @@ int stream_blocks(int64_t T, int64_t d) {
   return d > 4096 ? 1 : d > 2048 ? 2 : d > 1024 ? 4 : d > 512 || T < 8 * 16 * 152 ? 8 : 16;
 }
 
-template <typename T, bool kLayer, bool kRes>
+template <typename T, bool kLayer, bool kRes, bool kShift>
 cudaError_t launch_stream(const NormBackwardArgs& n, const BackwardPtrs& p, int parts,
                           cudaStream_t stream) {
   constexpr int N = 16 / sizeof(T), kP = 16 / N;
-  const int chunks = n.d / N, threads = (chunks + 32 * kP - 1) / (32 * kP) * 32;
-  auto kernel = threads * kP == chunks ? norm_backward_stream_kernel<T, kP, kLayer, kRes, true>
-                                       : norm_backward_stream_kernel<T, kP, kLayer, kRes, false>;
+  const int chunks = kShift ? span_chunks<N>(n.d) : n.d / N;
+  const int threads = (chunks + 32 * kP - 1) / (32 * kP) * 32;
+  auto kernel = norm_backward_stream_kernel<T, kP, kLayer, kRes, false, kShift>;
+  if (!kShift && threads * kP == chunks)
+    kernel = norm_backward_stream_kernel<T, kP, kLayer, kRes, !kShift, kShift>;
   const int one = (2 + kRes + (p.dh && p.dx ? 1 : 0)) * chunks * 16;
   // What is under way on an SM: 132 KB and two rows at least.  Less leaves the
   // memory waiting, more makes reads and writes get in each other's way (8192 x 7168
@@ -810,13 +862,16 @@ cudaError_t two_passes(const NormBackwardArgs& n, BackwardPtrs p, cudaStream_t s
 // is the faster (us with it / with partial rows, bf16: layer form, 100 x 7168
 // 5.9 / 10.6, 1000 x 4096 12.1 / 14, 1500 x 2048 10.6 / 11.8, 1500 x 4096 16.0 / 16.0;
 // RMS 700 x 4096 8.4 / 9.6, 1000 x 2048 7.7 / 7.7), but for short rows, a warp each
-// (1000 x 256 6.3 / 5.4), and so it is for rows without 16-byte chunks, which the
-// bulk copies cannot take.  With more of them it loses (RMS 700 x 7168 12.5 / 11.0,
+// (1000 x 256 6.3 / 5.4).  With more of them it loses (RMS 700 x 7168 12.5 / 11.0,
 // 1000 x 4096 10.7 / 9.8; layer form 2000 x 1024 10.7 / 10.0, 2000 x 4096 20.4 / 17.6,
 // fp32 1500 x 1024 9.6 / 8.0): a warp of the second launch has more rows, and the
 // tensors leave L2.
-template <typename T, bool kLayer>
-constexpr int64_t kTwoPassRows = kLayer && sizeof(T) == 2 ? 1536 : 1024;
+// Rows of no whole chunks take more of them (2000 x 1001 layer form 10.9 / 13.6, RMS
+// 10.1 / 11.1, 3000 x 1001 14.5 / 14.2 and 13.4 / 11.7).
+template <typename T, int N, bool kLayer>
+constexpr int64_t kTwoPassRows = N * sizeof(T) < 16    ? (kLayer ? 3000 : 2048)
+                                 : kLayer && sizeof(T) == 2 ? 1536
+                                                            : 1024;
 template <bool kLayer>
 constexpr int64_t kTwoPassBytes = (kLayer ? 24ll : 13ll) << 20;
 constexpr int kShort = 256;
@@ -831,10 +886,12 @@ cudaError_t dispatch(const NormBackwardArgs& n, cudaStream_t stream) {
       return launch_pdl(norm_backward_wide_kernel<T, W, kLayer>, dim3(static_cast<unsigned>(n.T)),
                         dim3(1024), 0, stream, q, n.eps, n.d);
     });
-  const bool few = n.T <= (n.d <= kShort ? 256 : kTwoPassRows<T, kLayer>) &&
+  constexpr bool kShift = N * sizeof(T) < 16;
+  const bool few = n.T <= (n.d <= kShort ? 256 : kTwoPassRows<T, N, kLayer>) &&
                    2 * n.T * n.d * static_cast<int64_t>(sizeof(T)) <= kTwoPassBytes<kLayer>;
-  const bool narrow = N * sizeof(T) < 16 && n.d > kShort;
-  if (!sums || few || narrow || n.d > 8192)
+  // rows of no whole chunks are streamed up to the kernel's 512 threads
+  const int most_d = kShift ? 8192 - 2 * 16 / static_cast<int>(sizeof(T)) : 8192;
+  if (!sums || few || n.d > most_d)
     return two_passes<T, N, kLayer>(n, p, stream, [&](const BackwardPtrs& q) {
       // threads of a row with at most Q values each
       auto threads = [&](int Q) { return dim3((n.d + 32 * Q - 1) / (32 * Q) * 32); };
@@ -855,21 +912,23 @@ cudaError_t dispatch(const NormBackwardArgs& n, cudaStream_t stream) {
   // short rows a block has four at least: fewer make more partial rows than pay
   // (2500 x 512 10.3 and 9.2 us).
   const bool streamed =
-      kLayer ? n.d > kShort
+      kLayer || kShift ? n.d > kShort
              : n.d > 1024 ||
                    (n.d > 512 && n.T * n.d * static_cast<int64_t>(sizeof(T)) > 16 << 20);
   const int64_t teams = streamed ? (n.T + 3) / 4 : (n.T + kRowWarps - 1) / kRowWarps;
   const int64_t most = streamed ? 152 * stream_blocks(n.T, n.d) : kNormParts;
-  const int parts = static_cast<int>(teams < most ? teams : most);
+  int parts = static_cast<int>(teams < most ? teams : most);
+  if (kShift && streamed) parts = (parts + 7) / 8 * 8;  // `most` is a multiple of 8
   p.pw = n.dw ? n.partials : nullptr;
   p.pb = n.db ? n.partials + static_cast<int64_t>(parts) * n.d : nullptr;
   cudaError_t err = cudaSuccess;
   if (n.d <= kShort) {
     err = launch_warps<T, N, 8 / N, kLayer, 2>(n, p, parts, stream);
-  } else if constexpr (N * sizeof(T) == 16) {
-    err = !streamed ? launch_warps<T, N, 32 / N, kLayer, 1>(n, p, parts, stream)
-          : n.r     ? launch_stream<T, kLayer, true>(n, p, parts, stream)
-                    : launch_stream<T, kLayer, false>(n, p, parts, stream);
+  } else if (!streamed) {
+    if constexpr (!kShift) err = launch_warps<T, N, 32 / N, kLayer, 1>(n, p, parts, stream);
+  } else {
+    err = n.r ? launch_stream<T, kLayer, true, kShift>(n, p, parts, stream)
+              : launch_stream<T, kLayer, false, kShift>(n, p, parts, stream);
   }
   if (err != cudaSuccess) return err;
   const float *pw = p.pw, *pb = p.pb;

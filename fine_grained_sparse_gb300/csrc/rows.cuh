@@ -269,4 +269,65 @@ __device__ __forceinline__ void pack(const Vec<4>& v, Chunk<float, 4>& c) {
 }
 __device__ __forceinline__ void pack(const Vec<1>& v, Chunk<float, 1>& c) { c.u = v.v; }
 
+// A chunk of global memory into shared memory, past the registers and L1.
+template <int kBytes>
+__device__ __forceinline__ void copy_async(uint32_t dst, const void* src) {
+  if constexpr (kBytes == 16)
+    asm volatile("cp.async.cg.shared.global [%0], [%1], 16;" ::"r"(dst), "l"(src) : "memory");
+  else
+    asm volatile("cp.async.ca.shared.global [%0], [%1], %2;" ::"r"(dst), "l"(src), "n"(kBytes)
+                 : "memory");
+}
+__device__ __forceinline__ void commit_copies() {
+  asm volatile("cp.async.commit_group;" ::: "memory");
+}
+
+// Rows that begin inside a chunk.  Chunks that a row of d values reaches into at
+// most:
+template <int N>
+__host__ __device__ constexpr int span_chunks(int d) {
+  return (d + 2 * N - 2) / N;
+}
+// w[at] .. w[at + N - 1], 0 outside [0, d).
+template <typename T, int N>
+__device__ __forceinline__ Chunk<T, N> gather(const T* w, int at, int d) {
+  Vec<N> v;
+  float x[N];
+#pragma unroll
+  for (int k = 0; k < N; ++k)
+    x[k] = at + k >= 0 && at + k < d ? static_cast<float>(w[at + k]) : 0.0f;
+#pragma unroll
+  for (int k = 0; k < N; k += 2) v.v[k / 2] = make_pair2(x[k], x[k + 1]);
+  Chunk<T, N> c;
+  pack(v, c);
+  return c;
+}
+// `to` in place of the values outside [lo, hi), whatever they are.
+template <int N>
+__device__ __forceinline__ void clip(Vec<N>& v, int lo, int hi, float to) {
+#pragma unroll
+  for (int k = 0; k < N; k += 2) {
+    float a, b;
+    split(v.v[k / 2], a, b);
+    v.v[k / 2] = make_pair2(k >= lo && k < hi ? a : to, k + 1 >= lo && k + 1 < hi ? b : to);
+  }
+}
+template <typename T, int N>
+__device__ __forceinline__ void clip(Chunk<T, N>& c, int lo, int hi) {
+  Vec<N> v = unpack(c);
+  clip(v, lo, hi, 0.0f);
+  pack(v, c);
+}
+template <typename T, int N>
+__device__ __forceinline__ void store_part(T* to, const Vec<N>& v, int lo, int hi) {
+#pragma unroll
+  for (int k = 0; k < N; k += 2) {
+    float a, b;
+    split(v.v[k / 2], a, b);
+    const float x[1] = {a}, y[1] = {b};
+    if (k >= lo && k < hi) store<1>(to + k, x);
+    if (k + 1 >= lo && k + 1 < hi) store<1>(to + k + 1, y);
+  }
+}
+
 }  // namespace fgs

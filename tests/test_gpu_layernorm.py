@@ -76,6 +76,31 @@ def test_forward(T, d, dtype, residual, bias, h):
     _check_forward(dtype, x, r, w, b, *_forward(fgs, dtype, x, r, w, b, h=h))
 
 
+@pytest.mark.parametrize("T,d,dtype", [(1601, 257, "bf16"), (1600, 262, "bf16"), (1001, 1001, "bf16"),
+                                       (700, 1002, "bf16"), (401, 1001, "f32"), (5001, 258, "f32"),
+                                       (603, 7001, "bf16"), (305, 8175, "bf16"), (400, 8177, "bf16"),
+                                       (333, 8183, "f32"), (20001, 300, "bf16")])
+def test_forward_many_odd_rows(T, d, dtype):
+    """Rows that begin inside a 16-byte chunk, in every place of it, beside rows of
+    infinities and NaN; the last row ends where the tensors do."""
+    need_gpu()
+    fgs = lib()
+    x, r, w, b, _, _ = _inputs(T, d, dtype)
+    h, y = _forward(fgs, dtype, x, r, w, b)
+    _check_forward(dtype, x, r, w, b, h, y)
+    none = _forward(fgs, dtype, x, None, w, None, h=False)[1]
+    _check_forward(dtype, x, None, w, None, None, none)
+    xd, rd = x.cuda(), r.cuda()
+    fgs.moe_add_layernorm(_code(fgs, dtype), T, d, xd, rd, w.cuda(), b.cuda(), EPS, xd, rd)
+    assert torch.equal(xd.cpu(), h) and torch.equal(rd.cpu(), y)
+    for row in (0, 200, T - 1):
+        bad, keep = x.clone(), torch.arange(T) != row
+        bad[row] = float("nan") if row else float("inf")
+        h1, y1 = _forward(fgs, dtype, bad, r, w, b)
+        assert torch.equal(h1[keep], h[keep]) and torch.equal(y1[keep], y[keep])
+        assert y1[row].isnan().all()
+
+
 @pytest.mark.parametrize("d", [64, 1000, 7168, 20000])
 def test_forward_large_mean(d):
     """Rows whose mean is a thousand times their spread: sums of squares would
@@ -225,6 +250,50 @@ def test_backward_in_place(d, kind):
         got = _backward(fgs, kind, "bf16", t[0], t[1], w, t[2], t[3], dx=t[at])
         for name in full:
             assert full[name] is None or torch.equal(got[name], full[name])
+
+
+ODD = [(3001, 257, "bf16"), (3002, 262, "bf16"), (3007, 1001, "bf16"), (3003, 1002, "bf16"),
+       (3005, 1001, "f32"), (3010, 258, "f32"), (3004, 3333, "bf16"), (1603, 7001, "bf16"),
+       (1540, 8175, "bf16"), (1540, 8177, "bf16"), (1029, 8183, "f32"), (400, 8003, "f32"),
+       (2000, 1001, "bf16"), (20001, 300, "bf16"), (19503, 301, "bf16")]
+
+
+@pytest.mark.parametrize("kind", ["rms", "layer"])
+@pytest.mark.parametrize("residual,dh", [(False, True), (True, False)])
+@pytest.mark.parametrize("T,d,dtype", ODD)
+def test_backward_many_odd_rows(T, d, dtype, residual, dh, kind):
+    """Rows that begin inside a 16-byte chunk, in every place of it; the last row
+    ends where the tensors do."""
+    need_gpu()
+    fgs = lib()
+    x, r, w, _, dy, g = _inputs(T, d, dtype)
+    r, g = r if residual else None, g if dh else None
+    got = _backward(fgs, kind, dtype, x, r, w, dy, g)
+    _check_backward(kind, dtype, x, r, w, dy, g, got)
+    for at, src in (("dy", dy), ("x", x)):  # dx in place of an input
+        t = src.cuda()
+        again = _backward(fgs, kind, dtype, t if at == "x" else x, r, w, t if at == "dy" else dy, g,
+                          dx=t)
+        for name in got:
+            assert got[name] is None or torch.equal(got[name], again[name])
+
+
+@pytest.mark.parametrize("kind", ["rms", "layer"])
+@pytest.mark.parametrize("T,d,dtype", [(3001, 1001, "bf16"), (3006, 1002, "bf16"), (3003, 999, "f32")])
+def test_backward_odd_rows_keep_to_themselves(T, d, dtype, kind):
+    """A row of infinities and NaN stays in its own dx."""
+    need_gpu()
+    fgs = lib()
+    x, r, w, _, dy, dh = _inputs(T, d, dtype)
+    full = _backward(fgs, kind, dtype, x, r, w, dy, dh)["dx"]
+    for row in (0, 700, T - 1):
+        a = [t.clone() for t in (x, r, dy, dh)]
+        for t, v in zip(a, (float("nan"), float("inf"), float("nan"), float("inf"))):
+            t[row] = v
+        got = _backward(fgs, kind, dtype, a[0], a[1], w, a[2], a[3])["dx"]
+        keep = torch.arange(T) != row
+        assert torch.equal(got[keep], full[keep])
+        assert not got[row].isfinite().any()
 
 
 @pytest.mark.parametrize("kind", ["rms", "layer"])
