@@ -578,9 +578,11 @@ def adamw_table(tensors: Sequence[dict]) -> AdamwTable:
     ``exp_avg``, ``exp_avg_sq`` and, or None, ``master``, ``exp_avg_scale``,
     ``exp_avg_sq_scale`` (contiguous tensors on one GPU), ``n`` (param's size
     when missing) and ``weight_decay`` (0 when missing).  Raises ValueError for
-    tensors that are not contiguous, on several devices, or smaller than n."""
+    tensors that are not contiguous, on several devices, or smaller than n, and for
+    a buffer that the step would write twice or write and read as a gradient."""
     entries = (AdamwTensor * len(tensors))()
     device, keep = None, []
+    written, grads = set(), set()
     for e, t in zip(entries, tensors):
         n = t.get("n")
         e.n = n = t["param"].numel() if n is None else int(n)
@@ -597,7 +599,12 @@ def adamw_table(tensors: Sequence[dict]) -> AdamwTable:
             if x.device != device or x.numel() < need:
                 raise ValueError(f"adamw_table: {name} on {x.device} with {x.numel()} elements, "
                                  f"not on {device} with {need}")
-            setattr(e, name, x.data_ptr())
+            at = x.data_ptr()
+            if n and (at in written or (name != "grad" and at in grads)):
+                raise ValueError(f"adamw_table: {name} is a buffer that is there already")
+            if n:
+                (grads if name == "grad" else written).add(at)
+            setattr(e, name, at)
             keep.append(x)
     return AdamwTable(entries, keep)
 

@@ -583,9 +583,11 @@ size_t moe_norm_backward_workspace_size(int64_t T, int32_t d);
  *   dbias [d] fp32 out or NULL (dbias: layer norm only).
  * At least one output.  x, residual, weight, dy, dh and dx are `dtype`.  dx may
  * be x, residual, dy or dh; no other overlap is allowed.  The rows' sums are
- * taken in an order that T and d alone decide.
+ * taken in an order that the sizes, the type and which arguments are given
+ * decide, so a call repeated gives the same bits.
  *   workspace: moe_norm_backward_workspace_size(T, d) bytes, with dweight or
- *   dbias; otherwise it may be NULL. */
+ *   dbias; otherwise it may be NULL.  A bounded wait that expires is recorded in
+ *   its status word (moe_get_device_status). */
 int32_t moe_norm_backward(int32_t kind, int32_t dtype, int64_t T, int32_t d, const void* x,
                           const void* residual, const void* weight, float eps, const void* dy,
                           const void* dh, void* dx, float* dweight, float* dbias, void* workspace,

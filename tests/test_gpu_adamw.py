@@ -376,3 +376,17 @@ def test_large_tensor():
     assert np.array_equal(d["exp_avg_sq"][first:].cpu().numpy(), t["v"])
     assert np.array_equal(d["exp_avg"][first:].cpu().numpy(), t["m"])
     assert not d["param"][:first].any()
+
+
+def test_table_refuses_a_buffer_twice():
+    need_gpu()
+    fgs = lib()
+    a, b, g, m, v, m2, v2 = (torch.zeros(256, device="cuda") for _ in range(7))
+    one = dict(param=a, grad=g, exp_avg=m, exp_avg_sq=v)
+    for two in (dict(param=a, grad=g, exp_avg=m2, exp_avg_sq=v2),
+                dict(param=b, grad=g, exp_avg=m, exp_avg_sq=v2),
+                dict(param=b, grad=a, exp_avg=m2, exp_avg_sq=v2),
+                dict(param=g, grad=b, exp_avg=m2, exp_avg_sq=v2)):
+        with pytest.raises(ValueError, match="already"):
+            fgs.adamw_table([one, two])
+    assert len(fgs.adamw_table([one, dict(param=b, grad=g, exp_avg=m2, exp_avg_sq=v2)])) == 2
