@@ -260,7 +260,7 @@ __device__ __forceinline__ float4 block_sum4(float v0, float v1, float v2, float
 // values:
 //   mean(s - P) = m, mu = P + m, mean (s - mu)^2 = mean (s - P)^2 - m^2,
 //   sum g (s - mu) = sum g (s - P) - m sum g
-// which needs one reduction (77.1 us) and not two (83.4).  32 values are off the
+// which needs one reduction (77.8 us, with four rows a ring) and not two (83.4).  32 values are off the
 // mean by at most sqrt(d / 32) standard deviations, whatever the row, as their
 // squares cannot exceed the row's; so m^2 is at most d / 32 variances, and taking it
 // off costs no more than that many roundings, which is what a sum of d in 32 lanes
@@ -825,7 +825,7 @@ cudaError_t launch_stream(const NormBackwardArgs& n, const BackwardPtrs& p, int 
   // What is under way on an SM: 132 KB and two rows at least.  Less leaves the
   // memory waiting, more makes reads and writes get in each other's way (8192 x 7168
   // RMS, of 43 KB a row, two rows 75.5 us, three 73.7, four 77.6, five 80.3; 57344 x
-  // 1024, of 48 KB in eight blocks, two 75.1, three 78.8, four 84).
+  // 1024, of 48 KB in eight blocks, two 75.1, three 78.8, four 81.1).
   const int room = 216 * 1024 / stream_blocks(n.T, n.d) / one;
   int stages = 132 * 1024 / stream_blocks(n.T, n.d) / one;
   stages = stages < 2 ? 2 : stages > kStreamStages ? kStreamStages : stages;
@@ -859,8 +859,8 @@ cudaError_t two_passes(const NormBackwardArgs& n, BackwardPtrs p, cudaStream_t s
 }
 
 // Two readings or partial rows.  A second reading of few rows that stay in L2
-// is the faster (us with it / with partial rows, bf16: layer form, 100 x 7168
-// 5.9 / 10.6, 1000 x 4096 12.1 / 14, 1500 x 2048 10.6 / 11.8, 1500 x 4096 16.0 / 16.0;
+// is the faster (us with it / with partial rows, bf16: layer form, 1100 x 2048
+// 9.0 / 10.5, 1100 x 4096 13.0 / 14.1, 1500 x 2048 10.6 / 11.8, 1500 x 4096 16.0 / 16.0;
 // RMS 700 x 4096 8.4 / 9.6, 1000 x 2048 7.7 / 7.7), but for short rows, a warp each
 // (1000 x 256 6.3 / 5.4).  With more of them it loses (RMS 700 x 7168 12.5 / 11.0,
 // 1000 x 4096 10.7 / 9.8; layer form 2000 x 1024 10.7 / 10.0, 2000 x 4096 20.4 / 17.6,
@@ -908,7 +908,7 @@ cudaError_t dispatch(const NormBackwardArgs& n, cudaStream_t stream) {
     });
   // A block's rows from bulk copies, or a warp a row (bf16 RMS, 8192 x 512 11.2 and
   // 10.6 us, 4096 x 1024 11.1 / 10.4, 8192 x 1024 14.2 / 13.9, 16384 x 1024 21.5 / 30,
-  // 57344 x 1024 75 / 84; layer form 8192 x 512 13.4 / 23, 8192 x 1024 17 / 29).  Of
+  // 57344 x 1024 75 / 84; layer form 8192 x 512 13.4 / 23).  Of
   // short rows a block has four at least: fewer make more partial rows than pay
   // (2500 x 512 10.3 and 9.2 us).
   const bool streamed =
@@ -933,8 +933,8 @@ cudaError_t dispatch(const NormBackwardArgs& n, cudaStream_t stream) {
   if (err != cudaSuccess) return err;
   const float *pw = p.pw, *pb = p.pb;
   // A thread sums one column or four: with few columns more blocks share the work
-  // (the whole call with one / with four, bf16 layer form, 8192 x 512 16.9 / 19.5 us,
-  // 57344 x 1024 95.4 / 98.5), with many the loads are wide (8192 x 7168 109 / 106).
+  // (bf16 layer form, 8192 x 512 2.6 us less with one, 57344 x 1024 3.1), with many
+  // the loads are wide (8192 x 7168 3 us less with four).
   constexpr int kWide = N >= 4 ? 4 : 1;
   const int C = n.d > 2048 ? kWide : 1;
   const dim3 grid(static_cast<unsigned>((n.d + 32 * C - 1) / (32 * C)), n.db ? 2 : 1);

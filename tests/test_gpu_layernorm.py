@@ -450,6 +450,47 @@ def test_forward_and_backward_captured():
             assert torch.equal(one[k], three[k]) and torch.equal(two[k], three[k])
 
 
+@pytest.mark.parametrize("kind", ["rms", "layer"])
+@pytest.mark.parametrize("T,d", [(3000, 1032), (3001, 1001), (20001, 136)])
+def test_many_rows_captured_beside_another_stream(T, d, kind):
+    """A captured call replayed on new rows while the same call runs on a second
+    stream with its own buffers."""
+    need_gpu()
+    fgs = lib()
+    x, r, w, b, dy, dh = (t.cuda() for t in _inputs(T, d, "bf16"))
+    n = fgs.moe_norm_backward_workspace_size(T, d)
+
+    def buffers():
+        e = lambda: torch.empty((T, d), dtype=torch.bfloat16, device="cuda")  # noqa: E731
+        return dict(y=e(), dx=e(), dw=torch.empty(d, device="cuda"), db=torch.empty(d, device="cuda"),
+                    ws=torch.zeros(n, dtype=torch.uint8, device="cuda"))
+
+    def step(o, stream=None):
+        fgs.moe_add_layernorm(fgs.MOE_BF16, T, d, x, r, w, b, EPS, None, o["y"], stream=stream)
+        fgs.moe_norm_backward(KIND[kind], fgs.MOE_BF16, T, d, x, r, w, EPS, dy, dh, o["dx"], o["dw"],
+                              o["db"] if kind == "layer" else None, o["ws"], n, stream=stream)
+
+    one, two, three = buffers(), buffers(), buffers()
+    step(one)
+    graph = torch.cuda.CUDAGraph()
+    torch.cuda.synchronize()
+    with torch.cuda.graph(graph):
+        step(one)
+    for t, v in zip((x, r, dy, dh), [_inputs(T, d, "bf16", 5)[i] for i in (0, 1, 4, 5)]):
+        t.copy_(v)
+    torch.cuda.synchronize()
+    side = torch.cuda.Stream()
+    for _ in range(3):
+        graph.replay()
+        step(two, side)
+    torch.cuda.synchronize()
+    step(three)
+    torch.cuda.synchronize()
+    for k in ("y", "dx", "dw") + (("db",) if kind == "layer" else ()):
+        assert torch.equal(one[k], three[k]) and torch.equal(two[k], three[k])
+    assert fgs.moe_get_device_status(one["ws"]) == 0
+
+
 def test_long_rows_offsets():
     """Elements past 2^31: rows x columns beyond 32 bits."""
     need_gpu()
