@@ -178,6 +178,7 @@ __global__ void __launch_bounds__(kMaxThreads, kMinBlocks)
   int64_t row = blockIdx.x;
   if (row < p.T) fetch(row, 0);
   commit_copies();
+  __syncthreads();  // h may be an input: no warp writes the row before all have its first values
   for (int turn = 0; row < p.T; row += gridDim.x, turn ^= 1) {
     float pivot = first;
 #pragma unroll

@@ -908,9 +908,8 @@ cudaError_t dispatch(const NormBackwardArgs& n, cudaStream_t stream) {
     });
   // A block's rows from bulk copies, or a warp a row (bf16 RMS, 8192 x 512 11.2 and
   // 10.6 us, 4096 x 1024 11.1 / 10.4, 8192 x 1024 14.2 / 13.9, 16384 x 1024 21.5 / 30,
-  // 57344 x 1024 75 / 84; layer form 8192 x 512 13.4 / 23).  Of
-  // short rows a block has four at least: fewer make more partial rows than pay
-  // (2500 x 512 10.3 and 9.2 us).
+  // 57344 x 1024 75 / 84; layer form 8192 x 512 13.4 / 23).  Of short rows a block has
+  // four at least: fewer make more partial rows than pay (2500 x 512 10.3 and 9.2 us).
   const bool streamed =
       kLayer || kShift ? n.d > kShort
              : n.d > 1024 ||

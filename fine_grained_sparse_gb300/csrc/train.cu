@@ -89,7 +89,7 @@ struct Row8<false> {
 
 // A CTA per token and kB of its pairs.  Each piece of dy is multiplied with
 // the same piece of the pairs' rows (dw, summed in fp32: over a thread's
-// pieces, the warp, the Cnum_sms) and written to their rows of dY, scaled.  dY may
+// pieces, the warp, the CTA) and written to their rows of dY, scaled.  dY may
 // be Y: an element is read before its thread writes it.
 template <bool BF16, int kB, int kThreads>
 __global__ void __launch_bounds__(kThreads) combine_backward_kernel(

@@ -101,6 +101,23 @@ def test_forward_many_odd_rows(T, d, dtype):
         assert y1[row].isnan().all()
 
 
+@pytest.mark.parametrize("T,d,dtype", [(304, 7001, "bf16"), (400, 5555, "f32"), (2432, 1001, "bf16")])
+def test_forward_odd_rows_in_place_repeats(T, d, dtype):
+    """h in place of an input whose rows' first values every warp reads: the same
+    bits each time."""
+    need_gpu()
+    fgs = lib()
+    x, r, w, b, _, _ = (t.cuda() for t in _inputs(T, d, dtype))
+    h, y = torch.empty_like(x), torch.empty_like(x)
+    fgs.moe_add_layernorm(_code(fgs, dtype), T, d, x, r, w, b, EPS, h, y)
+    for _ in range(10):
+        for first in (True, False):
+            xd, rd, out = x.clone(), r.clone(), torch.empty_like(x)
+            at = xd if first else rd
+            fgs.moe_add_layernorm(_code(fgs, dtype), T, d, xd, rd, w, b, EPS, at, out)
+            assert torch.equal(at, h) and torch.equal(out, y)
+
+
 @pytest.mark.parametrize("d", [64, 1000, 7168, 20000])
 def test_forward_large_mean(d):
     """Rows whose mean is a thousand times their spread: sums of squares would
