@@ -4,12 +4,17 @@
 //   g = grad c,  m = b1 m + (1 - b1) g,  v = b2 v + (1 - b2) g g,  r = sqrt v
 //   p = p (1 - lr wd) - (m / (r / sqrt(1 - b2^t) + eps)) lr / (1 - b1^t)
 // States in 8 bits: m and r as E4M3 codes with one fp32 scale per 128
-// elements, max / 448.  m is rounded to nearest: it moves by a tenth of g - m
-// in a step, as much as its codes are apart.  v moves by a hundredth or a
-// thousandth, which rounding to nearest would take back in every step, so r
-// goes to one of the two codes beside it with the probabilities that keep its
-// mean, by 16 random bits an element.  A root above 0 has a code above 0: of
-// two codes 0 the update m / (0 + eps) of the next step would be unbounded.
+// elements, max / 448.  v moves by a hundredth or a thousandth in a step, which
+// rounding to nearest would take back every time, so r goes to one of the two
+// codes beside it with the probabilities that keep its mean, by 16 random bits
+// an element.  A root above 0 has a code above 0: of two codes 0 the update
+// m / (0 + eps) of the next step would be unbounded.
+// m falls by (1 - b1) of itself where no gradient comes.  E4M3's normal codes are
+// at most 1/8 apart, so with b1 up to 29/32 that is 3/4 of a step or more, and
+// rounded to nearest m falls.  Its subnormal codes 1 to 4, and with a larger b1
+// normal ones too, would come back for ever, while r falls and the weight moves on
+// by m / r in every step.  So there, where nearest gives back the stored code, m
+// is rounded at random as r is.
 // Bound by HBM; the 8-bit form also by its instructions.
 #include "common.cuh"
 #include "internal.h"
@@ -204,6 +209,9 @@ __device__ __forceinline__ void quotients(float (&v)[8], float m, float scale) {
   }
 }
 
+// What tells the random bits of m from those of r.
+constexpr uint32_t kMomentBits = 0x6A09E667u;
+
 // 32 random bits from a pair's number and the tensor's key, already mixed: the
 // finaliser of MurmurHash3.
 __device__ __forceinline__ uint32_t random_bits(uint32_t h) {
@@ -223,6 +231,26 @@ __device__ __forceinline__ void random_codes(float a, float b, uint32_t h, uint3
   split(mul2(make_pair2(a, b), make_pair2(0x1p-120f, 0x1p-120f)), a, b);
   ca = max(__float_as_uint(a) * 16u + ((h << 8 & 0xffff00u) | 0x80u), 1u << 24);
   cb = max(__float_as_uint(b) * 16u + ((h >> 8 & 0xffff00u) | 0x80u), 1u << 24);
+}
+// Codes of m that nearest gave back: a byte of `code` of the magnitude of `old`'s,
+// below 8 or (may: 0) any but NaN.  They take a random code of |m| / scale instead.
+// h: the random bits' seed of the four elements' first pair.
+__device__ __forceinline__ uint32_t held_bytes(uint32_t code, uint32_t old, uint32_t may) {
+  const uint32_t t = ((code ^ old) & 0x7f7f7f7fu) | (old & may);
+  return ~(t + 0x7f7f7f7fu) & 0x80808080u;  // the top bit of a byte of t that is 0
+}
+__device__ __forceinline__ uint32_t held_codes(uint32_t code, uint32_t held, const float* q,
+                                               uint32_t h) {
+#pragma unroll
+  for (int k = 0; k < 4; ++k) {
+    const uint32_t byte = 0x7fu << 8 * k;
+    if (!(held >> 8 * k & 0x80) || (code & byte) == byte) continue;
+    const uint32_t bits = random_bits(h ^ k / 2);
+    const uint32_t noise = (k & 1 ? bits >> 8 : bits << 8) & 0xffff00u;
+    const uint32_t c = __float_as_uint(fabsf(q[k]) * 0x1p-120f) * 16u + (noise | 0x80u);
+    code = (code & ~byte) | c >> 24 << 8 * k;
+  }
+  return code;
 }
 __device__ __forceinline__ uint32_t top_bytes(uint32_t a, uint32_t b, uint32_t c, uint32_t d) {
   return __byte_perm(__byte_perm(a, b, 0x0073), __byte_perm(c, d, 0x0073), 0x5410);
@@ -265,6 +293,7 @@ __device__ __forceinline__ void step8(const AdamwTensor& t, const AdamwScalars& 
   const int64_t n = t.n;
   const int64_t block = at / kAdamwBlock;
   float p[8], g[8], m[8], v[8], r[8];
+  uint2 old;  // codes of m
   if constexpr (kFull) {
     in.g.unpack(g);
     if (t.master)
@@ -272,7 +301,8 @@ __device__ __forceinline__ void step8(const AdamwTensor& t, const AdamwScalars& 
     else
       in.p.unpack(p);
     if constexpr (k8) {
-      decode(in.mc, in.ms, m);
+      old = in.mc;
+      decode(old, in.ms, m);
       decode(in.vc, in.vs, v);
     } else {
       in.m.unpack(m);
@@ -285,7 +315,8 @@ __device__ __forceinline__ void step8(const AdamwTensor& t, const AdamwScalars& 
     else
       load_tail(static_cast<const P*>(t.param), at, n, p);
     if constexpr (k8) {
-      decode(load_codes_tail(t.m, at, n), at < n ? t.m_scale[block] : 0.0f, m);
+      old = load_codes_tail(t.m, at, n);
+      decode(old, at < n ? t.m_scale[block] : 0.0f, m);
       decode(load_codes_tail(t.v, at, n), at < n ? t.v_scale[block] : 0.0f, v);
     } else {
       load_tail(static_cast<const float*>(t.m), at, n, m);
@@ -348,12 +379,12 @@ __device__ __forceinline__ void step8(const AdamwTensor& t, const AdamwScalars& 
     const float mm = block_max(max8_nan(m)), rm = block_max(max8_nan(r));
     const float ms = __fmul_rn(mm, 1.0f / 448.0f), rs = __fmul_rn(rm, 1.0f / 448.0f);
     quotients(m, mm, ms);
+    const uint64_t j = static_cast<uint64_t>(at) >> 1;  // a multiple of 4
+    const uint32_t mixed =
+        static_cast<uint32_t>(j) ^ t.key ^ static_cast<uint32_t>(j >> 32) * 0x9E3779B9u;
     uint2 code = make_uint2(0x7f7f7f7fu, 0x7f7f7f7fu);  // NaN
     if (rm < __int_as_float(0x7f800000)) {
       quotients(r, rm, rs);
-      const uint64_t j = static_cast<uint64_t>(at) >> 1;  // a multiple of 4
-      const uint32_t mixed =
-          static_cast<uint32_t>(j) ^ t.key ^ static_cast<uint32_t>(j >> 32) * 0x9E3779B9u;
       uint32_t b[8];
 #pragma unroll
       for (int k = 0; k < 8; k += 2)
@@ -361,8 +392,13 @@ __device__ __forceinline__ void step8(const AdamwTensor& t, const AdamwScalars& 
       code.x = top_bytes(b[0], b[1], b[2], b[3]) & ~zero[0];
       code.y = top_bytes(b[4], b[5], b[6], b[7]) & ~zero[1];
     }
-    const uint2 mc = make_uint2(e4m3x2(m[0], m[1]) | e4m3x2(m[2], m[3]) << 16,
-                                e4m3x2(m[4], m[5]) | e4m3x2(m[6], m[7]) << 16);
+    uint2 mc = make_uint2(e4m3x2(m[0], m[1]) | e4m3x2(m[2], m[3]) << 16,
+                          e4m3x2(m[4], m[5]) | e4m3x2(m[6], m[7]) << 16);
+    const uint32_t hx = held_bytes(mc.x, old.x, c.held), hy = held_bytes(mc.y, old.y, c.held);
+    if ((hx | hy) && mm > 0.0f) {
+      mc.x = held_codes(mc.x, hx, m, mixed ^ kMomentBits);
+      mc.y = held_codes(mc.y, hy, m + 4, mixed ^ kMomentBits ^ 2);
+    }
     store_codes8<kFull>(t.m, at, n, mc);
     store_codes8<kFull>(t.v, at, n, code);
     if ((threadIdx.x & 15) == 0 && (kFull || at < n)) {
@@ -374,8 +410,8 @@ __device__ __forceinline__ void step8(const AdamwTensor& t, const AdamwScalars& 
 
 // kMany: kSteps steps a block, each but the first read while the one before it
 // is computed; otherwise one, in fewer registers.  352M bf16 elements with a
-// master copy and 8-bit states (5.68 GB): 896 us, 6.34 TB/s, 95% of the copy
-// rate, with 72% of the issue slots taken; without the master copy 134M take
+// master copy and 8-bit states (5.68 GB): 912 us, 6.23 TB/s, 93% of the copy
+// rate (895 without the codes of m that are rounded at random), with 72% of the issue slots taken; without the master copy 134M take
 // 338 us, 60%, bound by the instructions (about 75 an element).  With products
 // and roots one at a time instead of in pairs 938, with the library's roots and
 // quotients 1177.

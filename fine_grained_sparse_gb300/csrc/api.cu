@@ -1467,6 +1467,7 @@ int32_t moe_adamw(int32_t n_tensors, const moe_adamw_tensor* tensors_host, int32
   c.size = static_cast<float>(lr / (1.0 - std::pow(beta1, static_cast<double>(step))));
   c.nsize = -c.size;
   c.one = 1.0f;
+  c.held = beta1 > 29.0 / 32.0 ? 0u : 0x78787878u;
   c.grad_scale = grad_scale;
   for (int32_t k = 0; k < n_tensors;) {
     int count = 0;

@@ -368,6 +368,7 @@ struct AdamwScalars {
   float eps;
   float size, nsize;       // lr / (1 - beta1^t), and its negative
   float one;               // a 1 that the kernel's compiler does not know
+  uint32_t held;           // bits that a code of m which nearest may hold has not
   const float* grad_scale; // device scalar, or null
 };
 // A launch, by value: its tensors, and what the launch itself fills in, the

@@ -610,13 +610,16 @@ int32_t moe_norm_backward(int32_t kind, int32_t dtype, int64_t T, int32_t d, con
  *   state_bits 8: exp_avg holds m and exp_avg_sq holds r = sqrt(v), as E4M3
  *   codes with one fp32 scale per 128 elements, max|.| (1 / 448), value = code
  *   value * scale; zeroed buffers are the state before the first step.  The
- *   codes of m are the quotients m / scale rounded to nearest.  Those of r are
- *   rounded up with the probability of what lies above the code below, to
- *   the nearest 2^-16 (rounding to nearest would hold a slow v where it is),
+ *   codes of m are the quotients m / scale rounded to nearest, but where that
+ *   gives back the magnitude of the code that was there and this is below 8 (a
+ *   subnormal of E4M3) or beta1 > 29/32: nearest could hold such an m for ever
+ *   where no gradient comes, and it is rounded at random.  So are the codes of r
+ *   (nearest would hold a slow v where it is): |m| / scale and r / scale are rounded
+ *   up with the probability of what lies above the code below, to the nearest 2^-16,
  *   by 16 random bits an element: of h, the MurmurHash3 finaliser of j ^ key ^ (j >> 32)
- *   0x9E3779B9 in 32 bits, j the number of the element's pair in its tensor,
- *   the low half for the even element, the high for the odd; key: the upper
- *   half of the splitmix64 finaliser of seed + 0x9E3779B97F4A7C15 k, k the
+ *   0x9E3779B9 (for m: ^ 0x6A09E667) in 32 bits, j the number of the element's pair
+ *   in its tensor, the low half for the even element, the high for the odd; key: the
+ *   upper half of the splitmix64 finaliser of seed + 0x9E3779B97F4A7C15 k, k the
  *   number of the tensor in tensors_host.  A root above 0 never has code 0.  A
  *   block of 128 with a value that is not finite has NaN codes or a scale
  *   that is not finite.  Pass another seed in every step (the step's number
