@@ -115,11 +115,12 @@ __global__ void __launch_bounds__(kMaxThreads, kMinBlocks)
 // apart, so that each begins at the same value of its first chunk: the block holds
 // the weights for that shift, reads the chunks that a row reaches into, the next
 // row's while it works on one, and clears what there belongs to the rows beside it.
-// The sums are taken about a pivot, the mean of the row's first 32 values (at most
-// sqrt(d / 32) standard deviations off the mean, whatever the row):
-//   mu = pivot + m, m = mean(s - pivot), variance = mean (s - pivot)^2 - m^2
-// 8192 x 7001 bf16 with a residual 105 us, 4.4 TB/s, by single values 231; 16384 x
-// 1001 32.7 and 55.7; 4096 x 7001 fp32 103 and 204.
+// The sums are taken about a pivot, the mean of the row's first 32 values:
+//   mu = pivot + m, m = mean(s - pivot), variance v = mean (s - pivot)^2 - m^2
+// Taking m^2 off multiplies the roundings by (v + m^2) / v, up to d / 32 where the first
+// values are unlike the rest: so where m^2 exceeds v they are taken once more, about mu.
+// 8192 x 7001 bf16 with a residual 106 us, 4.3 TB/s, by single values 231; 16384 x
+// 1001 32.5 and 55.7; 4096 x 7001 fp32 106 and 204.
 template <typename T, int kP, int kMaxThreads, int kMinBlocks>
 __global__ void __launch_bounds__(kMaxThreads, kMinBlocks)
     add_layernorm_shift_kernel(const LayerNormArgs p) {
@@ -179,6 +180,7 @@ __global__ void __launch_bounds__(kMaxThreads, kMinBlocks)
   if (row < p.T) fetch(row, 0);
   commit_copies();
   __syncthreads();  // h may be an input: no warp writes the row before all have its first values
+  int sum = 0;  // the part of the next sums
   for (int turn = 0; row < p.T; row += gridDim.x, turn ^= 1) {
     float pivot = first;
 #pragma unroll
@@ -210,21 +212,34 @@ __global__ void __launch_bounds__(kMaxThreads, kMinBlocks)
         *dst = out;
       }
     };
-    V m = all<N>(0.0f), q = m;
-    const V np = all<N>(-pivot);
+    if (p.h) {
 #pragma unroll
-    for (int j = 0; j < kP; ++j) {
-      if (tid + j * threads >= chunks) continue;
-      if (p.h) put(p.h, j, s[j]);
-      int lo, hi;
-      if (edge(j, lo, hi)) clip(s[j], lo, hi, pivot);  // 0 to the sums
-      s[j] = add(s[j], np);
-      m = add(m, s[j]);
-      q = fma(s[j], s[j], q);
+      for (int j = 0; j < kP; ++j)
+        if (tid + j * threads < chunks) put(p.h, j, s[j]);
     }
-    const float2 t = block_sum(total(m), total(q), part[turn]);
-    const float mu = t.x * inv_d;
-    const V rs = all<N>(rsqrtf(fmaf(-mu, mu, t.y * inv_d) + p.eps)), nm = all<N>(-mu);
+    // s, the row, less `at`, and the sums of it and of its squares
+    auto sums = [&](float at) {
+      V m = all<N>(0.0f), q = m;
+      const V na = all<N>(-at);
+#pragma unroll
+      for (int j = 0; j < kP; ++j) {
+        if (tid + j * threads >= chunks) continue;
+        int lo, hi;
+        if (edge(j, lo, hi)) clip(s[j], lo, hi, at);  // 0 to the sums
+        s[j] = add(s[j], na);
+        m = add(m, s[j]);
+        q = fma(s[j], s[j], q);
+      }
+      sum ^= 1;
+      return block_sum(total(m), total(q), part[sum]);
+    };
+    float2 t = sums(pivot);
+    float mu = t.x * inv_d, var = fmaf(-mu, mu, t.y * inv_d);
+    if (mu * mu > var) {  // the same in all threads
+      t = sums(mu);
+      mu = t.x * inv_d, var = fmaf(-mu, mu, t.y * inv_d);
+    }
+    const V rs = all<N>(rsqrtf(var + p.eps)), nm = all<N>(-mu);
 #pragma unroll
     for (int j = 0; j < kP; ++j)
       if (tid + j * threads < chunks)

@@ -260,12 +260,12 @@ __device__ __forceinline__ float4 block_sum4(float v0, float v1, float v2, float
 // values:
 //   mean(s - P) = m, mu = P + m, mean (s - mu)^2 = mean (s - P)^2 - m^2,
 //   sum g (s - mu) = sum g (s - P) - m sum g
-// which needs one reduction (77.8 us, with four rows a ring) and not two (83.4).  32 values are off the
-// mean by at most sqrt(d / 32) standard deviations, whatever the row, as their
-// squares cannot exceed the row's; so m^2 is at most d / 32 variances, and taking it
-// off costs no more than that many roundings, which is what a sum of d in 32 lanes
-// may cost in any case.  For rows like one another's values m is a fifth of a
-// standard deviation, and it costs nothing.
+// which needs one reduction (77.8 us, with four rows a ring) and not two (83.4).
+// Taking m^2 off multiplies the roundings of the mean square by (v + m^2) / v, v the
+// variance: by 1.03 for rows like one another's values, whose m is a fifth of a
+// standard deviation, but by up to d / 32 where the first values are unlike the rest.
+// So where m^2 exceeds v the block takes the sums once more, about mu.  (s - P is off
+// by half an ulp of at most sqrt(d / 32) + |s - mu| / sigma standard deviations.)
 //
 // kShift: rows that are not whole chunks begin inside one.  A block's rows are a
 // multiple of N apart, so that all of them begin at the same value of their first
@@ -403,30 +403,47 @@ __global__ void __launch_bounds__(512, 1)
       if (tid == 0 && next < rows) fetch(next, stage);
     };
     float mg = 0.0f, ms, gs;
-    V a = all<N>(0.0f), b = a;
     if constexpr (kLayer) {
-      const V np = all<N>(-pivot);
-      V m = a, g = a;
+      // vs, the row, less `at`, and the means of it, of its squares, of g and of g vs
+      auto sums = [&](float at) {
+        const V np = all<N>(-at);
+        V m = all<N>(0.0f), g = m, p = m, q = m;
 #pragma unroll
-      for (int j = 0; j < kP; ++j) {
-        if (!has(j)) continue;
-        const V y = mul(dy(j), unpack(cw[j]));
-        vs[j] = add(vs[j], np);
-        m = add(m, vs[j]);
-        a = fma(vs[j], vs[j], a);
-        g = add(g, y);
-        b = fma(y, vs[j], b);
-      }
-      const float4 t = block_sum4(total(a), total(b), total(m), total(g), part[turn]);
-      const float mu = t.z * inv_d;
-      mg = t.w * inv_d;
+        for (int j = 0; j < kP; ++j) {
+          if (!has(j)) continue;
+          const V y = mul(dy(j), unpack(cw[j]));
+          vs[j] = add(vs[j], np);
+          m = add(m, vs[j]);
+          p = fma(vs[j], vs[j], p);
+          g = add(g, y);
+          q = fma(y, vs[j], q);
+        }
+        return block_sum4(total(p), total(q), total(m), total(g), part[turn]);
+      };
+      float4 t = sums(pivot);
+      refill();
+      float mu = t.z * inv_d;
       ms = fmaf(-mu, mu, t.x * inv_d);
+      if (mu * mu > ms) {  // the same in all threads
+        turn ^= 1;
+        // what is not the row's takes mu, for 0 to the sums
+#pragma unroll
+        for (int j = 0; j < kP; ++j) {
+          int lo, hi;
+          if (has(j) && edge(j, lo, hi)) clip(vs[j], lo, hi, mu);
+        }
+        t = sums(mu);
+        mu = t.z * inv_d;
+        ms = fmaf(-mu, mu, t.x * inv_d);
+      }
+      mg = t.w * inv_d;
       gs = fmaf(-mu, t.w, t.y);
       const V nm = all<N>(-mu);
 #pragma unroll
       for (int j = 0; j < kP; ++j)
         if (has(j)) vs[j] = add(vs[j], nm);
     } else {
+      V a = all<N>(0.0f), b = a;
 #pragma unroll
       for (int j = 0; j < kP; ++j) {
         if (!has(j)) continue;
@@ -438,7 +455,7 @@ __global__ void __launch_bounds__(512, 1)
       gs = t.y;
     }
     turn ^= 1;
-    refill();
+    if constexpr (!kLayer) refill();
     const float rs = rsqrtf(ms + eps);
     const V vrs = all<N>(rs), c = all<N>(-rs * (rs * (gs * inv_d))), vg = all<N>(-rs * mg);
 #pragma unroll
