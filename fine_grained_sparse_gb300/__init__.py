@@ -148,7 +148,9 @@ def _ptr(t) -> Optional[int]:
         return None
     try:
         return t.data_ptr()
-    except AttributeError:  # a raw pointer
+    except AttributeError:
+        if type(t) is not int:  # a raw pointer; ctypes takes strings, bytes and booleans too
+            raise
         return t
 
 
