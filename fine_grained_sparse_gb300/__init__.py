@@ -566,25 +566,32 @@ def moe_norm_backward(kind, dtype, T, d, x, residual, weight, eps, dy, dh, dx, d
 
 
 class AdamwTable:
-    """The tensors of moe_adamw, in the C layout; keeps them alive."""
+    """The tensors of moe_adamw, in the C layout; keeps them alive.  ``types``: the
+    param_dtype, grad_dtype and state_bits that they are of, None without any."""
 
-    def __init__(self, entries, tensors):
-        self.entries, self.tensors = entries, tensors
+    def __init__(self, entries, tensors, types=(None, None, None)):
+        self.entries, self.tensors, self.types = entries, tensors, types
 
     def __len__(self):
         return len(self.entries)
+
+
+_ADAMW_TYPES = {"torch.float32": MOE_F32, "torch.bfloat16": MOE_BF16}
+_ADAMW_BITS = {"torch.float32": 32, "torch.uint8": 8, "torch.float8_e4m3fn": 8}
 
 
 def adamw_table(tensors: Sequence[dict]) -> AdamwTable:
     """An AdamwTable of dicts with the fields of AdamwTensor: ``param``, ``grad``,
     ``exp_avg``, ``exp_avg_sq`` and, or None, ``master``, ``exp_avg_scale``,
     ``exp_avg_sq_scale`` (contiguous tensors on one GPU), ``n`` (param's size
-    when missing) and ``weight_decay`` (0 when missing).  Raises ValueError for
+    when missing) and ``weight_decay`` (0 when missing).  Params and gradients are
+    float32 or bfloat16, the same for all, states float32, uint8 or float8_e4m3fn,
+    the same for all, the rest float32.  Raises ValueError for other types, for
     tensors that are not contiguous, on several devices, or smaller than n, and for
-    a buffer that the step would write twice or write and read as a gradient."""
+    a buffer that overlaps one that the step writes."""
     entries = (AdamwTensor * len(tensors))()
-    device, keep = None, []
-    written, grads = set(), set()
+    device, keep, ranges = None, [], []
+    types = [None, None, None]
     for e, t in zip(entries, tensors):
         n = t.get("n")
         e.n = n = t["param"].numel() if n is None else int(n)
@@ -602,18 +609,39 @@ def adamw_table(tensors: Sequence[dict]) -> AdamwTable:
                 raise ValueError(f"adamw_table: {name} on {x.device} with {x.numel()} elements, "
                                  f"not on {device} with {need}")
             at = x.data_ptr()
-            if n and (at in written or (name != "grad" and at in grads)):
-                raise ValueError(f"adamw_table: {name} is a buffer that is there already")
-            if n:
-                (grads if name == "grad" else written).add(at)
             setattr(e, name, at)
             keep.append(x)
-    return AdamwTable(entries, keep)
+            if n <= 0:
+                continue
+            dtype, slot = str(x.dtype), {"param": 0, "grad": 1, "exp_avg": 2, "exp_avg_sq": 2}.get(name)
+            if slot is None:
+                if dtype != "torch.float32":
+                    raise ValueError(f"adamw_table: {name} is {dtype}, not torch.float32")
+            else:
+                kind = (_ADAMW_BITS if slot == 2 else _ADAMW_TYPES).get(dtype)
+                if kind is None or types[slot] not in (None, kind):
+                    raise ValueError(f"adamw_table: {name} of type {dtype}"
+                                     + ("" if kind is None else " beside others"))
+                types[slot] = kind
+            ranges.append((at, at + need * x.element_size(), name))
+    written = read = 0  # the ends of what is written, and of all, up to here
+    for at, end, name in sorted(ranges):
+        if at < written or (at < read and name != "grad"):
+            raise ValueError(f"adamw_table: {name} overlaps a buffer that is there already")
+        read = max(read, end)
+        if name != "grad":
+            written = max(written, end)
+    return AdamwTable(entries, keep, tuple(types))
 
 
 def moe_adamw(table, param_dtype, grad_dtype, state_bits, lr, beta1, beta2, eps, step,
               grad_scale=None, seed=0, stream=None):
-    """One AdamW step over the tensors of an AdamwTable."""
+    """One AdamW step over the tensors of an AdamwTable.  Raises ValueError where
+    their types are others than the call's."""
+    given = (param_dtype, grad_dtype, state_bits)
+    if table.types != given and any(a not in (None, b) for a, b in zip(table.types, given)):
+        raise ValueError(f"moe_adamw: param_dtype, grad_dtype and state_bits {given} for a table "
+                         f"of {table.types}")
     _check(lib.moe_adamw(len(table), ctypes.addressof(table.entries), param_dtype, grad_dtype,
                          state_bits, lr, beta1, beta2, eps, step, _ptr(grad_scale), seed,
                          _stream(stream)), "moe_adamw")
