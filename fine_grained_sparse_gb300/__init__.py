@@ -640,8 +640,8 @@ def moe_adamw(table, param_dtype, grad_dtype, state_bits, lr, beta1, beta2, eps,
     their types are others than the call's."""
     given = (param_dtype, grad_dtype, state_bits)
     if table.types != given and any(a not in (None, b) for a, b in zip(table.types, given)):
-        raise ValueError(f"moe_adamw: param_dtype, grad_dtype and state_bits {given} for a table "
-                         f"of {table.types}")
+        raise ValueError(f"moe_adamw: types (param_dtype, grad_dtype, state_bits) {given} for a "
+                         f"table of {table.types}")
     _check(lib.moe_adamw(len(table), ctypes.addressof(table.entries), param_dtype, grad_dtype,
                          state_bits, lr, beta1, beta2, eps, step, _ptr(grad_scale), seed,
                          _stream(stream)), "moe_adamw")
