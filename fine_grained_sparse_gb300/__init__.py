@@ -12,6 +12,7 @@ device memory and the stream); plain integers are accepted as raw pointers.
 """
 from __future__ import annotations
 
+import bisect
 import ctypes
 import os
 from typing import Optional, Sequence
@@ -567,13 +568,45 @@ def moe_norm_backward(kind, dtype, T, d, x, residual, weight, eps, dy, dh, dx, d
 
 class AdamwTable:
     """The tensors of moe_adamw, in the C layout; keeps them alive.  ``types``: the
-    param_dtype, grad_dtype and state_bits that they are of, None without any."""
+    param_dtype, grad_dtype and state_bits that they are of, None without any.
 
-    def __init__(self, entries, tensors, types=(None, None, None)):
+    The table has the buffers' addresses: gradients must stay in theirs (backward
+    into gradients that are there, ``zero_grad(set_to_none=False)``), or set_grads
+    takes the new ones before the step."""
+
+    def __init__(self, entries, tensors, types=(None, None, None), grads=(), written=()):
         self.entries, self.tensors, self.types = entries, tensors, types
+        self.grads = list(grads)
+        self._written = written  # (begin, end) of what the step writes, in order
 
     def __len__(self):
         return len(self.entries)
+
+    def set_grads(self, grads) -> None:
+        """``grads``, one for each of the table's tensors, in place of its gradients.
+        Raises ValueError for what adamw_table refuses, or for another type; the
+        table is then as it was.  Calls that were captured keep the old addresses."""
+        grads = list(grads)
+        if len(grads) != len(self.entries):
+            raise ValueError(f"set_grads: {len(grads)} gradients of {len(self.entries)} tensors")
+        device = self.tensors[0].device if self.tensors else None
+        at = []
+        for e, x in zip(self.entries, grads):
+            if e.n == 0:
+                at.append(None if x is None else x.data_ptr())
+                continue
+            if x is None or not x.is_cuda or not x.is_contiguous() or x.device != device:
+                raise ValueError(f"set_grads: not a contiguous tensor on {device}")
+            if x.numel() < e.n or _ADAMW_TYPES.get(str(x.dtype)) != self.types[1]:
+                raise ValueError(f"set_grads: {x.numel()} elements of {x.dtype} for {e.n}")
+            begin = x.data_ptr()
+            i = bisect.bisect_left(self._written, (begin + e.n * x.element_size(),))
+            if i and self._written[i - 1][1] > begin:
+                raise ValueError("set_grads: a gradient overlaps a buffer that the step writes")
+            at.append(begin)
+        for e, a in zip(self.entries, at):
+            e.grad = a
+        self.grads = grads
 
 
 _ADAMW_TYPES = {"torch.float32": MOE_F32, "torch.bfloat16": MOE_BF16}
@@ -590,12 +623,13 @@ def adamw_table(tensors: Sequence[dict]) -> AdamwTable:
     tensors that are not contiguous, on several devices, or smaller than n, and for
     a buffer that overlaps one that the step writes."""
     entries = (AdamwTensor * len(tensors))()
-    device, keep, ranges = None, [], []
+    device, keep, grads, ranges = None, [], [], []
     types = [None, None, None]
     for e, t in zip(entries, tensors):
         n = t.get("n")
         e.n = n = t["param"].numel() if n is None else int(n)
         e.weight_decay = float(t.get("weight_decay", 0.0))
+        grads.append(t.get("grad"))
         for name in ("param", "grad", "master", "exp_avg", "exp_avg_sq", "exp_avg_scale",
                      "exp_avg_sq_scale"):
             x = t.get(name)
@@ -610,7 +644,8 @@ def adamw_table(tensors: Sequence[dict]) -> AdamwTable:
                                  f"not on {device} with {need}")
             at = x.data_ptr()
             setattr(e, name, at)
-            keep.append(x)
+            if name != "grad":
+                keep.append(x)
             if n <= 0:
                 continue
             dtype, slot = str(x.dtype), {"param": 0, "grad": 1, "exp_avg": 2, "exp_avg_sq": 2}.get(name)
@@ -624,14 +659,16 @@ def adamw_table(tensors: Sequence[dict]) -> AdamwTable:
                                      + ("" if kind is None else " beside others"))
                 types[slot] = kind
             ranges.append((at, at + need * x.element_size(), name))
+    ranges.sort()
     written = read = 0  # the ends of what is written, and of all, up to here
-    for at, end, name in sorted(ranges):
+    for at, end, name in ranges:
         if at < written or (at < read and name != "grad"):
             raise ValueError(f"adamw_table: {name} overlaps a buffer that is there already")
         read = max(read, end)
         if name != "grad":
             written = max(written, end)
-    return AdamwTable(entries, keep, tuple(types))
+    return AdamwTable(entries, keep, tuple(types), grads,
+                      [(at, end) for at, end, name in ranges if name != "grad"])
 
 
 def moe_adamw(table, param_dtype, grad_dtype, state_bits, lr, beta1, beta2, eps, step,

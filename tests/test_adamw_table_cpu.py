@@ -116,3 +116,52 @@ def test_table_refuses_overlaps(fgs):
     with pytest.raises(ValueError, match="already"):
         fgs.adamw_table([_entry(bits=8, exp_avg_scale=Fake(8, at=base + 64)), _entry(
             bits=8, exp_avg_sq_scale=Fake(8, at=base + 80))])
+
+
+def test_set_grads(fgs):
+    a, b = _entry(), _entry(300)
+    t = fgs.adamw_table([a, b, _entry(0)])
+    assert [e.grad for e in t.entries][:2] == [a["grad"].at, b["grad"].at]
+    g = [Fake(1000), Fake(301), None]
+    t.set_grads(g)
+    assert [e.grad for e in t.entries] == [g[0].at, g[1].at, None]
+    assert t.grads == g and a["grad"] not in t.tensors  # the old ones are let go
+    assert [e.param for e in t.entries][:2] == [a["param"].at, b["param"].at]
+    beside = Fake(300, at=b["param"].at + 1200)
+    t.set_grads((Fake(1000), beside, None))
+    t.set_grads([beside_both := Fake(1000), beside_both, None])  # read twice
+    fgs.adamw_table([]).set_grads([])
+
+
+@pytest.mark.parametrize("bad", ["few", "many", "none", "small", "type", "cpu", "device", "strided",
+                                 "written"])
+def test_set_grads_refuses(fgs, bad):
+    a, b = _entry(), _entry(300)
+    t = fgs.adamw_table([a, b])
+    g = [Fake(1000), Fake(300)]
+    if bad == "few":
+        g.pop()
+    elif bad == "many":
+        g.append(Fake(1))
+    elif bad == "none":
+        g[1] = None
+    elif bad == "small":
+        g[1] = Fake(299)
+    elif bad == "type":
+        g[1] = Fake(600, "bfloat16")
+    elif bad == "cpu":
+        g[1].is_cuda = False
+    elif bad == "device":
+        g[1].device = "cuda:1"
+    elif bad == "strided":
+        g[1].is_contiguous = lambda: False
+    else:
+        for name in ("param", "exp_avg", "exp_avg_sq"):
+            for off in (0, 1196, -1196):
+                with pytest.raises(ValueError, match="set_grads"):
+                    t.set_grads([g[0], Fake(300, at=b[name].at + off)])
+        g[1] = Fake(300, at=a["exp_avg"].at + 2000)
+    with pytest.raises(ValueError, match="set_grads"):
+        t.set_grads(g)
+    assert [e.grad for e in t.entries] == [a["grad"].at, b["grad"].at]
+    assert t.grads == [a["grad"], b["grad"]]

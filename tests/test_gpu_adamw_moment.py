@@ -135,3 +135,29 @@ def test_untouched_blocks_stay_zero():
             _same(t, d, "f32")
         assert not t["m"][:512].any() and not t["ms"][:4].any()
         assert np.abs(_blocks(t["p"])).max() > 0
+
+
+@pytest.mark.parametrize("bits", [8, 32])
+def test_new_gradients(bits):
+    """Gradients that a backward pass made anew: the step takes them, not those that
+    the table was made with."""
+    need_gpu()
+    fgs = lib()
+    gen = torch.Generator().manual_seed(9)
+    ts = [_tensor(n, gen, "f32", "bf16", False, bits, 0.1, _key(3, k))
+          for k, n in enumerate((1000, 7, 5000))]
+    ds = [_device(t, "f32", "bf16") for t in ts]
+    table = fgs.adamw_table(ds)
+    for step in (1, 2):
+        if step == 2:
+            for t, d in zip(ts, ds):
+                t["g"] = (torch.randn(t["g"].shape, generator=gen) * 1e-3).bfloat16().float().numpy()
+                d["grad"] = torch.cat((torch.from_numpy(t["g"]).bfloat16(),
+                                       torch.full((64,), 5.0, dtype=torch.bfloat16))).cuda()
+            table.set_grads(d["grad"] for d in ds)
+        c = (1e-3, 0.9, 0.95, 1e-8, step, 1.0, 3)
+        for t in ts:
+            (_step if bits == 8 else _step32)(t, c)
+        _call(fgs, table, "f32", "bf16", bits, c, None)
+        for t, d in zip(ts, ds):
+            _same(t, d, "f32")
