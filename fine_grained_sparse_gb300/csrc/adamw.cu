@@ -135,7 +135,7 @@ __device__ __forceinline__ pair add2(pair a, float one, pair b) {
 // Square roots of values in [2^-90, 2^90], correctly rounded: from y, 1 / sqrt v
 // to 2^-22, and g = v y, a Newton step of g and the correction (v - g g) y / 2
 // (Markstein, IBM J. Res. Dev. 34, 1990); all 2^24 mantissas of both parities
-// of the exponent were compared with the exact roots.
+// of the exponent are compared with the exact roots in the tests.
 __device__ __forceinline__ pair sqrt2(pair v) {
   float a, b, ya, yb;
   split(v, a, b);
@@ -185,6 +185,17 @@ __device__ __forceinline__ float min3(float a, float b, float c) {
   asm("min.f32 %0, %1, %2, %3;" : "=f"(r) : "f"(a), "f"(b), "f"(c));
   return r;
 }
+__device__ __forceinline__ float min8(const float (&v)[8]) {  // of |v|, past NaN
+  return min3(min3(fabsf(v[0]), fabsf(v[1]), fabsf(v[2])),
+              min3(fabsf(v[3]), fabsf(v[4]), fabsf(v[5])), fminf(fabsf(v[6]), fabsf(v[7])));
+}
+// A bound of the smallest of those that are not 0, within an ulp below it; NaN if all are.
+__device__ __forceinline__ float min8_not_zero(const float (&v)[8]) {
+  uint32_t u = 0xffffffffu;
+#pragma unroll
+  for (int k = 0; k < 8; ++k) u = min(u, __float_as_uint(v[k]) * 2u - 1u);  // 0 becomes the largest
+  return __uint_as_float(u >> 1);
+}
 // The maximum over the 16 lanes that hold a block of 128.
 __device__ __forceinline__ float block_max(float m) {
 #pragma unroll
@@ -209,9 +220,6 @@ __device__ __forceinline__ void quotients(float (&v)[8], float m, float scale) {
   }
 }
 
-// What tells the random bits of m from those of r.
-constexpr uint32_t kMomentBits = 0x6A09E667u;
-
 // 32 random bits from a pair's number and the tensor's key, already mixed: the
 // finaliser of MurmurHash3.
 __device__ __forceinline__ uint32_t random_bits(uint32_t h) {
@@ -232,28 +240,27 @@ __device__ __forceinline__ void random_codes(float a, float b, uint32_t h, uint3
   ca = max(__float_as_uint(a) * 16u + ((h << 8 & 0xffff00u) | 0x80u), 1u << 24);
   cb = max(__float_as_uint(b) * 16u + ((h >> 8 & 0xffff00u) | 0x80u), 1u << 24);
 }
-// Codes of m that nearest gave back: a byte of `code` of the magnitude of `old`'s,
-// below 8 or (may: 0) any but NaN.  They take a random code of |m| / scale instead.
-// h: the random bits' seed of the four elements' first pair.
-__device__ __forceinline__ uint32_t held_bytes(uint32_t code, uint32_t old, uint32_t may) {
-  const uint32_t t = ((code ^ old) & 0x7f7f7f7fu) | (old & may);
-  return ~(t + 0x7f7f7f7fu) & 0x80808080u;  // the top bit of a byte of t that is 0
-}
-__device__ __forceinline__ uint32_t held_codes(uint32_t code, uint32_t held, const float* q,
-                                               uint32_t h) {
-#pragma unroll
-  for (int k = 0; k < 4; ++k) {
-    const uint32_t byte = 0x7fu << 8 * k;
-    if (!(held >> 8 * k & 0x80) || (code & byte) == byte) continue;
-    const uint32_t bits = random_bits(h ^ k / 2);
-    const uint32_t noise = (k & 1 ? bits >> 8 : bits << 8) & 0xffff00u;
-    const uint32_t c = __float_as_uint(fabsf(q[k]) * 0x1p-120f) * 16u + (noise | 0x80u);
-    code = (code & ~byte) | c >> 24 << 8 * k;
-  }
-  return code;
-}
 __device__ __forceinline__ uint32_t top_bytes(uint32_t a, uint32_t b, uint32_t c, uint32_t d) {
   return __byte_perm(__byte_perm(a, b, 0x0073), __byte_perm(c, d, 0x0073), 0x5410);
+}
+// Codes of m that nearest gave back, bytes of `code` of the magnitude of `old`'s below
+// 8 or (may: 0) of any, take a random code of |m| / scale, q, instead.  h: the random
+// bits of the four elements' pairs, of which an element takes the half that its
+// neighbour's r takes.
+__device__ __forceinline__ uint32_t held_codes(uint32_t code, uint32_t old, uint32_t may,
+                                               const float* q, const uint32_t* h) {
+  const uint32_t t = ((code ^ old) & 0x7f7f7f7fu) | (old & may);
+  const uint32_t held = ~(t + 0x7f7f7f7fu) & 0x80808080u;  // the top bit where a byte of t is 0
+  uint32_t c[4];
+#pragma unroll
+  for (int k = 0; k < 4; k += 2) {
+    float a, b;
+    split(mul2(make_pair2(q[k], q[k + 1]), make_pair2(0x1p-120f, 0x1p-120f)), a, b);
+    c[k] = __float_as_uint(a) * 16u + ((h[k / 2] >> 8 & 0xffff00u) | 0x80u);  // past the sign
+    c[k + 1] = __float_as_uint(b) * 16u + ((h[k / 2] << 8 & 0xffff00u) | 0x80u);
+  }
+  const uint32_t mask = (held >> 7) * 0x7fu;
+  return (code & ~mask) | (top_bytes(c[0], c[1], c[2], c[3]) & mask);
 }
 
 // What a step reads of eight elements, as it lies in memory: loaded a step
@@ -293,7 +300,6 @@ __device__ __forceinline__ void step8(const AdamwTensor& t, const AdamwScalars& 
   const int64_t n = t.n;
   const int64_t block = at / kAdamwBlock;
   float p[8], g[8], m[8], v[8], r[8];
-  uint2 old;  // codes of m
   if constexpr (kFull) {
     in.g.unpack(g);
     if (t.master)
@@ -301,8 +307,7 @@ __device__ __forceinline__ void step8(const AdamwTensor& t, const AdamwScalars& 
     else
       in.p.unpack(p);
     if constexpr (k8) {
-      old = in.mc;
-      decode(old, in.ms, m);
+      decode(in.mc, in.ms, m);
       decode(in.vc, in.vs, v);
     } else {
       in.m.unpack(m);
@@ -315,8 +320,7 @@ __device__ __forceinline__ void step8(const AdamwTensor& t, const AdamwScalars& 
     else
       load_tail(static_cast<const P*>(t.param), at, n, p);
     if constexpr (k8) {
-      old = load_codes_tail(t.m, at, n);
-      decode(old, at < n ? t.m_scale[block] : 0.0f, m);
+      decode(load_codes_tail(t.m, at, n), at < n ? t.m_scale[block] : 0.0f, m);
       decode(load_codes_tail(t.v, at, n), at < n ? t.v_scale[block] : 0.0f, v);
     } else {
       load_tail(static_cast<const float*>(t.m), at, n, m);
@@ -335,11 +339,14 @@ __device__ __forceinline__ void step8(const AdamwTensor& t, const AdamwScalars& 
     split(mm, m[k], m[k + 1]);
     split(vv, v[k], v[k + 1]);
   }
-  // v in a range where no step of the fast forms underflows or overflows
-  const float vmax = max8_nan(v);
+  // v and m in a range where no step of the fast forms underflows or overflows: the
+  // divisor is in [2^-45, 2^60] (c.vmax), so a quotient in [2^-120, 2^105] and its
+  // residual a multiple of 2^-108; an m of 0 gives 0 in any case
+  const float vmax = max8_nan(v), mmax = max8_nan(m);
+  float mmin = min8(m);
+  if (mmin == 0.0f) mmin = min8_not_zero(m);
   const bool tame =
-      min3(min3(v[0], v[1], v[2]), min3(v[3], v[4], v[5]), fminf(v[6], v[7])) >= 0x1p-90f &&
-      vmax <= 0x1p90f;
+      min8(v) >= 0x1p-90f && vmax <= c.vmax && mmax <= 0x1p60f && !(mmin < 0x1p-60f);
   uint32_t zero[2] = {0, 0};  // bytes 0xff where r is 0
   if (tame) {
 #pragma unroll
@@ -352,7 +359,7 @@ __device__ __forceinline__ void step8(const AdamwTensor& t, const AdamwScalars& 
       split(rr, r[k], r[k + 1]);
       split(q, p[k], p[k + 1]);
     }
-  } else if (vmax == 0.0f && c.eps > 0.0f && max8_nan(m) == 0.0f) {
+  } else if (vmax == 0.0f && c.eps > 0.0f && mmax == 0.0f) {
     // what no gradient has reached: 0 / eps is m's 0
 #pragma unroll
     for (int k = 0; k < 8; ++k) {
@@ -361,7 +368,7 @@ __device__ __forceinline__ void step8(const AdamwTensor& t, const AdamwScalars& 
     }
     zero[0] = zero[1] = 0xffffffffu;
   } else {
-    // v of 0, tiny, huge or not finite
+    // v or m of 0, tiny, huge or not finite
 #pragma unroll
     for (int k = 0; k < 8; ++k) {
       r[k] = __fsqrt_rn(v[k]);
@@ -376,28 +383,33 @@ __device__ __forceinline__ void step8(const AdamwTensor& t, const AdamwScalars& 
     store8<kFull>(static_cast<float*>(t.m), at, n, m);
     store8<kFull>(static_cast<float*>(t.v), at, n, v);
   } else {
-    const float mm = block_max(max8_nan(m)), rm = block_max(max8_nan(r));
+    const float mm = block_max(mmax), rm = block_max(max8_nan(r));
     const float ms = __fmul_rn(mm, 1.0f / 448.0f), rs = __fmul_rn(rm, 1.0f / 448.0f);
     quotients(m, mm, ms);
     const uint64_t j = static_cast<uint64_t>(at) >> 1;  // a multiple of 4
     const uint32_t mixed =
         static_cast<uint32_t>(j) ^ t.key ^ static_cast<uint32_t>(j >> 32) * 0x9E3779B9u;
+    uint32_t h[4];
+#pragma unroll
+    for (int k = 0; k < 4; ++k) h[k] = random_bits(mixed ^ k);
     uint2 code = make_uint2(0x7f7f7f7fu, 0x7f7f7f7fu);  // NaN
     if (rm < __int_as_float(0x7f800000)) {
       quotients(r, rm, rs);
       uint32_t b[8];
 #pragma unroll
-      for (int k = 0; k < 8; k += 2)
-        random_codes(r[k], r[k + 1], random_bits(mixed ^ k / 2), b[k], b[k + 1]);
+      for (int k = 0; k < 8; k += 2) random_codes(r[k], r[k + 1], h[k / 2], b[k], b[k + 1]);
       code.x = top_bytes(b[0], b[1], b[2], b[3]) & ~zero[0];
       code.y = top_bytes(b[4], b[5], b[6], b[7]) & ~zero[1];
     }
     uint2 mc = make_uint2(e4m3x2(m[0], m[1]) | e4m3x2(m[2], m[3]) << 16,
                           e4m3x2(m[4], m[5]) | e4m3x2(m[6], m[7]) << 16);
-    const uint32_t hx = held_bytes(mc.x, old.x, c.held), hy = held_bytes(mc.y, old.y, c.held);
-    if ((hx | hy) && mm > 0.0f) {
-      mc.x = held_codes(mc.x, hx, m, mixed ^ kMomentBits);
-      mc.y = held_codes(mc.y, hy, m + 4, mixed ^ kMomentBits ^ 2);
+    // a code below 8 is of less than 2^-6 scales (c.held_below; all may be held: inf)
+    if (mmin < c.held_below * ms && mm < __int_as_float(0x7f800000)) {
+      // the old codes are still there; read again, as kept they would cost registers
+      const uint2 old = kFull ? *reinterpret_cast<const uint2*>(static_cast<const uint8_t*>(t.m) + at)
+                              : load_codes_tail(t.m, at, n);
+      mc.x = held_codes(mc.x, old.x, c.held, m, h);
+      mc.y = held_codes(mc.y, old.y, c.held, m + 4, h + 2);
     }
     store_codes8<kFull>(t.m, at, n, mc);
     store_codes8<kFull>(t.v, at, n, code);
@@ -410,11 +422,13 @@ __device__ __forceinline__ void step8(const AdamwTensor& t, const AdamwScalars& 
 
 // kMany: kSteps steps a block, each but the first read while the one before it
 // is computed; otherwise one, in fewer registers.  352M bf16 elements with a
-// master copy and 8-bit states (5.68 GB): 912 us, 6.23 TB/s, 93% of the copy
-// rate (895 without the codes of m that are rounded at random), with 72% of the issue slots taken; without the master copy 134M take
-// 338 us, 60%, bound by the instructions (about 75 an element).  With products
-// and roots one at a time instead of in pairs 938, with the library's roots and
-// quotients 1177.
+// master copy and 8-bit states (5.68 GB): 915 us, 6.21 TB/s, 93% of the copy rate,
+// with about three quarters of the issue slots taken; without the master copy 134M
+// take 349 us, bound by the instructions (about 80 an element).  Of these the range
+// check of m and the codes that it is rounded at random are 2 to 4% (895 and 337
+// without them), and 17% with beta1 above 29/32, where every code is looked at (396).
+// With products and roots one at a time instead of in pairs 938, with the library's
+// roots and quotients 1177 (before those two).
 template <typename P, typename G, bool k8, bool kMany>
 __global__ void __launch_bounds__(kThreads, k8 && kMany ? 3 : 2)
     adamw_kernel(const __grid_constant__ AdamwGroup a) {

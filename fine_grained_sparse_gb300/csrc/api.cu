@@ -1464,10 +1464,13 @@ int32_t moe_adamw(int32_t n_tensors, const moe_adamw_tensor* tensors_host, int32
   c.ob2 = static_cast<float>(1.0 - beta2);
   c.root = static_cast<float>(1.0 / std::sqrt(1.0 - std::pow(beta2, static_cast<double>(step))));
   c.eps = static_cast<float>(eps);
+  // sqrt(v) root <= 2^59, as root < 2^27, and eps beside it
+  c.vmax = eps <= 0x1p59 ? 0x1p64f : -1.0f;
   c.size = static_cast<float>(lr / (1.0 - std::pow(beta1, static_cast<double>(step))));
   c.nsize = -c.size;
   c.one = 1.0f;
   c.held = beta1 > 29.0 / 32.0 ? 0u : 0x78787878u;
+  c.held_below = beta1 > 29.0 / 32.0 ? INFINITY : 0x1p-6f;
   c.grad_scale = grad_scale;
   for (int32_t k = 0; k < n_tensors;) {
     int count = 0;

@@ -366,9 +366,11 @@ struct AdamwScalars {
   float b1, ob1, b2, ob2;  // beta and 1 - beta
   float root;              // 1 / sqrt(1 - beta2^t)
   float eps;
+  float vmax;              // the largest v whose divisor is at most 2^60
   float size, nsize;       // lr / (1 - beta1^t), and its negative
   float one;               // a 1 that the kernel's compiler does not know
   uint32_t held;           // bits that a code of m which nearest may hold has not
+  float held_below;        // and what its value is below, in scales
   const float* grad_scale; // device scalar, or null
 };
 // A launch, by value: its tensors, and what the launch itself fills in, the

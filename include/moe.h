@@ -617,8 +617,8 @@ int32_t moe_norm_backward(int32_t kind, int32_t dtype, int64_t T, int32_t d, con
  *   (nearest would hold a slow v where it is): |m| / scale and r / scale are rounded
  *   up with the probability of what lies above the code below, to the nearest 2^-16,
  *   by 16 random bits an element: of h, the MurmurHash3 finaliser of j ^ key ^ (j >> 32)
- *   0x9E3779B9 (for m: ^ 0x6A09E667) in 32 bits, j the number of the element's pair
- *   in its tensor, the low half for the even element, the high for the odd; key: the
+ *   0x9E3779B9 in 32 bits, j the number of the element's pair in its tensor, for r
+ *   the low half for the even element and the high for the odd, for m the other; key: the
  *   upper half of the splitmix64 finaliser of seed + 0x9E3779B97F4A7C15 k, k the
  *   number of the tensor in tensors_host.  A root above 0 never has code 0.  A
  *   block of 128 with a value that is not finite has NaN codes or a scale

@@ -6,8 +6,8 @@ import pytest
 import torch
 
 from _gpu_common import lib, need_gpu
-from test_gpu_adamw import (_blocks, _call, _device, _key, _quotients, _same, _step32, _tensor,
-                            _values)
+from test_gpu_adamw import (_bits, _blocks, _call, _device, _key, _quotients, _same, _step32,
+                            _tensor, _values)
 
 pytestmark = pytest.mark.gpu
 
@@ -15,13 +15,8 @@ f32 = np.float32
 
 
 def _moment_bits(n, key):
-    """16 random bits of the first moment's elements."""
-    i = np.arange(n, dtype=np.uint64)
-    h = (i >> np.uint64(1)).astype(np.uint32) ^ np.uint32(key) ^ np.uint32(0x6A09E667)
-    h = (h ^ h >> np.uint32(16)) * np.uint32(0x85EBCA6B)
-    h = (h ^ h >> np.uint32(13)) * np.uint32(0xC2B2AE35)
-    h = h ^ h >> np.uint32(16)
-    return np.where(i & np.uint64(1), h >> np.uint32(16), h & np.uint32(0xFFFF)).astype(np.int64)
+    """16 random bits of the first moment's elements: those of the neighbour's root."""
+    return _bits(n + n % 2, key).reshape(-1, 2)[:, ::-1].reshape(-1)[:n]
 
 
 def _step(t, c):
