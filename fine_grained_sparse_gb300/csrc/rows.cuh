@@ -9,9 +9,11 @@ namespace fgs {
 
 constexpr int kRowGroup = 128;  // columns of a row with one scale
 
-// N values of a row as fp32, 16 bytes (or one value) at a time.
+// N values of a row as fp32, 16 bytes or one value at a time: load and store take
+// no other N.
 template <typename T, int N>
 struct Piece {
+  static_assert(N == 1 || N * sizeof(T) == 16, "one value or 16 bytes");
   float v[N];
 };
 
@@ -44,6 +46,7 @@ __device__ __forceinline__ Piece<float, N> load(const float* p) {
 }
 template <int N>
 __device__ __forceinline__ void store(__nv_bfloat16* p, const float (&v)[N]) {
+  static_assert(N == 1 || N == 8, "one value or 16 bytes");
   if constexpr (N == 1)
     *p = __float2bfloat16_rn(v[0]);
   else
@@ -52,6 +55,7 @@ __device__ __forceinline__ void store(__nv_bfloat16* p, const float (&v)[N]) {
 }
 template <int N>
 __device__ __forceinline__ void store(float* p, const float (&v)[N]) {
+  static_assert(N == 1 || N == 4, "one value or 16 bytes");
   if constexpr (N == 1)
     *p = v[0];
   else
