@@ -323,9 +323,10 @@ struct LayerNormArgs {
 };
 cudaError_t launch_add_layernorm(const LayerNormArgs& n, int num_sms, cudaStream_t stream);
 
-// Blocks of rows whose dweight and dbias are summed apart (two for each of a
-// GB300's 152 SMs; a fixed count, so that a workspace sized on one device fits
-// the call on another and results do not depend on the device).
+// Partial rows of dweight and dbias of the kernel of a warp a row: blocks whose rows are
+// summed apart (two for each of a GB300's 152 SMs; the stream kernel has up to 16 for
+// each).  Fixed counts, so that a workspace sized on one device fits the call on
+// another and results do not depend on the device.
 constexpr int64_t kNormParts = 304;
 struct NormBackwardArgs {
   bool layer = false;        // layer norm, or RMS norm

@@ -839,10 +839,13 @@ cudaError_t launch_stream(const NormBackwardArgs& n, const BackwardPtrs& p, int 
   if (!kShift && threads * kP == chunks)
     kernel = norm_backward_stream_kernel<T, kP, kLayer, kRes, !kShift, kShift>;
   const int one = (2 + kRes + (p.dh && p.dx ? 1 : 0)) * chunks * 16;
-  // What is under way on an SM: 132 KB and two rows at least.  Less leaves the
-  // memory waiting, more makes reads and writes get in each other's way (8192 x 7168
-  // RMS, of 43 KB a row, two rows 75.5 us, three 73.7, four 77.6, five 80.3; 57344 x
-  // 1024, of 48 KB in eight blocks, two 75.1, three 78.8, four 81.1).
+  // What is under way on an SM: 132 KB, and two rows at least where they fit (room).
+  // Less leaves the memory waiting, more makes reads and writes get in each other's way
+  // (8192 x 7168 RMS, of 43 KB a row, two rows 75.5 us, three 73.7, four 77.6, five 80.3;
+  // 57344 x 1024, of 48 KB in eight blocks, two 75.1, three 78.8, four 81.1).  fp32 rows
+  // with a residual and dh have room for one in the upper sixth of each range of
+  // stream_blocks (865 to 1024 columns, 1729 to 2048, 3457 to 4096, 6913 to 8192): a
+  // block then copies no row ahead (4096 x 7168 layer form 102 us, 86% of the copy rate).
   const int room = 216 * 1024 / stream_blocks(n.T, n.d) / one;
   int stages = 132 * 1024 / stream_blocks(n.T, n.d) / one;
   stages = stages < 2 ? 2 : stages > kStreamStages ? kStreamStages : stages;
@@ -941,7 +944,7 @@ cudaError_t dispatch(const NormBackwardArgs& n, cudaStream_t stream) {
   if (n.d <= kShort) {
     err = launch_warps<T, N, 8 / N, kLayer, 2>(n, p, parts, stream);
   } else if (!streamed) {
-    if constexpr (!kShift) err = launch_warps<T, N, 32 / N, kLayer, 1>(n, p, parts, stream);
+    if constexpr (!kShift && !kLayer) err = launch_warps<T, N, 32 / N, false, 1>(n, p, parts, stream);
   } else {
     err = n.r ? launch_stream<T, kLayer, true, kShift>(n, p, parts, stream)
               : launch_stream<T, kLayer, false, kShift>(n, p, parts, stream);
