@@ -256,8 +256,9 @@ __device__ __forceinline__ uint32_t held_codes(uint32_t code, uint32_t old, uint
   for (int k = 0; k < 4; k += 2) {
     float a, b;
     split(mul2(make_pair2(q[k], q[k + 1]), make_pair2(0x1p-120f, 0x1p-120f)), a, b);
-    c[k] = __float_as_uint(a) * 16u + ((h[k / 2] >> 8 & 0xffff00u) | 0x80u);  // past the sign
-    c[k + 1] = __float_as_uint(b) * 16u + ((h[k / 2] << 8 & 0xffff00u) | 0x80u);
+    // the sign goes; a scale of a few bits, below 2^-133, may leave q above 448
+    c[k] = min(__float_as_uint(a) * 16u + ((h[k / 2] >> 8 & 0xffff00u) | 0x80u), 0x7effffffu);
+    c[k + 1] = min(__float_as_uint(b) * 16u + ((h[k / 2] << 8 & 0xffff00u) | 0x80u), 0x7effffffu);
   }
   const uint32_t mask = (held >> 7) * 0x7fu;
   return (code & ~mask) | (top_bytes(c[0], c[1], c[2], c[3]) & mask);
@@ -404,7 +405,7 @@ __device__ __forceinline__ void step8(const AdamwTensor& t, const AdamwScalars& 
     uint2 mc = make_uint2(e4m3x2(m[0], m[1]) | e4m3x2(m[2], m[3]) << 16,
                           e4m3x2(m[4], m[5]) | e4m3x2(m[6], m[7]) << 16);
     // a code below 8 is of less than 2^-6 scales (c.held_below; all may be held: inf)
-    if (mmin < c.held_below * ms && mm < __int_as_float(0x7f800000)) {
+    if (mmin <= __fmul_ru(c.held_below, ms) && mm < __int_as_float(0x7f800000)) {
       // the old codes are still there; read again, as kept they would cost registers
       const uint2 old = kFull ? *reinterpret_cast<const uint2*>(static_cast<const uint8_t*>(t.m) + at)
                               : load_codes_tail(t.m, at, n);
@@ -426,7 +427,7 @@ __device__ __forceinline__ void step8(const AdamwTensor& t, const AdamwScalars& 
 // with about three quarters of the issue slots taken; without the master copy 134M
 // take 349 us, bound by the instructions (about 80 an element).  Of these the range
 // check of m and the codes that it is rounded at random are 2 to 4% (895 and 337
-// without them), and 17% with beta1 above 29/32, where every code is looked at (396).
+// without them), and 17% with beta1 above 29/32, where every code is looked at (398).
 // With products and roots one at a time instead of in pairs 938, with the library's
 // roots and quotients 1177 (before those two).
 template <typename P, typename G, bool k8, bool kMany>
