@@ -31,7 +31,8 @@
  *     before anything is enqueued.  Errors found on the device (an expert
  *     index out of range, a bounded wait that expired) are written to the
  *     status word at the start of the workspace; read them with
- *     moe_get_device_status().  No exception crosses this interface.
+ *     moe_get_device_status().  The word has to be 0 before the first of them:
+ *     zero a workspace once, or read its status once.  No exception crosses this interface.
  *   - The same workspace may not be used by two calls that run concurrently.
  *     moe_workspace_size(cfg, T) bytes suffice for every call below with
  *     that cfg and a row count <= T.
@@ -496,8 +497,9 @@ int32_t moe_add_rmsnorm(int32_t dtype, int64_t T, int32_t d, const void* x, cons
 
 /*
  * Training around the experts' products.  A caller with its own expert
- * products runs moe_router_from_logits (or moe_router), moe_permute and
- * moe_gather, its products on the rows of each expert
+ * products runs moe_router_from_logits on its fp32 logits x W_r^T, which
+ * moe_router_backward needs again (moe_router forms them and gives none), moe_permute
+ * and moe_gather, its products on the rows of each expert
  * (x_perm[offsets[e]] .. x_perm[offsets[e + 1] - 1]), and moe_combine; and back
  * through moe_combine_backward, its products' gradients, moe_combine again
  * (the gradient of moe_gather) and moe_router_backward.
