@@ -610,7 +610,7 @@ class AdamwTable:
 
 
 _ADAMW_TYPES = {"torch.float32": MOE_F32, "torch.bfloat16": MOE_BF16}
-_ADAMW_BITS = {"torch.float32": 32, "torch.uint8": 8, "torch.float8_e4m3fn": 8}
+_ADAMW_BITS = {"torch.float32": 32, "torch.uint8": 8, "torch.int8": 8, "torch.float8_e4m3fn": 8}
 
 
 def adamw_table(tensors: Sequence[dict]) -> AdamwTable:
@@ -618,8 +618,8 @@ def adamw_table(tensors: Sequence[dict]) -> AdamwTable:
     ``exp_avg``, ``exp_avg_sq`` and, or None, ``master``, ``exp_avg_scale``,
     ``exp_avg_sq_scale`` (contiguous tensors on one GPU), ``n`` (param's size
     when missing) and ``weight_decay`` (0 when missing).  Params and gradients are
-    float32 or bfloat16, the same for all, states float32, uint8 or float8_e4m3fn,
-    the same for all, the rest float32.  Raises ValueError for other types, for
+    float32 or bfloat16, the same for all, states float32 or codes (uint8, int8 or
+    float8_e4m3fn), the same for all, the rest float32.  Raises ValueError for other types, for
     tensors that are not contiguous, on several devices, or smaller than n, and for
     a buffer that overlaps one that the step writes."""
     entries = (AdamwTensor * len(tensors))()

@@ -5,8 +5,6 @@ import subprocess
 
 import pytest
 
-from fine_grained_sparse_gb300 import build as b
-
 CALL = {"load": "auto v = fgs::load<{n}>(p); q[0] = v.v[0];",
         "store": "const float v[{n}] = {{}}; fgs::store<{n}>(p, v); q[0] = v[0];"}
 
@@ -16,6 +14,8 @@ CALL = {"load": "auto v = fgs::load<{n}>(p); q[0] = v.v[0];",
                                           ("__nv_bfloat16", 8, True), ("float", 4, True)])
 @pytest.mark.parametrize("call", ["load", "store"])
 def test_sizes(call, type_, n, fits, tmp_path):
+    import __graft_entry__
+    b = __graft_entry__._build_module()
     src = tmp_path / "t.cu"
     src.write_text('#include "rows.cuh"\n__global__ void k(' + type_ + "* p, float* q) { "
                    + CALL[call].format(n=n) + " }\n")
