@@ -264,8 +264,10 @@ __device__ __forceinline__ float4 block_sum4(float v0, float v1, float v2, float
 // Taking m^2 off multiplies the roundings of the mean square by (v + m^2) / v, v the
 // variance: by 1.03 for rows like one another's values, whose m is a fifth of a
 // standard deviation, but by up to d / 32 where the first values are unlike the rest.
-// So where m^2 exceeds v the block takes the sums once more, about mu.  (s - P is off
-// by half an ulp of at most sqrt(d / 32) + |s - mu| / sigma standard deviations.)
+// And the roundings of the sum of s - P, of values of m where most of the row lies there,
+// are those of m.  So where m^2 exceeds v / 4 (one row in 200 of like values) the block
+// takes the sums once more, about mu.  (s - P is off by half an ulp of at most sqrt(d / 32)
+// + |s - mu| / sigma standard deviations.)
 //
 // kShift: rows that are not whole chunks begin inside one.  A block's rows are a
 // multiple of N apart, so that all of them begin at the same value of their first
@@ -424,7 +426,7 @@ __global__ void __launch_bounds__(512, 1)
       refill();
       float mu = t.z * inv_d;
       ms = fmaf(-mu, mu, t.x * inv_d);
-      if (mu * mu > ms) {  // the same in all threads
+      if (4.0f * mu * mu > ms) {  // the same in all threads
         turn ^= 1;
         // what is not the row's takes mu, for 0 to the sums
 #pragma unroll

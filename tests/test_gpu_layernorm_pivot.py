@@ -49,6 +49,23 @@ def test_forward_odd_rows(T, d, dtype, residual):
     assert torch.equal(xd.cpu(), h) and torch.equal(out.cpu(), y)
 
 
+@pytest.mark.parametrize("others", [0, 1, 3])
+@pytest.mark.parametrize("T,d", [(2485, 1042), (3100, 577), (400, 7001)])
+def test_forward_one_value_far_off(T, d, others):
+    """One of the first values 1000 or 10000 deviations off, and as far off on either
+    side some behind: the rest of the row lies about a deviation off the pivot, and its
+    sum's roundings are not to be those of such values."""
+    need_gpu()
+    fgs = lib()
+    for k in (1e3, 1e4):
+        _, _, w, b, _, _ = _inputs(1, d, "f32")
+        x = torch.randn((T, d), generator=torch.Generator().manual_seed(4))
+        x[:, 5] += k
+        for j in range(others):
+            x[:, 200 + 100 * j] += k if j % 2 else -k
+        _check_forward("f32", x, None, w, b, *_forward(fgs, "f32", x, None, w, b))
+
+
 def _check(dtype, x, r, w, dy, dh, got):
     """As _check_backward, but dx ends in three roundings of its size where dh makes
     it up: of dh - r mean g, of the sum of that and r u c, and of the sum of that
