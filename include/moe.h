@@ -617,7 +617,8 @@ int32_t moe_norm_backward(int32_t kind, int32_t dtype, int64_t T, int32_t d, con
  *   subnormal of E4M3) or beta1 > 29/32: nearest could hold such an m for ever
  *   where no gradient comes, and it is rounded at random.  So are the codes of r
  *   (nearest would hold a slow v where it is): |m| / scale and r / scale are rounded
- *   up with the probability of what lies above the code below, to the nearest 2^-16,
+ *   up with the probability of what lies above the code below, to the nearest 2^-16
+ *   and to 448 at most,
  *   by 16 random bits an element: of h, the MurmurHash3 finaliser of j ^ key ^ (j >> 32)
  *   0x9E3779B9 in 32 bits, j the number of the element's pair in its tensor, for r
  *   the low half for the even element and the high for the odd, for m the other; key: the
