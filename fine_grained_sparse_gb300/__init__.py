@@ -672,13 +672,15 @@ def adamw_table(tensors: Sequence[dict]) -> AdamwTable:
 
 
 def moe_adamw(table, param_dtype, grad_dtype, state_bits, lr, beta1, beta2, eps, step,
-              grad_scale=None, seed=0, stream=None):
+              grad_scale=None, seed=None, stream=None):
     """One AdamW step over the tensors of an AdamwTable.  Raises ValueError where
-    their types are others than the call's."""
+    their types are others than the call's.  ``seed``: of 8-bit states' random
+    roundings, another in every step; the step's number when missing (the same bits in
+    every step would hold a moment where it is)."""
     given = (param_dtype, grad_dtype, state_bits)
     if table.types != given and any(a not in (None, b) for a, b in zip(table.types, given)):
         raise ValueError(f"moe_adamw: types (param_dtype, grad_dtype, state_bits) {given} for a "
                          f"table of {table.types}")
     _check(lib.moe_adamw(len(table), ctypes.addressof(table.entries), param_dtype, grad_dtype,
-                         state_bits, lr, beta1, beta2, eps, step, _ptr(grad_scale), seed,
-                         _stream(stream)), "moe_adamw")
+                         state_bits, lr, beta1, beta2, eps, step, _ptr(grad_scale),
+                         step if seed is None else seed, _stream(stream)), "moe_adamw")

@@ -627,7 +627,8 @@ int32_t moe_norm_backward(int32_t kind, int32_t dtype, int64_t T, int32_t d, con
  *   block of 128 with a value that is not finite has NaN codes or a scale
  *   that is not finite.  Pass another seed in every step (the step's number
  *   does).
- * lr, step and seed are values of the call: a captured call repeats them.
+ * lr, step and seed are values of the call: a captured call repeats them (and
+ * rounds 8-bit states alike in every replay, which can hold a moment where it is).
  * One launch takes up to 256 tensors.  Needs no workspace. */
 int32_t moe_adamw(int32_t n_tensors, const moe_adamw_tensor* tensors_host, int32_t param_dtype,
                   int32_t grad_dtype, int32_t state_bits, double lr, double beta1, double beta2,

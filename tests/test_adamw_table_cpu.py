@@ -165,3 +165,19 @@ def test_set_grads_refuses(fgs, bad):
         t.set_grads(g)
     assert [e.grad for e in t.entries] == [a["grad"].at, b["grad"].at]
     assert t.grads == [a["grad"], b["grad"]]
+
+
+def test_seed_of_a_step(fgs, monkeypatch):
+    """Without one the step's number: random roundings differ from step to step."""
+    seen = []
+
+    class Lib:
+        def moe_adamw(self, *args):
+            seen.append(args)
+            return 0
+    monkeypatch.setattr(fgs, "lib", Lib())
+    for step in (1, 2, 1000):
+        fgs.moe_adamw(fgs.adamw_table([]), 1, 1, 8, 1e-3, 0.9, 0.95, 1e-8, step, stream=0)
+    fgs.moe_adamw(fgs.adamw_table([]), 1, 1, 8, 1e-3, 0.9, 0.95, 1e-8, 7, None, 0, 0)
+    fgs.moe_adamw(fgs.adamw_table([]), 1, 1, 8, 1e-3, 0.9, 0.95, 1e-8, 7, seed=55, stream=0)
+    assert [a[11] for a in seen] == [1, 2, 1000, 0, 55]
